@@ -443,6 +443,176 @@ rw4_status rw4_w4a4_gemm_g(const uint8_t* qa, const float* sa, const uint8_t* qw
 rw4_status rw4_dequantize_g(const uint8_t* q, const float* s, int64_t M, int64_t K, int32_t group, void* out,
                             rw4_dtype out_dtype, int64_t ldo, void* stream);
 
+/* ---- Serving with an INT4 KV cache ---------------------------------------
+ * The Rotated Runtime Smooth page's experimental setup quantizes the KV
+ * cache symmetrically (round to nearest) in groups of the head's channels,
+ * and the OstQuant page, section 3.2, puts an extra Hadamard on queries and
+ * keys after the rotary positions.  Four calls run a decoder layer's
+ * attention on such a cache, all asynchronous, allocation-free and safe
+ * under HIP graph capture:
+ *   rw4_kv_slots      pages and slots for the step's new tokens
+ *   rw4_qk_norm_rope  norms of queries and keys and their rotary positions
+ *   rw4_kv_append     the same, then rotate, quantize and store keys, values
+ *   rw4_kv_attention  attention of the step's queries over the cache
+ * Lengths, tables and positions live on the device and are never copied to
+ * the host; what cannot be checked there without a copy is checked in the
+ * kernels, as each call says, so that no value in them reads or writes out
+ * of bounds. */
+
+/* A paged INT4 KV cache, owned by the caller (this host struct is read
+ * during the call only; its pointers are device pointers).  Row (page, head,
+ * slot) holds the head_dim codes of one token's key (value) in the stored
+ * form of rw4_quantize_act, head_dim / 2 bytes, and one fp32 scale:
+ *   codes + page * code_page + head * code_head + slot * code_slot  (bytes)
+ *   scales + page * scale_page + head * scale_head + slot * scale_slot
+ * (floats).  [pages, heads, page_size, ...] contiguous reads fastest; the
+ * rows [pages * page_size, heads * head_dim] that rw4_quantize_act_g writes
+ * (group = head_dim = the Hadamard block) are such a cache too, with
+ * code_head = head_dim / 2 and scale_head = 1.
+ *   head_dim 64, 128 or 256; page_size a power of two in [16, 2^20];
+ *   pages in [1, 2^31) with pages * page_size < 2^31 * 16; heads in
+ *   [1, 1024]; code pointers 16-byte aligned, scale pointers 4-byte; code
+ *   strides multiples of 16; strides in [0, 2^40), rows must not overlap. */
+typedef struct {
+  uint8_t* k_codes;
+  float* k_scales;
+  uint8_t* v_codes;
+  float* v_scales;
+  int64_t pages;
+  int32_t page_size;
+  int32_t heads;
+  int32_t head_dim;
+  int64_t code_page, code_head, code_slot;
+  int64_t scale_page, scale_head, scale_slot;
+} rw4_kv_cache;
+
+/* kv_slots: the pages and slots of one step's new tokens, from the lengths
+ * of B requests (B <= 4096).  Request b holds ctx_len[b] tokens in the pages
+ * block_table[b][0 .. ceil(ctx_len[b] / page_size)) and
+ *   new_len[b] >= 0  adds that many tokens: the pages it lacks are taken off
+ *                    the free list, in request order, and written behind its
+ *                    pages in block_table; kv_len[b] = ctx_len + new_len.
+ *                    A request whose pages do not fit in table_width is
+ *                    refused and takes none; from the first request that
+ *                    the free list cannot give all its pages, every request
+ *                    that needs a page is refused.  Refused: kv_len[b] =
+ *                    ctx_len[b], its tokens get slot and position -1.
+ *   new_len[b] < 0   has finished: its pages go back to the free list (to be
+ *                    handed out from the next call on), kv_len[b] = 0; its
+ *                    row of block_table is left as it is.
+ * The free list is a ring of `capacity` entries (capacity >= the pool's
+ * pages): free_state = {head, count}, entries free_pages[(head + i) %
+ * capacity], i < count.  Pages are taken at the head and returned at the
+ * tail.  The new state goes to free_state_out.
+ *   served [B] int32: 1, or 0 where refused; cu_new [B + 1] int32: the
+ *   starts of the requests' tokens, cu_new[b + 1] - cu_new[b] =
+ *   max(new_len[b], 0), refused requests included;
+ *   slot_map [tokens] int64: page * page_size + offset of each new token in
+ *   that order; positions [tokens] int32: its place in its request.  Tokens
+ *   beyond cu_new[B] get -1 in both, tokens beyond `tokens` are not written.
+ * free_state_out may be free_state and kv_len may be ctx_len (the call then
+ * takes two launches instead of one when `tokens` is large); no other
+ * output may overlap an input.  Lengths below 0 count as 0 in ctx_len, a
+ * table entry below 0 gives slot -1, free_state is clamped to the ring, and
+ * a return that the ring has no room for is dropped.
+ * page_size a power of two in [1, 2^20]; table_width >= 0, its rows
+ * contiguous; capacity >= 1; tokens >= 0. */
+rw4_status rw4_kv_slots(const int32_t* ctx_len, const int32_t* new_len, int64_t B, int32_t page_size,
+                        int32_t* block_table, int64_t table_width, int32_t* free_pages, int64_t capacity,
+                        const int32_t* free_state, int32_t* free_state_out, int32_t* kv_len, int32_t* cu_new,
+                        int32_t* served, int64_t* slot_map, int32_t* positions, int64_t tokens, void* stream);
+
+/* qk_norm_rope: per-head RMS norm and rotary positions of queries [T, heads,
+ * head_dim] and keys [T, kv_heads, head_dim] in one pass:
+ *   y = x * w / sqrt(mean(x^2) + eps)          (w NULL: y = x),
+ *   (y_i, y_j) -> (y_i c - y_j s, y_j c + y_i s), c, s = cos, sin of row
+ *   positions[t] of cos_sin, for the pairs (i, i + rot / 2), or (2i, 2i + 1)
+ *   with `interleaved`, of the first rot channels   (cos_sin NULL: none),
+ *   y H_D / sqrt(D) when rotate != 0 (the head's Hadamard, Sylvester order),
+ * evaluated in fp32 and rounded once to out_dtype.
+ *   q, k: elements of x_dtype, unit stride in a head, strides in elements
+ *   (*_token, *_head), 16-byte aligned heads; kv_heads = 0: queries only (k
+ *   not read); outputs likewise, their heads apart from each other.  Outputs may be the inputs (same dtype and
+ *   strides); other overlaps are not allowed.
+ *   q_weight, k_weight: fp32 [head_dim] or NULL;
+ *   cos_sin: fp32 [max_pos, rot], rot / 2 cosines then rot / 2 sines a row;
+ *   positions: int32 [T].  A token whose position is outside [0, max_pos) is
+ *   skipped: its outputs are left as they were (padding of a batch).
+ *   head_dim 64, 128 or 256; rot a multiple of 16 in [16, head_dim];
+ *   heads >= 1; heads and kv_heads <= 1024; eps >= 0 and finite. */
+rw4_status rw4_qk_norm_rope(const void* q, int64_t q_token, int64_t q_head, const void* k, int64_t k_token,
+                            int64_t k_head, rw4_dtype x_dtype, int64_t T, int32_t heads, int32_t kv_heads,
+                            int32_t head_dim, const float* q_weight, const float* k_weight, float eps,
+                            const float* cos_sin, int64_t max_pos, int32_t rot, int32_t interleaved,
+                            const int32_t* positions, int32_t rotate, void* q_out, int64_t qo_token, int64_t qo_head,
+                            void* k_out, int64_t ko_token, int64_t ko_head, rw4_dtype out_dtype, void* stream);
+
+/* kv_append: new tokens into the cache.  Keys: norm and rotary positions as
+ * rw4_qk_norm_rope; values as they are; then, for both, the head's Hadamard
+ * (rotate != 0) and symmetric INT4 with one scale per (token, head):
+ *   u = y H_D (unnormalized), m = max|u|, code = rne(7 u / m), scale =
+ *   m / (7 sqrt(D))   (rotate = 0: u = y, scale = m / 7),
+ * stored in row slot_map[t] of the cache (page slot / page_size, slot
+ * slot % page_size).  Codes are those of the exact quotient of the row as
+ * evaluated in fp64, ties to even.  A row with an infinity or NaN gets the
+ * scale NaN and codes 0 (rotate = 0 as well), a row of zeros scale 0 and
+ * codes 0.  Queries (optional, q NULL: none): as rw4_qk_norm_rope with the
+ * same rotate, into q_out.
+ *   k, v [T, cache heads, head_dim] of x_dtype, strides in elements
+ *   (*_token, *_head), 16-byte aligned heads; slot_map int64 [T].  A token
+ *   whose slot is outside [0, pages * page_size) stores nothing, and one
+ *   whose position is outside [0, max_pos) (cos_sin not NULL) is skipped
+ *   altogether; two tokens must not share a slot.  Other arguments as
+ *   rw4_qk_norm_rope. */
+rw4_status rw4_kv_append(const rw4_kv_cache* cache_host, const void* k, int64_t k_token, int64_t k_head, const void* v,
+                         int64_t v_token, int64_t v_head, const int64_t* slot_map, const void* q, int64_t q_token,
+                         int64_t q_head, int32_t heads, rw4_dtype x_dtype, int64_t T, const float* q_weight,
+                         const float* k_weight, float eps, const float* cos_sin, int64_t max_pos, int32_t rot,
+                         int32_t interleaved, const int32_t* positions, int32_t rotate, void* q_out, int64_t qo_token,
+                         int64_t qo_head, rw4_dtype out_dtype, void* stream);
+
+/* Bytes of device workspace rw4_kv_attention needs for T query tokens of B
+ * requests (partial results where a long request is split); 0 for invalid
+ * sizes. */
+int64_t rw4_kv_attention_workspace_bytes(int64_t T, int64_t B, int32_t heads, int32_t kv_heads, int32_t head_dim);
+
+/* kv_attention: softmax attention of query tokens over the cache.  Request b
+ * owns the query tokens cu_q[b] .. cu_q[b + 1] and the first kv_len[b] cached
+ * tokens, token j in slot j % page_size of page block_table[b][j /
+ * page_size]; its query token i stands at place p = kv_len[b] - q_len + i
+ * (the step's own tokens are in the cache already).  Query head h reads KV
+ * head h / (heads / cache heads).
+ *   s_j = scale * sum_d q_d ck[j, d] sk[j],   over the j < kv_len[b] with
+ *   j <= p (causal) and j > p - window (window > 0),
+ *   out = sum_j softmax(s)_j cv[j, :] sv[j],  times H_D / sqrt(D) when
+ *   unrotate != 0 (undoing the rotation of the stored values),
+ *   lse (optional) = log sum_j exp(s_j).
+ * A row with no visible key gets out = 0 and lse = -infinity.  Queries are in
+ * the rotated domain when the cache is (kv_append's or qk_norm_rope's rotate,
+ * or rw4_rotate_act).  causal = 0 is attention to another sequence's states.
+ * Scores, softmax and sums are fp32; bf16 output: probabilities enter the
+ * product rounded to bf16, fp32 output: as three bf16 parts (exact).
+ *   q, out [T, heads, head_dim] of q_dtype / out_dtype, strides in elements
+ *   (*_token, *_head), 16-byte aligned heads; lse fp32 [T, heads] or NULL;
+ *   block_table int32 [B][table_width]; kv_len int32 [B]; cu_q int32 [B+1].
+ *   max_q_len: the largest number of query tokens of a request; chooses the
+ *   kernel, results do not depend on it.  window > 0 needs causal.
+ *   B <= 65535; heads a multiple of the cache heads, at most 64 query heads
+ *   per KV head; scale finite.
+ * Checked in the kernel: kv_len is clamped to [0, table_width * page_size],
+ * cu_q to [0, T] and rising order; a token whose page is outside [0, pages)
+ * is not visible.  Query tokens of no request are left as they were.  out
+ * must not overlap q.
+ *   workspace: rw4_kv_attention_workspace_bytes bytes, 16-byte aligned,
+ *   owned by the caller, overwritten; calls that may overlap in time need
+ *   one each. */
+rw4_status rw4_kv_attention(const rw4_kv_cache* cache_host, const void* q, rw4_dtype q_dtype, int64_t q_token,
+                            int64_t q_head, int64_t T, int32_t heads, const int32_t* block_table, int64_t table_width,
+                            const int32_t* kv_len, const int32_t* cu_q, int64_t B, int64_t max_q_len, float scale,
+                            int32_t causal, int64_t window, int32_t unrotate, void* out, rw4_dtype out_dtype,
+                            int64_t out_token, int64_t out_head, float* lse, void* workspace, int64_t workspace_bytes,
+                            void* stream);
+
 /* Static description of a status code. */
 const char* rw4_status_str(rw4_status s);
 

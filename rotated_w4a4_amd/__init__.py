@@ -28,6 +28,8 @@ __all__ = [
     "permute_codes", "prepare_permute_codes", "decode_fused", "prepare_decode_fused",
     "quantize_act_asym", "prepare_quantize_act_asym", "weight_code_sums", "w4a4_gemm_asym", "prepare_w4a4_gemm_asym",
     "dequantize_asym", "mixed_tables", "quantize_act_mixed", "prepare_quantize_act_mixed", "extend_weight_groups",
+    "KVCache", "KVSlots", "kv_slots", "prepare_kv_slots", "rope_table", "qk_norm_rope", "prepare_qk_norm_rope",
+    "kv_append", "prepare_kv_append", "kv_attention", "prepare_kv_attention", "kv_attention_workspace_bytes",
     "status_str", "version", "EXPORTED_SYMBOLS",
 ]
 
@@ -45,7 +47,8 @@ EXPORTED_SYMBOLS = (
     "rw4_dequantize_g", "rw4_w4a4_gemm_g", "rw4_rotate_act", "rw4_quantize_act_static", "rw4_status_str",
     "rw4_version", "rw4_rrs_reorder_workspace_bytes", "rw4_quantize_act_rrs_reorder", "rw4_pack_weight_per_channel",
     "rw4_permute_codes", "rw4_decode_fused", "rw4_quantize_act_asym", "rw4_weight_code_sums", "rw4_w4a4_gemm_asym",
-    "rw4_dequantize_asym", "rw4_quantize_act_mixed", "rw4_extend_weight_groups",
+    "rw4_dequantize_asym", "rw4_quantize_act_mixed", "rw4_extend_weight_groups", "rw4_kv_slots", "rw4_qk_norm_rope",
+    "rw4_kv_append", "rw4_kv_attention_workspace_bytes", "rw4_kv_attention",
 )
 
 
@@ -100,7 +103,8 @@ lib.rw4_dequantize_asym.argtypes = [_p, _p, _p, _i64, _i64, _p, ctypes.c_int, _i
 lib.rw4_quantize_act_mixed.argtypes = [_p, _p, ctypes.c_int, _i64, _i64, _p, _i64, _p, _p, _p]
 lib.rw4_extend_weight_groups.argtypes = [_p, _p, _i64, _i64, _p, _i64, _p, _p, _p]
 for _name in EXPORTED_SYMBOLS:
-    if _name not in ("rw4_status_str", "rw4_version", "rw4_transform_k", "rw4_rrs_reorder_workspace_bytes"):
+    if _name not in ("rw4_status_str", "rw4_version", "rw4_transform_k", "rw4_rrs_reorder_workspace_bytes",
+                     "rw4_kv_attention_workspace_bytes"):
         getattr(lib, _name).restype = ctypes.c_int
 
 
@@ -728,3 +732,8 @@ def prepare_w4a4_gemm(qa, sa, qw, sw, out_dtype=None, out=None) -> Call:
     args = (qa.data_ptr(), sa.data_ptr(), qw.data_ptr(), sw.data_ptr(), M, N, K, group, out.data_ptr(),
             _dtype_code(out), out.stride(0))
     return Call(lib.rw4_w4a4_gemm_g, args, dev, "rw4_w4a4_gemm", (qa, sa, qw, sw), out)
+
+
+from .kv import (  # noqa: E402  (the binding of the kv calls builds on the names above)
+    KVCache, KVSlots, kv_append, kv_attention, kv_attention_workspace_bytes, kv_slots, prepare_kv_append,
+    prepare_kv_attention, prepare_kv_slots, prepare_qk_norm_rope, qk_norm_rope, rope_table)

@@ -1,15 +1,19 @@
 // C ABI of the rotated W4A4 library: argument checks, transform objects,
 // dispatch to the kernel launchers.  See include/rw4.h for the contract.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <new>
+#include <utility>
 #include <vector>
 
 #include <hip/hip_runtime.h>
 
 #include "../../include/rw4.h"
+#include "kv_internal.h"
 #include "rw4_internal.h"
 
 struct rw4_transform {
@@ -606,6 +610,238 @@ rw4_status rw4_w4a4_gemm(const uint8_t* qa, const float* sa, const uint8_t* qw, 
                          int64_t M, int64_t N, int64_t K, void* y, rw4_dtype y_dtype, int64_t ldy,
                          void* stream) {
   return rw4_w4a4_gemm_g(qa, sa, qw, sw, M, N, K, 128, y, y_dtype, ldy, stream);
+}
+
+// ---- Serving with an INT4 KV cache ----
+
+static bool dtype_known(rw4_dtype d) { return d == RW4_F32 || d == RW4_BF16; }
+static bool head_dim_known(int32_t d) { return d == 64 || d == 128 || d == 256; }
+// Sizes and strides of device arrays stay below this, so that no product of
+// a stride and an index leaves 64 bits.
+constexpr int64_t kMaxStride = int64_t(1) << 40;
+constexpr int32_t kMaxHeads = 1024;
+constexpr int64_t kMaxTokens = int64_t(1) << 31;
+
+static int log2_of(int64_t v) {
+  int n = 0;
+  while ((int64_t(1) << n) < v) ++n;
+  return n;
+}
+
+// Whether the rows (of `unit` elements) of a strided array of up to 3
+// dimensions lie apart from each other.
+static bool rows_apart(std::initializer_list<std::pair<int64_t, int64_t>> size_stride, int64_t unit) {
+  std::pair<int64_t, int64_t> d[3];  // (stride, size), by rising stride
+  int n = 0;
+  for (const auto& x : size_stride)
+    if (x.first > 1) d[n++] = {x.second, x.first};
+  std::sort(d, d + n);
+  for (int i = 0; i < n; ++i) {
+    if (d[i].first < unit) return false;
+    unit += d[i].first * (d[i].second - 1);  // sizes below 2^31, strides below 2^40: the next stride ends it
+    if (unit < 0 || unit > (int64_t(1) << 62)) return i + 1 == n;
+  }
+  return true;
+}
+
+// A strided [tokens, heads, D] array with 16-byte rows.
+static bool rows_ok(const void* p, int64_t token, int64_t head, rw4_dtype dt) {
+  const int64_t esz = dt == RW4_BF16 ? 2 : 4;
+  return p && aligned16(p) && token >= 0 && head >= 0 && token < kMaxStride && head < kMaxStride &&
+         (token * esz) % 16 == 0 && (head * esz) % 16 == 0;
+}
+
+static rw4_status kv_cache_of(const rw4_kv_cache* c, rw4::KvCache* out) {
+  if (!c) return RW4_ERR_ARG;
+  if (!head_dim_known(c->head_dim) || !pow2(c->page_size) || c->page_size < 16 || c->page_size > (1 << 20) ||
+      c->pages < 1 || c->pages > 0x7FFFFFFF || c->heads < 1 || c->heads > kMaxHeads)
+    return RW4_ERR_SHAPE;
+  const int log2_page = log2_of(c->page_size);
+  if ((c->pages << log2_page) >= int64_t(16) * kMaxTokens) return RW4_ERR_SHAPE;
+  if (!c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales) return RW4_ERR_ARG;
+  if (!aligned16(c->k_codes) || !aligned16(c->v_codes)) return RW4_ERR_ARG;
+  if ((reinterpret_cast<uintptr_t>(c->k_scales) & 3u) || (reinterpret_cast<uintptr_t>(c->v_scales) & 3u))
+    return RW4_ERR_ARG;
+  for (int64_t v : {c->code_page, c->code_head, c->code_slot})
+    if (v < 0 || v >= kMaxStride || v % 16) return RW4_ERR_ARG;
+  for (int64_t v : {c->scale_page, c->scale_head, c->scale_slot})
+    if (v < 0 || v >= kMaxStride) return RW4_ERR_ARG;
+  if (!rows_apart({{c->pages, c->code_page}, {c->heads, c->code_head}, {c->page_size, c->code_slot}}, c->head_dim / 2) ||
+      !rows_apart({{c->pages, c->scale_page}, {c->heads, c->scale_head}, {c->page_size, c->scale_slot}}, 1))
+    return RW4_ERR_ARG;
+  *out = rw4::KvCache{c->k_codes, c->k_scales, c->v_codes, c->v_scales, c->pages, c->pages << log2_page, log2_page,
+                      c->heads, c->code_page, c->code_head, c->code_slot, c->scale_page, c->scale_head, c->scale_slot};
+  return RW4_OK;
+}
+
+rw4_status rw4_kv_slots(const int32_t* ctx_len, const int32_t* new_len, int64_t B, int32_t page_size,
+                        int32_t* block_table, int64_t table_width, int32_t* free_pages, int64_t capacity,
+                        const int32_t* free_state, int32_t* free_state_out, int32_t* kv_len, int32_t* cu_new,
+                        int32_t* served, int64_t* slot_map, int32_t* positions, int64_t tokens, void* stream) {
+  if (B < 0 || B > 4096 || !pow2(page_size) || page_size > (1 << 20) || table_width < 0 ||
+      table_width > 0x7FFFFFFF || capacity < 1 || capacity > 0x7FFFFFFF || tokens < 0 || tokens > 0x7FFFFFFF)
+    return RW4_ERR_SHAPE;
+  if (!free_pages || !free_state || !free_state_out || !cu_new) return RW4_ERR_ARG;
+  if (B > 0 && (!ctx_len || !new_len || !kv_len || !served || (table_width > 0 && !block_table))) return RW4_ERR_ARG;
+  if (tokens > 0 && (!slot_map || !positions)) return RW4_ERR_ARG;
+  const rw4::SlotsArgs a{ctx_len, new_len, B, log2_of(page_size), block_table, table_width, free_pages, capacity,
+                         free_state, free_state_out, kv_len, cu_new, served, slot_map, positions, tokens};
+  return from_hip(rw4::launch_kv_slots(a, static_cast<hipStream_t>(stream)));
+}
+
+// The checks that rw4_qk_norm_rope and rw4_kv_append share: sizes, then (with
+// tokens) the rotary arguments.
+static rw4_status rows_args_ok(rw4_dtype x_dtype, rw4_dtype out_dtype, int64_t T, float eps) {
+  if (!dtype_known(x_dtype) || !dtype_known(out_dtype)) return RW4_ERR_ARG;
+  if (T < 0 || T >= kMaxTokens) return RW4_ERR_SHAPE;
+  if (!(eps >= 0.0f) || !std::isfinite(eps)) return RW4_ERR_ARG;
+  return RW4_OK;
+}
+static rw4_status rope_args_ok(const float* cos_sin, int64_t max_pos, int32_t rot, const int32_t* positions,
+                               int32_t head_dim) {
+  if (!cos_sin) return RW4_OK;
+  if (rot < 16 || rot % 16 || rot > head_dim || max_pos < 1 || max_pos > 0x7FFFFFFF) return RW4_ERR_SHAPE;
+  if (!positions || !aligned16(cos_sin)) return RW4_ERR_ARG;
+  return RW4_OK;
+}
+
+rw4_status rw4_qk_norm_rope(const void* q, int64_t q_token, int64_t q_head, const void* k, int64_t k_token,
+                            int64_t k_head, rw4_dtype x_dtype, int64_t T, int32_t heads, int32_t kv_heads,
+                            int32_t head_dim, const float* q_weight, const float* k_weight, float eps,
+                            const float* cos_sin, int64_t max_pos, int32_t rot, int32_t interleaved,
+                            const int32_t* positions, int32_t rotate, void* q_out, int64_t qo_token, int64_t qo_head,
+                            void* k_out, int64_t ko_token, int64_t ko_head, rw4_dtype out_dtype, void* stream) {
+  rw4_status st = rows_args_ok(x_dtype, out_dtype, T, eps);
+  if (st != RW4_OK) return st;
+  if (!head_dim_known(head_dim) || heads < 1 || heads > kMaxHeads || kv_heads < 0 || kv_heads > kMaxHeads)
+    return RW4_ERR_SHAPE;
+  st = rope_args_ok(cos_sin, max_pos, rot, positions, head_dim);
+  if (st != RW4_OK) return st;
+  if (T == 0) return RW4_OK;
+  if (!rows_ok(q, q_token, q_head, x_dtype) || !rows_ok(q_out, qo_token, qo_head, out_dtype) ||
+      !rows_apart({{T, qo_token}, {heads, qo_head}}, head_dim))
+    return RW4_ERR_ARG;
+  if (kv_heads > 0 && (!rows_ok(k, k_token, k_head, x_dtype) || !rows_ok(k_out, ko_token, ko_head, out_dtype) ||
+                       !rows_apart({{T, ko_token}, {kv_heads, ko_head}}, head_dim)))
+    return RW4_ERR_ARG;
+  if ((q_weight && !aligned16(q_weight)) || (k_weight && !aligned16(k_weight))) return RW4_ERR_ARG;
+  rw4::RowsArgs a{};
+  a.q = rw4::DenseRows{q, q_token, q_head, q_out, qo_token, qo_head, heads};
+  a.k = rw4::DenseRows{k, k_token, k_head, k_out, ko_token, ko_head, kv_heads};
+  a.T = T;
+  a.head_dim = head_dim;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.eps = eps;
+  a.cos_sin = cos_sin;
+  a.max_pos = max_pos;
+  a.rot = rot;
+  a.interleaved = interleaved != 0;
+  a.rotate = rotate != 0;
+  a.out_bf16 = out_dtype == RW4_BF16;
+  a.positions = positions;
+  return from_hip(rw4::launch_qk_norm_rope(a, x_dtype == RW4_BF16, static_cast<hipStream_t>(stream)));
+}
+
+rw4_status rw4_kv_append(const rw4_kv_cache* cache_host, const void* k, int64_t k_token, int64_t k_head, const void* v,
+                         int64_t v_token, int64_t v_head, const int64_t* slot_map, const void* q, int64_t q_token,
+                         int64_t q_head, int32_t heads, rw4_dtype x_dtype, int64_t T, const float* q_weight,
+                         const float* k_weight, float eps, const float* cos_sin, int64_t max_pos, int32_t rot,
+                         int32_t interleaved, const int32_t* positions, int32_t rotate, void* q_out, int64_t qo_token,
+                         int64_t qo_head, rw4_dtype out_dtype, void* stream) {
+  rw4_status st = rows_args_ok(x_dtype, out_dtype, T, eps);
+  if (st != RW4_OK) return st;
+  rw4::RowsArgs a{};
+  st = kv_cache_of(cache_host, &a.cache);
+  if (st != RW4_OK) return st;
+  const int32_t head_dim = cache_host->head_dim;
+  if (q && (heads < 1 || heads > kMaxHeads)) return RW4_ERR_SHAPE;
+  st = rope_args_ok(cos_sin, max_pos, rot, positions, head_dim);
+  if (st != RW4_OK) return st;
+  if (T == 0) return RW4_OK;
+  if (!rows_ok(k, k_token, k_head, x_dtype) || !rows_ok(v, v_token, v_head, x_dtype) || !slot_map) return RW4_ERR_ARG;
+  if (q && (!rows_ok(q, q_token, q_head, x_dtype) || !rows_ok(q_out, qo_token, qo_head, out_dtype) ||
+            !rows_apart({{T, qo_token}, {heads, qo_head}}, head_dim)))
+    return RW4_ERR_ARG;
+  if ((q_weight && !aligned16(q_weight)) || (k_weight && !aligned16(k_weight))) return RW4_ERR_ARG;
+  a.q = rw4::DenseRows{q, q_token, q_head, q_out, qo_token, qo_head, q ? heads : 0};
+  a.k = rw4::DenseRows{k, k_token, k_head, nullptr, 0, 0, cache_host->heads};
+  a.v = v;
+  a.v_token = v_token;
+  a.v_head = v_head;
+  a.slot_map = slot_map;
+  a.T = T;
+  a.head_dim = head_dim;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.eps = eps;
+  a.cos_sin = cos_sin;
+  a.max_pos = max_pos;
+  a.rot = rot;
+  a.interleaved = interleaved != 0;
+  a.rotate = rotate != 0;
+  a.out_bf16 = out_dtype == RW4_BF16;
+  a.positions = positions;
+  return from_hip(rw4::launch_kv_append(a, x_dtype == RW4_BF16, static_cast<hipStream_t>(stream)));
+}
+
+static bool attention_sizes_ok(int64_t T, int64_t B, int32_t heads, int32_t kv_heads, int32_t head_dim) {
+  return T >= 0 && T < kMaxTokens && B >= 0 && B <= 65535 && head_dim_known(head_dim) && kv_heads >= 1 &&
+         kv_heads <= kMaxHeads && heads >= kv_heads && heads <= int64_t(64) * kv_heads && heads % kv_heads == 0;
+}
+
+int64_t rw4_kv_attention_workspace_bytes(int64_t T, int64_t B, int32_t heads, int32_t kv_heads, int32_t head_dim) {
+  if (!attention_sizes_ok(T, B, heads, kv_heads, head_dim)) return 0;
+  return rw4::kv_attention_workspace_bytes(T, B, heads, kv_heads, head_dim);
+}
+
+rw4_status rw4_kv_attention(const rw4_kv_cache* cache_host, const void* q, rw4_dtype q_dtype, int64_t q_token,
+                            int64_t q_head, int64_t T, int32_t heads, const int32_t* block_table, int64_t table_width,
+                            const int32_t* kv_len, const int32_t* cu_q, int64_t B, int64_t max_q_len, float scale,
+                            int32_t causal, int64_t window, int32_t unrotate, void* out, rw4_dtype out_dtype,
+                            int64_t out_token, int64_t out_head, float* lse, void* workspace, int64_t workspace_bytes,
+                            void* stream) {
+  if (!dtype_known(q_dtype) || !dtype_known(out_dtype) || !std::isfinite(scale)) return RW4_ERR_ARG;
+  rw4::AttnArgs a{};
+  const rw4_status st = kv_cache_of(cache_host, &a.cache);
+  if (st != RW4_OK) return st;
+  if (!attention_sizes_ok(T, B, heads, cache_host->heads, cache_host->head_dim) || table_width < 0 ||
+      table_width > 0x7FFFFFFF || max_q_len < 0 || window < 0)
+    return RW4_ERR_SHAPE;
+  if (window > 0 && !causal) return RW4_ERR_UNSUPPORTED;
+  if (T == 0 || B == 0) return RW4_OK;
+  if (!rows_ok(q, q_token, q_head, q_dtype) || !rows_ok(out, out_token, out_head, out_dtype) ||
+      !rows_apart({{T, out_token}, {heads, out_head}}, cache_host->head_dim))
+    return RW4_ERR_ARG;
+  if (!kv_len || !cu_q || (table_width > 0 && !block_table)) return RW4_ERR_ARG;
+  if (!workspace || !aligned16(workspace) ||
+      workspace_bytes <
+          rw4::kv_attention_workspace_bytes(T, B, heads, cache_host->heads, cache_host->head_dim))
+    return RW4_ERR_ARG;
+  a.q = q;
+  a.q_token = q_token;
+  a.q_head = q_head;
+  a.T = T;
+  a.heads = heads;
+  a.head_dim = cache_host->head_dim;
+  a.q_bf16 = q_dtype == RW4_BF16;
+  a.out_bf16 = out_dtype == RW4_BF16;
+  a.block_table = block_table;
+  a.table_width = table_width;
+  a.kv_len = kv_len;
+  a.cu_q = cu_q;
+  a.B = B;
+  a.max_q_len = max_q_len;
+  a.scale = scale;
+  a.causal = causal != 0;
+  a.unrotate = unrotate != 0;
+  a.window = window;
+  a.out = out;
+  a.out_token = out_token;
+  a.out_head = out_head;
+  a.lse = lse;
+  a.workspace = workspace;
+  return from_hip(rw4::launch_kv_attention(a, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,507 @@
+// Serving with an INT4 KV cache, the token side: pages and slots from request
+// lengths (kv_slots), and the per-head rows of a step's new tokens -- RMS
+// norm, rotary positions, Hadamard rotation, INT4 quantization and the store
+// into the cache's pages (qk_norm_rope, kv_append).
+#include "kv_internal.h"
+#include "rw4_device.h"
+
+namespace rw4 {
+
+// ---------------------------------------------------------------------------
+// kv_slots.  Three running sums over the requests give everything: the starts
+// of the new tokens, the pages each request takes off the free list (need_b =
+// ceil((ctx + new) / P) - ceil(ctx / P)) and the pages finished requests give
+// back.  A request is served when its inclusive page sum fits in the list's
+// count (sums rise, so from the first one that does not fit all later ones
+// that need pages are refused too).  Every block forms the sums itself (one
+// pass over 2 B integers) and keeps them in LDS, then tokens, taken pages and
+// returned pages are independent entries found by binary search.  Pops read
+// ring entries [head, head + count), pushes write behind them, so the phases
+// need no order between blocks.
+// ---------------------------------------------------------------------------
+constexpr int kSlotsThreads = 256;
+
+struct SlotsLens {
+  int64_t ctx, add;  // tokens held, tokens to add (< 0: finished)
+  int64_t have, need, back;
+  bool fits;
+};
+
+__device__ __forceinline__ SlotsLens slots_lens(const SlotsArgs& a, int64_t b) {
+  SlotsLens r;
+  const int64_t page = int64_t(1) << a.log2_page;
+  r.ctx = a.ctx_len[b] > 0 ? a.ctx_len[b] : 0;
+  r.add = a.new_len[b];
+  r.have = (r.ctx + page - 1) >> a.log2_page;
+  const int64_t want = (r.ctx + (r.add > 0 ? r.add : 0) + page - 1) >> a.log2_page;
+  r.fits = want <= a.table_width;
+  r.need = r.add >= 0 && r.fits ? want - r.have : 0;
+  r.back = r.add >= 0 ? 0 : r.have < a.table_width ? r.have : a.table_width;
+  return r;
+}
+
+__device__ __forceinline__ int32_t sat32(int64_t v) { return v > 0x7FFFFFFF ? 0x7FFFFFFF : int32_t(v); }
+
+// The last b in [0, n) with start[b] <= j (start[0] = 0 <= j).
+__device__ __forceinline__ int slots_find(const int32_t* start, int n, int64_t j) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (start[mid] <= j) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// wide: tokens and pages; finish: lengths, starts, flags and the new state
+// (which may be the arrays the wide part reads, hence after it).
+__global__ __launch_bounds__(kSlotsThreads) void kv_slots_kernel(SlotsArgs a, bool wide, bool finish) {
+  extern __shared__ int32_t sums[];  // [3][B + 1]
+  const int B = int(a.B), tid = threadIdx.x;
+  int32_t* tok0 = sums;
+  int32_t* need0 = sums + (B + 1);
+  int32_t* back0 = sums + 2 * (B + 1);
+  __shared__ int64_t wave_sum[kSlotsThreads / kWave][3];
+  __shared__ int32_t taken_s;
+
+  const int64_t cap = a.capacity;
+  int64_t head = a.free_state[0] % cap, count = a.free_state[1];
+  if (head < 0) head += cap;
+  count = count < 0 ? 0 : count > cap ? cap : count;
+  if (tid == 0) taken_s = 0;
+
+  const int per = (B + kSlotsThreads - 1) / kSlotsThreads;
+  const int b0 = tid * per < B ? tid * per : B, b1 = b0 + per < B ? b0 + per : B;
+  int64_t run[3] = {0, 0, 0};
+  for (int b = b0; b < b1; ++b) {
+    const SlotsLens r = slots_lens(a, b);
+    run[0] += r.add > 0 ? r.add : 0;
+    run[1] += r.need;
+    run[2] += r.back;
+  }
+  const int lane = tid & (kWave - 1), wave = tid / kWave;
+  int64_t upto[3];
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    upto[i] = run[i];
+    for (int d = 1; d < kWave; d <<= 1) {
+      const int64_t o = __shfl_up(static_cast<long long>(upto[i]), d);
+      if (lane >= d) upto[i] += o;
+    }
+    if (lane == kWave - 1) wave_sum[wave][i] = upto[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    int64_t before = upto[i] - run[i];
+    for (int w = 0; w < wave; ++w) before += wave_sum[w][i];
+    run[i] = before;
+  }
+  int32_t most = 0;
+  for (int b = b0; b < b1; ++b) {
+    const SlotsLens r = slots_lens(a, b);
+    tok0[b] = sat32(run[0]);
+    need0[b] = sat32(run[1]);
+    back0[b] = sat32(run[2]);
+    run[0] += r.add > 0 ? r.add : 0;
+    run[1] += r.need;
+    run[2] += r.back;
+    if (run[1] <= count) most = int32_t(run[1]);
+  }
+  if (b1 == B && b0 < B) {
+    tok0[B] = sat32(run[0]);
+    need0[B] = sat32(run[1]);
+    back0[B] = sat32(run[2]);
+  }
+  atomicMax(&taken_s, most);
+  __syncthreads();
+  const int64_t taken = taken_s;
+  const int64_t given = back0[B] < cap - count ? back0[B] : cap - count;
+
+  if (wide) {
+    const int64_t first = int64_t(blockIdx.x) * kSlotsThreads + tid, step = int64_t(gridDim.x) * kSlotsThreads;
+    const int64_t page = int64_t(1) << a.log2_page;
+    for (int64_t t = first; t < a.tokens; t += step) {
+      int64_t slot = -1;
+      int32_t pos = -1;
+      if (t < tok0[B]) {
+        const int b = slots_find(tok0, B, t);
+        const SlotsLens r = slots_lens(a, b);
+        if (r.fits && (need0[b + 1] == need0[b] || need0[b + 1] <= count)) {
+          const int64_t p = r.ctx + t - tok0[b], nth = p >> a.log2_page;
+          const int32_t id = nth < r.have ? a.block_table[b * a.table_width + nth]
+                                          : a.free_pages[(head + need0[b] + nth - r.have) % cap];
+          if (id >= 0) slot = int64_t(id) * page + (p & (page - 1));
+          pos = int32_t(p);
+        }
+      }
+      a.slot_map[t] = slot;
+      a.positions[t] = pos;
+    }
+    for (int64_t j = first; j < taken; j += step) {
+      const int b = slots_find(need0, B, j);
+      const SlotsLens r = slots_lens(a, b);
+      a.block_table[b * a.table_width + r.have + j - need0[b]] = a.free_pages[(head + j) % cap];
+    }
+    for (int64_t j = first; j < given; j += step) {
+      const int b = slots_find(back0, B, j);
+      a.free_pages[(head + count + j) % cap] = a.block_table[b * a.table_width + j - back0[b]];
+    }
+  }
+  if (finish && blockIdx.x == 0) {
+    __syncthreads();  // the wide part's reads of lengths and state come first
+    for (int b = tid; b < B; b += kSlotsThreads) {
+      const SlotsLens r = slots_lens(a, b);
+      const bool ok = r.add < 0 || (r.fits && (need0[b + 1] == need0[b] || need0[b + 1] <= count));
+      a.kv_len[b] = r.add < 0 ? 0 : sat32(ok ? r.ctx + r.add : r.ctx);
+      a.served[b] = ok ? 1 : 0;
+      a.cu_new[b] = tok0[b];
+    }
+    if (tid == 0) {
+      a.cu_new[B] = tok0[B];
+      a.free_state_out[0] = int32_t((head + taken) % cap);
+      a.free_state_out[1] = int32_t(count - taken + given);
+    }
+  }
+}
+
+hipError_t launch_kv_slots(const SlotsArgs& a, hipStream_t st) {
+  const size_t lds = 3 * size_t(a.B + 1) * sizeof(int32_t);
+  int64_t blocks = (a.tokens + 511) / 512;
+  blocks = blocks < 1 ? 1 : blocks > 256 ? 256 : blocks;
+  const bool alias = a.kv_len == a.ctx_len || a.free_state_out == a.free_state;
+  const bool two = alias && blocks > 1;  // other blocks may still read what the finish part writes
+  hipLaunchKernelGGL(kv_slots_kernel, dim3(unsigned(blocks)), dim3(kSlotsThreads), lds, st, a, true, !two);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !two) return e;
+  hipLaunchKernelGGL(kv_slots_kernel, dim3(1), dim3(kSlotsThreads), lds, st, a, false, true);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// Head rows.  A head row (D channels) lies in L = D / 8 lanes, 8 consecutive
+// channels each, so a wave holds 64 / L rows; channel index = 8 lane + e, and
+// the Sylvester butterflies run over e in registers and over the lane bits
+// across lanes.  Queries (and dense keys) are evaluated in fp32; rows that
+// are quantized in fp64: their codes are then those of the exact quotient
+// 7 u / m for any input whose sums are exact in fp64 (bf16 values always),
+// and near a border they do not depend on the order of the sums.
+// ---------------------------------------------------------------------------
+template <int M>
+__device__ __forceinline__ double lane_xor(double v) {
+  const int lo = __float_as_int(lane_xor<M>(__int_as_float(__double2loint(v))));
+  const int hi = __float_as_int(lane_xor<M>(__int_as_float(__double2hiint(v))));
+  return __hiloint2double(hi, lo);
+}
+
+__device__ __forceinline__ float lane_get(float v, int src) {
+  return __int_as_float(__builtin_amdgcn_ds_bpermute(src << 2, __float_as_int(v)));
+}
+__device__ __forceinline__ double lane_get(double v, int src) {
+  return __hiloint2double(__builtin_amdgcn_ds_bpermute(src << 2, __double2hiint(v)),
+                          __builtin_amdgcn_ds_bpermute(src << 2, __double2loint(v)));
+}
+
+__device__ __forceinline__ float inv_root(float x) { return 1.0f / sqrtf(x); }
+// the hardware estimate (better than 2^-20) and two Newton steps
+__device__ __forceinline__ double inv_root(double x) {
+  double y = __builtin_amdgcn_rsq(x);
+  y = y * (1.5 - 0.5 * x * y * y);
+  return y * (1.5 - 0.5 * x * y * y);
+}
+
+template <typename T, int L>
+__device__ __forceinline__ T row_sum(T s) {
+  s += lane_xor<1>(s);
+  s += lane_xor<2>(s);
+  s += lane_xor<4>(s);
+  if constexpr (L > 8) s += lane_xor<8>(s);
+  if constexpr (L > 16) s += lane_xor<16>(s);
+  return s;
+}
+template <int L>
+__device__ __forceinline__ double row_max(double m) {
+  m = fmax(m, lane_xor<1>(m));
+  m = fmax(m, lane_xor<2>(m));
+  m = fmax(m, lane_xor<4>(m));
+  if constexpr (L > 8) m = fmax(m, lane_xor<8>(m));
+  if constexpr (L > 16) m = fmax(m, lane_xor<16>(m));
+  return m;
+}
+
+template <int M, typename T>
+__device__ __forceinline__ void lane_stage(T (&v)[8], int lane) {
+  const T sign = (lane & M) ? T(-1) : T(1);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = sign * v[e] + lane_xor<M>(v[e]);
+}
+
+// y H_D (Sylvester order, entries +-1) of a row.
+template <typename T, int L>
+__device__ __forceinline__ void row_hadamard(T (&v)[8], int lane) {
+#pragma unroll
+  for (int h = 1; h < 8; h <<= 1) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if ((e & h) == 0) {
+        const T a = v[e], b = v[e | h];
+        v[e] = a + b;
+        v[e | h] = a - b;
+      }
+    }
+  }
+  lane_stage<1>(v, lane);
+  lane_stage<2>(v, lane);
+  lane_stage<4>(v, lane);
+  if constexpr (L > 8) lane_stage<8>(v, lane);
+  if constexpr (L > 16) lane_stage<16>(v, lane);
+}
+
+// The rotary factors of a lane's 8 channels: y'_e = c_e y_e + s_e y_partner(e).
+struct RopeLane {
+  float c[8], s[8];
+  int partner;  // lane of the partner channels (halves form)
+  bool on;      // the lane's channels are rotated
+};
+
+__device__ __forceinline__ RopeLane rope_lane(const RowsArgs& a, int64_t pos, int lane, int l) {
+  RopeLane r;
+  const int e0 = 8 * l, half = a.rot >> 1;
+  r.on = e0 < a.rot;
+  r.partner = lane;
+  if (!r.on) return r;
+  const float* row = a.cos_sin + pos * a.rot;
+  if (a.interleaved) {
+    const float4 c = *reinterpret_cast<const float4*>(row + e0 / 2);
+    const float4 s = *reinterpret_cast<const float4*>(row + half + e0 / 2);
+    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      r.c[2 * i] = r.c[2 * i + 1] = cc[i];
+      r.s[2 * i] = -ss[i];
+      r.s[2 * i + 1] = ss[i];
+    }
+  } else {
+    const bool low = e0 < half;
+    const int i0 = low ? e0 : e0 - half;
+    r.partner = low ? lane + half / 8 : lane - half / 8;
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) {
+      const float4 c = *reinterpret_cast<const float4*>(row + i0 + i);
+      const float4 s = *reinterpret_cast<const float4*>(row + half + i0 + i);
+      r.c[i] = c.x; r.c[i + 1] = c.y; r.c[i + 2] = c.z; r.c[i + 3] = c.w;
+      r.s[i] = low ? -s.x : s.x;
+      r.s[i + 1] = low ? -s.y : s.y;
+      r.s[i + 2] = low ? -s.z : s.z;
+      r.s[i + 3] = low ? -s.w : s.w;
+    }
+  }
+  return r;
+}
+
+template <typename T>
+__device__ __forceinline__ void rope_apply(const RowsArgs& a, const RopeLane& r, T (&v)[8]) {
+  if (a.interleaved) {
+    if (r.on) {
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        const T x = v[e], y = v[e + 1];
+        v[e] = x * T(r.c[e]) + y * T(r.s[e]);
+        v[e + 1] = y * T(r.c[e + 1]) + x * T(r.s[e + 1]);
+      }
+    }
+  } else {
+    T p[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) p[e] = lane_get(v[e], r.partner);
+    if (r.on) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = v[e] * T(r.c[e]) + p[e] * T(r.s[e]);
+    }
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void load_row8(const void* base, int64_t off, float (&v)[8]) {
+  RowSrc<BF16>{base, 0}.load8(0, off, v);
+}
+
+__device__ __forceinline__ void store_row8(void* base, bool bf16, int64_t off, const float (&v)[8]) {
+  if (bf16) {
+    __bf16 h[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = static_cast<__bf16>(v[i]);  // round to nearest even
+    *reinterpret_cast<uint4*>(reinterpret_cast<__bf16*>(base) + off) = *reinterpret_cast<const uint4*>(h);
+  } else {
+    float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(base) + off);
+    dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+    dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+  }
+}
+
+// One dense row (queries; keys without a cache).
+template <int D, bool BF16>
+__device__ __forceinline__ void dense_row(const RowsArgs& a, const DenseRows& r, const float* weight, int64_t t, int h,
+                                          bool live, const RopeLane& rope, int lane, int l) {
+  constexpr int L = D / 8;
+  float v[8];
+  load_row8<BF16>(r.in, t * r.in_token + h * r.in_head + 8 * l, v);
+  if (weight) {
+    float ss = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
+    const float inv = inv_root(row_sum<float, L>(ss) * (1.0f / D) + a.eps);
+    float w[8];
+    load_row8<false>(weight, 8 * l, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = v[e] * inv * w[e];
+  }
+  if (a.cos_sin) rope_apply(a, rope, v);
+  if (a.rotate) {
+    row_hadamard<float, L>(v, lane);
+    constexpr float post = D == 64 ? 0.125f : D == 256 ? 0.0625f : 0.08838834764831845f;  // 1 / sqrt(D)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= post;
+  }
+  if (live) store_row8(r.out, a.out_bf16, t * r.out_token + h * r.out_head + 8 * l, v);
+}
+
+// One quantized row into the cache.
+template <int D, bool BF16>
+__device__ __forceinline__ void cache_row(const RowsArgs& a, const void* in, int64_t in_token, int64_t in_head,
+                                          const float* weight, bool roped, uint8_t* codes, float* scales, int64_t t,
+                                          int h, bool live, int64_t slot, const RopeLane& rope, int lane, int l) {
+  constexpr int L = D / 8;
+  float x[8];
+  load_row8<BF16>(in, t * in_token + h * in_head + 8 * l, x);
+  double u[8];
+  double inv = 1.0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) u[e] = x[e];
+  if (weight) {
+    // the norm's factor is common to the row: it does not move the codes, so
+    // it enters the scale alone
+    double ss = 0.0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss = fma(u[e], u[e], ss);
+    inv = inv_root(row_sum<double, L>(ss) * (1.0 / D) + double(a.eps));
+    float w[8];
+    load_row8<false>(weight, 8 * l, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) u[e] *= double(w[e]);
+  }
+  if (roped) rope_apply(a, rope, u);
+  if (a.rotate) row_hadamard<double, L>(u, lane);
+  double m = 0.0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const double p = fabs(u[e]);
+    m = p < __builtin_huge_val() ? fmax(m, p) : __builtin_huge_val();  // NaN counts as infinite
+  }
+  m = row_max<L>(m);
+  const bool bad = !(m < __builtin_huge_val()), zero = !(m > 0.0);
+  const double r7 = bad || zero ? 0.0 : 7.0 / m;
+  uint32_t b[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    // nearest code of the exact quotient: the rounded product, put right by
+    // the exact remainder (ties to even)
+    double q = bad ? 0.0 : rint(u[e] * r7);
+    if (!bad) {
+      const double rem = fma(-q, m, 7.0 * u[e]), twice = 2.0 * fabs(rem);
+      const bool odd = int(q) & 1;
+      if (twice > m || (twice == m && odd)) q += rem > 0.0 ? 1.0 : -1.0;
+    }
+    b[e] = kRoundMagicBits + uint32_t(int(q));
+  }
+  const uint32_t word = pack8_bits(b, (l & 2) != 0);
+  if (!live) return;
+  const int64_t page = slot >> a.cache.log2_page, off = slot & ((int64_t(1) << a.cache.log2_page) - 1);
+  *reinterpret_cast<uint32_t*>(codes + page * a.cache.code_page + h * a.cache.code_head + off * a.cache.code_slot +
+                               4 * l) = word;
+  if (l == 0) {
+    constexpr double root = D == 64 ? 8.0 : D == 256 ? 16.0 : 11.313708498984761;
+    const double s = m * inv / (a.rotate ? 7.0 * root : 7.0);
+    scales[page * a.cache.scale_page + h * a.cache.scale_head + off * a.cache.scale_slot] =
+        bad ? __int_as_float(0x7FC00000) : zero ? 0.0f : float(s);
+  }
+}
+
+// A wave takes one token's head groups (64 / L heads of one kind: queries,
+// keys, values) part, part + parts, ...; the rotary factors stay in registers
+// across them.
+template <int D, bool BF16, bool APPEND>
+__global__ __launch_bounds__(256) void kv_rows_kernel(RowsArgs a, int parts) {
+  constexpr int L = D / 8, R = kWave / L;
+  const int lane = threadIdx.x & (kWave - 1), l = lane & (L - 1);
+  const int64_t w =
+      __builtin_amdgcn_readfirstlane(int(blockIdx.x * (blockDim.x / kWave) + threadIdx.x / kWave));
+  const int64_t t = w / parts;
+  if (t >= a.T) return;
+  const int part = int(w % parts);
+  int64_t pos = 0;
+  RopeLane rope;
+  if (a.cos_sin) {
+    pos = a.positions[t];
+    if (pos < 0 || pos >= a.max_pos) return;
+    rope = rope_lane(a, pos, lane, l);
+  }
+  int64_t slot = -1;
+  if constexpr (APPEND) slot = a.slot_map[t];
+  const bool stored = APPEND && slot >= 0 && slot < a.cache.slots;
+  const int gq = (a.q.heads + R - 1) / R, gk = (a.k.heads + R - 1) / R;
+  const int groups = gq + gk + (APPEND ? gk : 0);
+  for (int g = part; g < groups; g += parts) {
+    const int kind = g < gq ? 0 : g < gq + gk ? 1 : 2;
+    const int heads = kind == 0 ? a.q.heads : a.k.heads;
+    int h = (kind == 0 ? g : kind == 1 ? g - gq : g - gq - gk) * R + lane / L;
+    const bool live = h < heads;
+    h = live ? h : heads - 1;
+    if (kind == 0) {
+      dense_row<D, BF16>(a, a.q, a.q_weight, t, h, live, rope, lane, l);
+    } else if constexpr (APPEND) {
+      if (!stored) continue;
+      if (kind == 1)
+        cache_row<D, BF16>(a, a.k.in, a.k.in_token, a.k.in_head, a.k_weight, a.cos_sin != nullptr, a.cache.k_codes,
+                           a.cache.k_scales, t, h, live, slot, rope, lane, l);
+      else
+        cache_row<D, BF16>(a, a.v, a.v_token, a.v_head, nullptr, false, a.cache.v_codes, a.cache.v_scales, t, h, live,
+                           slot, rope, lane, l);
+    } else {
+      dense_row<D, BF16>(a, a.k, a.k_weight, t, h, live, rope, lane, l);
+    }
+  }
+}
+
+template <int D, bool BF16, bool APPEND>
+static hipError_t launch_rows(const RowsArgs& a, hipStream_t st) {
+  constexpr int R = kWave / (D / 8);
+  const int64_t gq = (a.q.heads + R - 1) / R, gk = (a.k.heads + R - 1) / R;
+  const int64_t groups = gq + gk * (APPEND ? 2 : 1);
+  // few tokens: a wave per head group; many: a wave keeps a token's rotary
+  // factors for several groups, with at least 16384 waves in the grid
+  int64_t parts = (16384 + a.T - 1) / a.T;
+  parts = parts < 1 ? 1 : parts > groups ? groups : parts;
+  const int64_t waves = a.T * parts, blocks = (waves + 3) / 4;
+  if (blocks > 0x1FFFFFFF) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((kv_rows_kernel<D, BF16, APPEND>), dim3(unsigned(blocks)), dim3(256), 0, st, a, int(parts));
+  return hipGetLastError();
+}
+
+template <bool APPEND>
+static hipError_t launch_rows_any(const RowsArgs& a, bool x_bf16, hipStream_t st) {
+  switch (a.head_dim) {
+    case 64: return x_bf16 ? launch_rows<64, true, APPEND>(a, st) : launch_rows<64, false, APPEND>(a, st);
+    case 128: return x_bf16 ? launch_rows<128, true, APPEND>(a, st) : launch_rows<128, false, APPEND>(a, st);
+    default: return x_bf16 ? launch_rows<256, true, APPEND>(a, st) : launch_rows<256, false, APPEND>(a, st);
+  }
+}
+
+hipError_t launch_qk_norm_rope(const RowsArgs& a, bool x_bf16, hipStream_t st) {
+  return launch_rows_any<false>(a, x_bf16, st);
+}
+hipError_t launch_kv_append(const RowsArgs& a, bool x_bf16, hipStream_t st) {
+  return launch_rows_any<true>(a, x_bf16, st);
+}
+
+}  // namespace rw4

@@ -1,0 +1,356 @@
+"""Serving with an INT4 KV cache: binding of the library's kv calls.
+
+    cache = KVCache.empty(pages, page_size, kv_heads, head_dim, "cuda")
+    step = kv_slots(ctx_len, new_len, block_table, free_pages, free_state, page_size, tokens)
+    q = kv_append(cache, k, v, step.slot_map, q, q_weight, k_weight, cos_sin, step.positions)
+    o = kv_attention(q, cache, block_table, step.kv_len, step.cu_new)
+
+Marshalling and argument checks only, like the rest of the package; every
+call has a prepare_ form that checks once and launches again on each call.
+"""
+from __future__ import annotations
+
+import collections
+import ctypes
+import math
+
+import numpy as np
+
+from . import RW4_BF16, RW4_F32, RW4_OK, Call, RW4Error, _on_gpu, _out, _stream, _torch, lib
+
+__all__ = ["KVCache", "KVSlots", "kv_slots", "prepare_kv_slots", "rope_table", "qk_norm_rope", "prepare_qk_norm_rope",
+           "kv_append", "prepare_kv_append", "kv_attention", "prepare_kv_attention", "kv_attention_workspace_bytes"]
+
+_p, _i64, _i32, _f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
+
+
+class _CacheStruct(ctypes.Structure):
+    _fields_ = [("k_codes", _p), ("k_scales", _p), ("v_codes", _p), ("v_scales", _p), ("pages", _i64),
+                ("page_size", _i32), ("heads", _i32), ("head_dim", _i32), ("code_page", _i64), ("code_head", _i64),
+                ("code_slot", _i64), ("scale_page", _i64), ("scale_head", _i64), ("scale_slot", _i64)]
+
+
+lib.rw4_kv_slots.argtypes = [_p, _p, _i64, _i32, _p, _i64, _p, _i64, _p, _p, _p, _p, _p, _p, _p, _i64, _p]
+lib.rw4_qk_norm_rope.argtypes = [_p, _i64, _i64, _p, _i64, _i64, ctypes.c_int, _i64, _i32, _i32, _i32, _p, _p, _f32,
+                                 _p, _i64, _i32, _i32, _p, _i32, _p, _i64, _i64, _p, _i64, _i64, ctypes.c_int, _p]
+lib.rw4_kv_append.argtypes = [_p, _p, _i64, _i64, _p, _i64, _i64, _p, _p, _i64, _i64, _i32, ctypes.c_int, _i64, _p, _p,
+                              _f32, _p, _i64, _i32, _i32, _p, _i32, _p, _i64, _i64, ctypes.c_int, _p]
+lib.rw4_kv_attention_workspace_bytes.argtypes = [_i64, _i64, _i32, _i32, _i32]
+lib.rw4_kv_attention_workspace_bytes.restype = _i64
+lib.rw4_kv_attention.argtypes = [_p, _p, ctypes.c_int, _i64, _i64, _i64, _i32, _p, _i64, _p, _p, _i64, _i64, _f32, _i32,
+                                 _i64, _i32, _p, ctypes.c_int, _i64, _i64, _p, _p, _i64, _p]
+for _name in ("rw4_kv_slots", "rw4_qk_norm_rope", "rw4_kv_append", "rw4_kv_attention"):
+    getattr(lib, _name).restype = ctypes.c_int
+
+
+class KVCall(Call):
+    """A prepared call that also makes its tensors' GPU current while it launches."""
+
+    __slots__ = ()
+
+    def __call__(self):
+        torch = _torch()
+        if torch.cuda.current_device() != self._dev:
+            with torch.cuda.device(self._dev):
+                status = self._fn(*self._args, _stream(self._dev))
+        else:
+            status = self._fn(*self._args, _stream(self._dev))
+        if status != RW4_OK:
+            raise RW4Error(status, self._what)
+        return self.result
+
+
+def _code(dtype) -> int:
+    torch = _torch()
+    if dtype is torch.bfloat16:
+        return RW4_BF16
+    if dtype is torch.float32:
+        return RW4_F32
+    raise TypeError(f"unsupported dtype {dtype} (float32 or bfloat16)")
+
+
+def _vec(name, t, dtype, n, dev):
+    """A contiguous one-dimensional tensor of n entries (None: any number)."""
+    _on_gpu(name, t, dev)
+    if t.dtype is not dtype or t.dim() != 1 or not t.is_contiguous() or (n is not None and t.shape[0] != n):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor" + ("" if n is None else f" of {n} entries"))
+    return t.data_ptr()
+
+
+def _rows(name, t, dev, shape=None):
+    """A [tokens, heads, D] tensor with unit stride in a head: (token stride, head stride)."""
+    _on_gpu(name, t, dev)
+    if t.dim() != 3 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must be " + ("[tokens, heads, head_dim]" if shape is None else str(list(shape))))
+    st, sh, sd = t.stride()
+    if sd != 1:
+        raise ValueError(f"{name} must have unit stride along the head's channels")
+    return (st if t.shape[0] > 1 else 0), (sh if t.shape[1] > 1 else 0)
+
+
+class KVCache:
+    """A paged INT4 KV cache over caller-owned tensors.
+
+    k, v: uint8 [pages, kv_heads, page_size, head_dim / 2], one stored row per
+    token; k_scale, v_scale: fp32 [pages, kv_heads, page_size].  Any strides
+    with unit stride in a row (equal for k and v), so the rows that
+    quantize_act writes are a cache too (from_rows).
+    """
+
+    __slots__ = ("k", "v", "k_scale", "v_scale", "pages", "page_size", "kv_heads", "head_dim", "device", "_dev",
+                 "_struct", "_ptr")
+
+    def __init__(self, k, v, k_scale, v_scale):
+        torch = _torch()
+        self._dev = _on_gpu("k", k)
+        for name, t in (("v", v), ("k_scale", k_scale), ("v_scale", v_scale)):
+            _on_gpu(name, t, self._dev)
+        if k.dim() != 4 or k.dtype is not torch.uint8 or v.dtype is not torch.uint8 or v.shape != k.shape \
+                or k_scale.dtype is not torch.float32 or v_scale.dtype is not torch.float32 \
+                or k_scale.shape != k.shape[:3] or v_scale.shape != k.shape[:3]:
+            raise ValueError("k and v must be uint8 [pages, kv_heads, page_size, head_dim / 2] and their scales "
+                             "float32 [pages, kv_heads, page_size]")
+        cs, ss = k.stride(), k_scale.stride()
+        if v.stride() != cs or v_scale.stride() != ss or cs[3] != 1:
+            raise ValueError("k and v must have the same strides, with unit stride in a row (their scales likewise)")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.pages, self.kv_heads, self.page_size, half = k.shape
+        self.head_dim, self.device = 2 * half, k.device
+        self._struct = _CacheStruct(k.data_ptr(), k_scale.data_ptr(), v.data_ptr(), v_scale.data_ptr(), self.pages,
+                                    self.page_size, self.kv_heads, self.head_dim, cs[0], cs[1], cs[2], ss[0], ss[1],
+                                    ss[2])
+        self._ptr = ctypes.addressof(self._struct)
+
+    @classmethod
+    def empty(cls, pages: int, page_size: int, kv_heads: int, head_dim: int, device="cuda") -> "KVCache":
+        """A cache of zeros, pages contiguous by head."""
+        torch = _torch()
+        k, v = (torch.zeros((pages, kv_heads, page_size, head_dim // 2), dtype=torch.uint8, device=device)
+                for _ in range(2))
+        ks, vs = (torch.zeros((pages, kv_heads, page_size), dtype=torch.float32, device=device) for _ in range(2))
+        return cls(k, v, ks, vs)
+
+    @classmethod
+    def from_rows(cls, qk, sk, qv, sv, page_size: int, kv_heads: int) -> "KVCache":
+        """The rows [pages * page_size, kv_heads * head_dim / 2] and scales [pages * page_size, kv_heads] that
+        quantize_act writes (group = Hadamard block = head_dim), seen as pages."""
+        rows, width = qk.shape
+        if rows % page_size or width % kv_heads:
+            raise ValueError("rows must be a multiple of page_size and hold kv_heads heads")
+        codes = [t.view(rows // page_size, page_size, kv_heads, width // kv_heads).transpose(1, 2) for t in (qk, qv)]
+        scales = [t.view(rows // page_size, page_size, kv_heads).transpose(1, 2) for t in (sk, sv)]
+        return cls(codes[0], codes[1], scales[0], scales[1])
+
+
+KVSlots = collections.namedtuple("KVSlots", "kv_len cu_new served slot_map positions free_state")
+
+
+def kv_slots(ctx_len, new_len, block_table, free_pages, free_state, page_size: int, tokens: int, **out) -> KVSlots:
+    """Pages and slots for one step's new tokens (new_len < 0: finished, its pages return to the free list).
+
+    ctx_len, new_len int32 [B]; block_table int32 [B, width] and free_pages int32 [capacity] are updated in place;
+    free_state int32 [2] (head, count of the ring free_pages).  Returns KVSlots(kv_len, cu_new, served, slot_map,
+    positions, free_state); `out` may hold any of these by name (kv_len may be ctx_len, free_state_out free_state).
+    """
+    return prepare_kv_slots(ctx_len, new_len, block_table, free_pages, free_state, page_size, tokens, **out)()
+
+
+def prepare_kv_slots(ctx_len, new_len, block_table, free_pages, free_state, page_size: int, tokens: int, *,
+                     kv_len=None, cu_new=None, served=None, slot_map=None, positions=None,
+                     free_state_out=None) -> Call:
+    torch = _torch()
+    i32, dev = torch.int32, _on_gpu("ctx_len", ctx_len)
+    B = ctx_len.shape[0]
+    device = ctx_len.device
+    _vec("ctx_len", ctx_len, i32, None, dev)
+    _vec("new_len", new_len, i32, B, dev)
+    _vec("free_pages", free_pages, i32, None, dev)
+    _vec("free_state", free_state, i32, 2, dev)
+    _on_gpu("block_table", block_table, dev)
+    if block_table.dtype is not i32 or block_table.dim() != 2 or block_table.shape[0] != B \
+            or not block_table.is_contiguous():
+        raise ValueError(f"block_table must be a contiguous int32 tensor of {B} rows")
+    if kv_len is None or cu_new is None or served is None or positions is None or free_state_out is None:
+        # one allocation for the small outputs
+        pool = torch.empty((3 * B + 3 + tokens,), dtype=i32, device=device)
+        parts = pool.split((B, B + 1, B, 2, tokens))
+        kv_len = parts[0] if kv_len is None else kv_len
+        cu_new = parts[1] if cu_new is None else cu_new
+        served = parts[2] if served is None else served
+        free_state_out = parts[3] if free_state_out is None else free_state_out
+        positions = parts[4] if positions is None else positions
+    if slot_map is None:
+        slot_map = torch.empty((tokens,), dtype=torch.int64, device=device)
+    args = (ctx_len.data_ptr(), new_len.data_ptr(), B, int(page_size), block_table.data_ptr(), block_table.shape[1],
+            free_pages.data_ptr(), free_pages.shape[0], free_state.data_ptr(),
+            _vec("free_state_out", free_state_out, i32, 2, dev), _vec("kv_len", kv_len, i32, B, dev),
+            _vec("cu_new", cu_new, i32, B + 1, dev), _vec("served", served, i32, B, dev),
+            _vec("slot_map", slot_map, torch.int64, tokens, dev), _vec("positions", positions, i32, tokens, dev),
+            int(tokens))
+    return KVCall(lib.rw4_kv_slots, args, dev, "rw4_kv_slots",
+                  (ctx_len, new_len, block_table, free_pages, free_state),
+                  KVSlots(kv_len, cu_new, served, slot_map, positions, free_state_out))
+
+
+def rope_table(max_pos: int, rot: int, base: float = 10000.0, device="cuda"):
+    """cos_sin fp32 [max_pos, rot] for qk_norm_rope and kv_append: rot / 2 cosines, then rot / 2 sines of the angles
+    p * base^(-2 i / rot), evaluated in float64."""
+    torch = _torch()
+    angle = np.arange(max_pos, dtype=np.float64)[:, None] * float(base) ** (-np.arange(0, rot, 2) / rot)
+    return torch.from_numpy(np.concatenate([np.cos(angle), np.sin(angle)], 1).astype(np.float32)).to(device)
+
+
+def _weight(name, w, D, dev):
+    return None if w is None else _vec(name, w, _torch().float32, D, dev)
+
+
+def _rope_args(cos_sin, positions, T, dev):
+    """(cos_sin pointer, max_pos, rot, positions pointer)."""
+    torch = _torch()
+    if cos_sin is None:
+        return None, 0, 0, None
+    _on_gpu("cos_sin", cos_sin, dev)
+    if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+        raise ValueError("cos_sin must be a contiguous float32 tensor [max_pos, rot]")
+    if positions is None:
+        raise ValueError("cos_sin needs positions")
+    return cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], _vec("positions", positions, torch.int32, T, dev)
+
+
+def qk_norm_rope(q, k=None, q_weight=None, k_weight=None, cos_sin=None, positions=None, *, eps: float = 1e-6,
+                 interleaved: bool = False, rotate: bool = False, q_out=None, k_out=None, out_dtype=None):
+    """Per-head RMS norm (weights fp32 [D], None: no norm) and rotary positions (cos_sin [max_pos, rot], None: none)
+    of queries [T, heads, D] and keys [T, kv_heads, D] in one pass, then the head's Hadamard when `rotate`.
+
+    Returns (q_out, k_out); with q_out = q and k_out = k in place.  k may be None."""
+    return prepare_qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps=eps, interleaved=interleaved,
+                                rotate=rotate, q_out=q_out, k_out=k_out, out_dtype=out_dtype)()
+
+
+def prepare_qk_norm_rope(q, k=None, q_weight=None, k_weight=None, cos_sin=None, positions=None, *, eps: float = 1e-6,
+                         interleaved: bool = False, rotate: bool = False, q_out=None, k_out=None,
+                         out_dtype=None) -> Call:
+    torch = _torch()
+    dev = _on_gpu("q", q)
+    qs = _rows("q", q, dev)
+    T, heads, D = q.shape
+    if out_dtype is None:
+        out_dtype = q.dtype if q_out is None else q_out.dtype
+    if q_out is None:
+        q_out = torch.empty((T, heads, D), dtype=out_dtype, device=q.device)
+    qos = _rows("q_out", q_out, dev, (T, heads, D))
+    kv_heads, kp, ks, kop, kos = 0, None, (0, 0), None, (0, 0)
+    if k is not None:
+        kv_heads = k.shape[1] if k.dim() == 3 else 0
+        ks = _rows("k", k, dev, (T, kv_heads, D))
+        if k_out is None:
+            k_out = torch.empty((T, kv_heads, D), dtype=out_dtype, device=q.device)
+        kos = _rows("k_out", k_out, dev, (T, kv_heads, D))
+        if k.dtype is not q.dtype or k_out.dtype is not q_out.dtype:
+            raise TypeError("q and k (and their outputs) must have the same dtype")
+        kp, kop = k.data_ptr(), k_out.data_ptr()
+    elif k_out is not None:
+        raise ValueError("k_out needs k")
+    cs, max_pos, rot, pos = _rope_args(cos_sin, positions, T, dev)
+    args = (q.data_ptr(), qs[0], qs[1], kp, ks[0], ks[1], _code(q.dtype), T, heads, kv_heads, D,
+            _weight("q_weight", q_weight, D, dev), _weight("k_weight", k_weight, D, dev), float(eps), cs, max_pos, rot,
+            int(interleaved), pos, int(rotate), q_out.data_ptr(), qos[0], qos[1], kop, kos[0], kos[1],
+            _code(q_out.dtype))
+    return KVCall(lib.rw4_qk_norm_rope, args, dev, "rw4_qk_norm_rope",
+                  (q, k, q_weight, k_weight, cos_sin, positions), (q_out, k_out))
+
+
+def kv_append(cache: KVCache, k, v, slot_map, q=None, q_weight=None, k_weight=None, cos_sin=None, positions=None, *,
+              eps: float = 1e-6, interleaved: bool = False, rotate: bool = True, q_out=None, out_dtype=None):
+    """New tokens into the cache: keys [T, kv_heads, D] normed and given their positions (as qk_norm_rope), keys and
+    values rotated by the head's Hadamard (`rotate`) and stored as INT4 in rows slot_map (int64 [T]).  Queries, if
+    given, go through qk_norm_rope in the same launch; returns q_out (None without q)."""
+    return prepare_kv_append(cache, k, v, slot_map, q, q_weight, k_weight, cos_sin, positions, eps=eps,
+                             interleaved=interleaved, rotate=rotate, q_out=q_out, out_dtype=out_dtype)()
+
+
+def prepare_kv_append(cache: KVCache, k, v, slot_map, q=None, q_weight=None, k_weight=None, cos_sin=None,
+                      positions=None, *, eps: float = 1e-6, interleaved: bool = False, rotate: bool = True,
+                      q_out=None, out_dtype=None) -> Call:
+    torch = _torch()
+    dev, D = cache._dev, cache.head_dim
+    T = k.shape[0]
+    ks = _rows("k", k, dev, (T, cache.kv_heads, D))
+    vs = _rows("v", v, dev, (T, cache.kv_heads, D))
+    if v.dtype is not k.dtype:
+        raise TypeError("k and v must have the same dtype")
+    qp, qs, qop, qos, heads, qo_code = None, (0, 0), None, (0, 0), 0, RW4_F32
+    if q is not None:
+        heads = q.shape[1] if q.dim() == 3 else 0
+        qs = _rows("q", q, dev, (T, heads, D))
+        if q.dtype is not k.dtype:
+            raise TypeError("q and k must have the same dtype")
+        if q_out is None:
+            q_out = torch.empty((T, heads, D), dtype=q.dtype if out_dtype is None else out_dtype, device=q.device)
+        qos = _rows("q_out", q_out, dev, (T, heads, D))
+        qp, qop, qo_code = q.data_ptr(), q_out.data_ptr(), _code(q_out.dtype)
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    cs, max_pos, rot, pos = _rope_args(cos_sin, positions, T, dev)
+    args = (cache._ptr, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
+            _vec("slot_map", slot_map, torch.int64, T, dev), qp, qs[0], qs[1], heads, _code(k.dtype), T,
+            _weight("q_weight", q_weight, D, dev), _weight("k_weight", k_weight, D, dev), float(eps), cs, max_pos, rot,
+            int(interleaved), pos, int(rotate), qop, qos[0], qos[1], qo_code)
+    return KVCall(lib.rw4_kv_append, args, dev, "rw4_kv_append",
+                  (cache, k, v, slot_map, q, q_weight, k_weight, cos_sin, positions), q_out)
+
+
+def kv_attention_workspace_bytes(tokens: int, requests: int, heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(lib.rw4_kv_attention_workspace_bytes(tokens, requests, heads, kv_heads, head_dim))
+
+
+def kv_attention(q, cache: KVCache, block_table, kv_len, cu_q, *, max_q_len=None, scale=None, causal: bool = True,
+                 window: int = 0, unrotate: bool = True, out=None, out_dtype=None, return_lse: bool = False, lse=None,
+                 workspace=None):
+    """Softmax attention of q [T, heads, D] over the cache: request b owns query tokens cu_q[b]:cu_q[b + 1] and the
+    first kv_len[b] cached tokens, in the pages block_table[b].
+
+    causal: a request's queries are its last tokens; window > 0: the last `window` keys only.  scale defaults to
+    1 / sqrt(D); unrotate applies the head's Hadamard to the output (for a cache of rotated values).  max_q_len (the
+    largest number of query tokens of a request, default all) only chooses the kernel.  Returns out [T, heads, D],
+    with return_lse (out, lse fp32 [T, heads]).  A row that sees no key gives 0 and -inf."""
+    return prepare_kv_attention(q, cache, block_table, kv_len, cu_q, max_q_len=max_q_len, scale=scale, causal=causal,
+                                window=window, unrotate=unrotate, out=out, out_dtype=out_dtype, return_lse=return_lse,
+                                lse=lse, workspace=workspace)()
+
+
+def prepare_kv_attention(q, cache: KVCache, block_table, kv_len, cu_q, *, max_q_len=None, scale=None,
+                         causal: bool = True, window: int = 0, unrotate: bool = True, out=None, out_dtype=None,
+                         return_lse: bool = False, lse=None, workspace=None) -> Call:
+    torch = _torch()
+    i32, dev, D = torch.int32, cache._dev, cache.head_dim
+    qs = _rows("q", q, dev)
+    T, heads, dq = q.shape
+    if dq != D or heads % cache.kv_heads:
+        raise ValueError(f"q must be [tokens, a multiple of {cache.kv_heads}, {D}]")
+    B = kv_len.shape[0]
+    _on_gpu("block_table", block_table, dev)
+    if block_table.dtype is not i32 or block_table.dim() != 2 or block_table.shape[0] != B \
+            or not block_table.is_contiguous():
+        raise ValueError(f"block_table must be a contiguous int32 tensor of {B} rows")
+    if out is None:
+        out = torch.empty((T, heads, D), dtype=q.dtype if out_dtype is None else out_dtype, device=q.device)
+    os = _rows("out", out, dev, (T, heads, D))
+    if lse is not None:
+        _out("lse", lse, (T, heads), torch.float32, dev)
+    elif return_lse:
+        lse = torch.empty((T, heads), dtype=torch.float32, device=q.device)
+    nbytes = lib.rw4_kv_attention_workspace_bytes(T, B, heads, cache.kv_heads, D)
+    if workspace is None:
+        workspace = torch.empty((max(nbytes, 16),), dtype=torch.uint8, device=q.device)
+    _on_gpu("workspace", workspace, dev)
+    wbytes = workspace.numel() * workspace.element_size()
+    if not workspace.is_contiguous() or wbytes < nbytes:
+        raise ValueError(f"workspace must be a contiguous tensor of at least {nbytes} bytes")
+    args = (cache._ptr, q.data_ptr(), _code(q.dtype), qs[0], qs[1], T, heads, block_table.data_ptr(),
+            block_table.shape[1], _vec("kv_len", kv_len, i32, B, dev), _vec("cu_q", cu_q, i32, B + 1, dev), B,
+            T if max_q_len is None else int(max_q_len), 1.0 / math.sqrt(D) if scale is None else float(scale),
+            int(causal), int(window), int(unrotate), out.data_ptr(), _code(out.dtype), os[0], os[1],
+            None if lse is None else lse.data_ptr(), workspace.data_ptr(), wbytes)
+    return KVCall(lib.rw4_kv_attention, args, dev, "rw4_kv_attention",
+                  (q, cache, block_table, kv_len, cu_q, workspace), (out, lse) if return_lse else out)
