@@ -810,6 +810,7 @@ rw4_status rw4_kv_attention(const rw4_kv_cache* cache_host, const void* q, rw4_d
     return RW4_ERR_SHAPE;
   if (window > 0 && !causal) return RW4_ERR_UNSUPPORTED;
   if (T == 0 || B == 0) return RW4_OK;
+  if (T * heads > 0x7FFFFFFF) return RW4_ERR_SHAPE;
   if (!rows_ok(q, q_token, q_head, q_dtype) || !rows_ok(out, out_token, out_head, out_dtype) ||
       !rows_apart({{T, out_token}, {heads, out_head}}, cache_host->head_dim))
     return RW4_ERR_ARG;
@@ -823,6 +824,7 @@ rw4_status rw4_kv_attention(const rw4_kv_cache* cache_host, const void* q, rw4_d
   a.q_head = q_head;
   a.T = T;
   a.heads = heads;
+  a.group = heads / cache_host->heads;
   a.head_dim = cache_host->head_dim;
   a.q_bf16 = q_dtype == RW4_BF16;
   a.out_bf16 = out_dtype == RW4_BF16;
@@ -835,7 +837,7 @@ rw4_status rw4_kv_attention(const rw4_kv_cache* cache_host, const void* q, rw4_d
   a.scale = scale;
   a.causal = causal != 0;
   a.unrotate = unrotate != 0;
-  a.window = window;
+  a.window = window < kMaxStride ? window : kMaxStride;  // longer than any request
   a.out = out;
   a.out_token = out_token;
   a.out_head = out_head;

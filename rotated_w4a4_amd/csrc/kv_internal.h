@@ -68,7 +68,7 @@ struct AttnArgs {
   const void* q;
   int64_t q_token, q_head;
   int64_t T;
-  int heads, head_dim;
+  int heads, head_dim, group;  // group: query heads of a KV head
   int q_bf16, out_bf16;
   const int32_t* block_table;
   int64_t table_width;

@@ -2,8 +2,8 @@
 // lengths (kv_slots), and the per-head rows of a step's new tokens -- RMS
 // norm, rotary positions, Hadamard rotation, INT4 quantization and the store
 // into the cache's pages (qk_norm_rope, kv_append).
+#include "kv_device.h"
 #include "kv_internal.h"
-#include "rw4_device.h"
 
 namespace rw4 {
 
@@ -187,13 +187,6 @@ hipError_t launch_kv_slots(const SlotsArgs& a, hipStream_t st) {
 // 7 u / m for any input whose sums are exact in fp64 (bf16 values always),
 // and near a border they do not depend on the order of the sums.
 // ---------------------------------------------------------------------------
-template <int M>
-__device__ __forceinline__ double lane_xor(double v) {
-  const int lo = __float_as_int(lane_xor<M>(__int_as_float(__double2loint(v))));
-  const int hi = __float_as_int(lane_xor<M>(__int_as_float(__double2hiint(v))));
-  return __hiloint2double(hi, lo);
-}
-
 __device__ __forceinline__ float lane_get(float v, int src) {
   return __int_as_float(__builtin_amdgcn_ds_bpermute(src << 2, __float_as_int(v)));
 }
@@ -227,34 +220,6 @@ __device__ __forceinline__ double row_max(double m) {
   if constexpr (L > 8) m = fmax(m, lane_xor<8>(m));
   if constexpr (L > 16) m = fmax(m, lane_xor<16>(m));
   return m;
-}
-
-template <int M, typename T>
-__device__ __forceinline__ void lane_stage(T (&v)[8], int lane) {
-  const T sign = (lane & M) ? T(-1) : T(1);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = sign * v[e] + lane_xor<M>(v[e]);
-}
-
-// y H_D (Sylvester order, entries +-1) of a row.
-template <typename T, int L>
-__device__ __forceinline__ void row_hadamard(T (&v)[8], int lane) {
-#pragma unroll
-  for (int h = 1; h < 8; h <<= 1) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if ((e & h) == 0) {
-        const T a = v[e], b = v[e | h];
-        v[e] = a + b;
-        v[e | h] = a - b;
-      }
-    }
-  }
-  lane_stage<1>(v, lane);
-  lane_stage<2>(v, lane);
-  lane_stage<4>(v, lane);
-  if constexpr (L > 8) lane_stage<8>(v, lane);
-  if constexpr (L > 16) lane_stage<16>(v, lane);
 }
 
 // The rotary factors of a lane's 8 channels: y'_e = c_e y_e + s_e y_partner(e).
@@ -326,19 +291,6 @@ __device__ __forceinline__ void load_row8(const void* base, int64_t off, float (
   RowSrc<BF16>{base, 0}.load8(0, off, v);
 }
 
-__device__ __forceinline__ void store_row8(void* base, bool bf16, int64_t off, const float (&v)[8]) {
-  if (bf16) {
-    __bf16 h[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = static_cast<__bf16>(v[i]);  // round to nearest even
-    *reinterpret_cast<uint4*>(reinterpret_cast<__bf16*>(base) + off) = *reinterpret_cast<const uint4*>(h);
-  } else {
-    float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(base) + off);
-    dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-    dst[1] = make_float4(v[4], v[5], v[6], v[7]);
-  }
-}
-
 // One dense row (queries; keys without a cache).
 template <int D, bool BF16>
 __device__ __forceinline__ void dense_row(const RowsArgs& a, const DenseRows& r, const float* weight, int64_t t, int h,
@@ -359,7 +311,7 @@ __device__ __forceinline__ void dense_row(const RowsArgs& a, const DenseRows& r,
   if (a.cos_sin) rope_apply(a, rope, v);
   if (a.rotate) {
     row_hadamard<float, L>(v, lane);
-    constexpr float post = D == 64 ? 0.125f : D == 256 ? 0.0625f : 0.08838834764831845f;  // 1 / sqrt(D)
+    constexpr float post = kHeadPost<D>;
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] *= post;
   }
