@@ -14,14 +14,14 @@
 // fp32 queries are split the same way).
 //
 // Work.  A unit is a tile of query rows (row = query token x query head of one
-// KV head) of one request and KV head; a unit's keys are cut into chunks of C
-// tokens, and a (unit, chunk) is an item.  C follows on the device from the
-// lengths: as many items as the grid takes at once, at least kMinChunk keys
-// each.  Every wave works the schedule out by itself from kv_len and cu_q (64
-// requests at a time, one per lane), so ragged batches need no plan and a
-// captured graph follows its lengths.  A unit of one chunk writes its output;
-// the others leave unnormalized partial results (o, m, l) in the workspace
-// for the combine kernel.
+// KV head) of one request and KV head.  The keys of all units, in steps of
+// kStep, form one line that is cut into equal shares, one for each block of
+// the grid, so ragged batches are balanced whatever their lengths: a share
+// holds the end of one unit, whole units and the start of another.  Whole
+// units write their output; the pieces of cut ones leave unnormalized partial
+// results (o, m, l) in the workspace, at most two for each block, for the
+// combine kernel.  Every block works the line out by itself from kv_len and
+// cu_q: no plan, no copy to the host, and a captured graph follows its lengths.
 #include "kv_device.h"
 #include "kv_internal.h"
 
@@ -39,19 +39,12 @@ typedef __bf16 v32bf __attribute__((ext_vector_type(32)));
 typedef unsigned int v4u __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr int kMinChunk = 128;
+constexpr int kCUs = 256;
 constexpr int kNarrowRows = 16;
-constexpr int kNarrowTarget = 1024;           // items aimed at: 4 blocks on each of 256 CUs
-constexpr int kNarrowWhole = 4 * kNarrowTarget;  // from this many units on, requests are not split
-
-struct Sched {
-  int rows;            // query rows of a unit
-  int64_t target;      // items aimed at
-  int64_t whole;       // with this many units or more, one chunk each
-};
+constexpr int kStep = 128;  // keys of a step: 32 for each of a block's 4 waves
 
 // ---------------------------------------------------------------------------
-// The schedule.
+// The line of work.
 // ---------------------------------------------------------------------------
 struct Req {
   int q0, qn, kv;   // first query token, query tokens, keys
@@ -61,15 +54,15 @@ struct Req {
 
 __device__ __forceinline__ int clamp_int(int64_t v, int64_t hi) { return int(v < 0 ? 0 : v > hi ? hi : v); }
 
-__device__ __forceinline__ Req request(const AttnArgs& a, int64_t b, int rows) {
-  Req r{0, 0, 0, 0, 0, 0};
-  if (b >= a.B) return r;
+__device__ __forceinline__ Req request(const AttnArgs& a, int b, int rows) {
+  Req r;
   const int q1 = clamp_int(a.cu_q[b + 1], a.T);
   r.q0 = clamp_int(a.cu_q[b], a.T);
   r.qn = q1 > r.q0 ? q1 - r.q0 : 0;
   const int64_t room = a.table_width << a.cache.log2_page;
   r.kv = clamp_int(a.kv_len[b], room < 0x7FFFFF00 ? room : 0x7FFFFF00);
-  r.tiles = int((int64_t(r.qn) * a.group + rows - 1) / rows);
+  r.tiles = (r.qn * a.group + rows - 1) / rows;  // T * heads < 2^31
+  r.lo = 0;
   if (a.window > 0) {
     const int64_t first = int64_t(r.kv) - r.qn + 1 - a.window;
     r.lo = first > 0 ? int(first) & ~63 : 0;
@@ -78,93 +71,95 @@ __device__ __forceinline__ Req request(const AttnArgs& a, int64_t b, int rows) {
   return r;
 }
 
-__device__ __forceinline__ int64_t wave_sum64(int64_t v) {
-  for (int d = 32; d; d >>= 1) v += __shfl_xor(static_cast<long long>(v), d);
-  return v;
-}
-__device__ __forceinline__ int64_t wave_prefix64(int64_t v, int lane) {
+template <typename T>
+__device__ __forceinline__ T wave_prefix(T v, int lane) {
   for (int d = 1; d < kWave; d <<= 1) {
-    const int64_t o = __shfl_up(static_cast<long long>(v), d);
+    const T o = __shfl_up(v, d);
     if (lane >= d) v += o;
   }
   return v;
 }
-__device__ __forceinline__ int lane_int(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
-__device__ __forceinline__ int64_t lane_int64(int64_t v, int lane) {
-  return int64_t(uint32_t(lane_int(int(v), lane))) | (int64_t(lane_int(int(v >> 32), lane)) << 32);
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  return int64_t(uint32_t(uniform(int(v)))) | (int64_t(uniform(int(v >> 32))) << 32);
 }
 
-// Keys of a chunk, the same on every wave of every kernel of a call.
-__device__ __forceinline__ int chunk_keys(const AttnArgs& a, const Sched& s, int lane) {
-  int64_t keys = 0, units = 0;
-  for (int64_t b = lane; b - lane < a.B; b += kWave) {
-    const Req r = request(a, b, s.rows);
-    keys += int64_t(r.tiles) * r.span;
-    units += r.tiles;
-  }
-  keys = wave_sum64(keys) * a.cache.heads;
-  units = wave_sum64(units) * a.cache.heads;
-  if (units >= s.whole) return 0x7FFFFF00;
-  int64_t c = (keys + s.target - 1) / s.target;
-  c = (c + 127) & ~int64_t(127);
-  return int(c < kMinChunk ? kMinChunk : c > 0x7FFFFF00 ? 0x7FFFFF00 : c);
-}
+__device__ __forceinline__ int req_steps(const Req& r) { return r.span > 0 ? (r.span + kStep - 1) / kStep : 1; }
 
-// Walks the items (or units) of the requests in order, 64 requests at a time.
-struct Cursor {
-  int64_t base;            // first request of the window
-  int64_t items, units;    // before the window
-  Req r;                   // the lane's request
-  int chunks;
-  int64_t upto_items, upto_units;  // inclusive sums over the window's lanes
-};
-
-__device__ __forceinline__ void cursor_load(const AttnArgs& a, const Sched& s, int C, Cursor& c, int lane) {
-  c.r = request(a, c.base + lane, s.rows);
-  c.chunks = c.r.span > C ? int((int64_t(c.r.span) + C - 1) / C) : 1;
-  const int64_t units = int64_t(c.r.tiles) * a.cache.heads;
-  c.upto_units = wave_prefix64(units, lane);
-  c.upto_items = wave_prefix64(units * c.chunks, lane);
-}
-
-struct Item {
+// The piece of a unit at a position of the line.
+struct Piece {
   Req r;
-  int64_t b;
-  int chunks, chunk, head, tile;  // head: KV head
-  int64_t slot;                   // workspace slot of the unit's first chunk
+  int b, head, tile;   // request, KV head, row tile
+  int steps, at;       // steps of the unit, the position's step in it
 };
 
-// Item (by_units: unit, chunk 0) number n; false past the end.
-__device__ __forceinline__ bool cursor_seek(const AttnArgs& a, const Sched& s, int C, Cursor& c, int64_t n,
-                                            bool by_units, int lane, Item& it) {
-  for (;;) {
-    if (c.base >= a.B) return false;
-    const int64_t last = lane_int64(by_units ? c.upto_units : c.upto_items, kWave - 1);
-    const int64_t before = by_units ? c.units : c.items;
-    if (n < before + last) break;
-    c.items += lane_int64(c.upto_items, kWave - 1);
-    c.units += lane_int64(c.upto_units, kWave - 1);
-    c.base += kWave;
-    if (c.base < a.B) cursor_load(a, s, C, c, lane);
+// Steps before each thread's requests (256 threads take consecutive ones).
+struct Line {
+  long long before[257];
+  long long wave_sum[4];
+};
+
+__device__ __forceinline__ void line_build(const AttnArgs& a, int rows, Line& line) {
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  const int B = int(a.B), per = (B + 255) / 256;
+  const int b0 = tid * per < B ? tid * per : B, b1 = b0 + per < B ? b0 + per : B;
+  long long sum = 0;
+  for (int b = b0; b < b1; ++b) {
+    const Req r = request(a, b, rows);
+    sum += (long long)(r.tiles) * a.cache.heads * req_steps(r);
   }
-  const int64_t local = n - (by_units ? c.units : c.items);
-  const uint64_t above = __ballot((by_units ? c.upto_units : c.upto_items) > local);
-  const int src = __builtin_ctzll(above);
-  it.r = Req{lane_int(c.r.q0, src), lane_int(c.r.qn, src), lane_int(c.r.kv, src), lane_int(c.r.tiles, src),
-             lane_int(c.r.lo, src), lane_int(c.r.span, src)};
-  it.b = c.base + src;
-  it.chunks = lane_int(c.chunks, src);
-  const int64_t units = int64_t(it.r.tiles) * a.cache.heads;
-  const int64_t units0 = lane_int64(c.upto_units, src) - units;
-  const int64_t items0 = lane_int64(c.upto_items, src) - units * it.chunks;
-  const int64_t in_req = local - (by_units ? units0 : items0);
-  const int unit = int(by_units ? in_req : in_req / it.chunks);
-  it.chunk = by_units ? 0 : int(in_req % it.chunks);
-  it.head = unit % a.cache.heads;
-  it.tile = it.r.tiles - 1 - unit / a.cache.heads;  // the longest rows first
-  it.slot = c.items + items0 + int64_t(unit) * it.chunks;
-  return true;
+  const long long upto = wave_prefix(sum, lane);
+  if (lane == kWave - 1) line.wave_sum[wave] = upto;
+  __syncthreads();
+  long long before = upto - sum;
+  for (int w = 0; w < wave; ++w) before += line.wave_sum[w];
+  line.before[tid] = before;
+  if (tid == 255) line.before[256] = before + sum;
+  __syncthreads();
 }
+
+__device__ __forceinline__ int64_t line_total(const Line& line) { return uniform(int64_t(line.before[256])); }
+
+// A block's share: at least one step.
+__device__ __forceinline__ int64_t line_share(int64_t total, int blocks) {
+  const int64_t share = (total + blocks - 1) / blocks;
+  return share > 0 ? share : 1;
+}
+
+// The piece at position pos < total; every wave finds it by itself.
+__device__ __forceinline__ Piece line_find(const AttnArgs& a, int rows, const Line& line, int64_t pos) {
+  const int lane = threadIdx.x & (kWave - 1);
+  int seg = -1;  // the last thread whose requests start at or before pos
+#pragma unroll
+  for (int i = 0; i < 4; ++i) seg += __popcll(__ballot(line.before[kWave * i + lane] <= pos));
+  const int per = (int(a.B) + 255) / 256;
+  Piece p;
+  p.b = seg * per;
+  int64_t local = pos - uniform(int64_t(line.before[seg]));
+  for (;; ++p.b) {
+    const Req r = request(a, p.b, rows);
+    p.r = Req{uniform(r.q0), uniform(r.qn), uniform(r.kv), uniform(r.tiles), uniform(r.lo), uniform(r.span)};
+    p.steps = req_steps(p.r);
+    const int64_t all = int64_t(p.r.tiles) * a.cache.heads * p.steps;
+    if (local < all) break;
+    local -= all;
+  }
+  int unit;
+  if (local >> 31) {
+    unit = int(local / p.steps);
+    p.at = int(local % p.steps);
+  } else {
+    unit = int(local) / p.steps;
+    p.at = int(local) % p.steps;
+  }
+  p.head = unit % a.cache.heads;
+  p.tile = unit / a.cache.heads;
+  return p;
+}
+
+// Workspace slot of block w's piece: its first, or the one that the next
+// block goes on with.
+__device__ __forceinline__ int64_t piece_slot(int64_t w, bool first) { return 2 * w + (first ? 0 : 1); }
 
 // Keys [begin, end) that query token i of a request sees.
 __device__ __forceinline__ void row_range(const AttnArgs& a, const Req& r, int i, int& begin, int& end) {
@@ -300,8 +295,12 @@ struct NarrowLds {
   static_assert(kNarrowRows * kOutRow * 4 <= kWaveBytes, "merge rows fit the V rows");
 };
 
+// Blocks a CU holds by registers (168 for bf16 at D = 128; 4 blocks would spill).
 template <int D, bool PRECISE>
-__global__ __launch_bounds__(256) void kv_attention_narrow_kernel(AttnArgs a, Sched s) {
+constexpr int kNarrowBlocks = D == 256 ? (PRECISE ? 1 : 2) : (PRECISE ? 2 : 3);
+
+template <int D, bool PRECISE>
+__global__ __launch_bounds__(256, (kNarrowBlocks<D, PRECISE>)) void kv_attention_narrow_kernel(AttnArgs a) {
   constexpr int N = PRECISE ? 3 : 1;
   constexpr int NL = D / 64;                 // 16-byte loads a lane makes for 32 rows of codes
   constexpr int NK = D == 64 ? 4 : D / 32;   // query operands
@@ -313,11 +312,18 @@ __global__ __launch_bounds__(256) void kv_attention_narrow_kernel(AttnArgs a, Sc
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   char* vbuf = lds + wave * L::kWaveBytes;
   const KvCache& kv = a.cache;
-  const int C = chunk_keys(a, s, lane);
-  Cursor cur{0, 0, 0};
-  cursor_load(a, s, C, cur, lane);
-  Item it;
-  for (int64_t item = blockIdx.x; cursor_seek(a, s, C, cur, item, false, lane, it); item += gridDim.x) {
+  __shared__ Line line;
+  line_build(a, kNarrowRows, line);
+  const int64_t total = line_total(line), share = line_share(total, gridDim.x);
+  const int64_t begin_pos = share * blockIdx.x;
+  const int64_t end_pos = begin_pos + share < total ? begin_pos + share : total;
+  for (int64_t pos = begin_pos; pos < end_pos;) {
+    const Piece it = line_find(a, kNarrowRows, line, pos);
+    const int steps = end_pos - pos < it.steps - it.at ? int(end_pos - pos) : it.steps - it.at;
+    const bool complete = steps == it.steps;
+    const int64_t slot = piece_slot(blockIdx.x, pos == begin_pos);
+    pos += steps;
+
     const int row = it.tile * kNarrowRows + n;
     const bool live = row < it.r.qn * a.group;
     const int tok = live ? row / a.group : 0, head = it.head * a.group + (live ? row % a.group : 0);
@@ -332,6 +338,7 @@ __global__ __launch_bounds__(256) void kv_attention_narrow_kernel(AttnArgs a, Sc
         query_operand<N>(a, base + 32 * chunk + 8 * pair_order(i & 3), live, q[i]);
       }
     }
+    const float scale2 = a.scale * kLog2e;
     // keys: of the lane's row, of the tile's first and last rows
     int begin, end, lo, hi;
     row_range(a, it.r, tok, begin, end);
@@ -342,10 +349,13 @@ __global__ __launch_bounds__(256) void kv_attention_narrow_kernel(AttnArgs a, Sc
     int full_lo, full_hi;  // keys that every row sees
     row_range(a, it.r, first_tok, lo, full_hi);
     row_range(a, it.r, last_tok, full_lo, hi);
-    const int chunk0 = it.r.lo + it.chunk * C;  // C = 2^31 - 2^8 has a single chunk
-    const int64_t chunk1 = int64_t(chunk0) + C;
+    const int chunk0 = it.r.lo + it.at * kStep;
+    const int64_t stop = int64_t(chunk0) + int64_t(steps) * kStep;
+    const int chunk1 = stop < it.r.kv ? int(stop) : it.r.kv;
     lo = lo > chunk0 ? lo : chunk0;
-    hi = hi < chunk1 ? hi : int(chunk1);
+    hi = hi < chunk1 ? hi : chunk1;
+    begin = begin > chunk0 ? begin : chunk0;
+    end = end < chunk1 ? end : chunk1;
     lo &= ~31;
 
     v4f o[D / 16];
@@ -353,35 +363,63 @@ __global__ __launch_bounds__(256) void kv_attention_narrow_kernel(AttnArgs a, Sc
     for (int c = 0; c < D / 16; ++c) o[c] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     float m = -INFINITY, l = 0.0f;
 
-    for (int j0 = lo + 32 * wave; j0 < hi; j0 += 128) {
-      // pages of the two 16-key halves (a half behind hi repeats the last key's page)
-      int page[2], slot[2];
-      bool seen[2];
+    // Page ids of 32 tiles at a time (two 16-key halves each), one per lane; -1: no key of the half is visible.
+    int ids = -1;
+    auto load_ids = [&](int j) {
+      j += 128 * (lane >> 1) + 16 * (lane & 1);
+      ids = -1;
+      if (j < hi) {
+        ids = a.block_table[it.b * a.table_width + (j >> kv.log2_page)];
+        if (ids >= kv.pages) ids = -1;
+      }
+    };
+    // A tile's codes and scales; each is loaded for the next tile as soon as
+    // the current tile's registers are used up.
+    v4u kraw[NL], vraw[NL];
+    v4f sk[2], sv[2];
+    bool next_seen[2];
+    int64_t code_at[2], scale_at[2];  // of the halves' first rows
+    const int64_t code_lane = n * kv.code_slot + 16 * (D == 64 ? (g & 1) : g);
+    const int64_t scale_lane = 4 * g * kv.scale_slot;
+    auto locate = [&](int j, int tile) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int j = j0 + 16 * h, jj = j < hi ? j : hi - 1;
-        const int id = a.block_table[it.b * a.table_width + (jj >> kv.log2_page)];
-        seen[h] = j < hi && id >= 0 && id < kv.pages;
-        page[h] = seen[h] ? id : 0;
-        slot[h] = j & ((1 << kv.log2_page) - 1);
+        const int id = __builtin_amdgcn_readlane(ids, 2 * (tile & 31) + h);
+        const int slot = (j + 16 * h) & ((1 << kv.log2_page) - 1);
+        next_seen[h] = id >= 0;
+        const int64_t page = id >= 0 ? id : 0;  // a half without keys reads page 0, unused
+        code_at[h] = page * kv.code_page + it.head * kv.code_head + slot * kv.code_slot;
+        scale_at[h] = page * kv.scale_page + it.head * kv.scale_head + slot * kv.scale_slot;
       }
-      v4u kraw[NL], vraw[NL];
+    };
+    auto load_codes = [&](const uint8_t* codes, v4u(&raw)[NL]) {
 #pragma unroll
       for (int i = 0; i < NL; ++i) {
-        const int h = D == 64 ? (g >> 1) : D == 128 ? i : i >> 1;
-        const int chunk = D == 64 ? (g & 1) : D == 128 ? g : 4 * (i & 1) + g;
-        const int64_t off = int64_t(h ? page[1] : page[0]) * kv.code_page + it.head * kv.code_head +
-                            int64_t((h ? slot[1] : slot[0]) + n) * kv.code_slot + 16 * chunk;
-        kraw[i] = *reinterpret_cast<const v4u*>(kv.k_codes + off);
-        vraw[i] = *reinterpret_cast<const v4u*>(kv.v_codes + off);
+        const int64_t at = D == 64 ? (g >> 1 ? code_at[1] : code_at[0]) : D == 128 ? code_at[i] : code_at[i >> 1];
+        raw[i] = *reinterpret_cast<const v4u*>(codes + at + code_lane + (D == 256 ? 64 * (i & 1) : 0));
       }
-      v4f sk[2], sv[2];
+    };
+    auto load_scales = [&](const float* scales, v4f(&to)[2]) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int64_t off = int64_t(page[h]) * kv.scale_page + it.head * kv.scale_head +
-                            int64_t(slot[h] + 4 * g) * kv.scale_slot;
-        sk[h] = scales4(kv.k_scales + off, kv.scale_slot);
-        sv[h] = scales4(kv.v_scales + off, kv.scale_slot);
+      for (int h = 0; h < 2; ++h) to[h] = scales4(scales + scale_at[h] + scale_lane, kv.scale_slot);
+    };
+
+    int j0 = lo + 32 * wave, tile = 0;
+    load_ids(j0);
+    if (j0 < hi) {
+      locate(j0, 0);
+      load_codes(kv.k_codes, kraw);
+      load_codes(kv.v_codes, vraw);
+      load_scales(kv.k_scales, sk);
+      load_scales(kv.v_scales, sv);
+    }
+    for (; j0 < hi; j0 += 128, ++tile) {
+      const bool seen[2] = {next_seen[0], next_seen[1]};
+      const int jn = j0 + 128;
+      const bool more = jn < hi;
+      if (more) {
+        if (((tile + 1) & 31) == 0) load_ids(jn);
+        locate(jn, tile + 1);
       }
       // scores
       v4f sc[2] = {v4f{0.0f, 0.0f, 0.0f, 0.0f}, v4f{0.0f, 0.0f, 0.0f, 0.0f}};
@@ -405,6 +443,7 @@ __global__ __launch_bounds__(256) void kv_attention_narrow_kernel(AttnArgs a, Sc
           }
         }
       }
+      if (more) load_codes(kv.k_codes, kraw);
       // values to LDS
 #pragma unroll
       for (int i = 0; i < NL; ++i) {
@@ -415,18 +454,20 @@ __global__ __launch_bounds__(256) void kv_attention_narrow_kernel(AttnArgs a, Sc
 #pragma unroll
         for (int e = 0; e < 4; ++e) *reinterpret_cast<v8bf*>(dst + 16 * pair_order(e)) = part8(v32, e);
       }
+      if (more) load_codes(kv.v_codes, vraw);
       // softmax
       float x[8];
-      bool vis[8];
       const bool whole = seen[0] && seen[1] && j0 >= full_lo && j0 + 32 <= full_hi && j0 + 32 <= hi;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = sc[e >> 2][e & 3] * (sk[e >> 2][e & 3] * (a.scale * kLog2e));
+      for (int e = 0; e < 8; ++e) x[e] = sc[e >> 2][e & 3] * (sk[e >> 2][e & 3] * scale2);
+      if (more) load_scales(kv.k_scales, sk);
       if (!whole) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int j = j0 + 16 * (e >> 2) + 4 * g + (e & 3);
-          vis[e] = seen[e >> 2] && j >= begin && j < end && j >= chunk0 && j < chunk1;
-          x[e] = vis[e] ? x[e] : -INFINITY;
+          const bool vis = seen[e >> 2] && j >= begin && j < end;
+          x[e] = vis ? x[e] : -INFINITY;  // probability 0
+          sv[e >> 2][e & 3] = vis ? sv[e >> 2][e & 3] : 0.0f;  // whatever lies behind the last key
         }
       }
       float top = x[0];
@@ -446,18 +487,14 @@ __global__ __launch_bounds__(256) void kv_attention_narrow_kernel(AttnArgs a, Sc
       v8bf pr[N];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        float p = __builtin_amdgcn_exp2f(x[e] - ref);
-        float pv = p * sv[e >> 2][e & 3];
-        if (!whole) {
-          p = vis[e] ? p : 0.0f;
-          pv = vis[e] ? pv : 0.0f;
-        }
+        const float p = __builtin_amdgcn_exp2f(x[e] - ref);
         l += p;
         __bf16 part[N];
-        split_bf16<N>(pv, part);
+        split_bf16<N>(p * sv[e >> 2][e & 3], part);
 #pragma unroll
         for (int i = 0; i < N; ++i) pr[i][e] = part[i];
       }
+      if (more) load_scales(kv.v_scales, sv);
       // output: keys of lane group g: 4 g + 0..3 and 16 + 4 g + 0..3
       wave_lds_order();
       const char* vsrc = vbuf + (4 * g + (n >> 2)) * L::kRow + 8 * (n & 3);
@@ -501,10 +538,10 @@ __global__ __launch_bounds__(256) void kv_attention_narrow_kernel(AttnArgs a, Sc
 #pragma unroll
           for (int e = 0; e < 8; ++e) acc[e] += src[e];
         }
-        if (it.chunks == 1) {
+        if (complete) {
           finish_row<D>(a, it.r, it.head, it.tile * kNarrowRows + r, acc, top, sum, lane);
         } else {
-          float* part = reinterpret_cast<float*>(a.workspace) + (it.slot + it.chunk) * (kNarrowRows * (D + 2));
+          float* part = reinterpret_cast<float*>(a.workspace) + slot * (kNarrowRows * (D + 2));
           store_row8(part, false, r * D + 8 * (tid & (LR - 1)), acc);
           if ((tid & (LR - 1)) == 0) {
             part[kNarrowRows * D + r] = top;
@@ -518,71 +555,118 @@ __global__ __launch_bounds__(256) void kv_attention_narrow_kernel(AttnArgs a, Sc
 }
 
 // ---------------------------------------------------------------------------
-// The partial results of split units put together: D / 8 lanes a row.
+// The pieces of cut units put together.  Block (w, part) looks at the border
+// between blocks w - 1 and w of the attention's grid: if it is the first
+// border inside a unit, it merges 64 / LR rows (LR = D / 8 lanes a row) of that
+// unit, its 4 waves every fourth piece each, eight pieces in flight, and the
+// waves through LDS.
 // ---------------------------------------------------------------------------
 template <int D>
-__global__ __launch_bounds__(256) void kv_attention_combine_kernel(AttnArgs a, Sched s) {
-  constexpr int LR = D / 8, PASS = 256 / LR;
-  const int tid = threadIdx.x, lane = tid & (kWave - 1);
-  const int C = chunk_keys(a, s, lane);
-  Cursor cur{0, 0, 0};
-  cursor_load(a, s, C, cur, lane);
-  Item it;
-  for (int64_t unit = blockIdx.x; cursor_seek(a, s, C, cur, unit, true, lane, it); unit += gridDim.x) {
-    if (it.chunks == 1) continue;
-    const int size = s.rows * (D + 2);
-    const float* first = reinterpret_cast<const float*>(a.workspace) + it.slot * size;
-    for (int r0 = 0; r0 < s.rows; r0 += PASS) {
-      const int r = r0 + tid / LR, row = it.tile * s.rows + r;
-      if (r0 + (tid & ~(kWave - 1)) / LR >= s.rows) break;  // whole waves
-      if (row - (lane / LR) >= it.r.qn * a.group) break;
-      float top = -INFINITY, sum = 0.0f, acc[8] = {};
-      for (int c = 0; c < it.chunks; ++c) top = fmaxf(top, first[int64_t(c) * size + s.rows * D + r]);
-      for (int c = 0; c < it.chunks; ++c) {
-        const float* part = first + int64_t(c) * size;
-        const float m = part[s.rows * D + r], w = m == -INFINITY ? 0.0f : exp2f(m - top);
-        float v[8];
-        RowSrc<false>{part, 0}.load8(0, r * D + 8 * (tid & (LR - 1)), v);
-        sum += m == -INFINITY ? 0.0f : part[s.rows * (D + 1) + r] * w;
+__global__ __launch_bounds__(256) void kv_attention_combine_kernel(AttnArgs a, int rows, int blocks) {
+  constexpr int LR = D / 8, R = kWave / LR;
+  __shared__ float acc_s[4][kWave][9];
+  __shared__ float m_s[4][R], l_s[4][R];
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), l8 = lane & (LR - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int parts = rows / R;
+  __shared__ Line line;
+  line_build(a, rows, line);
+  const int64_t total = line_total(line), share = line_share(total, blocks);
+  const int64_t w = 1 + blockIdx.x / parts, border = w * share;
+  if (border >= total) return;
+  const Piece it = line_find(a, rows, line, border);
+  // cut here, and not before
+  if (it.at == 0 || it.at > share) return;
+  {
+    const int r0 = int(blockIdx.x % parts) * R, r = r0 + lane / LR;
+    if (it.tile * rows + r0 >= it.r.qn * a.group) return;  // the whole block
+    const int size = rows * (D + 2);
+    // pieces: block w - 1's (its first one only if the unit fills its share), then the first of w, w + 1, ...
+    const int pieces = 2 + int((it.steps - it.at - 1) / share);
+    const float* work = reinterpret_cast<const float*>(a.workspace);
+    const float* head_part = work + piece_slot(w - 1, it.at == share) * size;
+    const float* rest = work + piece_slot(w, true) * size;
+    float m = -INFINITY, l = 0.0f, acc[8] = {};
+    for (int c0 = wave; c0 < pieces; c0 += 32) {
+      float mc[8], lc[8], v[8][8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] = fmaf(v[e], w, acc[e]);
+      for (int i = 0; i < 8; ++i) {
+        const int c = c0 + 4 * i;
+        if (c < pieces) {  // uniform
+          const float* part = c == 0 ? head_part : rest + int64_t(c - 1) * (2 * size);
+          mc[i] = part[rows * D + r];
+          lc[i] = part[rows * (D + 1) + r];
+          RowSrc<false>{part, 0}.load8(0, r * D + 8 * l8, v[i]);
+        }
       }
-      finish_row<D>(a, it.r, it.head, row, acc, top, sum, lane);
+      float top = m;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c0 + 4 * i < pieces) top = fmaxf(top, mc[i]);
+      const float keep = m == -INFINITY ? 0.0f : exp2f(m - top);
+      m = top;
+      l *= keep;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] *= keep;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (c0 + 4 * i < pieces) {
+          const float x = mc[i] == -INFINITY ? 0.0f : exp2f(mc[i] - m);
+          l = fmaf(lc[i], x, l);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[e] = fmaf(v[i][e], x, acc[e]);
+        }
+      }
+    }
+    if (l8 == 0) {
+      m_s[wave][lane / LR] = m;
+      l_s[wave][lane / LR] = l;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc_s[wave][lane][e] = acc[e];
+    __syncthreads();
+    if (wave == 0) {
+      float top = m, sum = 0.0f, o[8] = {};
+#pragma unroll
+      for (int i = 1; i < 4; ++i) top = fmaxf(top, m_s[i][lane / LR]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float mi = m_s[i][lane / LR], x = mi == -INFINITY ? 0.0f : exp2f(mi - top);
+        sum = fmaf(l_s[i][lane / LR], x, sum);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = fmaf(acc_s[i][lane][e], x, o[e]);
+      }
+      finish_row<D>(a, it.r, it.head, it.tile * rows + r, o, top, sum, lane);
     }
   }
 }
 
-// Units a call can have, and the workspace slots of its chunks: at most
-// target items and one partial chunk for each unit, and nothing is split from
-// `whole` units on.
-int64_t units_max(int64_t T, int64_t B, int64_t group, int64_t kv_heads, int rows) {
-  return kv_heads * (T * group / rows + (B < T ? B : T));
-}
-int64_t narrow_slots(int64_t T, int64_t B, int64_t group, int64_t kv_heads) {
-  const int64_t units = units_max(T, B, group, kv_heads, kNarrowRows);
-  return kNarrowTarget + (units < kNarrowWhole ? units : kNarrowWhole);
+// Steps a call can have at most, as far as the host knows.
+int64_t steps_max(const AttnArgs& a, int rows) {
+  const int64_t units = a.cache.heads * (a.T * a.group / rows + (a.B < a.T ? a.B : a.T));
+  const int64_t room = a.table_width << a.cache.log2_page, steps = room > kStep ? (room + kStep - 1) / kStep : 1;
+  return units > (int64_t(1) << 40) / steps ? int64_t(1) << 40 : units * steps;
 }
 
 template <int D, bool PRECISE>
 hipError_t launch_narrow(const AttnArgs& a, hipStream_t st) {
-  const Sched s{kNarrowRows, kNarrowTarget, kNarrowWhole};
-  const int64_t slots = narrow_slots(a.T, a.B, a.group, a.cache.heads);
-  const int64_t units = units_max(a.T, a.B, a.group, a.cache.heads, kNarrowRows);
-  const int64_t most = units > slots ? units : slots;
-  const unsigned blocks = unsigned(most < kNarrowTarget ? most : kNarrowTarget);
-  hipLaunchKernelGGL((kv_attention_narrow_kernel<D, PRECISE>), dim3(blocks), dim3(256), 0, st, a, s);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || (a.table_width << a.cache.log2_page) <= kMinChunk) return e;  // nothing can be split
-  const unsigned again = unsigned(units < 1024 ? units : 1024);
-  hipLaunchKernelGGL((kv_attention_combine_kernel<D>), dim3(again), dim3(256), 0, st, a, s);
+  const int64_t most = steps_max(a, kNarrowRows);
+  const int full = kCUs * kNarrowBlocks<D, PRECISE>;
+  const int blocks = most < full ? int(most) : full;
+  hipLaunchKernelGGL((kv_attention_narrow_kernel<D, PRECISE>), dim3(blocks), dim3(256), 0, st, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || (a.table_width << a.cache.log2_page) <= kStep) return e;  // no unit has two steps
+  if (blocks == 1) return e;
+  constexpr int kParts = kNarrowRows / (kWave / (D / 8));
+  hipLaunchKernelGGL((kv_attention_combine_kernel<D>), dim3((blocks - 1) * kParts), dim3(256), 0, st, a, kNarrowRows,
+                     blocks);
   return hipGetLastError();
 }
 
 }  // namespace
 
-int64_t kv_attention_workspace_bytes(int64_t T, int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim) {
-  const int64_t slots = narrow_slots(T, B, heads / kv_heads, kv_heads);
-  return slots * kNarrowRows * (head_dim + 2) * int64_t(sizeof(float));
+int64_t kv_attention_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t head_dim) {
+  return int64_t(2) * kCUs * 3 * kNarrowRows * (head_dim + 2) * int64_t(sizeof(float));
 }
 
 hipError_t launch_kv_attention(const AttnArgs& a, hipStream_t st) {
