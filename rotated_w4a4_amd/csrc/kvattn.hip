@@ -39,9 +39,13 @@ typedef __bf16 v32bf __attribute__((ext_vector_type(32)));
 typedef unsigned int v4u __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kSlack = 8.0f;  // probabilities may reach 2^kSlack before the maximum is raised
 constexpr int kCUs = 256;
 constexpr int kNarrowRows = 16;
-constexpr int kStep = 128;  // keys of a step: 32 for each of a block's 4 waves
+constexpr int kNarrowStep = 128;  // keys of a step: 32 for each of a block's 4 waves
+constexpr int kWideStep = 64;
+constexpr int kMaxBlocks = kCUs * 3;
+constexpr int kNarrowMost = 32;  // up to this many rows of a request the narrow kernel is used
 
 // ---------------------------------------------------------------------------
 // The line of work.
@@ -79,12 +83,18 @@ __device__ __forceinline__ T wave_prefix(T v, int lane) {
   }
   return v;
 }
+__device__ __forceinline__ int wave_total(int v) {
+  for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
+  return v;
+}
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ __forceinline__ int64_t uniform(int64_t v) {
   return int64_t(uint32_t(uniform(int(v)))) | (int64_t(uniform(int(v >> 32))) << 32);
 }
 
-__device__ __forceinline__ int req_steps(const Req& r) { return r.span > 0 ? (r.span + kStep - 1) / kStep : 1; }
+__device__ __forceinline__ int req_steps(const Req& r, int step) {
+  return r.span > 0 ? (r.span + step - 1) / step : 1;
+}
 
 // The piece of a unit at a position of the line.
 struct Piece {
@@ -93,21 +103,40 @@ struct Piece {
   int steps, at;       // steps of the unit, the position's step in it
 };
 
+// How a kernel cuts the work: query rows of a unit, keys of a step, and with
+// how many units or more (0: never) every block takes whole units instead.
+struct Cut {
+  int rows, step, whole;
+};
+
 // Steps before each thread's requests (256 threads take consecutive ones).
 struct Line {
   long long before[257];
   long long wave_sum[4];
+  int wave_units[4];
+  bool by_units;  // a step for each unit
 };
 
-__device__ __forceinline__ void line_build(const AttnArgs& a, int rows, Line& line) {
+__device__ __forceinline__ void line_build(const AttnArgs& a, const Cut& cut, Line& line) {
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
   const int B = int(a.B), per = (B + 255) / 256;
   const int b0 = tid * per < B ? tid * per : B, b1 = b0 + per < B ? b0 + per : B;
   long long sum = 0;
+  int units = 0;
   for (int b = b0; b < b1; ++b) {
-    const Req r = request(a, b, rows);
-    sum += (long long)(r.tiles) * a.cache.heads * req_steps(r);
+    const Req r = request(a, b, cut.rows);
+    sum += (long long)(r.tiles) * a.cache.heads * req_steps(r, cut.step);
+    units += r.tiles * a.cache.heads;
   }
+  bool by_units = false;
+  if (cut.whole > 0) {
+    const int wave_units = wave_total(units);
+    if (lane == 0) line.wave_units[wave] = wave_units;
+    __syncthreads();
+    by_units = line.wave_units[0] + line.wave_units[1] + line.wave_units[2] + line.wave_units[3] >= cut.whole;
+    if (by_units) sum = units;
+  }
+  if (tid == 0) line.by_units = by_units;
   const long long upto = wave_prefix(sum, lane);
   if (lane == kWave - 1) line.wave_sum[wave] = upto;
   __syncthreads();
@@ -127,19 +156,20 @@ __device__ __forceinline__ int64_t line_share(int64_t total, int blocks) {
 }
 
 // The piece at position pos < total; every wave finds it by itself.
-__device__ __forceinline__ Piece line_find(const AttnArgs& a, int rows, const Line& line, int64_t pos) {
+__device__ __forceinline__ Piece line_find(const AttnArgs& a, const Cut& cut, const Line& line, int64_t pos) {
   const int lane = threadIdx.x & (kWave - 1);
   int seg = -1;  // the last thread whose requests start at or before pos
 #pragma unroll
   for (int i = 0; i < 4; ++i) seg += __popcll(__ballot(line.before[kWave * i + lane] <= pos));
   const int per = (int(a.B) + 255) / 256;
   Piece p;
+  const bool by_units = uniform(int(line.by_units));
   p.b = seg * per;
   int64_t local = pos - uniform(int64_t(line.before[seg]));
   for (;; ++p.b) {
-    const Req r = request(a, p.b, rows);
+    const Req r = request(a, p.b, cut.rows);
     p.r = Req{uniform(r.q0), uniform(r.qn), uniform(r.kv), uniform(r.tiles), uniform(r.lo), uniform(r.span)};
-    p.steps = req_steps(p.r);
+    p.steps = by_units ? 1 : req_steps(p.r, cut.step);
     const int64_t all = int64_t(p.r.tiles) * a.cache.heads * p.steps;
     if (local < all) break;
     local -= all;
@@ -153,13 +183,40 @@ __device__ __forceinline__ Piece line_find(const AttnArgs& a, int rows, const Li
     p.at = int(local) % p.steps;
   }
   p.head = unit % a.cache.heads;
-  p.tile = unit / a.cache.heads;
+  p.tile = p.r.tiles - 1 - unit / a.cache.heads;  // the rows that see most first
   return p;
 }
 
-// Workspace slot of block w's piece: its first, or the one that the next
-// block goes on with.
-__device__ __forceinline__ int64_t piece_slot(int64_t w, bool first) { return 2 * w + (first ? 0 : 1); }
+// The workspace: a descriptor for each border between blocks, then the
+// partial results, two for each block: its first piece, and the one that the
+// next block goes on with.
+struct Border {
+  int pieces;       // of the unit cut here for the first time; 0: none is
+  int first;        // slot of its first piece (the others are 2 w, 2 (w + 1), ...)
+  int q0, qn, head, tile;
+  int unused[2];
+};
+__device__ __forceinline__ Border* borders(const AttnArgs& a) { return reinterpret_cast<Border*>(a.workspace); }
+__device__ __forceinline__ float* partials(const AttnArgs& a) {
+  return reinterpret_cast<float*>(reinterpret_cast<char*>(a.workspace) + kMaxBlocks * sizeof(Border));
+}
+__device__ __forceinline__ int piece_slot(int w, bool first) { return 2 * w + (first ? 0 : 1); }
+
+// Block w writes what the combine kernel has to do at the border in front of
+// it; `it` is its first piece (steps left unused without one).
+__device__ __forceinline__ void write_border(const AttnArgs& a, int w, bool any, const Piece& it, int64_t share) {
+  if (threadIdx.x != 0) return;
+  Border d{};
+  if (any && it.at > 0 && it.at <= share) {  // cut here, and not before
+    d.pieces = 2 + int((it.steps - it.at - 1) / share);
+    d.first = piece_slot(w - 1, it.at == share);
+    d.q0 = it.r.q0;
+    d.qn = it.r.qn;
+    d.head = it.head;
+    d.tile = it.tile;
+  }
+  borders(a)[w] = d;
+}
 
 // Keys [begin, end) that query token i of a request sees.
 __device__ __forceinline__ void row_range(const AttnArgs& a, const Req& r, int i, int& begin, int& end) {
@@ -253,7 +310,7 @@ __device__ __forceinline__ v4f scales4(const float* p, int64_t stride) {
 // One finished row: o (8 channels of each of its D / 8 lanes), sum l, maximum
 // m: normalized, unrotated, rounded and stored.
 template <int D>
-__device__ __forceinline__ void finish_row(const AttnArgs& a, const Req& r, int head, int row, float (&o)[8], float m,
+__device__ __forceinline__ void finish_row(const AttnArgs& a, int q0, int qn, int head, int row, float (&o)[8], float m,
                                            float l, int lane) {
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
@@ -263,8 +320,8 @@ __device__ __forceinline__ void finish_row(const AttnArgs& a, const Req& r, int 
 #pragma unroll
     for (int e = 0; e < 8; ++e) o[e] *= kHeadPost<D>;
   }
-  if (row >= r.qn * a.group) return;
-  const int64_t t = r.q0 + row / a.group;
+  if (row >= qn * a.group) return;
+  const int64_t t = q0 + row / a.group;
   const int h = head * a.group + row % a.group, c8 = lane & (D / 8 - 1);
   store_row8(a.out, a.out_bf16, t * a.out_token + h * a.out_head + 8 * c8, o);
   if (a.lse && c8 == 0) a.lse[t * a.heads + h] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
@@ -313,15 +370,18 @@ __global__ __launch_bounds__(256, (kNarrowBlocks<D, PRECISE>)) void kv_attention
   char* vbuf = lds + wave * L::kWaveBytes;
   const KvCache& kv = a.cache;
   __shared__ Line line;
-  line_build(a, kNarrowRows, line);
+  constexpr Cut cut{kNarrowRows, kNarrowStep, 0};
+  line_build(a, cut, line);
   const int64_t total = line_total(line), share = line_share(total, gridDim.x);
   const int64_t begin_pos = share * blockIdx.x;
   const int64_t end_pos = begin_pos + share < total ? begin_pos + share : total;
+  if (begin_pos >= end_pos) write_border(a, blockIdx.x, false, Piece{}, share);
   for (int64_t pos = begin_pos; pos < end_pos;) {
-    const Piece it = line_find(a, kNarrowRows, line, pos);
+    const Piece it = line_find(a, cut, line, pos);
     const int steps = end_pos - pos < it.steps - it.at ? int(end_pos - pos) : it.steps - it.at;
     const bool complete = steps == it.steps;
     const int64_t slot = piece_slot(blockIdx.x, pos == begin_pos);
+    if (pos == begin_pos) write_border(a, blockIdx.x, true, it, share);
     pos += steps;
 
     const int row = it.tile * kNarrowRows + n;
@@ -349,8 +409,8 @@ __global__ __launch_bounds__(256, (kNarrowBlocks<D, PRECISE>)) void kv_attention
     int full_lo, full_hi;  // keys that every row sees
     row_range(a, it.r, first_tok, lo, full_hi);
     row_range(a, it.r, last_tok, full_lo, hi);
-    const int chunk0 = it.r.lo + it.at * kStep;
-    const int64_t stop = int64_t(chunk0) + int64_t(steps) * kStep;
+    const int chunk0 = it.r.lo + it.at * kNarrowStep;
+    const int64_t stop = int64_t(chunk0) + int64_t(steps) * kNarrowStep;
     const int chunk1 = stop < it.r.kv ? int(stop) : it.r.kv;
     lo = lo > chunk0 ? lo : chunk0;
     hi = hi < chunk1 ? hi : chunk1;
@@ -458,8 +518,10 @@ __global__ __launch_bounds__(256, (kNarrowBlocks<D, PRECISE>)) void kv_attention
       // softmax
       float x[8];
       const bool whole = seen[0] && seen[1] && j0 >= full_lo && j0 + 32 <= full_hi && j0 + 32 <= hi;
+      // relative to the running maximum
+      float ref = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = sc[e >> 2][e & 3] * (sk[e >> 2][e & 3] * scale2);
+      for (int e = 0; e < 8; ++e) x[e] = fmaf(sc[e >> 2][e & 3], sk[e >> 2][e & 3] * scale2, -ref);
       if (more) load_scales(kv.k_scales, sk);
       if (!whole) {
 #pragma unroll
@@ -470,24 +532,25 @@ __global__ __launch_bounds__(256, (kNarrowBlocks<D, PRECISE>)) void kv_attention
           sv[e >> 2][e & 3] = vis ? sv[e >> 2][e & 3] : 0.0f;  // whatever lies behind the last key
         }
       }
-      float top = x[0];
-#pragma unroll
-      for (int e = 1; e < 8; ++e) top = fmaxf(top, x[e]);
-      if (__ballot(top > m + 8.0f)) {
+      float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+      const float limit = m == -INFINITY ? -INFINITY : kSlack;
+      if (__ballot(top > limit)) {
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
-        const float m_new = top > m + 8.0f ? top : m;  // a row's results do not depend on its neighbours'
-        const float alpha = m == -INFINITY ? 0.0f : exp2f(m - m_new);
-        m = m_new;
-        l *= alpha;
+        if (top > limit) {  // by rows: a row's results do not depend on its neighbours'
+          const float alpha = m == -INFINITY ? 0.0f : exp2f(-top);
+          m = ref + top;
+          l *= alpha;
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) o[c] *= alpha;
+          for (int c = 0; c < D / 16; ++c) o[c] *= alpha;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] -= top;
+        }
       }
-      const float ref = m == -INFINITY ? 0.0f : m;
       v8bf pr[N];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float p = __builtin_amdgcn_exp2f(x[e] - ref);
+        const float p = __builtin_amdgcn_exp2f(x[e]);
         l += p;
         __bf16 part[N];
         split_bf16<N>(p * sv[e >> 2][e & 3], part);
@@ -539,9 +602,9 @@ __global__ __launch_bounds__(256, (kNarrowBlocks<D, PRECISE>)) void kv_attention
           for (int e = 0; e < 8; ++e) acc[e] += src[e];
         }
         if (complete) {
-          finish_row<D>(a, it.r, it.head, it.tile * kNarrowRows + r, acc, top, sum, lane);
+          finish_row<D>(a, it.r.q0, it.r.qn, it.head, it.tile * kNarrowRows + r, acc, top, sum, lane);
         } else {
-          float* part = reinterpret_cast<float*>(a.workspace) + slot * (kNarrowRows * (D + 2));
+          float* part = partials(a) + slot * (kNarrowRows * (D + 2));
           store_row8(part, false, r * D + 8 * (tid & (LR - 1)), acc);
           if ((tid & (LR - 1)) == 0) {
             part[kNarrowRows * D + r] = top;
@@ -555,37 +618,351 @@ __global__ __launch_bounds__(256, (kNarrowBlocks<D, PRECISE>)) void kv_attention
 }
 
 // ---------------------------------------------------------------------------
+// Many query rows (prompts, chunks): 32 RB rows for each of a block's 4 waves,
+// 64 keys a step.  The block opens a step's codes once, into two LDS buffers
+// (rows of bf16 codes, keys and values alike, and the keys' scales, sk already
+// times scale log2(e)), while it computes on the step before; one barrier a
+// step.  The products are those of the narrow kernel in 32 x 32 tiles: S^T =
+// K Q^T leaves a query row in lanes n and n + 32, keys 8 b + 4 h + i in
+// registers (h the lane's half), which is the column operand of O^T = V^T P^T
+// with keys ordered (16 b + 4 h + 0..3, 16 b + 8 + 4 h + 0..3) per half.
+// ---------------------------------------------------------------------------
+typedef float v16f __attribute__((ext_vector_type(16)));
+
+#ifndef WRB
+#define WRB 1
+#endif
+template <int D>
+constexpr int kWideRB = D == 256 ? 1 : WRB;  // 32-row blocks of a wave
+// Blocks of the grid for each CU.
+template <int D, bool PRECISE, int RB>
+constexpr int kWideBlocks = (D == 256 || PRECISE || RB == 2) ? 1 : 2;
+
+template <int D>
+struct WideLds {
+  static constexpr int kRow = 2 * D + 32;  // bytes of a row: 8 consecutive rows hit 8 bank groups
+  static constexpr int kHalf = kWideStep * kRow;
+  static constexpr int kBuffer = 2 * kHalf;  // keys, values
+  static constexpr int kOutRow = D + 4;      // floats of an output row
+  static constexpr int kOutWave = 32 * kOutRow * 4;
+  static constexpr int kBytes = 2 * kBuffer > 4 * kOutWave ? 2 * kBuffer : 4 * kOutWave;
+};
+
+template <int D, bool PRECISE, int RB>
+__global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE, RB>)) void kv_attention_wide_kernel(AttnArgs a, Cut cut, int blocks) {
+  constexpr int N = PRECISE ? 3 : 1;
+  constexpr int kRows = 128 * RB;
+  constexpr int CH = D / 32;                          // chunks of a row
+  constexpr int NS = (2 * kWideStep * CH) / 256;      // chunks a thread opens a step (1: keys or values)
+  constexpr int NH = NS > 1 ? NS / 2 : 1;             // of one kind
+  using L = WideLds<D>;
+  extern __shared__ __align__(16) char lds[];
+  __shared__ float scale_s[2][2][kWideStep];
+  __shared__ int seen_s[2][kWideStep];
+  __shared__ float row_m[kRows], row_l[kRows];
+  __shared__ Line line;
+
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), n = lane & 31, h = lane >> 5;
+  const int wave = uniform(tid / kWave);
+  const KvCache& kv = a.cache;
+  line_build(a, cut, line);
+  const int64_t total = line_total(line);
+  const bool by_units = uniform(int(line.by_units));
+  const int64_t share = by_units ? 1 : line_share(total, blocks);
+  const int64_t begin_pos = share * blockIdx.x;
+  const int64_t end_pos = begin_pos + share < total ? begin_pos + share : total;
+  if (begin_pos >= end_pos && int(blockIdx.x) < blocks) write_border(a, blockIdx.x, false, Piece{}, share);
+  for (int64_t pos = begin_pos; pos < end_pos;) {
+    const Piece it = line_find(a, cut, line, pos);
+    const int steps = end_pos - pos < it.steps - it.at ? int(end_pos - pos) : it.steps - it.at;
+    const bool complete = steps == it.steps;
+    const int64_t slot = piece_slot(blockIdx.x, pos == begin_pos);
+    if (pos == begin_pos && int(blockIdx.x) < blocks) write_border(a, blockIdx.x, true, it, share);
+    pos += steps;
+
+    const int rows = it.r.qn * a.group, row0 = it.tile * kRows + wave * 32 * RB;
+    v8bf q[RB][D / 16][N];
+    int begin[RB], end[RB];
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+      const int row = row0 + 32 * rb + n;
+      const bool live = row < rows;
+      const int tok = live ? row / a.group : 0, head = it.head * a.group + (live ? row % a.group : 0);
+      const int64_t base = (it.r.q0 + tok) * a.q_token + head * a.q_head;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) query_operand<N>(a, base + 16 * i + 8 * h, live, q[rb][i]);
+      row_range(a, it.r, tok, begin[rb], end[rb]);
+    }
+    // keys of the unit's rows and of the wave's: all that any row sees, and those that every row sees
+    int lo, hi, wave_hi = 0, full_lo = 0, full_hi = 0, skip;
+    {
+      const int last = (it.tile + 1) * kRows < rows ? (it.tile + 1) * kRows - 1 : rows - 1;
+      row_range(a, it.r, it.tile * kRows / a.group, lo, skip);
+      row_range(a, it.r, last / a.group, skip, hi);
+      if (row0 < rows) {
+        const int wave_last = row0 + 32 * RB < rows ? row0 + 32 * RB - 1 : rows - 1;
+        row_range(a, it.r, row0 / a.group, skip, full_hi);
+        row_range(a, it.r, wave_last / a.group, full_lo, wave_hi);
+      }
+    }
+    const int chunk0 = it.r.lo + (by_units ? 0 : it.at * kWideStep);
+    const int64_t stop = by_units ? it.r.kv : int64_t(chunk0) + int64_t(steps) * kWideStep;
+    const int chunk1 = stop < it.r.kv ? int(stop) : it.r.kv;
+    lo = lo > chunk0 ? lo : chunk0;
+    hi = hi < chunk1 ? hi : chunk1;
+    wave_hi = wave_hi < chunk1 ? wave_hi : chunk1;
+    full_hi = full_hi < chunk1 ? full_hi : chunk1;
+    lo = chunk0 + ((lo - chunk0) & ~(kWideStep - 1));
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+      begin[rb] = begin[rb] > chunk0 ? begin[rb] : chunk0;
+      end[rb] = end[rb] < chunk1 ? end[rb] : chunk1;
+    }
+
+    v16f o[RB][D / 32];
+    float m[RB], l[RB];
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) o[rb][c] = v16f{};
+      m[rb] = -INFINITY;
+      l[rb] = 0.0f;
+    }
+
+    // staging: the thread's chunks of a step (row my_row + i * rows_apart, chunk my_chunk)
+    constexpr int kApart = 256 / CH;
+    const bool half_v = NS == 1 && tid >= 128;  // D = 64: one half of the threads takes keys, the other values
+    const int my_row = NS == 1 ? (tid & 127) / CH : tid / CH, my_chunk = tid % CH;
+    const float scale2 = a.scale * kLog2e;
+    int ids[NH], scale_id;
+    auto load_ids = [&](int j0) {
+#pragma unroll
+      for (int i = 0; i < NH; ++i) {
+        const int j = j0 + my_row + i * kApart;
+        ids[i] = -1;
+        if (j < hi) {
+          const int id = a.block_table[it.b * a.table_width + (j >> kv.log2_page)];
+          ids[i] = id < kv.pages ? id : -1;
+        }
+      }
+      scale_id = -1;
+      if (tid < kWideStep && j0 + tid < hi) {
+        const int id = a.block_table[it.b * a.table_width + ((j0 + tid) >> kv.log2_page)];
+        scale_id = id < kv.pages ? id : -1;
+      }
+    };
+    v4u raw[NS];
+    float scales[2];
+    int seen = 0;
+    auto load_step = [&](int j0) {
+#pragma unroll
+      for (int i = 0; i < NH; ++i) {
+        const int j = j0 + my_row + i * kApart, at = j & ((1 << kv.log2_page) - 1);
+        const int64_t page = ids[i] >= 0 ? ids[i] : 0;
+        const int64_t off = page * kv.code_page + it.head * kv.code_head + int64_t(at) * kv.code_slot + 16 * my_chunk;
+        if constexpr (NS == 1) {
+          raw[0] = *reinterpret_cast<const v4u*>((half_v ? kv.v_codes : kv.k_codes) + off);
+        } else {
+          raw[i] = *reinterpret_cast<const v4u*>(kv.k_codes + off);
+          raw[NH + i] = *reinterpret_cast<const v4u*>(kv.v_codes + off);
+        }
+      }
+      if (tid < kWideStep) {  // the keys' scales, from the first wave
+        const int at = (j0 + tid) & ((1 << kv.log2_page) - 1);
+        seen = scale_id >= 0;
+        const int64_t off = int64_t(seen ? scale_id : 0) * kv.scale_page + it.head * kv.scale_head + int64_t(at) * kv.scale_slot;
+        scales[0] = kv.k_scales[off];
+        scales[1] = kv.v_scales[off];
+      }
+    };
+    auto store_step = [&](int buf) {
+      char* base = lds + buf * L::kBuffer;
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        const v32bf x = open_chunk(raw[i]);
+        const bool v = NS == 1 ? half_v : i >= NH;
+        char* dst = base + (v ? L::kHalf : 0) + (my_row + (i % NH) * kApart) * L::kRow + 64 * my_chunk;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) *reinterpret_cast<v8bf*>(dst + 16 * pair_order(e)) = part8(x, e);
+      }
+      if (tid < kWideStep) {
+        scale_s[buf][0][tid] = scales[0] * scale2;
+        scale_s[buf][1][tid] = seen ? scales[1] : 0.0f;
+        seen_s[buf][tid] = seen;
+      }
+    };
+
+    if (lo < hi) {
+      load_ids(lo);
+      load_step(lo);
+      load_ids(lo + kWideStep);
+      store_step(0);
+    }
+    int buf = 0;
+    for (int j0 = lo; j0 < hi; j0 += kWideStep, buf ^= 1) {
+      __syncthreads();
+      const bool more = j0 + kWideStep < hi;
+      if (more) {
+        load_step(j0 + kWideStep);
+        load_ids(j0 + 2 * kWideStep);
+      }
+      if (j0 < wave_hi) {
+        const char* kbase = lds + buf * L::kBuffer;
+        const char* vbase = kbase + L::kHalf;
+        const uint64_t vis = __ballot(seen_s[buf][lane] != 0);
+        const bool whole = vis == ~uint64_t(0) && j0 >= full_lo && j0 + kWideStep <= full_hi;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+          v16f sc[RB];
+#pragma unroll
+          for (int rb = 0; rb < RB; ++rb) sc[rb] = v16f{};
+          const char* krow = kbase + (32 * kb + n) * L::kRow + 16 * h;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            const v8bf k8 = *reinterpret_cast<const v8bf*>(krow + 32 * i);
+#pragma unroll
+            for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+              for (int p = 0; p < N; ++p)
+                sc[rb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k8, q[rb][i][p], sc[rb], 0, 0, 0);
+          }
+          v4f sk[4], sv[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            sk[e] = *reinterpret_cast<const v4f*>(&scale_s[buf][0][32 * kb + 8 * e + 4 * h]);
+            sv[e] = *reinterpret_cast<const v4f*>(&scale_s[buf][1][32 * kb + 8 * e + 4 * h]);
+          }
+          v8bf pr[RB][2][N];
+#pragma unroll
+          for (int rb = 0; rb < RB; ++rb) {
+            const float ref = m[rb] == -INFINITY ? 0.0f : m[rb];
+            v16f x;
+            v4f svr[4];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = fmaf(sc[rb][e], sk[e >> 2][e & 3], -ref);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) svr[e] = sv[e];
+            if (!whole) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const int key = 32 * kb + 8 * (e >> 2) + 4 * h + (e & 3), j = j0 + key;
+                const bool on = ((vis >> key) & 1) && j >= begin[rb] && j < end[rb];
+                x[e] = on ? x[e] : -INFINITY;
+                svr[e >> 2][e & 3] = on ? svr[e >> 2][e & 3] : 0.0f;
+              }
+            }
+            float top = x[0];
+#pragma unroll
+            for (int e = 1; e < 16; ++e) top = fmaxf(top, x[e]);
+            const float limit = m[rb] == -INFINITY ? -INFINITY : kSlack;
+            if (__ballot(top > limit)) {
+              top = fmaxf(top, __shfl_xor(top, 32));
+              if (top > limit) {
+                const float alpha = m[rb] == -INFINITY ? 0.0f : exp2f(-top);
+                m[rb] = ref + top;
+                l[rb] *= alpha;
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) o[rb][c] *= alpha;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x[e] -= top;
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float p = __builtin_amdgcn_exp2f(x[e]);
+              l[rb] += p;
+              __bf16 part[N];
+              split_bf16<N>(p * svr[e >> 2][e & 3], part);
+#pragma unroll
+              for (int i = 0; i < N; ++i) pr[rb][e >> 3][i][e & 7] = part[i];
+            }
+          }
+          const char* vrow = vbase + (32 * kb + 4 * h + ((lane & 15) >> 2)) * L::kRow + 32 * ((lane >> 4) & 1) + 8 * (lane & 3);
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              const v8bf vt = lds_transposed(vrow + 16 * b * L::kRow + 64 * c, vrow + (16 * b + 8) * L::kRow + 64 * c);
+#pragma unroll
+              for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                  o[rb][c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vt, pr[rb][b][i], o[rb][c], 0, 0, 0);
+            }
+        }
+      }
+      if (more) store_step(buf ^ 1);
+    }
+
+    // the wave's rows, 32 at a time, through its part of the LDS
+    __syncthreads();
+    constexpr int LR = D / 8, R = kWave / LR;
+    float* out = reinterpret_cast<float*>(lds + wave * L::kOutWave);
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+      const float sum = l[rb] + __shfl_xor(l[rb], 32);
+      const int r32 = wave * 32 * RB + 32 * rb;
+      if (h == 0) {
+        row_m[r32 + n] = m[rb];
+        row_l[r32 + n] = sum;
+      }
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          *reinterpret_cast<v4f*>(out + n * L::kOutRow + 32 * c + 8 * e + 4 * h) =
+              v4f{o[rb][c][4 * e], o[rb][c][4 * e + 1], o[rb][c][4 * e + 2], o[rb][c][4 * e + 3]};
+      wave_lds_order();
+#pragma unroll 1
+      for (int r0 = 0; r0 < 32; r0 += R) {
+        const int r = r0 + lane / LR, at = r32 + r;
+        if (row0 + 32 * rb + r0 >= rows) break;  // the whole wave
+        float acc[8];
+        RowSrc<false>{out, 0}.load8(0, r * L::kOutRow + 8 * (lane & (LR - 1)), acc);
+        const float top = row_m[at], mass = row_l[at];
+        if (complete) {
+          finish_row<D>(a, it.r.q0, it.r.qn, it.head, it.tile * kRows + at, acc, top, mass, lane);
+        } else {
+          float* part = partials(a) + slot * (kRows * (D + 2));
+          store_row8(part, false, at * D + 8 * (lane & (LR - 1)), acc);
+          if ((lane & (LR - 1)) == 0) {
+            part[kRows * D + at] = top;
+            part[kRows * (D + 1) + at] = mass;
+          }
+        }
+      }
+      wave_lds_order();
+    }
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
 // The pieces of cut units put together.  Block (w, part) looks at the border
-// between blocks w - 1 and w of the attention's grid: if it is the first
-// border inside a unit, it merges 64 / LR rows (LR = D / 8 lanes a row) of that
-// unit, its 4 waves every fourth piece each, eight pieces in flight, and the
-// waves through LDS.
+// between blocks w - 1 and w of the attention's grid: if that is the first
+// border inside a unit (block w wrote down what it found), it merges 64 / LR
+// rows (LR = D / 8 lanes a row) of that unit, its 4 waves every fourth piece
+// each, eight pieces in flight, and the waves through LDS.
 // ---------------------------------------------------------------------------
 template <int D>
-__global__ __launch_bounds__(256) void kv_attention_combine_kernel(AttnArgs a, int rows, int blocks) {
+__global__ __launch_bounds__(256) void kv_attention_combine_kernel(AttnArgs a, int rows) {
   constexpr int LR = D / 8, R = kWave / LR;
   __shared__ float acc_s[4][kWave][9];
   __shared__ float m_s[4][R], l_s[4][R];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), l8 = lane & (LR - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int parts = rows / R;
-  __shared__ Line line;
-  line_build(a, rows, line);
-  const int64_t total = line_total(line), share = line_share(total, blocks);
-  const int64_t w = 1 + blockIdx.x / parts, border = w * share;
-  if (border >= total) return;
-  const Piece it = line_find(a, rows, line, border);
-  // cut here, and not before
-  if (it.at == 0 || it.at > share) return;
+  const int w = 1 + blockIdx.x / parts;
+  const Border* d = borders(a) + w;
+  const int pieces = uniform(d->pieces);
+  if (pieces == 0) return;
   {
+    const int tile = uniform(d->tile), q0 = uniform(d->q0), qn = uniform(d->qn), head = uniform(d->head);
     const int r0 = int(blockIdx.x % parts) * R, r = r0 + lane / LR;
-    if (it.tile * rows + r0 >= it.r.qn * a.group) return;  // the whole block
+    if (tile * rows + r0 >= qn * a.group) return;  // the whole block
     const int size = rows * (D + 2);
-    // pieces: block w - 1's (its first one only if the unit fills its share), then the first of w, w + 1, ...
-    const int pieces = 2 + int((it.steps - it.at - 1) / share);
-    const float* work = reinterpret_cast<const float*>(a.workspace);
-    const float* head_part = work + piece_slot(w - 1, it.at == share) * size;
-    const float* rest = work + piece_slot(w, true) * size;
+    const float* head_part = partials(a) + int64_t(uniform(d->first)) * size;
+    const float* rest = partials(a) + int64_t(piece_slot(w, true)) * size;
     float m = -INFINITY, l = 0.0f, acc[8] = {};
     for (int c0 = wave; c0 < pieces; c0 += 32) {
       float mc[8], lc[8], v[8][8];
@@ -636,45 +1013,77 @@ __global__ __launch_bounds__(256) void kv_attention_combine_kernel(AttnArgs a, i
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = fmaf(acc_s[i][lane][e], x, o[e]);
       }
-      finish_row<D>(a, it.r, it.head, it.tile * rows + r, o, top, sum, lane);
+      finish_row<D>(a, q0, qn, head, tile * rows + r, o, top, sum, lane);
     }
   }
 }
 
-// Steps a call can have at most, as far as the host knows.
-int64_t steps_max(const AttnArgs& a, int rows) {
-  const int64_t units = a.cache.heads * (a.T * a.group / rows + (a.B < a.T ? a.B : a.T));
-  const int64_t room = a.table_width << a.cache.log2_page, steps = room > kStep ? (room + kStep - 1) / kStep : 1;
+// Units and steps a call can have at most, as far as the host knows.
+int64_t units_max(const AttnArgs& a, int rows) {
+  return a.cache.heads * (a.T * a.group / rows + (a.B < a.T ? a.B : a.T));
+}
+int64_t steps_max(const AttnArgs& a, int rows, int step) {
+  const int64_t units = units_max(a, rows);
+  const int64_t room = a.table_width << a.cache.log2_page, steps = room > step ? (room + step - 1) / step : 1;
   return units > (int64_t(1) << 40) / steps ? int64_t(1) << 40 : units * steps;
+}
+
+template <int D>
+hipError_t launch_combine(const AttnArgs& a, int rows, int step, int blocks, hipStream_t st) {
+  if (blocks < 2 || (a.table_width << a.cache.log2_page) <= step) return hipSuccess;  // no unit can be cut
+  const int parts = rows / (kWave / (D / 8));
+  hipLaunchKernelGGL((kv_attention_combine_kernel<D>), dim3((blocks - 1) * parts), dim3(256), 0, st, a, rows);
+  return hipGetLastError();
 }
 
 template <int D, bool PRECISE>
 hipError_t launch_narrow(const AttnArgs& a, hipStream_t st) {
-  const int64_t most = steps_max(a, kNarrowRows);
+  const int64_t most = steps_max(a, kNarrowRows, kNarrowStep);
   const int full = kCUs * kNarrowBlocks<D, PRECISE>;
   const int blocks = most < full ? int(most) : full;
   hipLaunchKernelGGL((kv_attention_narrow_kernel<D, PRECISE>), dim3(blocks), dim3(256), 0, st, a);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || (a.table_width << a.cache.log2_page) <= kStep) return e;  // no unit has two steps
-  if (blocks == 1) return e;
-  constexpr int kParts = kNarrowRows / (kWave / (D / 8));
-  hipLaunchKernelGGL((kv_attention_combine_kernel<D>), dim3((blocks - 1) * kParts), dim3(256), 0, st, a, kNarrowRows,
+  return e != hipSuccess ? e : launch_combine<D>(a, kNarrowRows, kNarrowStep, blocks, st);
+}
+
+template <int D, bool PRECISE, int RB>
+hipError_t launch_wide(const AttnArgs& a, hipStream_t st) {
+  constexpr int kRows = 128 * RB;
+  const int64_t most = steps_max(a, kRows, kWideStep), units = units_max(a, kRows);
+  const int full = kCUs * kWideBlocks<D, PRECISE, RB>;
+  const int blocks = most < full ? int(most) : full;
+  const Cut cut{kRows, kWideStep, 2 * full};
+  const auto kernel = kv_attention_wide_kernel<D, PRECISE, RB>;
+  const hipError_t set = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, WideLds<D>::kBytes);
+  if (set != hipSuccess) return set;
+  hipLaunchKernelGGL(kernel, dim3(unsigned(units > blocks ? units : blocks)), dim3(256), WideLds<D>::kBytes, st, a, cut,
                      blocks);
-  return hipGetLastError();
+  const hipError_t e = hipGetLastError();
+  return e != hipSuccess ? e : launch_combine<D>(a, kRows, kWideStep, blocks, st);
+}
+
+template <int D>
+hipError_t launch_head(const AttnArgs& a, hipStream_t st) {
+  const bool precise = !(a.q_bf16 && a.out_bf16);
+  const int64_t most = a.max_q_len < a.T ? a.max_q_len : a.T;
+  if (most * a.group <= kNarrowMost) return precise ? launch_narrow<D, true>(a, st) : launch_narrow<D, false>(a, st);
+  return precise ? launch_wide<D, true, 1>(a, st) : launch_wide<D, false, kWideRB<D>>(a, st);
 }
 
 }  // namespace
 
 int64_t kv_attention_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t head_dim) {
-  return int64_t(2) * kCUs * 3 * kNarrowRows * (head_dim + 2) * int64_t(sizeof(float));
+  const int64_t narrow = int64_t(kCUs) * 3 * kNarrowRows, wide = int64_t(kCUs) * 2 * 128;
+  return kMaxBlocks * int64_t(sizeof(Border)) +
+         2 * (narrow > wide ? narrow : wide) * (head_dim + 2) * int64_t(sizeof(float));
 }
 
 hipError_t launch_kv_attention(const AttnArgs& a, hipStream_t st) {
-  const bool precise = !(a.q_bf16 && a.out_bf16);
   switch (a.head_dim) {
-    case 64: return precise ? launch_narrow<64, true>(a, st) : launch_narrow<64, false>(a, st);
-    case 128: return precise ? launch_narrow<128, true>(a, st) : launch_narrow<128, false>(a, st);
-    default: return precise ? launch_narrow<256, true>(a, st) : launch_narrow<256, false>(a, st);
+    case 64: return launch_head<64>(a, st);
+    case 128: return launch_head<128>(a, st);
+    default: return launch_head<256>(a, st);
   }
 }
 
