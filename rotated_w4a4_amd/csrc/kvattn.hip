@@ -43,7 +43,7 @@ constexpr float kSlack = 8.0f;  // probabilities may reach 2^kSlack before the m
 constexpr int kCUs = 256;
 constexpr int kNarrowRows = 16;
 constexpr int kNarrowStep = 128;  // keys of a step: 32 for each of a block's 4 waves
-constexpr int kWideStep = 64;
+constexpr int kWideRows = 128, kWideStep = 64;
 constexpr int kMaxBlocks = kCUs * 3;
 constexpr int kNarrowMost = 32;  // up to this many rows of a request the narrow kernel is used
 
@@ -301,6 +301,13 @@ __device__ __forceinline__ void wave_lds_order() {
   __builtin_amdgcn_wave_barrier();
 }
 
+// Keeps a rarely taken, uniform branch a branch: as selects its work would be
+// done for every step.
+__device__ __forceinline__ void keep_branch() { asm volatile(""); }
+
+// Bits 0 .. n - 1 (n of any size).
+__device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+
 // The 4 scales of slots s .. s + 3 of a page.
 __device__ __forceinline__ v4f scales4(const float* p, int64_t stride) {
   if (stride == 1) return *reinterpret_cast<const v4f_u*>(p);
@@ -524,6 +531,7 @@ __global__ __launch_bounds__(256, (kNarrowBlocks<D, PRECISE>)) void kv_attention
       for (int e = 0; e < 8; ++e) x[e] = fmaf(sc[e >> 2][e & 3], sk[e >> 2][e & 3] * scale2, -ref);
       if (more) load_scales(kv.k_scales, sk);
       if (!whole) {
+        keep_branch();
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int j = j0 + 16 * (e >> 2) + 4 * g + (e & 3);
@@ -618,7 +626,7 @@ __global__ __launch_bounds__(256, (kNarrowBlocks<D, PRECISE>)) void kv_attention
 }
 
 // ---------------------------------------------------------------------------
-// Many query rows (prompts, chunks): 32 RB rows for each of a block's 4 waves,
+// Many query rows (prompts, chunks): 32 rows for each of a block's 4 waves,
 // 64 keys a step.  The block opens a step's codes once, into two LDS buffers
 // (rows of bf16 codes, keys and values alike, and the keys' scales, sk already
 // times scale log2(e)), while it computes on the step before; one barrier a
@@ -629,29 +637,39 @@ __global__ __launch_bounds__(256, (kNarrowBlocks<D, PRECISE>)) void kv_attention
 // ---------------------------------------------------------------------------
 typedef float v16f __attribute__((ext_vector_type(16)));
 
-#ifndef WRB
-#define WRB 1
+#ifndef WBLK
+#define WBLK 2
+#endif
+// Blocks of the grid for each CU.
+template <int D, bool PRECISE>
+constexpr int kWideBlocks = (D == 256 || PRECISE) ? 1 : WBLK;
+
+#ifndef WBUF
+#define WBUF 2
 #endif
 template <int D>
-constexpr int kWideRB = D == 256 ? 1 : WRB;  // 32-row blocks of a wave
-// Blocks of the grid for each CU.
-template <int D, bool PRECISE, int RB>
-constexpr int kWideBlocks = (D == 256 || PRECISE || RB == 2) ? 1 : 2;
-
-template <int D>
 struct WideLds {
-  static constexpr int kRow = 2 * D + 32;  // bytes of a row: 8 consecutive rows hit 8 bank groups
-  static constexpr int kHalf = kWideStep * kRow;
-  static constexpr int kBuffer = 2 * kHalf;  // keys, values
-  static constexpr int kOutRow = D + 4;      // floats of an output row
+  // Keys: rows of 2 D + 16 bytes, so that 16 lanes reading 16 bytes of 16 rows
+  // hit every bank once, like 16 lanes writing 4 chunks of 4 rows (2 of 8).
+  static constexpr int kKeyRow = 2 * D + 16;
+  // Values: rows of 2 D bytes, their 16-byte units exchanged by a swizzle of
+  // the row, for the same of 32 lanes reading 64 bytes of 4 rows.
+  static constexpr int kValueRow = 2 * D;
+  static constexpr int kValues = kWideStep * kKeyRow;  // where the values start
+  static constexpr int kBuffer = kValues + kWideStep * kValueRow;
+  static constexpr int kBuffers = WBUF;
+  static constexpr int kOutRow = D + 4;  // floats of an output row
   static constexpr int kOutWave = 32 * kOutRow * 4;
-  static constexpr int kBytes = 2 * kBuffer > 4 * kOutWave ? 2 * kBuffer : 4 * kOutWave;
+  static constexpr int kOutPass = kBuffers * kBuffer >= 4 * kOutWave ? 4 : kBuffers * kBuffer >= 2 * kOutWave ? 2 : 1;
+  static constexpr int kBytes = kBuffers * kBuffer;
+  __device__ static constexpr int swizzle(int row) {
+    return D == 64 ? ((row >> 1) & 3) + 4 * ((row >> 1) & 1) : 5 * (row & 3);
+  }
 };
 
-template <int D, bool PRECISE, int RB>
-__global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE, RB>)) void kv_attention_wide_kernel(AttnArgs a, Cut cut, int blocks) {
+template <int D, bool PRECISE>
+__global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_wide_kernel(AttnArgs a, Cut cut, int blocks) {
   constexpr int N = PRECISE ? 3 : 1;
-  constexpr int kRows = 128 * RB;
   constexpr int CH = D / 32;                          // chunks of a row
   constexpr int NS = (2 * kWideStep * CH) / 256;      // chunks a thread opens a step (1: keys or values)
   constexpr int NH = NS > 1 ? NS / 2 : 1;             // of one kind
@@ -659,7 +677,7 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE, RB>)) void kv_attenti
   extern __shared__ __align__(16) char lds[];
   __shared__ float scale_s[2][2][kWideStep];
   __shared__ int seen_s[2][kWideStep];
-  __shared__ float row_m[kRows], row_l[kRows];
+  __shared__ float row_m[kWideRows], row_l[kWideRows];
   __shared__ Line line;
 
   const int tid = threadIdx.x, lane = tid & (kWave - 1), n = lane & 31, h = lane >> 5;
@@ -680,27 +698,26 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE, RB>)) void kv_attenti
     if (pos == begin_pos && int(blockIdx.x) < blocks) write_border(a, blockIdx.x, true, it, share);
     pos += steps;
 
-    const int rows = it.r.qn * a.group, row0 = it.tile * kRows + wave * 32 * RB;
-    v8bf q[RB][D / 16][N];
-    int begin[RB], end[RB];
-#pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-      const int row = row0 + 32 * rb + n;
+    const int rows = it.r.qn * a.group, row0 = it.tile * kWideRows + wave * 32;
+    v8bf q[D / 16][N];
+    int begin, end;
+    {
+      const int row = row0 + n;
       const bool live = row < rows;
       const int tok = live ? row / a.group : 0, head = it.head * a.group + (live ? row % a.group : 0);
       const int64_t base = (it.r.q0 + tok) * a.q_token + head * a.q_head;
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) query_operand<N>(a, base + 16 * i + 8 * h, live, q[rb][i]);
-      row_range(a, it.r, tok, begin[rb], end[rb]);
+      for (int i = 0; i < D / 16; ++i) query_operand<N>(a, base + 16 * i + 8 * h, live, q[i]);
+      row_range(a, it.r, tok, begin, end);
     }
     // keys of the unit's rows and of the wave's: all that any row sees, and those that every row sees
     int lo, hi, wave_hi = 0, full_lo = 0, full_hi = 0, skip;
     {
-      const int last = (it.tile + 1) * kRows < rows ? (it.tile + 1) * kRows - 1 : rows - 1;
-      row_range(a, it.r, it.tile * kRows / a.group, lo, skip);
+      const int last = (it.tile + 1) * kWideRows < rows ? (it.tile + 1) * kWideRows - 1 : rows - 1;
+      row_range(a, it.r, it.tile * kWideRows / a.group, lo, skip);
       row_range(a, it.r, last / a.group, skip, hi);
       if (row0 < rows) {
-        const int wave_last = row0 + 32 * RB < rows ? row0 + 32 * RB - 1 : rows - 1;
+        const int wave_last = row0 + 32 < rows ? row0 + 31 : rows - 1;
         row_range(a, it.r, row0 / a.group, skip, full_hi);
         row_range(a, it.r, wave_last / a.group, full_lo, wave_hi);
       }
@@ -713,21 +730,13 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE, RB>)) void kv_attenti
     wave_hi = wave_hi < chunk1 ? wave_hi : chunk1;
     full_hi = full_hi < chunk1 ? full_hi : chunk1;
     lo = chunk0 + ((lo - chunk0) & ~(kWideStep - 1));
-#pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-      begin[rb] = begin[rb] > chunk0 ? begin[rb] : chunk0;
-      end[rb] = end[rb] < chunk1 ? end[rb] : chunk1;
-    }
+    begin = begin > chunk0 ? begin : chunk0;
+    end = end < chunk1 ? end : chunk1;
 
-    v16f o[RB][D / 32];
-    float m[RB], l[RB];
+    v16f o[D / 32];
 #pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) o[rb][c] = v16f{};
-      m[rb] = -INFINITY;
-      l[rb] = 0.0f;
-    }
+    for (int c = 0; c < D / 32; ++c) o[c] = v16f{};
+    float m = -INFINITY, l = 0.0f;
 
     // staging: the thread's chunks of a step (row my_row + i * rows_apart, chunk my_chunk)
     constexpr int kApart = 256 / CH;
@@ -781,9 +790,11 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE, RB>)) void kv_attenti
       for (int i = 0; i < NS; ++i) {
         const v32bf x = open_chunk(raw[i]);
         const bool v = NS == 1 ? half_v : i >= NH;
-        char* dst = base + (v ? L::kHalf : 0) + (my_row + (i % NH) * kApart) * L::kRow + 64 * my_chunk;
+        const int row = my_row + (i % NH) * kApart;
+        char* dst = base + (v ? L::kValues + row * L::kValueRow : row * L::kKeyRow);
+        const int mix = v ? L::swizzle(row) : 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) *reinterpret_cast<v8bf*>(dst + 16 * pair_order(e)) = part8(x, e);
+        for (int e = 0; e < 4; ++e) *reinterpret_cast<v8bf*>(dst + 16 * ((4 * my_chunk + pair_order(e)) ^ mix)) = part8(x, e);
       }
       if (tid < kWideStep) {
         scale_s[buf][0][tid] = scales[0] * scale2;
@@ -799,7 +810,7 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE, RB>)) void kv_attenti
       store_step(0);
     }
     int buf = 0;
-    for (int j0 = lo; j0 < hi; j0 += kWideStep, buf ^= 1) {
+    for (int j0 = lo; j0 < hi; j0 += kWideStep, buf ^= L::kBuffers - 1) {
       __syncthreads();
       const bool more = j0 + kWideStep < hi;
       if (more) {
@@ -808,130 +819,141 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE, RB>)) void kv_attenti
       }
       if (j0 < wave_hi) {
         const char* kbase = lds + buf * L::kBuffer;
-        const char* vbase = kbase + L::kHalf;
+        const char* vbase = kbase + L::kValues;
         const uint64_t vis = __ballot(seen_s[buf][lane] != 0);
         const bool whole = vis == ~uint64_t(0) && j0 >= full_lo && j0 + kWideStep <= full_hi;
+        // scores of the step's two 32-key halves
+        v16f x[2] = {v16f{}, v16f{}};
+        const char* krow = kbase + n * L::kKeyRow + 16 * h;
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-          v16f sc[RB];
+        for (int i = 0; i < D / 16; ++i) {
 #pragma unroll
-          for (int rb = 0; rb < RB; ++rb) sc[rb] = v16f{};
-          const char* krow = kbase + (32 * kb + n) * L::kRow + 16 * h;
+          for (int kb = 0; kb < 2; ++kb) {
+            const v8bf k8 = *reinterpret_cast<const v8bf*>(krow + 32 * kb * L::kKeyRow + 32 * i);
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            const v8bf k8 = *reinterpret_cast<const v8bf*>(krow + 32 * i);
-#pragma unroll
-            for (int rb = 0; rb < RB; ++rb)
-#pragma unroll
-              for (int p = 0; p < N; ++p)
-                sc[rb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k8, q[rb][i][p], sc[rb], 0, 0, 0);
+            for (int p = 0; p < N; ++p) x[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k8, q[i][p], x[kb], 0, 0, 0);
           }
-          v4f sk[4], sv[4];
+        }
+        v4f sv[2][4];
+        const float ref = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            sk[e] = *reinterpret_cast<const v4f*>(&scale_s[buf][0][32 * kb + 8 * e + 4 * h]);
-            sv[e] = *reinterpret_cast<const v4f*>(&scale_s[buf][1][32 * kb + 8 * e + 4 * h]);
+            const v4f sk = *reinterpret_cast<const v4f*>(&scale_s[buf][0][32 * kb + 8 * e + 4 * h]);
+            sv[kb][e] = *reinterpret_cast<const v4f*>(&scale_s[buf][1][32 * kb + 8 * e + 4 * h]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[kb][4 * e + i] = fmaf(x[kb][4 * e + i], sk[i], -ref);
           }
-          v8bf pr[RB][2][N];
-#pragma unroll
-          for (int rb = 0; rb < RB; ++rb) {
-            const float ref = m[rb] == -INFINITY ? 0.0f : m[rb];
-            v16f x;
-            v4f svr[4];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = fmaf(sc[rb][e], sk[e >> 2][e & 3], -ref);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) svr[e] = sv[e];
-            if (!whole) {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const int key = 32 * kb + 8 * (e >> 2) + 4 * h + (e & 3), j = j0 + key;
-                const bool on = ((vis >> key) & 1) && j >= begin[rb] && j < end[rb];
-                x[e] = on ? x[e] : -INFINITY;
-                svr[e >> 2][e & 3] = on ? svr[e >> 2][e & 3] : 0.0f;
-              }
-            }
-            float top = x[0];
-#pragma unroll
-            for (int e = 1; e < 16; ++e) top = fmaxf(top, x[e]);
-            const float limit = m[rb] == -INFINITY ? -INFINITY : kSlack;
-            if (__ballot(top > limit)) {
-              top = fmaxf(top, __shfl_xor(top, 32));
-              if (top > limit) {
-                const float alpha = m[rb] == -INFINITY ? 0.0f : exp2f(-top);
-                m[rb] = ref + top;
-                l[rb] *= alpha;
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c) o[rb][c] *= alpha;
-#pragma unroll
-                for (int e = 0; e < 16; ++e) x[e] -= top;
-              }
-            }
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float p = __builtin_amdgcn_exp2f(x[e]);
-              l[rb] += p;
-              __bf16 part[N];
-              split_bf16<N>(p * svr[e >> 2][e & 3], part);
-#pragma unroll
-              for (int i = 0; i < N; ++i) pr[rb][e >> 3][i][e & 7] = part[i];
-            }
-          }
-          const char* vrow = vbase + (32 * kb + 4 * h + ((lane & 15) >> 2)) * L::kRow + 32 * ((lane >> 4) & 1) + 8 * (lane & 3);
+        // values: 8 bytes of row 32 kb + 16 b + 4 h + (l % 16) / 4 (and 8 rows on), 32-channel tile c
+        const int vr = 4 * h + ((lane & 15) >> 2), vu = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+        const char* vrow = vbase + vr * L::kValueRow + 8 * (lane & 1);
+        v8bf vt[2][D / 32];
+        auto load_values = [&](int kb) {
 #pragma unroll
           for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
-              const v8bf vt = lds_transposed(vrow + 16 * b * L::kRow + 64 * c, vrow + (16 * b + 8) * L::kRow + 64 * c);
-#pragma unroll
-              for (int rb = 0; rb < RB; ++rb)
-#pragma unroll
-                for (int i = 0; i < N; ++i)
-                  o[rb][c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vt, pr[rb][b][i], o[rb][c], 0, 0, 0);
+              const char* v0 = vrow + (32 * kb + 16 * b) * L::kValueRow + 16 * ((4 * c + vu) ^ L::swizzle(vr));
+              vt[b][c] = lds_transposed(v0, v0 + 8 * L::kValueRow);
             }
+        };
+        load_values(0);
+        if (!whole) {
+          keep_branch();
+#pragma unroll
+          for (int kb = 0; kb < 2; ++kb) {
+            // bit 8 b + i: key 32 kb + 8 b + 4 h + i of the step
+            const int j = j0 + 32 * kb + 4 * h;
+            const uint32_t bits = (uint32_t(vis >> (32 * kb)) >> (4 * h)) & bits_below(end - j) & ~bits_below(begin - j);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const bool on = bits & (1u << (8 * (e >> 2) + (e & 3)));
+              x[kb][e] = on ? x[kb][e] : -INFINITY;
+              sv[kb][e >> 2][e & 3] = on ? sv[kb][e >> 2][e & 3] : 0.0f;
+            }
+          }
+        }
+        float top = x[0][0];
+#pragma unroll
+        for (int e = 1; e < 32; ++e) top = fmaxf(top, x[e >> 4][e & 15]);
+        const float limit = m == -INFINITY ? -INFINITY : kSlack;
+        if (__ballot(top > limit)) {
+          top = fmaxf(top, __shfl_xor(top, 32));
+          if (top > limit) {
+            const float alpha = m == -INFINITY ? 0.0f : exp2f(-top);
+            m = ref + top;
+            l *= alpha;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) o[c] *= alpha;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e >> 4][e & 15] -= top;
+          }
+        }
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+          v8bf pr[2][N];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float p = __builtin_amdgcn_exp2f(x[kb][e]);
+            l += p;
+            __bf16 part[N];
+            split_bf16<N>(p * sv[kb][e >> 2][e & 3], part);
+#pragma unroll
+            for (int i = 0; i < N; ++i) pr[e >> 3][i][e & 7] = part[i];
+          }
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+              for (int i = 0; i < N; ++i)
+                o[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vt[b][c], pr[b][i], o[c], 0, 0, 0);
+          if (kb == 0) load_values(1);
         }
       }
-      if (more) store_step(buf ^ 1);
+      if (L::kBuffers == 1) __syncthreads();
+      if (more) store_step(buf ^ (L::kBuffers - 1));
     }
 
     // the wave's rows, 32 at a time, through its part of the LDS
     __syncthreads();
     constexpr int LR = D / 8, R = kWave / LR;
-    float* out = reinterpret_cast<float*>(lds + wave * L::kOutWave);
-#pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-      const float sum = l[rb] + __shfl_xor(l[rb], 32);
-      const int r32 = wave * 32 * RB + 32 * rb;
-      if (h == 0) {
-        row_m[r32 + n] = m[rb];
-        row_l[r32 + n] = sum;
-      }
+    float* out = reinterpret_cast<float*>(lds + (wave % L::kOutPass) * L::kOutWave);
+    l += __shfl_xor(l, 32);
+    if (h == 0) {
+      row_m[wave * 32 + n] = m;
+      row_l[wave * 32 + n] = l;
+    }
+#pragma unroll 1
+    for (int turn = 0; turn < 4 / L::kOutPass; ++turn) {  // the waves that fit at a time
+      if (turn > 0) __syncthreads();
+      if (wave / L::kOutPass != turn) continue;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           *reinterpret_cast<v4f*>(out + n * L::kOutRow + 32 * c + 8 * e + 4 * h) =
-              v4f{o[rb][c][4 * e], o[rb][c][4 * e + 1], o[rb][c][4 * e + 2], o[rb][c][4 * e + 3]};
+              v4f{o[c][4 * e], o[c][4 * e + 1], o[c][4 * e + 2], o[c][4 * e + 3]};
       wave_lds_order();
 #pragma unroll 1
       for (int r0 = 0; r0 < 32; r0 += R) {
-        const int r = r0 + lane / LR, at = r32 + r;
-        if (row0 + 32 * rb + r0 >= rows) break;  // the whole wave
+        const int r = r0 + lane / LR, at = wave * 32 + r;
+        if (row0 + r0 >= rows) break;  // the whole wave
         float acc[8];
         RowSrc<false>{out, 0}.load8(0, r * L::kOutRow + 8 * (lane & (LR - 1)), acc);
         const float top = row_m[at], mass = row_l[at];
         if (complete) {
-          finish_row<D>(a, it.r.q0, it.r.qn, it.head, it.tile * kRows + at, acc, top, mass, lane);
+          finish_row<D>(a, it.r.q0, it.r.qn, it.head, it.tile * kWideRows + at, acc, top, mass, lane);
         } else {
-          float* part = partials(a) + slot * (kRows * (D + 2));
+          float* part = partials(a) + slot * (kWideRows * (D + 2));
           store_row8(part, false, at * D + 8 * (lane & (LR - 1)), acc);
           if ((lane & (LR - 1)) == 0) {
-            part[kRows * D + at] = top;
-            part[kRows * (D + 1) + at] = mass;
+            part[kWideRows * D + at] = top;
+            part[kWideRows * (D + 1) + at] = mass;
           }
         }
       }
-      wave_lds_order();
     }
     __syncthreads();
   }
@@ -1046,21 +1068,20 @@ hipError_t launch_narrow(const AttnArgs& a, hipStream_t st) {
   return e != hipSuccess ? e : launch_combine<D>(a, kNarrowRows, kNarrowStep, blocks, st);
 }
 
-template <int D, bool PRECISE, int RB>
+template <int D, bool PRECISE>
 hipError_t launch_wide(const AttnArgs& a, hipStream_t st) {
-  constexpr int kRows = 128 * RB;
-  const int64_t most = steps_max(a, kRows, kWideStep), units = units_max(a, kRows);
-  const int full = kCUs * kWideBlocks<D, PRECISE, RB>;
+  const int64_t most = steps_max(a, kWideRows, kWideStep), units = units_max(a, kWideRows);
+  const int full = kCUs * kWideBlocks<D, PRECISE>;
   const int blocks = most < full ? int(most) : full;
-  const Cut cut{kRows, kWideStep, 2 * full};
-  const auto kernel = kv_attention_wide_kernel<D, PRECISE, RB>;
+  const Cut cut{kWideRows, kWideStep, 2 * full};
+  const auto kernel = kv_attention_wide_kernel<D, PRECISE>;
   const hipError_t set = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, WideLds<D>::kBytes);
   if (set != hipSuccess) return set;
   hipLaunchKernelGGL(kernel, dim3(unsigned(units > blocks ? units : blocks)), dim3(256), WideLds<D>::kBytes, st, a, cut,
                      blocks);
   const hipError_t e = hipGetLastError();
-  return e != hipSuccess ? e : launch_combine<D>(a, kRows, kWideStep, blocks, st);
+  return e != hipSuccess ? e : launch_combine<D>(a, kWideRows, kWideStep, blocks, st);
 }
 
 template <int D>
@@ -1068,13 +1089,13 @@ hipError_t launch_head(const AttnArgs& a, hipStream_t st) {
   const bool precise = !(a.q_bf16 && a.out_bf16);
   const int64_t most = a.max_q_len < a.T ? a.max_q_len : a.T;
   if (most * a.group <= kNarrowMost) return precise ? launch_narrow<D, true>(a, st) : launch_narrow<D, false>(a, st);
-  return precise ? launch_wide<D, true, 1>(a, st) : launch_wide<D, false, kWideRB<D>>(a, st);
+  return precise ? launch_wide<D, true>(a, st) : launch_wide<D, false>(a, st);
 }
 
 }  // namespace
 
 int64_t kv_attention_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t head_dim) {
-  const int64_t narrow = int64_t(kCUs) * 3 * kNarrowRows, wide = int64_t(kCUs) * 2 * 128;
+  const int64_t narrow = int64_t(kCUs) * 3 * kNarrowRows, wide = int64_t(kCUs) * 3 * 128;
   return kMaxBlocks * int64_t(sizeof(Border)) +
          2 * (narrow > wide ? narrow : wide) * (head_dim + 2) * int64_t(sizeof(float));
 }
