@@ -472,7 +472,8 @@ rw4_status rw4_dequantize_g(const uint8_t* q, const float* s, int64_t M, int64_t
  *   head_dim 64, 128 or 256; page_size a power of two in [16, 2^20];
  *   pages in [1, 2^31) with pages * page_size < 2^31 * 16; heads in
  *   [1, 1024]; code pointers 16-byte aligned, scale pointers 4-byte; code
- *   strides multiples of 16; strides in [0, 2^40), rows must not overlap. */
+ *   strides multiples of 16; strides >= 0, below 2^32 for pages, 2^24 for
+ *   slots and 2^40 for heads; rows must not overlap. */
 typedef struct {
   uint8_t* k_codes;
   float* k_scales;

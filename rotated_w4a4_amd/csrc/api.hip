@@ -619,6 +619,7 @@ static bool head_dim_known(int32_t d) { return d == 64 || d == 128 || d == 256; 
 // Sizes and strides of device arrays stay below this, so that no product of
 // a stride and an index leaves 64 bits.
 constexpr int64_t kMaxStride = int64_t(1) << 40;
+constexpr int64_t kMaxPageStride = int64_t(1) << 32, kMaxSlotStride = int64_t(1) << 24;
 constexpr int32_t kMaxHeads = 1024;
 constexpr int64_t kMaxTokens = int64_t(1) << 31;
 
@@ -663,9 +664,11 @@ static rw4_status kv_cache_of(const rw4_kv_cache* c, rw4::KvCache* out) {
   if ((reinterpret_cast<uintptr_t>(c->k_scales) & 3u) || (reinterpret_cast<uintptr_t>(c->v_scales) & 3u))
     return RW4_ERR_ARG;
   for (int64_t v : {c->code_page, c->code_head, c->code_slot})
-    if (v < 0 || v >= kMaxStride || v % 16) return RW4_ERR_ARG;
-  for (int64_t v : {c->scale_page, c->scale_head, c->scale_slot})
-    if (v < 0 || v >= kMaxStride) return RW4_ERR_ARG;
+    if (v < 0 || v % 16) return RW4_ERR_ARG;
+  if (c->code_page >= kMaxPageStride || c->code_head >= kMaxStride || c->code_slot >= kMaxSlotStride) return RW4_ERR_ARG;
+  if (c->scale_page < 0 || c->scale_page >= kMaxPageStride || c->scale_head < 0 || c->scale_head >= kMaxStride ||
+      c->scale_slot < 0 || c->scale_slot >= kMaxSlotStride)
+    return RW4_ERR_ARG;
   if (!rows_apart({{c->pages, c->code_page}, {c->heads, c->code_head}, {c->page_size, c->code_slot}}, c->head_dim / 2) ||
       !rows_apart({{c->pages, c->scale_page}, {c->heads, c->scale_head}, {c->page_size, c->scale_slot}}, 1))
     return RW4_ERR_ARG;

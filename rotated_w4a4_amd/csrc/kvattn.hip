@@ -83,8 +83,15 @@ __device__ __forceinline__ T wave_prefix(T v, int lane) {
   }
   return v;
 }
-__device__ __forceinline__ int wave_total(int v) {
-  for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
+// The same for 32 bits in six DPP additions: shifts by 1, 2, 4, 8 within rows of
+// 16 lanes, then the rows' last lanes broadcast to the rows behind.
+__device__ __forceinline__ int wave_prefix_dpp(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // lane 15 to row 1, lane 47 to row 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // lane 31 to rows 2 and 3
   return v;
 }
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -103,23 +110,56 @@ struct Piece {
   int steps, at;       // steps of the unit, the position's step in it
 };
 
+// Orders a wave's own LDS writes and reads for the compiler (the hardware
+// executes a wave's LDS operations in order).
+__device__ __forceinline__ void wave_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // How a kernel cuts the work: query rows of a unit, keys of a step, and with
 // how many units or more (0: never) every block takes whole units instead.
 struct Cut {
   int rows, step, whole;
 };
 
-// Steps before each thread's requests (256 threads take consecutive ones).
+// Steps before each thread's requests (256 threads take consecutive ones), and
+// the requests themselves where a thread has one.
 struct Line {
   long long before[257];
+  Req reqs[256];
   long long wave_sum[4];
   int wave_units[4];
   bool by_units;  // a step for each unit
 };
 
+// Up to 64 requests and 2^30 steps (so 32 bits do): a lane each, every wave by
+// itself and with the same results, so no barrier (they write the same values).
+__device__ __forceinline__ bool line_build_wave(const AttnArgs& a, const Cut& cut, Line& line) {
+  const int lane = threadIdx.x & (kWave - 1);
+  Req r{};
+  if (lane < int(a.B)) r = request(a, lane, cut.rows);
+  const int units = r.tiles * a.cache.heads, steps = req_steps(r, cut.step);
+  if (__ballot(float(units) * float(steps) > 0x1p24f)) return false;
+  int upto = wave_prefix_dpp(units);
+  const bool by_units = cut.whole > 0 && __builtin_amdgcn_readlane(upto, kWave - 1) >= cut.whole;
+  int own = units;
+  if (!by_units) {
+    own = units * steps;
+    upto = wave_prefix_dpp(own);
+  }
+  line.before[lane] = upto - own;
+  line.reqs[lane] = r;
+  if (lane == kWave - 1) line.before[256] = upto;
+  if (lane == 0) line.by_units = by_units;
+  wave_lds_order();
+  return true;
+}
+
 __device__ __forceinline__ void line_build(const AttnArgs& a, const Cut& cut, Line& line) {
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
   const int B = int(a.B), per = (B + 255) / 256;
+  if (B <= kWave && line_build_wave(a, cut, line)) return;
   const int b0 = tid * per < B ? tid * per : B, b1 = b0 + per < B ? b0 + per : B;
   long long sum = 0;
   int units = 0;
@@ -127,10 +167,11 @@ __device__ __forceinline__ void line_build(const AttnArgs& a, const Cut& cut, Li
     const Req r = request(a, b, cut.rows);
     sum += (long long)(r.tiles) * a.cache.heads * req_steps(r, cut.step);
     units += r.tiles * a.cache.heads;
+    if (per == 1) line.reqs[tid] = r;
   }
   bool by_units = false;
   if (cut.whole > 0) {
-    const int wave_units = wave_total(units);
+    const int wave_units = __builtin_amdgcn_readlane(wave_prefix_dpp(units), kWave - 1);
     if (lane == 0) line.wave_units[wave] = wave_units;
     __syncthreads();
     by_units = line.wave_units[0] + line.wave_units[1] + line.wave_units[2] + line.wave_units[3] >= cut.whole;
@@ -158,16 +199,16 @@ __device__ __forceinline__ int64_t line_share(int64_t total, int blocks) {
 // The piece at position pos < total; every wave finds it by itself.
 __device__ __forceinline__ Piece line_find(const AttnArgs& a, const Cut& cut, const Line& line, int64_t pos) {
   const int lane = threadIdx.x & (kWave - 1);
-  int seg = -1;  // the last thread whose requests start at or before pos
-#pragma unroll
-  for (int i = 0; i < 4; ++i) seg += __popcll(__ballot(line.before[kWave * i + lane] <= pos));
   const int per = (int(a.B) + 255) / 256;
+  int seg = -1;  // the last thread whose requests start at or before pos
+  const int blocks64 = int(a.B) <= kWave ? 1 : 4;
+  for (int i = 0; i < blocks64; ++i) seg += __popcll(__ballot(line.before[kWave * i + lane] <= pos));
   Piece p;
   const bool by_units = uniform(int(line.by_units));
   p.b = seg * per;
   int64_t local = pos - uniform(int64_t(line.before[seg]));
   for (;; ++p.b) {
-    const Req r = request(a, p.b, cut.rows);
+    const Req r = per == 1 ? line.reqs[p.b] : request(a, p.b, cut.rows);
     p.r = Req{uniform(r.q0), uniform(r.qn), uniform(r.kv), uniform(r.tiles), uniform(r.lo), uniform(r.span)};
     p.steps = by_units ? 1 : req_steps(p.r, cut.step);
     const int64_t all = int64_t(p.r.tiles) * a.cache.heads * p.steps;
@@ -294,19 +335,20 @@ __device__ __forceinline__ v8bf lds_transposed(const char* p0, const char* p1) {
   return __builtin_bit_cast(v8bf, r);
 }
 
-// Orders a wave's own LDS writes and reads for the compiler (the hardware
-// executes a wave's LDS operations in order).
-__device__ __forceinline__ void wave_lds_order() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
 // Keeps a rarely taken, uniform branch a branch: as selects its work would be
 // done for every step.
 __device__ __forceinline__ void keep_branch() { asm volatile(""); }
 
 // Bits 0 .. n - 1 (n of any size).
 __device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+
+// Offset of a slot of a page (-1: page 0, read but not used); the strides of
+// pages are below 2^32 and those of slots below 2^24, so each product is one
+// 32 x 32 -> 64 bit multiply-add.
+__device__ __forceinline__ int64_t row_at(int id, int64_t page_stride, int slot, int64_t slot_stride) {
+  const uint64_t page = uint64_t(uint32_t(id >= 0 ? id : 0)) * uint32_t(page_stride);
+  return int64_t(page + uint64_t(uint32_t(slot)) * uint32_t(slot_stride));
+}
 
 // The 4 scales of slots s .. s + 3 of a page.
 __device__ __forceinline__ v4f scales4(const float* p, int64_t stride) {
@@ -763,12 +805,12 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_w
     v4u raw[NS];
     float scales[2];
     int seen = 0;
+    const int64_t head_codes = it.head * kv.code_head, head_scales = it.head * kv.scale_head;
     auto load_step = [&](int j0) {
 #pragma unroll
       for (int i = 0; i < NH; ++i) {
         const int j = j0 + my_row + i * kApart, at = j & ((1 << kv.log2_page) - 1);
-        const int64_t page = ids[i] >= 0 ? ids[i] : 0;
-        const int64_t off = page * kv.code_page + it.head * kv.code_head + int64_t(at) * kv.code_slot + 16 * my_chunk;
+        const int64_t off = head_codes + row_at(ids[i], kv.code_page, at, kv.code_slot) + 16 * my_chunk;
         if constexpr (NS == 1) {
           raw[0] = *reinterpret_cast<const v4u*>((half_v ? kv.v_codes : kv.k_codes) + off);
         } else {
@@ -779,7 +821,7 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_w
       if (tid < kWideStep) {  // the keys' scales, from the first wave
         const int at = (j0 + tid) & ((1 << kv.log2_page) - 1);
         seen = scale_id >= 0;
-        const int64_t off = int64_t(seen ? scale_id : 0) * kv.scale_page + it.head * kv.scale_head + int64_t(at) * kv.scale_slot;
+        const int64_t off = head_scales + row_at(scale_id, kv.scale_page, at, kv.scale_slot);
         scales[0] = kv.k_scales[off];
         scales[1] = kv.v_scales[off];
       }
@@ -936,7 +978,7 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_w
           *reinterpret_cast<v4f*>(out + n * L::kOutRow + 32 * c + 8 * e + 4 * h) =
               v4f{o[c][4 * e], o[c][4 * e + 1], o[c][4 * e + 2], o[c][4 * e + 3]};
       wave_lds_order();
-#pragma unroll 1
+#pragma unroll 2
       for (int r0 = 0; r0 < 32; r0 += R) {
         const int r = r0 + lane / LR, at = wave * 32 + r;
         if (row0 + r0 >= rows) break;  // the whole wave
