@@ -700,14 +700,98 @@ struct WideLds {
   static constexpr int kValues = kWideStep * kKeyRow;  // where the values start
   static constexpr int kBuffer = kValues + kWideStep * kValueRow;
   static constexpr int kBuffers = WBUF;
-  static constexpr int kOutRow = D + 4;  // floats of an output row
-  static constexpr int kOutWave = 32 * kOutRow * 4;
-  static constexpr int kOutPass = kBuffers * kBuffer >= 4 * kOutWave ? 4 : kBuffers * kBuffer >= 2 * kOutWave ? 2 : 1;
   static constexpr int kBytes = kBuffers * kBuffer;
   __device__ static constexpr int swizzle(int row) {
     return D == 64 ? ((row >> 1) & 3) + 4 * ((row >> 1) & 1) : 5 * (row & 3);
   }
 };
+
+// Exchanges the upper 32 lanes of a with the lower 32 lanes of b.
+__device__ __forceinline__ void swap_halves(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+__device__ __forceinline__ void swap_halves(float& a, float& b) {
+  uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
+  swap_halves(x, y);
+  a = __uint_as_float(x);
+  b = __uint_as_float(y);
+}
+
+// y H_D of rows in the layout of the wide kernel's output (channel 32 c + 8 b +
+// 4 h + i: c, b, i in registers, h the lane's half): all butterflies but the
+// one over h are between registers; that one works on two registers at a time,
+// whose halves are exchanged before and after it.
+template <int D>
+__device__ __forceinline__ void wide_hadamard(v16f (&o)[D / 32]) {
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) {
+#pragma unroll
+    for (int st = 1; st < 16; st <<= 1) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        if ((e & st) == 0) {
+          const float x = o[c][e], y = o[c][e | st];
+          o[c][e] = x + y;
+          o[c][e | st] = x - y;
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+      float x = o[c][e], y = o[c][e + 1];
+      swap_halves(x, y);
+      float u = x + y, v = x - y;
+      swap_halves(u, v);
+      o[c][e] = u;
+      o[c][e + 1] = v;
+    }
+  }
+#pragma unroll
+  for (int st = 1; st < D / 32; st <<= 1) {
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+      if ((c & st) == 0) {
+        const v16f x = o[c], y = o[c | st];
+        o[c] = x + y;
+        o[c | st] = x - y;
+      }
+    }
+  }
+}
+
+// The rows of that layout, rounded and stored 16 bytes a lane: bf16 pairs of
+// blocks b and b + 1 are exchanged between the halves, so that a lane holds 8
+// consecutive channels.
+template <int D, class It>
+__device__ __forceinline__ void wide_store(const AttnArgs& a, const It& it, const v16f (&o)[D / 32], int row, bool live,
+                                           int h) {
+  const int tok = row / a.group;
+  const int64_t at = (it.r.q0 + tok) * a.out_token + (it.head * a.group + row - tok * a.group) * a.out_head;
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) {
+    if (a.out_bf16) {
+#pragma unroll
+      for (int b = 0; b < 4; b += 2) {
+        v8bf p;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) p[e] = static_cast<__bf16>(o[c][4 * b + e]);  // round to nearest even
+        v4u w = __builtin_bit_cast(v4u, p);
+        uint32_t w0 = w[0], w1 = w[1], w2 = w[2], w3 = w[3];
+        swap_halves(w0, w2);
+        swap_halves(w1, w3);
+        if (live)
+          *reinterpret_cast<v4u*>(reinterpret_cast<__bf16*>(a.out) + at + 32 * c + 8 * (b + h)) = v4u{w0, w1, w2, w3};
+      }
+    } else if (live) {
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        *reinterpret_cast<v4f*>(reinterpret_cast<float*>(a.out) + at + 32 * c + 8 * b + 4 * h) =
+            v4f{o[c][4 * b], o[c][4 * b + 1], o[c][4 * b + 2], o[c][4 * b + 3]};
+    }
+  }
+}
 
 template <int D, bool PRECISE>
 __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_wide_kernel(AttnArgs a, Cut cut, int blocks) {
@@ -719,7 +803,6 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_w
   extern __shared__ __align__(16) char lds[];
   __shared__ float scale_s[2][2][kWideStep];
   __shared__ int seen_s[2][kWideStep];
-  __shared__ float row_m[kWideRows], row_l[kWideRows];
   __shared__ Line line;
 
   const int tid = threadIdx.x, lane = tid & (kWave - 1), n = lane & 31, h = lane >> 5;
@@ -958,81 +1041,70 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_w
       if (more) store_step(buf ^ (L::kBuffers - 1));
     }
 
-    // the wave's rows, 32 at a time, through its part of the LDS
-    __syncthreads();
-    constexpr int LR = D / 8, R = kWave / LR;
-    float* out = reinterpret_cast<float*>(lds + (wave % L::kOutPass) * L::kOutWave);
+    // the wave's rows: lane n, h holds channels 32 c + 8 b + 4 h + i of row n
     l += __shfl_xor(l, 32);
-    if (h == 0) {
-      row_m[wave * 32 + n] = m;
-      row_l[wave * 32 + n] = l;
-    }
-#pragma unroll 1
-    for (int turn = 0; turn < 4 / L::kOutPass; ++turn) {  // the waves that fit at a time
-      if (turn > 0) __syncthreads();
-      if (wave / L::kOutPass != turn) continue;
+    const int row = row0 + n;
+    if (complete) {
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) o[c] *= a.unrotate ? inv * kHeadPost<D> : inv;
+      if (a.unrotate) wide_hadamard<D>(o);
+      wide_store<D>(a, it, o, row, row < rows, h);
+      if (a.lse && h == 0 && row < rows)
+        a.lse[(it.r.q0 + row / a.group) * int64_t(a.heads) + it.head * a.group + row % a.group] =
+            l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+    } else if (row < rows) {
+      float* part = partials(a) + slot * (kWideRows * (D + 2));
+      const int at = wave * 32 + n;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          *reinterpret_cast<v4f*>(out + n * L::kOutRow + 32 * c + 8 * e + 4 * h) =
-              v4f{o[c][4 * e], o[c][4 * e + 1], o[c][4 * e + 2], o[c][4 * e + 3]};
-      wave_lds_order();
-#pragma unroll 2
-      for (int r0 = 0; r0 < 32; r0 += R) {
-        const int r = r0 + lane / LR, at = wave * 32 + r;
-        if (row0 + r0 >= rows) break;  // the whole wave
-        float acc[8];
-        RowSrc<false>{out, 0}.load8(0, r * L::kOutRow + 8 * (lane & (LR - 1)), acc);
-        const float top = row_m[at], mass = row_l[at];
-        if (complete) {
-          finish_row<D>(a, it.r.q0, it.r.qn, it.head, it.tile * kWideRows + at, acc, top, mass, lane);
-        } else {
-          float* part = partials(a) + slot * (kWideRows * (D + 2));
-          store_row8(part, false, at * D + 8 * (lane & (LR - 1)), acc);
-          if ((lane & (LR - 1)) == 0) {
-            part[kWideRows * D + at] = top;
-            part[kWideRows * (D + 1) + at] = mass;
-          }
-        }
+        for (int b = 0; b < 4; ++b)
+          *reinterpret_cast<v4f*>(part + at * D + 32 * c + 8 * b + 4 * h) =
+              v4f{o[c][4 * b], o[c][4 * b + 1], o[c][4 * b + 2], o[c][4 * b + 3]};
+      if (h == 0) {
+        part[kWideRows * D + at] = m;
+        part[kWideRows * (D + 1) + at] = l;
       }
     }
-    __syncthreads();
+    __syncthreads();  // the buffers are free for the next piece
   }
 }
 
 // ---------------------------------------------------------------------------
 // The pieces of cut units put together.  Block (w, part) looks at the border
 // between blocks w - 1 and w of the attention's grid: if that is the first
-// border inside a unit (block w wrote down what it found), it merges 64 / LR
-// rows (LR = D / 8 lanes a row) of that unit, its 4 waves every fourth piece
-// each, eight pieces in flight, and the waves through LDS.
+// border inside a unit (block w wrote down what it found), it merges rows of
+// that unit, D / 8 lanes a row, eight pieces in flight.  SPLIT (few rows, many
+// pieces): the 4 waves take every fourth piece of the same rows and merge
+// through LDS; otherwise each wave has rows of its own.
 // ---------------------------------------------------------------------------
-template <int D>
+template <int D, bool SPLIT>
 __global__ __launch_bounds__(256) void kv_attention_combine_kernel(AttnArgs a, int rows) {
   constexpr int LR = D / 8, R = kWave / LR;
   __shared__ float acc_s[4][kWave][9];
   __shared__ float m_s[4][R], l_s[4][R];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), l8 = lane & (LR - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  const int parts = rows / R;
+  const int parts = rows / (SPLIT ? R : 4 * R);
   const int w = 1 + blockIdx.x / parts;
   const Border* d = borders(a) + w;
   const int pieces = uniform(d->pieces);
   if (pieces == 0) return;
   {
     const int tile = uniform(d->tile), q0 = uniform(d->q0), qn = uniform(d->qn), head = uniform(d->head);
-    const int r0 = int(blockIdx.x % parts) * R, r = r0 + lane / LR;
-    if (tile * rows + r0 >= qn * a.group) return;  // the whole block
+    const int r0 = (SPLIT ? int(blockIdx.x % parts) : int(blockIdx.x % parts) * 4 + wave) * R, r = r0 + lane / LR;
+    if (tile * rows + r0 >= qn * a.group) return;  // the whole block or (not SPLIT) wave
     const int size = rows * (D + 2);
     const float* head_part = partials(a) + int64_t(uniform(d->first)) * size;
     const float* rest = partials(a) + int64_t(piece_slot(w, true)) * size;
     float m = -INFINITY, l = 0.0f, acc[8] = {};
-    for (int c0 = wave; c0 < pieces; c0 += 32) {
+    constexpr int kNext = SPLIT ? 4 : 1;
+    for (int c0 = SPLIT ? wave : 0; c0 < pieces; c0 += 8 * kNext) {
       float mc[8], lc[8], v[8][8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int c = c0 + 4 * i;
+        const int c = c0 + kNext * i;
         if (c < pieces) {  // uniform
           const float* part = c == 0 ? head_part : rest + int64_t(c - 1) * (2 * size);
           mc[i] = part[rows * D + r];
@@ -1043,7 +1115,7 @@ __global__ __launch_bounds__(256) void kv_attention_combine_kernel(AttnArgs a, i
       float top = m;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (c0 + 4 * i < pieces) top = fmaxf(top, mc[i]);
+        if (c0 + kNext * i < pieces) top = fmaxf(top, mc[i]);
       const float keep = m == -INFINITY ? 0.0f : exp2f(m - top);
       m = top;
       l *= keep;
@@ -1051,13 +1123,17 @@ __global__ __launch_bounds__(256) void kv_attention_combine_kernel(AttnArgs a, i
       for (int e = 0; e < 8; ++e) acc[e] *= keep;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        if (c0 + 4 * i < pieces) {
+        if (c0 + kNext * i < pieces) {
           const float x = mc[i] == -INFINITY ? 0.0f : exp2f(mc[i] - m);
           l = fmaf(lc[i], x, l);
 #pragma unroll
           for (int e = 0; e < 8; ++e) acc[e] = fmaf(v[i][e], x, acc[e]);
         }
       }
+    }
+    if constexpr (!SPLIT) {
+      finish_row<D>(a, q0, qn, head, tile * rows + r, acc, m, l, lane);
+      return;
     }
     if (l8 == 0) {
       m_s[wave][lane / LR] = m;
@@ -1092,11 +1168,11 @@ int64_t steps_max(const AttnArgs& a, int rows, int step) {
   return units > (int64_t(1) << 40) / steps ? int64_t(1) << 40 : units * steps;
 }
 
-template <int D>
+template <int D, bool SPLIT>
 hipError_t launch_combine(const AttnArgs& a, int rows, int step, int blocks, hipStream_t st) {
   if (blocks < 2 || (a.table_width << a.cache.log2_page) <= step) return hipSuccess;  // no unit can be cut
-  const int parts = rows / (kWave / (D / 8));
-  hipLaunchKernelGGL((kv_attention_combine_kernel<D>), dim3((blocks - 1) * parts), dim3(256), 0, st, a, rows);
+  const int parts = rows / (kWave / (D / 8)) / (SPLIT ? 1 : 4);
+  hipLaunchKernelGGL((kv_attention_combine_kernel<D, SPLIT>), dim3((blocks - 1) * parts), dim3(256), 0, st, a, rows);
   return hipGetLastError();
 }
 
@@ -1107,7 +1183,7 @@ hipError_t launch_narrow(const AttnArgs& a, hipStream_t st) {
   const int blocks = most < full ? int(most) : full;
   hipLaunchKernelGGL((kv_attention_narrow_kernel<D, PRECISE>), dim3(blocks), dim3(256), 0, st, a);
   const hipError_t e = hipGetLastError();
-  return e != hipSuccess ? e : launch_combine<D>(a, kNarrowRows, kNarrowStep, blocks, st);
+  return e != hipSuccess ? e : launch_combine<D, true>(a, kNarrowRows, kNarrowStep, blocks, st);
 }
 
 template <int D, bool PRECISE>
@@ -1123,7 +1199,7 @@ hipError_t launch_wide(const AttnArgs& a, hipStream_t st) {
   hipLaunchKernelGGL(kernel, dim3(unsigned(units > blocks ? units : blocks)), dim3(256), WideLds<D>::kBytes, st, a, cut,
                      blocks);
   const hipError_t e = hipGetLastError();
-  return e != hipSuccess ? e : launch_combine<D>(a, kWideRows, kWideStep, blocks, st);
+  return e != hipSuccess ? e : launch_combine<D, false>(a, kWideRows, kWideStep, blocks, st);
 }
 
 template <int D>
