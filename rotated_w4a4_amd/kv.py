@@ -12,11 +12,12 @@ from __future__ import annotations
 
 import collections
 import ctypes
-import math
 
 import numpy as np
 
-from . import RW4_BF16, RW4_F32, RW4_OK, Call, RW4Error, _on_gpu, _out, _stream, _torch, lib
+import torch
+
+from . import RW4_BF16, RW4_F32, RW4_OK, Call, RW4Error, _on_gpu, _out, _stream, lib
 
 __all__ = ["KVCache", "KVSlots", "kv_slots", "prepare_kv_slots", "rope_table", "qk_norm_rope", "prepare_qk_norm_rope",
            "kv_append", "prepare_kv_append", "kv_attention", "prepare_kv_attention", "kv_attention_workspace_bytes"]
@@ -43,49 +44,67 @@ for _name in ("rw4_kv_slots", "rw4_qk_norm_rope", "rw4_kv_append", "rw4_kv_atten
     getattr(lib, _name).restype = ctypes.c_int
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_DTYPES = {torch.bfloat16: RW4_BF16, torch.float32: RW4_F32}
+
+
+def _launch(fn, args, dev, what):
+    """The library call on the current stream of GPU `dev`, with that GPU current."""
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            status = fn(*args, _stream(dev))
+    else:
+        status = fn(*args, _stream(dev))
+    if status != RW4_OK:
+        raise RW4Error(status, what)
+
+
 class KVCall(Call):
     """A prepared call that also makes its tensors' GPU current while it launches."""
 
     __slots__ = ()
 
     def __call__(self):
-        torch = _torch()
-        if torch.cuda.current_device() != self._dev:
-            with torch.cuda.device(self._dev):
-                status = self._fn(*self._args, _stream(self._dev))
-        else:
-            status = self._fn(*self._args, _stream(self._dev))
-        if status != RW4_OK:
-            raise RW4Error(status, self._what)
+        _launch(self._fn, self._args, self._dev, self._what)
         return self.result
 
 
 def _code(dtype) -> int:
-    torch = _torch()
-    if dtype is torch.bfloat16:
-        return RW4_BF16
-    if dtype is torch.float32:
-        return RW4_F32
-    raise TypeError(f"unsupported dtype {dtype} (float32 or bfloat16)")
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype} (float32 or bfloat16)")
+    return code
 
 
 def _vec(name, t, dtype, n, dev):
-    """A contiguous one-dimensional tensor of n entries (None: any number)."""
-    _on_gpu(name, t, dev)
+    """A contiguous one-dimensional tensor of n entries (None: any number); its pointer."""
+    if t.get_device() != dev or not t.is_cuda:
+        _on_gpu(name, t, dev)
     if t.dtype is not dtype or t.dim() != 1 or not t.is_contiguous() or (n is not None and t.shape[0] != n):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor" + ("" if n is None else f" of {n} entries"))
     return t.data_ptr()
 
 
+def _table(t, B, dev):
+    """A block table: its pointer and width."""
+    if t.get_device() != dev or not t.is_cuda:
+        _on_gpu("block_table", t, dev)
+    if t.dtype is not torch.int32 or t.dim() != 2 or t.shape[0] != B or not t.is_contiguous():
+        raise ValueError(f"block_table must be a contiguous int32 tensor of {B} rows")
+    return t.data_ptr(), t.shape[1]
+
+
 def _rows(name, t, dev, shape=None):
-    """A [tokens, heads, D] tensor with unit stride in a head: (token stride, head stride)."""
-    _on_gpu(name, t, dev)
-    if t.dim() != 3 or (shape is not None and t.shape != shape):
+    """A [tokens, heads, D] tensor with unit stride in a head: (pointer, token stride, head stride)."""
+    if t.get_device() != dev or not t.is_cuda:
+        _on_gpu(name, t, dev)
+    size = t.shape
+    if len(size) != 3 or (shape is not None and size != shape):
         raise ValueError(f"{name} must be " + ("[tokens, heads, head_dim]" if shape is None else str(list(shape))))
     st, sh, sd = t.stride()
     if sd != 1:
         raise ValueError(f"{name} must have unit stride along the head's channels")
-    return (st if t.shape[0] > 1 else 0), (sh if t.shape[1] > 1 else 0)
+    return t.data_ptr(), (st if size[0] > 1 else 0), (sh if size[1] > 1 else 0)
 
 
 class KVCache:
@@ -101,7 +120,6 @@ class KVCache:
                  "_struct", "_ptr")
 
     def __init__(self, k, v, k_scale, v_scale):
-        torch = _torch()
         self._dev = _on_gpu("k", k)
         for name, t in (("v", v), ("k_scale", k_scale), ("v_scale", v_scale)):
             _on_gpu(name, t, self._dev)
@@ -124,7 +142,6 @@ class KVCache:
     @classmethod
     def empty(cls, pages: int, page_size: int, kv_heads: int, head_dim: int, device="cuda") -> "KVCache":
         """A cache of zeros, pages contiguous by head."""
-        torch = _torch()
         k, v = (torch.zeros((pages, kv_heads, page_size, head_dim // 2), dtype=torch.uint8, device=device)
                 for _ in range(2))
         ks, vs = (torch.zeros((pages, kv_heads, page_size), dtype=torch.float32, device=device) for _ in range(2))
@@ -152,61 +169,57 @@ def kv_slots(ctx_len, new_len, block_table, free_pages, free_state, page_size: i
     free_state int32 [2] (head, count of the ring free_pages).  Returns KVSlots(kv_len, cu_new, served, slot_map,
     positions, free_state); `out` may hold any of these by name (kv_len may be ctx_len, free_state_out free_state).
     """
-    return prepare_kv_slots(ctx_len, new_len, block_table, free_pages, free_state, page_size, tokens, **out)()
+    fn, args, dev, what, _, result = _slots(ctx_len, new_len, block_table, free_pages, free_state, page_size, tokens,
+                                            **out)
+    _launch(fn, args, dev, what)
+    return result
 
 
-def prepare_kv_slots(ctx_len, new_len, block_table, free_pages, free_state, page_size: int, tokens: int, *,
-                     kv_len=None, cu_new=None, served=None, slot_map=None, positions=None,
-                     free_state_out=None) -> Call:
-    torch = _torch()
-    i32, dev = torch.int32, _on_gpu("ctx_len", ctx_len)
-    B = ctx_len.shape[0]
-    device = ctx_len.device
-    _vec("ctx_len", ctx_len, i32, None, dev)
-    _vec("new_len", new_len, i32, B, dev)
-    _vec("free_pages", free_pages, i32, None, dev)
-    _vec("free_state", free_state, i32, 2, dev)
-    _on_gpu("block_table", block_table, dev)
-    if block_table.dtype is not i32 or block_table.dim() != 2 or block_table.shape[0] != B \
-            or not block_table.is_contiguous():
-        raise ValueError(f"block_table must be a contiguous int32 tensor of {B} rows")
-    if kv_len is None or cu_new is None or served is None or positions is None or free_state_out is None:
+def prepare_kv_slots(ctx_len, new_len, block_table, free_pages, free_state, page_size: int, tokens: int, **out) -> Call:
+    """kv_slots checked and marshalled once; calling the result runs it."""
+    return KVCall(*_slots(ctx_len, new_len, block_table, free_pages, free_state, page_size, tokens, **out))
+
+
+def _slots(ctx_len, new_len, block_table, free_pages, free_state, page_size, tokens, *, kv_len=None, cu_new=None,
+           served=None, slot_map=None, positions=None, free_state_out=None):
+    i32, dev, device = torch.int32, _on_gpu("ctx_len", ctx_len), ctx_len.device
+    if ctx_len.dim() != 1:
+        raise ValueError("ctx_len must be one-dimensional")
+    B, tokens = ctx_len.shape[0], int(tokens)
+    table, width = _table(block_table, B, dev)
+    if kv_len is None and cu_new is None and served is None and positions is None and free_state_out is None:
         # one allocation for the small outputs
-        pool = torch.empty((3 * B + 3 + tokens,), dtype=i32, device=device)
-        parts = pool.split((B, B + 1, B, 2, tokens))
-        kv_len = parts[0] if kv_len is None else kv_len
-        cu_new = parts[1] if cu_new is None else cu_new
-        served = parts[2] if served is None else served
-        free_state_out = parts[3] if free_state_out is None else free_state_out
-        positions = parts[4] if positions is None else positions
+        kv_len, cu_new, served, free_state_out, positions = torch.empty(
+            (3 * B + 3 + tokens,), dtype=i32, device=device).split_with_sizes((B, B + 1, B, 2, tokens))
+    else:
+        kv_len, cu_new, served, free_state_out, positions = (
+            torch.empty((n,), dtype=i32, device=device) if t is None else t
+            for t, n in ((kv_len, B), (cu_new, B + 1), (served, B), (free_state_out, 2), (positions, tokens)))
     if slot_map is None:
         slot_map = torch.empty((tokens,), dtype=torch.int64, device=device)
-    args = (ctx_len.data_ptr(), new_len.data_ptr(), B, int(page_size), block_table.data_ptr(), block_table.shape[1],
-            free_pages.data_ptr(), free_pages.shape[0], free_state.data_ptr(),
-            _vec("free_state_out", free_state_out, i32, 2, dev), _vec("kv_len", kv_len, i32, B, dev),
-            _vec("cu_new", cu_new, i32, B + 1, dev), _vec("served", served, i32, B, dev),
-            _vec("slot_map", slot_map, torch.int64, tokens, dev), _vec("positions", positions, i32, tokens, dev),
-            int(tokens))
-    return KVCall(lib.rw4_kv_slots, args, dev, "rw4_kv_slots",
-                  (ctx_len, new_len, block_table, free_pages, free_state),
-                  KVSlots(kv_len, cu_new, served, slot_map, positions, free_state_out))
+    args = (_vec("ctx_len", ctx_len, i32, None, dev), _vec("new_len", new_len, i32, B, dev), B, int(page_size), table,
+            width, _vec("free_pages", free_pages, i32, None, dev), free_pages.shape[0],
+            _vec("free_state", free_state, i32, 2, dev), _vec("free_state_out", free_state_out, i32, 2, dev),
+            _vec("kv_len", kv_len, i32, B, dev), _vec("cu_new", cu_new, i32, B + 1, dev),
+            _vec("served", served, i32, B, dev), _vec("slot_map", slot_map, torch.int64, tokens, dev),
+            _vec("positions", positions, i32, tokens, dev), tokens)
+    return (lib.rw4_kv_slots, args, dev, "rw4_kv_slots", (ctx_len, new_len, block_table, free_pages, free_state),
+            KVSlots(kv_len, cu_new, served, slot_map, positions, free_state_out))
 
 
 def rope_table(max_pos: int, rot: int, base: float = 10000.0, device="cuda"):
     """cos_sin fp32 [max_pos, rot] for qk_norm_rope and kv_append: rot / 2 cosines, then rot / 2 sines of the angles
     p * base^(-2 i / rot), evaluated in float64."""
-    torch = _torch()
     angle = np.arange(max_pos, dtype=np.float64)[:, None] * float(base) ** (-np.arange(0, rot, 2) / rot)
     return torch.from_numpy(np.concatenate([np.cos(angle), np.sin(angle)], 1).astype(np.float32)).to(device)
 
 
 def _weight(name, w, D, dev):
-    return None if w is None else _vec(name, w, _torch().float32, D, dev)
+    return None if w is None else _vec(name, w, torch.float32, D, dev)
 
 
 def _rope_args(cos_sin, positions, T, dev):
     """(cos_sin pointer, max_pos, rot, positions pointer)."""
-    torch = _torch()
     if cos_sin is None:
         return None, 0, 0, None
     _on_gpu("cos_sin", cos_sin, dev)
@@ -223,41 +236,46 @@ def qk_norm_rope(q, k=None, q_weight=None, k_weight=None, cos_sin=None, position
     of queries [T, heads, D] and keys [T, kv_heads, D] in one pass, then the head's Hadamard when `rotate`.
 
     Returns (q_out, k_out); with q_out = q and k_out = k in place.  k may be None."""
-    return prepare_qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps=eps, interleaved=interleaved,
-                                rotate=rotate, q_out=q_out, k_out=k_out, out_dtype=out_dtype)()
+    fn, args, dev, what, _, result = _norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved, rotate,
+                                                q_out, k_out, out_dtype)
+    _launch(fn, args, dev, what)
+    return result
 
 
 def prepare_qk_norm_rope(q, k=None, q_weight=None, k_weight=None, cos_sin=None, positions=None, *, eps: float = 1e-6,
                          interleaved: bool = False, rotate: bool = False, q_out=None, k_out=None,
                          out_dtype=None) -> Call:
-    torch = _torch()
+    """qk_norm_rope checked and marshalled once; calling the result runs it."""
+    return KVCall(*_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved, rotate, q_out, k_out,
+                              out_dtype))
+
+
+def _norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved, rotate, q_out, k_out, out_dtype):
     dev = _on_gpu("q", q)
-    qs = _rows("q", q, dev)
+    qp, qt, qh = _rows("q", q, dev)
     T, heads, D = q.shape
-    if out_dtype is None:
-        out_dtype = q.dtype if q_out is None else q_out.dtype
     if q_out is None:
-        q_out = torch.empty((T, heads, D), dtype=out_dtype, device=q.device)
-    qos = _rows("q_out", q_out, dev, (T, heads, D))
-    kv_heads, kp, ks, kop, kos = 0, None, (0, 0), None, (0, 0)
+        q_out = torch.empty((T, heads, D), dtype=q.dtype if out_dtype is None else out_dtype, device=q.device)
+    elif out_dtype is not None and q_out.dtype is not out_dtype:
+        raise TypeError(f"q_out must be {out_dtype}")
+    qop, qot, qoh = _rows("q_out", q_out, dev, (T, heads, D))
+    kv_heads, kp, kt, kh, kop, kot, koh = 0, None, 0, 0, None, 0, 0
     if k is not None:
         kv_heads = k.shape[1] if k.dim() == 3 else 0
-        ks = _rows("k", k, dev, (T, kv_heads, D))
+        kp, kt, kh = _rows("k", k, dev, (T, kv_heads, D))
         if k_out is None:
-            k_out = torch.empty((T, kv_heads, D), dtype=out_dtype, device=q.device)
-        kos = _rows("k_out", k_out, dev, (T, kv_heads, D))
+            k_out = torch.empty((T, kv_heads, D), dtype=q_out.dtype, device=q.device)
+        kop, kot, koh = _rows("k_out", k_out, dev, (T, kv_heads, D))
         if k.dtype is not q.dtype or k_out.dtype is not q_out.dtype:
             raise TypeError("q and k (and their outputs) must have the same dtype")
-        kp, kop = k.data_ptr(), k_out.data_ptr()
     elif k_out is not None:
         raise ValueError("k_out needs k")
     cs, max_pos, rot, pos = _rope_args(cos_sin, positions, T, dev)
-    args = (q.data_ptr(), qs[0], qs[1], kp, ks[0], ks[1], _code(q.dtype), T, heads, kv_heads, D,
-            _weight("q_weight", q_weight, D, dev), _weight("k_weight", k_weight, D, dev), float(eps), cs, max_pos, rot,
-            int(interleaved), pos, int(rotate), q_out.data_ptr(), qos[0], qos[1], kop, kos[0], kos[1],
-            _code(q_out.dtype))
-    return KVCall(lib.rw4_qk_norm_rope, args, dev, "rw4_qk_norm_rope",
-                  (q, k, q_weight, k_weight, cos_sin, positions), (q_out, k_out))
+    args = (qp, qt, qh, kp, kt, kh, _code(q.dtype), T, heads, kv_heads, D, _weight("q_weight", q_weight, D, dev),
+            _weight("k_weight", k_weight, D, dev), eps, cs, max_pos, rot, int(interleaved), pos, int(rotate), qop, qot,
+            qoh, kop, kot, koh, _code(q_out.dtype))
+    return (lib.rw4_qk_norm_rope, args, dev, "rw4_qk_norm_rope", (q, k, q_weight, k_weight, cos_sin, positions),
+            (q_out, k_out))
 
 
 def kv_append(cache: KVCache, k, v, slot_map, q=None, q_weight=None, k_weight=None, cos_sin=None, positions=None, *,
@@ -265,39 +283,49 @@ def kv_append(cache: KVCache, k, v, slot_map, q=None, q_weight=None, k_weight=No
     """New tokens into the cache: keys [T, kv_heads, D] normed and given their positions (as qk_norm_rope), keys and
     values rotated by the head's Hadamard (`rotate`) and stored as INT4 in rows slot_map (int64 [T]).  Queries, if
     given, go through qk_norm_rope in the same launch; returns q_out (None without q)."""
-    return prepare_kv_append(cache, k, v, slot_map, q, q_weight, k_weight, cos_sin, positions, eps=eps,
-                             interleaved=interleaved, rotate=rotate, q_out=q_out, out_dtype=out_dtype)()
+    fn, args, dev, what, _, result = _append(cache, k, v, slot_map, q, q_weight, k_weight, cos_sin, positions, eps,
+                                             interleaved, rotate, q_out, out_dtype)
+    _launch(fn, args, dev, what)
+    return result
 
 
 def prepare_kv_append(cache: KVCache, k, v, slot_map, q=None, q_weight=None, k_weight=None, cos_sin=None,
                       positions=None, *, eps: float = 1e-6, interleaved: bool = False, rotate: bool = True,
                       q_out=None, out_dtype=None) -> Call:
-    torch = _torch()
-    dev, D = cache._dev, cache.head_dim
+    """kv_append checked and marshalled once; calling the result runs it."""
+    return KVCall(*_append(cache, k, v, slot_map, q, q_weight, k_weight, cos_sin, positions, eps, interleaved, rotate,
+                           q_out, out_dtype))
+
+
+def _append(cache, k, v, slot_map, q, q_weight, k_weight, cos_sin, positions, eps, interleaved, rotate, q_out,
+            out_dtype):
+    dev, D, kv_heads = cache._dev, cache.head_dim, cache.kv_heads
     T = k.shape[0]
-    ks = _rows("k", k, dev, (T, cache.kv_heads, D))
-    vs = _rows("v", v, dev, (T, cache.kv_heads, D))
-    if v.dtype is not k.dtype:
+    kp, kt, kh = _rows("k", k, dev, (T, kv_heads, D))
+    vp, vt, vh = _rows("v", v, dev, (T, kv_heads, D))
+    dtype = k.dtype
+    if v.dtype is not dtype:
         raise TypeError("k and v must have the same dtype")
-    qp, qs, qop, qos, heads, qo_code = None, (0, 0), None, (0, 0), 0, RW4_F32
+    qp, qt, qh, qop, qot, qoh, heads, out_code = None, 0, 0, None, 0, 0, 0, RW4_F32
     if q is not None:
         heads = q.shape[1] if q.dim() == 3 else 0
-        qs = _rows("q", q, dev, (T, heads, D))
-        if q.dtype is not k.dtype:
+        qp, qt, qh = _rows("q", q, dev, (T, heads, D))
+        if q.dtype is not dtype:
             raise TypeError("q and k must have the same dtype")
         if q_out is None:
-            q_out = torch.empty((T, heads, D), dtype=q.dtype if out_dtype is None else out_dtype, device=q.device)
-        qos = _rows("q_out", q_out, dev, (T, heads, D))
-        qp, qop, qo_code = q.data_ptr(), q_out.data_ptr(), _code(q_out.dtype)
+            q_out = torch.empty((T, heads, D), dtype=dtype if out_dtype is None else out_dtype, device=q.device)
+        elif out_dtype is not None and q_out.dtype is not out_dtype:
+            raise TypeError(f"q_out must be {out_dtype}")
+        qop, qot, qoh = _rows("q_out", q_out, dev, (T, heads, D))
+        out_code = _code(q_out.dtype)
     elif q_out is not None:
         raise ValueError("q_out needs q")
     cs, max_pos, rot, pos = _rope_args(cos_sin, positions, T, dev)
-    args = (cache._ptr, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
-            _vec("slot_map", slot_map, torch.int64, T, dev), qp, qs[0], qs[1], heads, _code(k.dtype), T,
-            _weight("q_weight", q_weight, D, dev), _weight("k_weight", k_weight, D, dev), float(eps), cs, max_pos, rot,
-            int(interleaved), pos, int(rotate), qop, qos[0], qos[1], qo_code)
-    return KVCall(lib.rw4_kv_append, args, dev, "rw4_kv_append",
-                  (cache, k, v, slot_map, q, q_weight, k_weight, cos_sin, positions), q_out)
+    args = (cache._ptr, kp, kt, kh, vp, vt, vh, _vec("slot_map", slot_map, torch.int64, T, dev), qp, qt, qh, heads,
+            _code(dtype), T, _weight("q_weight", q_weight, D, dev), _weight("k_weight", k_weight, D, dev), eps, cs,
+            max_pos, rot, int(interleaved), pos, int(rotate), qop, qot, qoh, out_code)
+    return (lib.rw4_kv_append, args, dev, "rw4_kv_append",
+            (cache, k, v, slot_map, q, q_weight, k_weight, cos_sin, positions), q_out)
 
 
 def kv_attention_workspace_bytes(tokens: int, requests: int, heads: int, kv_heads: int, head_dim: int) -> int:
@@ -314,43 +342,52 @@ def kv_attention(q, cache: KVCache, block_table, kv_len, cu_q, *, max_q_len=None
     1 / sqrt(D); unrotate applies the head's Hadamard to the output (for a cache of rotated values).  max_q_len (the
     largest number of query tokens of a request, default all) only chooses the kernel.  Returns out [T, heads, D],
     with return_lse (out, lse fp32 [T, heads]).  A row that sees no key gives 0 and -inf."""
-    return prepare_kv_attention(q, cache, block_table, kv_len, cu_q, max_q_len=max_q_len, scale=scale, causal=causal,
-                                window=window, unrotate=unrotate, out=out, out_dtype=out_dtype, return_lse=return_lse,
-                                lse=lse, workspace=workspace)()
+    fn, args, dev, what, _, result = _attention(q, cache, block_table, kv_len, cu_q, max_q_len, scale, causal, window,
+                                                unrotate, out, out_dtype, return_lse, lse, workspace)
+    _launch(fn, args, dev, what)
+    return result
 
 
 def prepare_kv_attention(q, cache: KVCache, block_table, kv_len, cu_q, *, max_q_len=None, scale=None,
                          causal: bool = True, window: int = 0, unrotate: bool = True, out=None, out_dtype=None,
                          return_lse: bool = False, lse=None, workspace=None) -> Call:
-    torch = _torch()
-    i32, dev, D = torch.int32, cache._dev, cache.head_dim
-    qs = _rows("q", q, dev)
+    """kv_attention checked and marshalled once, with a workspace of its own; calling the result runs it."""
+    return KVCall(*_attention(q, cache, block_table, kv_len, cu_q, max_q_len, scale, causal, window, unrotate, out,
+                              out_dtype, return_lse, lse, workspace))
+
+
+def _attention(q, cache, block_table, kv_len, cu_q, max_q_len, scale, causal, window, unrotate, out, out_dtype,
+               return_lse, lse, workspace):
+    i32, dev, D, kv_heads = torch.int32, cache._dev, cache.head_dim, cache.kv_heads
+    qp, qt, qh = _rows("q", q, dev)
     T, heads, dq = q.shape
-    if dq != D or heads % cache.kv_heads:
-        raise ValueError(f"q must be [tokens, a multiple of {cache.kv_heads}, {D}]")
+    if dq != D or heads % kv_heads:
+        raise ValueError(f"q must be [tokens, a multiple of {kv_heads}, {D}]")
+    if kv_len.dim() != 1:
+        raise ValueError("kv_len must be one-dimensional")
     B = kv_len.shape[0]
-    _on_gpu("block_table", block_table, dev)
-    if block_table.dtype is not i32 or block_table.dim() != 2 or block_table.shape[0] != B \
-            or not block_table.is_contiguous():
-        raise ValueError(f"block_table must be a contiguous int32 tensor of {B} rows")
+    table, width = _table(block_table, B, dev)
     if out is None:
         out = torch.empty((T, heads, D), dtype=q.dtype if out_dtype is None else out_dtype, device=q.device)
-    os = _rows("out", out, dev, (T, heads, D))
+    elif out_dtype is not None and out.dtype is not out_dtype:
+        raise TypeError(f"out must be {out_dtype}")
+    op, ot, oh = _rows("out", out, dev, (T, heads, D))
     if lse is not None:
         _out("lse", lse, (T, heads), torch.float32, dev)
     elif return_lse:
         lse = torch.empty((T, heads), dtype=torch.float32, device=q.device)
-    nbytes = lib.rw4_kv_attention_workspace_bytes(T, B, heads, cache.kv_heads, D)
+    nbytes = lib.rw4_kv_attention_workspace_bytes(T, B, heads, kv_heads, D)
     if workspace is None:
-        workspace = torch.empty((max(nbytes, 16),), dtype=torch.uint8, device=q.device)
-    _on_gpu("workspace", workspace, dev)
-    wbytes = workspace.numel() * workspace.element_size()
-    if not workspace.is_contiguous() or wbytes < nbytes:
-        raise ValueError(f"workspace must be a contiguous tensor of at least {nbytes} bytes")
-    args = (cache._ptr, q.data_ptr(), _code(q.dtype), qs[0], qs[1], T, heads, block_table.data_ptr(),
-            block_table.shape[1], _vec("kv_len", kv_len, i32, B, dev), _vec("cu_q", cu_q, i32, B + 1, dev), B,
-            T if max_q_len is None else int(max_q_len), 1.0 / math.sqrt(D) if scale is None else float(scale),
-            int(causal), int(window), int(unrotate), out.data_ptr(), _code(out.dtype), os[0], os[1],
+        wbytes = nbytes if nbytes > 16 else 16
+        workspace = torch.empty((wbytes,), dtype=torch.uint8, device=q.device)
+    else:
+        _on_gpu("workspace", workspace, dev)
+        wbytes = workspace.numel() * workspace.element_size()
+        if not workspace.is_contiguous() or wbytes < nbytes:
+            raise ValueError(f"workspace must be a contiguous tensor of at least {nbytes} bytes")
+    args = (cache._ptr, qp, _code(q.dtype), qt, qh, T, heads, table, width, _vec("kv_len", kv_len, i32, B, dev),
+            _vec("cu_q", cu_q, i32, B + 1, dev), B, T if max_q_len is None else int(max_q_len),
+            D ** -0.5 if scale is None else scale, int(causal), int(window), int(unrotate), op, _code(out.dtype), ot, oh,
             None if lse is None else lse.data_ptr(), workspace.data_ptr(), wbytes)
-    return KVCall(lib.rw4_kv_attention, args, dev, "rw4_kv_attention",
-                  (q, cache, block_table, kv_len, cu_q, workspace), (out, lse) if return_lse else out)
+    return (lib.rw4_kv_attention, args, dev, "rw4_kv_attention",
+            (q, cache, block_table, kv_len, cu_q, workspace, lse), (out, lse) if return_lse else out)
