@@ -182,10 +182,18 @@ hipError_t launch_kv_slots(const SlotsArgs& a, hipStream_t st) {
 // Head rows.  A head row (D channels) lies in L = D / 8 lanes, 8 consecutive
 // channels each, so a wave holds 64 / L rows; channel index = 8 lane + e, and
 // the Sylvester butterflies run over e in registers and over the lane bits
-// across lanes.  Queries (and dense keys) are evaluated in fp32; rows that
-// are quantized in fp64: their codes are then those of the exact quotient
-// 7 u / m for any input whose sums are exact in fp64 (bf16 values always),
-// and near a border they do not depend on the order of the sums.
+// across lanes.  Dense rows (queries; keys without a cache) are evaluated in
+// fp32 and bound by memory.
+//
+// Rows that are quantized get the codes of the exact quotients 7 u / m of the
+// rotated row u, ties to even.  They are evaluated in fp32 first, together with
+// a bound of the error: every u_j is a signed sum of D terms that passes
+// through n roundings (the products with norm weight and rotary factors, log2 D
+// additions), so it and m are off by at most n 2^-24 S, S the sum of the terms'
+// magnitudes, and a quotient by (7 / m) 2 n 2^-24 S and the 5 roundings of its
+// own (of at most 7).  Where a quotient lies that close to a half (1 % of the
+// rows of 128 Gaussian values), the wave evaluates its rows again in fp64, in
+// which the sums of bf16 values are exact.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ float lane_get(float v, int src) {
   return __int_as_float(__builtin_amdgcn_ds_bpermute(src << 2, __float_as_int(v)));
@@ -196,13 +204,6 @@ __device__ __forceinline__ double lane_get(double v, int src) {
 }
 
 __device__ __forceinline__ float inv_root(float x) { return 1.0f / sqrtf(x); }
-// the hardware estimate (better than 2^-20) and two Newton steps
-__device__ __forceinline__ double inv_root(double x) {
-  double y = __builtin_amdgcn_rsq(x);
-  y = y * (1.5 - 0.5 * x * y * y);
-  return y * (1.5 - 0.5 * x * y * y);
-}
-
 template <typename T, int L>
 __device__ __forceinline__ T row_sum(T s) {
   s += lane_xor<1>(s);
@@ -212,8 +213,8 @@ __device__ __forceinline__ T row_sum(T s) {
   if constexpr (L > 16) s += lane_xor<16>(s);
   return s;
 }
-template <int L>
-__device__ __forceinline__ double row_max(double m) {
+template <int L, typename T>
+__device__ __forceinline__ T row_max(T m) {
   m = fmax(m, lane_xor<1>(m));
   m = fmax(m, lane_xor<2>(m));
   m = fmax(m, lane_xor<4>(m));
@@ -318,25 +319,19 @@ __device__ __forceinline__ void dense_row(const RowsArgs& a, const DenseRows& r,
   if (live) store_row8(r.out, a.out_bf16, t * r.out_token + h * r.out_head + 8 * l, v);
 }
 
-// One quantized row into the cache.
+// The exact codes (magic patterns, in Sylvester order of the lanes) and scale
+// of a row, in fp64; post: the scale over the maximum of the unrotated sums.
 template <int D, bool BF16>
-__device__ __forceinline__ void cache_row(const RowsArgs& a, const void* in, int64_t in_token, int64_t in_head,
-                                          const float* weight, bool roped, uint8_t* codes, float* scales, int64_t t,
-                                          int h, bool live, int64_t slot, const RopeLane& rope, int lane, int l) {
+__device__ __forceinline__ void exact_row(const RowsArgs& a, const void* in, int64_t at, const float* weight, bool roped,
+                                          const RopeLane& rope, int lane, int l, float post, uint32_t (&b)[8],
+                                          float& scale) {
   constexpr int L = D / 8;
   float x[8];
-  load_row8<BF16>(in, t * in_token + h * in_head + 8 * l, x);
+  load_row8<BF16>(in, at, x);
   double u[8];
-  double inv = 1.0;
 #pragma unroll
   for (int e = 0; e < 8; ++e) u[e] = x[e];
   if (weight) {
-    // the norm's factor is common to the row: it does not move the codes, so
-    // it enters the scale alone
-    double ss = 0.0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fma(u[e], u[e], ss);
-    inv = inv_root(row_sum<double, L>(ss) * (1.0 / D) + double(a.eps));
     float w[8];
     load_row8<false>(weight, 8 * l, w);
 #pragma unroll
@@ -344,39 +339,112 @@ __device__ __forceinline__ void cache_row(const RowsArgs& a, const void* in, int
   }
   if (roped) rope_apply(a, rope, u);
   if (a.rotate) row_hadamard<double, L>(u, lane);
-  double m = 0.0;
+  double top = 0.0;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const double p = fabs(u[e]);
-    m = p < __builtin_huge_val() ? fmax(m, p) : __builtin_huge_val();  // NaN counts as infinite
+    top = p < __builtin_huge_val() ? fmax(top, p) : __builtin_huge_val();  // NaN counts as infinite
   }
+  top = row_max<L>(top);
+  const bool bad = !(top < __builtin_huge_val());
+  const double r7 = bad || !(top > 0.0) ? 0.0 : 7.0 / top;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    // the rounded product, put right by the exact remainder
+    double q = bad ? 0.0 : rint(u[e] * r7);
+    const double rem = fma(-q, top, 7.0 * u[e]), twice = 2.0 * fabs(rem);
+    if (!bad && (twice > top || (twice == top && (int(q) & 1)))) q += rem > 0.0 ? 1.0 : -1.0;
+    b[e] = kRoundMagicBits + uint32_t(int(q));
+  }
+  scale = bad ? __int_as_float(0x7FC00000) : top > 0.0 ? float(top * double(post)) : 0.0f;
+}
+
+// Lane constants of the quantizer.  D = 128 takes the 16-lane stages fused into
+// multiply-adds, which leave lane l with (-1)^popcount(l) times the outputs of
+// Sylvester lane h128_lane_word(l); the other sizes leave them in place.
+struct QuantLane {
+  float c1, c2, c7, c8, sign;
+  int word;
+};
+template <int D>
+__device__ __forceinline__ QuantLane quant_lane(int l) {
+  if constexpr (D == 128)
+    return QuantLane{parity_sign(l & 5), parity_sign(l & 6), parity_sign(l & 4), parity_sign(l & 8), parity_sign(l),
+                     h128_lane_word(l)};
+  else
+    return QuantLane{0.0f, 0.0f, 0.0f, 0.0f, 1.0f, l};
+}
+
+// One quantized row into the cache.
+template <int D, bool BF16, bool KEY>
+__device__ __forceinline__ void cache_row(const RowsArgs& a, int64_t t, int h, bool live, int64_t slot,
+                                          const RopeLane& rope, const QuantLane& ql, int lane, int l) {
+  constexpr int L = D / 8;
+  const void* in = KEY ? a.k.in : a.v;
+  const int64_t at = KEY ? t * a.k.in_token + h * a.k.in_head + 8 * l : t * a.v_token + h * a.v_head + 8 * l;
+  const float* weight = KEY ? a.k_weight : nullptr;
+  const bool roped = KEY && a.cos_sin;
+  float v[8], inv = 1.0f;
+  load_row8<BF16>(in, at, v);
+  if (KEY && weight) {
+    // the norm's factor is common to the row: it does not move the codes, so
+    // it enters the scale alone
+    float ss = 0.0f, w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
+    inv = inv_root(row_sum<float, L>(ss) * (1.0f / D) + a.eps);
+    load_row8<false>(weight, 8 * l, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= w[e];
+  }
+  // S: a rotary pair's terms are at most |x| (|c| + |s|) each, summed over the pair
+  float size = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    size += KEY && roped && rope.on ? fabsf(v[e]) * (fabsf(rope.c[e]) + fabsf(rope.s[e])) : fabsf(v[e]);
+  if (roped) rope_apply(a, rope, v);
+  float sign = 1.0f;
+  int word = l;
+  if (a.rotate) {
+    if constexpr (D == 128) {
+      fwht8(v);
+      lane_stages_dpp(v, ql.c1, ql.c2, ql.c7, ql.c8);
+      sign = ql.sign;
+      word = ql.word;
+    } else {
+      row_hadamard<float, L>(v, lane);
+    }
+  }
+  size = row_sum<float, L>(size);
+  float m = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[e]));
   m = row_max<L>(m);
-  const bool bad = !(m < __builtin_huge_val()), zero = !(m > 0.0);
-  const double r7 = bad || zero ? 0.0 : 7.0 / m;
+  const float post = inv * (a.rotate ? kHeadPost<D> / 7.0f : 1.0f / 7.0f);
+  const float r7 = m > 0.0f ? __builtin_amdgcn_rcpf(m * (1.0f / 7.0f)) : 0.0f, rs = r7 * sign;
+  float scale = m > 0.0f ? m * post : 0.0f, far = 0.0f;
   uint32_t b[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    // nearest code of the exact quotient: the rounded product, put right by
-    // the exact remainder (ties to even)
-    double q = bad ? 0.0 : rint(u[e] * r7);
-    if (!bad) {
-      const double rem = fma(-q, m, 7.0 * u[e]), twice = 2.0 * fabs(rem);
-      const bool odd = int(q) & 1;
-      if (twice > m || (twice == m && odd)) q += rem > 0.0 ? 1.0 : -1.0;
-    }
-    b[e] = kRoundMagicBits + uint32_t(int(q));
+    const float r = fmaf(v[e], rs, kRoundMagic);
+    b[e] = __float_as_uint(r);
+    far = fmaxf(far, fabsf(fmaf(v[e], rs, kRoundMagic - r)));
   }
-  const uint32_t word = pack8_bits(b, (l & 2) != 0);
+  // 2 n 2^-24 with n = 8 additions, 3 products and some room for S itself: 2^-20 (values), 2^-19 (keys)
+  const float margin = fmaf(size * r7, KEY ? 0x1p-19f : 0x1p-20f, 0x1p-18f);
+  // also where the range of the fp32 steps does not do (zeros are fine), for infinities and NaN
+  if (__ballot(!(far < 0.5f - margin) || !(size < 0x1p120f) || (size > 0.0f && m < kTinyMax))) {
+    exact_row<D, BF16>(a, in, at, weight, roped, rope, lane, l, post, b, scale);
+    word = l;
+  }
+  const uint32_t bits = pack8_bits(b, (word & 2) != 0);
   if (!live) return;
-  const int64_t page = slot >> a.cache.log2_page, off = slot & ((int64_t(1) << a.cache.log2_page) - 1);
-  *reinterpret_cast<uint32_t*>(codes + page * a.cache.code_page + h * a.cache.code_head + off * a.cache.code_slot +
-                               4 * l) = word;
-  if (l == 0) {
-    constexpr double root = D == 64 ? 8.0 : D == 256 ? 16.0 : 11.313708498984761;
-    const double s = m * inv / (a.rotate ? 7.0 * root : 7.0);
-    scales[page * a.cache.scale_page + h * a.cache.scale_head + off * a.cache.scale_slot] =
-        bad ? __int_as_float(0x7FC00000) : zero ? 0.0f : float(s);
-  }
+  const KvCache& c = a.cache;
+  const int64_t page = slot >> c.log2_page, off = slot & ((int64_t(1) << c.log2_page) - 1);
+  *reinterpret_cast<uint32_t*>((KEY ? c.k_codes : c.v_codes) + page * c.code_page + h * c.code_head + off * c.code_slot +
+                               4 * word) = bits;
+  if (l == 0)
+    (KEY ? c.k_scales : c.v_scales)[page * c.scale_page + h * c.scale_head + off * c.scale_slot] = scale;
 }
 
 // A wave takes one token's head groups (64 / L heads of one kind: queries,
@@ -401,6 +469,7 @@ __global__ __launch_bounds__(256) void kv_rows_kernel(RowsArgs a, int parts) {
   int64_t slot = -1;
   if constexpr (APPEND) slot = a.slot_map[t];
   const bool stored = APPEND && slot >= 0 && slot < a.cache.slots;
+  const QuantLane ql = quant_lane<D>(l);
   const int gq = (a.q.heads + R - 1) / R, gk = (a.k.heads + R - 1) / R;
   const int groups = gq + gk + (APPEND ? gk : 0);
   for (int g = part; g < groups; g += parts) {
@@ -414,11 +483,9 @@ __global__ __launch_bounds__(256) void kv_rows_kernel(RowsArgs a, int parts) {
     } else if constexpr (APPEND) {
       if (!stored) continue;
       if (kind == 1)
-        cache_row<D, BF16>(a, a.k.in, a.k.in_token, a.k.in_head, a.k_weight, a.cos_sin != nullptr, a.cache.k_codes,
-                           a.cache.k_scales, t, h, live, slot, rope, lane, l);
+        cache_row<D, BF16, true>(a, t, h, live, slot, rope, ql, lane, l);
       else
-        cache_row<D, BF16>(a, a.v, a.v_token, a.v_head, nullptr, false, a.cache.v_codes, a.cache.v_scales, t, h, live,
-                           slot, rope, lane, l);
+        cache_row<D, BF16, false>(a, t, h, live, slot, rope, ql, lane, l);
     } else {
       dense_row<D, BF16>(a, a.k, a.k_weight, t, h, live, rope, lane, l);
     }

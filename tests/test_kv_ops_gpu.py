@@ -172,8 +172,9 @@ def test_append_matches_oracle(case, rotate, layout):
         want_c[slots // page, :, slots % page] = c
         want_s[slots // page, :, slots % page] = s
         assert np.array_equal(ku.opened(packed), want_c), name  # rows behind the slots as they were
-        # one rounding to fp32 of a value that fp64 gives to 2^-40
-        ku.close(ku.np64(sc), want_s, np.abs(want_s) * (ku.U24 + 2.0 ** -40), name + " scale")
+        # fp32: the maximum, 1 / 7, 1 / sqrt(D) and their products (6 roundings), the norm's factor (its sum, 14
+        # roundings halved by the root, root and division, 5)
+        ku.close(ku.np64(sc), want_s, np.abs(want_s) * 18 * ku.U24, name + " scale")
 
 
 def test_append_ties_zeros_and_special_rows():
