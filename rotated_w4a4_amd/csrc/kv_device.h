@@ -7,33 +7,16 @@
 namespace rw4 {
 
 template <int M>
-__device__ __forceinline__ double lane_xor(double v) {
-  const int lo = __float_as_int(lane_xor<M>(__int_as_float(__double2loint(v))));
-  const int hi = __float_as_int(lane_xor<M>(__int_as_float(__double2hiint(v))));
-  return __hiloint2double(hi, lo);
-}
-
-template <int M, typename T>
-__device__ __forceinline__ void lane_stage(T (&v)[8], int lane) {
-  const T sign = (lane & M) ? T(-1) : T(1);
+__device__ __forceinline__ void lane_stage(float (&v)[8], int lane) {
+  const float sign = (lane & M) ? -1.0f : 1.0f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] = sign * v[e] + lane_xor<M>(v[e]);
 }
 
 // y H_D (Sylvester order, entries +-1) of a row.
-template <typename T, int L>
-__device__ __forceinline__ void row_hadamard(T (&v)[8], int lane) {
-#pragma unroll
-  for (int h = 1; h < 8; h <<= 1) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if ((e & h) == 0) {
-        const T a = v[e], b = v[e | h];
-        v[e] = a + b;
-        v[e | h] = a - b;
-      }
-    }
-  }
+template <int L>
+__device__ __forceinline__ void row_hadamard(float (&v)[8], int lane) {
+  fwht8(v);
   lane_stage<1>(v, lane);
   lane_stage<2>(v, lane);
   lane_stage<4>(v, lane);

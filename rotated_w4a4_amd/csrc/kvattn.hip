@@ -365,7 +365,7 @@ __device__ __forceinline__ void finish_row(const AttnArgs& a, int q0, int qn, in
 #pragma unroll
   for (int e = 0; e < 8; ++e) o[e] *= inv;
   if (a.unrotate) {
-    row_hadamard<float, D / 8>(o, lane);
+    row_hadamard<D / 8>(o, lane);
 #pragma unroll
     for (int e = 0; e < 8; ++e) o[e] *= kHeadPost<D>;
   }

@@ -198,14 +198,32 @@ hipError_t launch_kv_slots(const SlotsArgs& a, hipStream_t st) {
 __device__ __forceinline__ float lane_get(float v, int src) {
   return __int_as_float(__builtin_amdgcn_ds_bpermute(src << 2, __float_as_int(v)));
 }
-__device__ __forceinline__ double lane_get(double v, int src) {
-  return __hiloint2double(__builtin_amdgcn_ds_bpermute(src << 2, __double2hiint(v)),
-                          __builtin_amdgcn_ds_bpermute(src << 2, __double2loint(v)));
+// 1 / sqrt(x): the hardware estimate (1 ulp) and a Newton step; 0 and infinity
+// give infinity and 0.
+__device__ __forceinline__ float inv_root(float x) {
+  const float y = __builtin_amdgcn_rsqf(x);
+  const float r = fmaf(-x * y, y, 1.0f);
+  return x > 0.0f && x < __builtin_huge_valf() ? fmaf(0.5f * y, r, y) : y;
+}
+// Sum over the 16 lanes of a DPP row (lane masks 1, 2, 7 and 8 span them), as
+// row16_max_dpp.
+__device__ __forceinline__ float row16_sum_dpp(float s) {
+  asm volatile(
+      "s_nop 1\n"
+      "v_add_f32_dpp %0, %0, %0 quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n"
+      "s_nop 1\n"
+      "v_add_f32_dpp %0, %0, %0 quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n"
+      "s_nop 1\n"
+      "v_add_f32_dpp %0, %0, %0 row_half_mirror row_mask:0xf bank_mask:0xf\n"
+      "s_nop 1\n"
+      "v_add_f32_dpp %0, %0, %0 row_ror:8 row_mask:0xf bank_mask:0xf\n"
+      : "+v"(s));
+  return s;
 }
 
-__device__ __forceinline__ float inv_root(float x) { return 1.0f / sqrtf(x); }
-template <typename T, int L>
-__device__ __forceinline__ T row_sum(T s) {
+template <int L>
+__device__ __forceinline__ float row_sum(float s) {
+  if constexpr (L == 16) return row16_sum_dpp(s);
   s += lane_xor<1>(s);
   s += lane_xor<2>(s);
   s += lane_xor<4>(s);
@@ -213,8 +231,9 @@ __device__ __forceinline__ T row_sum(T s) {
   if constexpr (L > 16) s += lane_xor<16>(s);
   return s;
 }
-template <int L, typename T>
-__device__ __forceinline__ T row_max(T m) {
+template <int L>
+__device__ __forceinline__ float row_max(float m) {
+  if constexpr (L == 16) return row16_max_dpp(m);
   m = fmax(m, lane_xor<1>(m));
   m = fmax(m, lane_xor<2>(m));
   m = fmax(m, lane_xor<4>(m));
@@ -265,24 +284,30 @@ __device__ __forceinline__ RopeLane rope_lane(const RowsArgs& a, int64_t pos, in
   return r;
 }
 
-template <typename T>
-__device__ __forceinline__ void rope_apply(const RowsArgs& a, const RopeLane& r, T (&v)[8]) {
+template <int L>
+__device__ __forceinline__ void rope_apply(const RowsArgs& a, const RopeLane& r, float (&v)[8]) {
   if (a.interleaved) {
     if (r.on) {
 #pragma unroll
       for (int e = 0; e < 8; e += 2) {
-        const T x = v[e], y = v[e + 1];
-        v[e] = x * T(r.c[e]) + y * T(r.s[e]);
-        v[e + 1] = y * T(r.c[e + 1]) + x * T(r.s[e + 1]);
+        const float x = v[e], y = v[e + 1];
+        v[e] = x * r.c[e] + y * r.s[e];
+        v[e + 1] = y * r.c[e + 1] + x * r.s[e + 1];
       }
     }
+  } else if (a.rot == 8 * L) {  // the whole head: the partner is half the lanes away
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float p = lane_xor<L / 2>(v[e]);
+      v[e] = v[e] * r.c[e] + p * r.s[e];
+    }
   } else {
-    T p[8];
+    float p[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) p[e] = lane_get(v[e], r.partner);
     if (r.on) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = v[e] * T(r.c[e]) + p[e] * T(r.s[e]);
+      for (int e = 0; e < 8; ++e) v[e] = v[e] * r.c[e] + p[e] * r.s[e];
     }
   }
 }
@@ -292,75 +317,8 @@ __device__ __forceinline__ void load_row8(const void* base, int64_t off, float (
   RowSrc<BF16>{base, 0}.load8(0, off, v);
 }
 
-// One dense row (queries; keys without a cache).
-template <int D, bool BF16>
-__device__ __forceinline__ void dense_row(const RowsArgs& a, const DenseRows& r, const float* weight, int64_t t, int h,
-                                          bool live, const RopeLane& rope, int lane, int l) {
-  constexpr int L = D / 8;
-  float v[8];
-  load_row8<BF16>(r.in, t * r.in_token + h * r.in_head + 8 * l, v);
-  if (weight) {
-    float ss = 0.0f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
-    const float inv = inv_root(row_sum<float, L>(ss) * (1.0f / D) + a.eps);
-    float w[8];
-    load_row8<false>(weight, 8 * l, w);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = v[e] * inv * w[e];
-  }
-  if (a.cos_sin) rope_apply(a, rope, v);
-  if (a.rotate) {
-    row_hadamard<float, L>(v, lane);
-    constexpr float post = kHeadPost<D>;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] *= post;
-  }
-  if (live) store_row8(r.out, a.out_bf16, t * r.out_token + h * r.out_head + 8 * l, v);
-}
-
-// The exact codes (magic patterns, in Sylvester order of the lanes) and scale
-// of a row, in fp64; post: the scale over the maximum of the unrotated sums.
-template <int D, bool BF16>
-__device__ __forceinline__ void exact_row(const RowsArgs& a, const void* in, int64_t at, const float* weight, bool roped,
-                                          const RopeLane& rope, int lane, int l, float post, uint32_t (&b)[8],
-                                          float& scale) {
-  constexpr int L = D / 8;
-  float x[8];
-  load_row8<BF16>(in, at, x);
-  double u[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) u[e] = x[e];
-  if (weight) {
-    float w[8];
-    load_row8<false>(weight, 8 * l, w);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) u[e] *= double(w[e]);
-  }
-  if (roped) rope_apply(a, rope, u);
-  if (a.rotate) row_hadamard<double, L>(u, lane);
-  double top = 0.0;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const double p = fabs(u[e]);
-    top = p < __builtin_huge_val() ? fmax(top, p) : __builtin_huge_val();  // NaN counts as infinite
-  }
-  top = row_max<L>(top);
-  const bool bad = !(top < __builtin_huge_val());
-  const double r7 = bad || !(top > 0.0) ? 0.0 : 7.0 / top;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    // the rounded product, put right by the exact remainder
-    double q = bad ? 0.0 : rint(u[e] * r7);
-    const double rem = fma(-q, top, 7.0 * u[e]), twice = 2.0 * fabs(rem);
-    if (!bad && (twice > top || (twice == top && (int(q) & 1)))) q += rem > 0.0 ? 1.0 : -1.0;
-    b[e] = kRoundMagicBits + uint32_t(int(q));
-  }
-  scale = bad ? __int_as_float(0x7FC00000) : top > 0.0 ? float(top * double(post)) : 0.0f;
-}
-
-// Lane constants of the quantizer.  D = 128 takes the 16-lane stages fused into
-// multiply-adds, which leave lane l with (-1)^popcount(l) times the outputs of
+// Lane constants of the fp32 Hadamard.  D = 128 takes the 16-lane stages fused
+// into multiply-adds, which leave lane l with (-1)^popcount(l) times the outputs of
 // Sylvester lane h128_lane_word(l); the other sizes leave them in place.
 struct QuantLane {
   float c1, c2, c7, c8, sign;
@@ -375,9 +333,116 @@ __device__ __forceinline__ QuantLane quant_lane(int l) {
     return QuantLane{0.0f, 0.0f, 0.0f, 0.0f, 1.0f, l};
 }
 
+// y H_D in fp32: lane l holds ql.sign times the outputs of word ql.word.
+template <int D>
+__device__ __forceinline__ void fast_hadamard(float (&v)[8], const QuantLane& ql, int lane) {
+  if constexpr (D == 128) {
+    fwht8(v);
+    lane_stages_dpp(v, ql.c1, ql.c2, ql.c7, ql.c8);
+  } else {
+    row_hadamard<D / 8>(v, lane);
+  }
+}
+
+// One dense row (queries; keys without a cache).  The norm's factor is common to
+// the row and enters at the end.
+template <int D, bool BF16>
+__device__ __forceinline__ void dense_row(const RowsArgs& a, const DenseRows& r, const float* weight, int64_t t, int h,
+                                          bool live, const RopeLane& rope, const QuantLane& ql, int lane, int l) {
+  constexpr int L = D / 8;
+  float v[8];
+  load_row8<BF16>(r.in, t * r.in_token + h * r.in_head + 8 * l, v);
+  float post = 1.0f;
+  if (weight) {
+    float ss = 0.0f, w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
+    post = inv_root(row_sum<L>(ss) * (1.0f / D) + a.eps);
+    load_row8<false>(weight, 8 * l, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= w[e];
+  }
+  if (a.cos_sin) rope_apply<L>(a, rope, v);
+  int word = l;
+  if (a.rotate) {
+    fast_hadamard<D>(v, ql, lane);
+    post *= kHeadPost<D> * ql.sign;
+    word = ql.word;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] *= post;
+  if (live) store_row8(r.out, a.out_bf16, t * r.out_token + h * r.out_head + 8 * word, v);
+}
+
+// The exact codes of one row, in fp64, by the whole wave: lane n has channels
+// E n .. E n + E - 1 (E = D / 64) and gets their codes (c[e]); returns the row's
+// maximum (infinite for infinities and NaN).  row: offset of the row's first
+// channel; cos_sin: its rotary factors or null.  All lanes take the same row.
+template <int D, bool BF16>
+__device__ __forceinline__ double exact_row(const RowsArgs& a, const void* in, int64_t row, const float* weight,
+                                            const float* cos_sin, int lane, int (&c)[D / 64]) {
+  constexpr int E = D / 64;
+  auto term = [&](int k) {  // channel k with its weight
+    const double x = BF16 ? double(__uint_as_float(uint32_t(reinterpret_cast<const uint16_t*>(in)[row + k]) << 16))
+                          : double(reinterpret_cast<const float*>(in)[row + k]);
+    return weight ? x * double(weight[k]) : x;
+  };
+  double u[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int k = E * lane + e, half = a.rot >> 1;
+    u[e] = term(k);
+    if (cos_sin && k < a.rot) {
+      const bool low = a.interleaved ? !(k & 1) : k < half;
+      const int i = a.interleaved ? k >> 1 : low ? k : k - half;
+      const int partner = a.interleaved ? k ^ 1 : low ? k + half : k - half;
+      const double s = cos_sin[half + i];
+      u[e] = u[e] * double(cos_sin[i]) + term(partner) * (low ? -s : s);
+    }
+  }
+  if (a.rotate) {
+#pragma unroll
+    for (int st = 1; st < E; st <<= 1) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        if ((e & st) == 0) {
+          const double x = u[e], y = u[e | st];
+          u[e] = x + y;
+          u[e | st] = x - y;
+        }
+      }
+    }
+    for (int st = 1; st < kWave; st <<= 1) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const double y = __shfl_xor(u[e], st);
+        u[e] = (lane & st) ? y - u[e] : u[e] + y;
+      }
+    }
+  }
+  double top = 0.0;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const double p = fabs(u[e]);
+    top = p < __builtin_huge_val() ? fmax(top, p) : __builtin_huge_val();  // NaN counts as infinite
+  }
+  for (int st = 1; st < kWave; st <<= 1) top = fmax(top, __shfl_xor(top, st));
+  const bool bad = !(top < __builtin_huge_val());
+  const double r7 = bad || !(top > 0.0) ? 0.0 : 7.0 / top;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    // the rounded product, put right by the exact remainder
+    double q = bad ? 0.0 : rint(u[e] * r7);
+    const double rem = fma(-q, top, 7.0 * u[e]), twice = 2.0 * fabs(rem);
+    if (!bad && (twice > top || (twice == top && (int(q) & 1)))) q += rem > 0.0 ? 1.0 : -1.0;
+    c[e] = int(q);
+  }
+  return top;
+}
+
 // One quantized row into the cache.
 template <int D, bool BF16, bool KEY>
-__device__ __forceinline__ void cache_row(const RowsArgs& a, int64_t t, int h, bool live, int64_t slot,
+__device__ __forceinline__ void cache_row(const RowsArgs& a, int64_t t, int h, bool live, int64_t slot, int64_t pos,
                                           const RopeLane& rope, const QuantLane& ql, int lane, int l) {
   constexpr int L = D / 8;
   const void* in = KEY ? a.k.in : a.v;
@@ -392,7 +457,7 @@ __device__ __forceinline__ void cache_row(const RowsArgs& a, int64_t t, int h, b
     float ss = 0.0f, w[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
-    inv = inv_root(row_sum<float, L>(ss) * (1.0f / D) + a.eps);
+    inv = inv_root(row_sum<L>(ss) * (1.0f / D) + a.eps);
     load_row8<false>(weight, 8 * l, w);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] *= w[e];
@@ -402,20 +467,15 @@ __device__ __forceinline__ void cache_row(const RowsArgs& a, int64_t t, int h, b
 #pragma unroll
   for (int e = 0; e < 8; ++e)
     size += KEY && roped && rope.on ? fabsf(v[e]) * (fabsf(rope.c[e]) + fabsf(rope.s[e])) : fabsf(v[e]);
-  if (roped) rope_apply(a, rope, v);
+  if (roped) rope_apply<L>(a, rope, v);
   float sign = 1.0f;
   int word = l;
   if (a.rotate) {
-    if constexpr (D == 128) {
-      fwht8(v);
-      lane_stages_dpp(v, ql.c1, ql.c2, ql.c7, ql.c8);
-      sign = ql.sign;
-      word = ql.word;
-    } else {
-      row_hadamard<float, L>(v, lane);
-    }
+    fast_hadamard<D>(v, ql, lane);
+    sign = ql.sign;
+    word = ql.word;
   }
-  size = row_sum<float, L>(size);
+  size = row_sum<L>(size);
   float m = 0.0f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[e]));
@@ -433,9 +493,30 @@ __device__ __forceinline__ void cache_row(const RowsArgs& a, int64_t t, int h, b
   // 2 n 2^-24 with n = 8 additions, 3 products and some room for S itself: 2^-20 (values), 2^-19 (keys)
   const float margin = fmaf(size * r7, KEY ? 0x1p-19f : 0x1p-20f, 0x1p-18f);
   // also where the range of the fp32 steps does not do (zeros are fine), for infinities and NaN
-  if (__ballot(!(far < 0.5f - margin) || !(size < 0x1p120f) || (size > 0.0f && m < kTinyMax))) {
-    exact_row<D, BF16>(a, in, at, weight, roped, rope, lane, l, post, b, scale);
-    word = l;
+  uint64_t near = __ballot(!(far < 0.5f - margin) || !(size < 0x1p120f) || (size > 0.0f && m < kTinyMax));
+  while (near) {  // a row at a time
+    constexpr int E = D / 64;
+    const int first = (__builtin_ctzll(near) / L) * L;
+    near &= ~(((uint64_t(1) << (L - 1) << 1) - 1) << first);
+    const int64_t row = int64_t(uint32_t(__builtin_amdgcn_readlane(int(at), first))) |
+                        (int64_t(__builtin_amdgcn_readlane(int(at >> 32), first)) << 32);
+    int c[E], lane_here = lane;
+    asm volatile("" : "+v"(lane_here));  // keeps this rare path's addresses out of the registers of the common one
+    const double top = exact_row<D, BF16>(a, in, row, weight, roped ? a.cos_sin + pos * a.rot : nullptr, lane_here, c);
+    uint32_t packed = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) packed |= (uint32_t(c[e]) & 0xFFu) << (8 * e);
+    const bool mine = lane - l == first;
+    uint32_t got[8 / E];
+#pragma unroll
+    for (int i = 0; i < 8 / E; ++i)
+      got[i] = uint32_t(__builtin_amdgcn_ds_bpermute((8 / E * (lane_here & (L - 1)) + i) << 2, int(packed)));
+    if (mine) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) b[e] = kRoundMagicBits + uint32_t(int(int8_t(got[e / E] >> (8 * (e % E)))));
+      word = l;
+      scale = !(top < __builtin_huge_val()) ? __int_as_float(0x7FC00000) : top > 0.0 ? float(top * double(post)) : 0.0f;
+    }
   }
   const uint32_t bits = pack8_bits(b, (word & 2) != 0);
   if (!live) return;
@@ -479,15 +560,15 @@ __global__ __launch_bounds__(256) void kv_rows_kernel(RowsArgs a, int parts) {
     const bool live = h < heads;
     h = live ? h : heads - 1;
     if (kind == 0) {
-      dense_row<D, BF16>(a, a.q, a.q_weight, t, h, live, rope, lane, l);
+      dense_row<D, BF16>(a, a.q, a.q_weight, t, h, live, rope, ql, lane, l);
     } else if constexpr (APPEND) {
       if (!stored) continue;
       if (kind == 1)
-        cache_row<D, BF16, true>(a, t, h, live, slot, rope, ql, lane, l);
+        cache_row<D, BF16, true>(a, t, h, live, slot, pos, rope, ql, lane, l);
       else
-        cache_row<D, BF16, false>(a, t, h, live, slot, rope, ql, lane, l);
+        cache_row<D, BF16, false>(a, t, h, live, slot, pos, rope, ql, lane, l);
     } else {
-      dense_row<D, BF16>(a, a.k, a.k_weight, t, h, live, rope, lane, l);
+      dense_row<D, BF16>(a, a.k, a.k_weight, t, h, live, rope, ql, lane, l);
     }
   }
 }
