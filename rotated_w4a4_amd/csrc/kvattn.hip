@@ -1080,20 +1080,20 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_w
 // through LDS; otherwise each wave has rows of its own.
 // ---------------------------------------------------------------------------
 template <int D, bool SPLIT>
-__global__ __launch_bounds__(256) void kv_attention_combine_kernel(AttnArgs a, int rows) {
+__global__ __launch_bounds__(256) void kv_attention_combine_kernel(AttnArgs a, int rows, int parts) {
   constexpr int LR = D / 8, R = kWave / LR;
   __shared__ float acc_s[4][kWave][9];
   __shared__ float m_s[4][R], l_s[4][R];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), l8 = lane & (LR - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  const int parts = rows / (SPLIT ? R : 4 * R);
   const int w = 1 + blockIdx.x / parts;
   const Border* d = borders(a) + w;
   const int pieces = uniform(d->pieces);
   if (pieces == 0) return;
-  {
-    const int tile = uniform(d->tile), q0 = uniform(d->q0), qn = uniform(d->qn), head = uniform(d->head);
-    const int r0 = (SPLIT ? int(blockIdx.x % parts) : int(blockIdx.x % parts) * 4 + wave) * R, r = r0 + lane / LR;
+  const int tile = uniform(d->tile), q0 = uniform(d->q0), qn = uniform(d->qn), head = uniform(d->head);
+  const int part = blockIdx.x % parts;
+  for (int r0 = (SPLIT ? part : part * 4 + wave) * R; r0 < rows; r0 += (SPLIT ? parts : 4 * parts) * R) {
+    const int r = r0 + lane / LR;
     if (tile * rows + r0 >= qn * a.group) return;  // the whole block or (not SPLIT) wave
     const int size = rows * (D + 2);
     const float* head_part = partials(a) + int64_t(uniform(d->first)) * size;
@@ -1133,7 +1133,7 @@ __global__ __launch_bounds__(256) void kv_attention_combine_kernel(AttnArgs a, i
     }
     if constexpr (!SPLIT) {
       finish_row<D>(a, q0, qn, head, tile * rows + r, acc, m, l, lane);
-      return;
+      continue;
     }
     if (l8 == 0) {
       m_s[wave][lane / LR] = m;
@@ -1155,6 +1155,7 @@ __global__ __launch_bounds__(256) void kv_attention_combine_kernel(AttnArgs a, i
       }
       finish_row<D>(a, q0, qn, head, tile * rows + r, o, top, sum, lane);
     }
+    __syncthreads();
   }
 }
 
@@ -1171,8 +1172,12 @@ int64_t steps_max(const AttnArgs& a, int rows, int step) {
 template <int D, bool SPLIT>
 hipError_t launch_combine(const AttnArgs& a, int rows, int step, int blocks, hipStream_t st) {
   if (blocks < 2 || (a.table_width << a.cache.log2_page) <= step) return hipSuccess;  // no unit can be cut
-  const int parts = rows / (kWave / (D / 8)) / (SPLIT ? 1 : 4);
-  hipLaunchKernelGGL((kv_attention_combine_kernel<D, SPLIT>), dim3((blocks - 1) * parts), dim3(256), 0, st, a, rows);
+  // blocks for the rows that max_q_len lets expect (they go on to the others if it is wrong)
+  constexpr int kBlockRows = kWave / (D / 8) * (SPLIT ? 1 : 4);
+  const int64_t live = a.max_q_len < rows ? a.max_q_len * a.group : rows;
+  const int parts = int((live < 1 ? 1 : live < rows ? live : rows) + kBlockRows - 1) / kBlockRows;
+  hipLaunchKernelGGL((kv_attention_combine_kernel<D, SPLIT>), dim3((blocks - 1) * parts), dim3(256), 0, st, a, rows,
+                     parts);
   return hipGetLastError();
 }
 
