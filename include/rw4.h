@@ -554,8 +554,9 @@ rw4_status rw4_qk_norm_rope(const void* q, int64_t q_token, int64_t q_head, cons
  *   u = y H_D (unnormalized), m = max|u|, code = rne(7 u / m), scale =
  *   m / (7 sqrt(D))   (rotate = 0: u = y, scale = m / 7),
  * stored in row slot_map[t] of the cache (page slot / page_size, slot
- * slot % page_size).  Codes are those of the exact quotient of the row as
- * evaluated in fp64, ties to even.  A row with an infinity or NaN gets the
+ * slot % page_size).  Codes are those of the exact quotients, ties to even (u
+ * in fp64 where that matters; the norm's factor does not enter them), scales
+ * are fp32.  A row with an infinity or NaN gets the
  * scale NaN and codes 0 (rotate = 0 as well), a row of zeros scale 0 and
  * codes 0.  Queries (optional, q NULL: none): as rw4_qk_norm_rope with the
  * same rotate, into q_out.
@@ -563,8 +564,8 @@ rw4_status rw4_qk_norm_rope(const void* q, int64_t q_token, int64_t q_head, cons
  *   (*_token, *_head), 16-byte aligned heads; slot_map int64 [T].  A token
  *   whose slot is outside [0, pages * page_size) stores nothing, and one
  *   whose position is outside [0, max_pos) (cos_sin not NULL) is skipped
- *   altogether; two tokens must not share a slot.  Other arguments as
- *   rw4_qk_norm_rope. */
+ *   altogether; two tokens must not share a slot.  q_out may be q; it must not
+ *   overlap k or v.  Other arguments as rw4_qk_norm_rope. */
 rw4_status rw4_kv_append(const rw4_kv_cache* cache_host, const void* k, int64_t k_token, int64_t k_head, const void* v,
                          int64_t v_token, int64_t v_head, const int64_t* slot_map, const void* q, int64_t q_token,
                          int64_t q_head, int32_t heads, rw4_dtype x_dtype, int64_t T, const float* q_weight,
@@ -588,7 +589,9 @@ int64_t rw4_kv_attention_workspace_bytes(int64_t T, int64_t B, int32_t heads, in
  *   out = sum_j softmax(s)_j cv[j, :] sv[j],  times H_D / sqrt(D) when
  *   unrotate != 0 (undoing the rotation of the stored values),
  *   lse (optional) = log sum_j exp(s_j).
- * A row with no visible key gets out = 0 and lse = -infinity.  Queries are in
+ * A row with no visible key gets out = 0 and lse = -infinity; a visible key
+ * with a scale (of key or value) that is not finite makes NaN of out, and of
+ * lse or leaves it as it is.  Queries are in
  * the rotated domain when the cache is (kv_append's or qk_norm_rope's rotate,
  * or rw4_rotate_act).  causal = 0 is attention to another sequence's states.
  * Scores, softmax and sums are fp32; bf16 output: probabilities enter the
@@ -599,7 +602,7 @@ int64_t rw4_kv_attention_workspace_bytes(int64_t T, int64_t B, int32_t heads, in
  *   max_q_len: the largest number of query tokens of a request; chooses the
  *   kernel, results do not depend on it.  window > 0 needs causal.
  *   B <= 65535; heads a multiple of the cache heads, at most 64 query heads
- *   per KV head; scale finite.
+ *   per KV head; T * heads <= 2^30; scale finite.
  * Checked in the kernel: kv_len is clamped to [0, table_width * page_size],
  * cu_q to [0, T] and rising order; a token whose page is outside [0, pages)
  * is not visible.  Query tokens of no request are left as they were.  out

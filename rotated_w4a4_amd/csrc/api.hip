@@ -813,7 +813,7 @@ rw4_status rw4_kv_attention(const rw4_kv_cache* cache_host, const void* q, rw4_d
     return RW4_ERR_SHAPE;
   if (window > 0 && !causal) return RW4_ERR_UNSUPPORTED;
   if (T == 0 || B == 0) return RW4_OK;
-  if (T * heads > 0x7FFFFFFF) return RW4_ERR_SHAPE;
+  if (T * heads > (int64_t(1) << 30)) return RW4_ERR_SHAPE;  // row numbers and tiles stay in 32 bits
   if (!rows_ok(q, q_token, q_head, q_dtype) || !rows_ok(out, out_token, out_head, out_dtype) ||
       !rows_apart({{T, out_token}, {heads, out_head}}, cache_host->head_dim))
     return RW4_ERR_ARG;

@@ -14,8 +14,8 @@
 // fp32 queries are split the same way).
 //
 // Work.  A unit is a tile of query rows (row = query token x query head of one
-// KV head) of one request and KV head.  The keys of all units, in steps of
-// kStep, form one line that is cut into equal shares, one for each block of
+// KV head) of one request and KV head.  The keys of all units, in steps of 64
+// or 128, form one line that is cut into equal shares, one for each block of
 // the grid, so ragged batches are balanced whatever their lengths: a share
 // holds the end of one unit, whole units and the start of another.  Whole
 // units write their output; the pieces of cut ones leave unnormalized partial
@@ -33,7 +33,6 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 typedef float v4f_u __attribute__((ext_vector_type(4), aligned(4)));
 typedef int v6i __attribute__((ext_vector_type(6)));
 typedef short v4s __attribute__((ext_vector_type(4)));
-typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef __bf16 v32bf __attribute__((ext_vector_type(32)));
 typedef unsigned int v4u __attribute__((ext_vector_type(4)));
@@ -44,7 +43,9 @@ constexpr int kCUs = 256;
 constexpr int kNarrowRows = 16;
 constexpr int kNarrowStep = 128;  // keys of a step: 32 for each of a block's 4 waves
 constexpr int kWideRows = 128, kWideStep = 64;
-constexpr int kMaxBlocks = kCUs * 3;
+// Blocks of a grid for each CU, at most: the workspace has room for these.
+constexpr int kNarrowBlocksMost = 3, kWideBlocksMost = 3;
+constexpr int kMaxBlocks = kCUs * (kNarrowBlocksMost > kWideBlocksMost ? kNarrowBlocksMost : kWideBlocksMost);
 constexpr int kNarrowMost = 32;  // up to this many rows of a request the narrow kernel is used
 
 // ---------------------------------------------------------------------------
@@ -129,18 +130,19 @@ struct Line {
   long long before[257];
   Req reqs[256];
   long long wave_sum[4];
-  int wave_units[4];
+  long long wave_units[4];
   bool by_units;  // a step for each unit
 };
 
-// Up to 64 requests and 2^30 steps (so 32 bits do): a lane each, every wave by
+// Up to 64 requests, and 32 bits for their steps: a lane each, every wave by
 // itself and with the same results, so no barrier (they write the same values).
+
 __device__ __forceinline__ bool line_build_wave(const AttnArgs& a, const Cut& cut, Line& line) {
   const int lane = threadIdx.x & (kWave - 1);
   Req r{};
   if (lane < int(a.B)) r = request(a, lane, cut.rows);
   const int units = r.tiles * a.cache.heads, steps = req_steps(r, cut.step);
-  if (__ballot(float(units) * float(steps) > 0x1p24f)) return false;
+  if (__ballot(float(units) * float(steps) > 0x1p24f)) return false;  // sums below 2^30
   int upto = wave_prefix_dpp(units);
   const bool by_units = cut.whole > 0 && __builtin_amdgcn_readlane(upto, kWave - 1) >= cut.whole;
   int own = units;
@@ -161,18 +163,17 @@ __device__ __forceinline__ void line_build(const AttnArgs& a, const Cut& cut, Li
   const int B = int(a.B), per = (B + 255) / 256;
   if (B <= kWave && line_build_wave(a, cut, line)) return;
   const int b0 = tid * per < B ? tid * per : B, b1 = b0 + per < B ? b0 + per : B;
-  long long sum = 0;
-  int units = 0;
+  long long sum = 0, units = 0;
   for (int b = b0; b < b1; ++b) {
     const Req r = request(a, b, cut.rows);
     sum += (long long)(r.tiles) * a.cache.heads * req_steps(r, cut.step);
-    units += r.tiles * a.cache.heads;
+    units += (long long)(r.tiles) * a.cache.heads;
     if (per == 1) line.reqs[tid] = r;
   }
   bool by_units = false;
   if (cut.whole > 0) {
-    const int wave_units = __builtin_amdgcn_readlane(wave_prefix_dpp(units), kWave - 1);
-    if (lane == 0) line.wave_units[wave] = wave_units;
+    const long long upto_units = wave_prefix(units, lane);
+    if (lane == kWave - 1) line.wave_units[wave] = upto_units;
     __syncthreads();
     by_units = line.wave_units[0] + line.wave_units[1] + line.wave_units[2] + line.wave_units[3] >= cut.whole;
     if (by_units) sum = units;
@@ -207,12 +208,12 @@ __device__ __forceinline__ Piece line_find(const AttnArgs& a, const Cut& cut, co
   const bool by_units = uniform(int(line.by_units));
   p.b = seg * per;
   int64_t local = pos - uniform(int64_t(line.before[seg]));
-  for (;; ++p.b) {
+  for (;; ++p.b) {  // ends at the last request at the latest: pos lies on the line
     const Req r = per == 1 ? line.reqs[p.b] : request(a, p.b, cut.rows);
     p.r = Req{uniform(r.q0), uniform(r.qn), uniform(r.kv), uniform(r.tiles), uniform(r.lo), uniform(r.span)};
     p.steps = by_units ? 1 : req_steps(p.r, cut.step);
     const int64_t all = int64_t(p.r.tiles) * a.cache.heads * p.steps;
-    if (local < all) break;
+    if (local < all || p.b + 1 >= int(a.B)) break;
     local -= all;
   }
   int unit;
@@ -274,7 +275,7 @@ __device__ __forceinline__ void row_range(const AttnArgs& a, const Req& r, int i
 // Operands.
 // ---------------------------------------------------------------------------
 // A 16-byte chunk's 32 codes as bf16, in the order of the stored pairs:
-// elements 8 i .. 8 i + 7 are channels 8 kPairOrder[i] .. of the chunk.
+// elements 8 i .. 8 i + 7 are channels 8 pair_order(i) .. of the chunk.
 __device__ __forceinline__ v32bf open_chunk(const v4u& w) {
   uint32_t d[6];
   open_pair<true>(w[0], w[3], d[0], d[1], d[2]);
@@ -679,16 +680,10 @@ __global__ __launch_bounds__(256, (kNarrowBlocks<D, PRECISE>)) void kv_attention
 // ---------------------------------------------------------------------------
 typedef float v16f __attribute__((ext_vector_type(16)));
 
-#ifndef WBLK
-#define WBLK 2
-#endif
 // Blocks of the grid for each CU.
 template <int D, bool PRECISE>
-constexpr int kWideBlocks = (D == 256 || PRECISE) ? 1 : WBLK;
+constexpr int kWideBlocks = (D == 256 || PRECISE) ? 1 : D == 64 ? 3 : 2;
 
-#ifndef WBUF
-#define WBUF 2
-#endif
 template <int D>
 struct WideLds {
   // Keys: rows of 2 D + 16 bytes, so that 16 lanes reading 16 bytes of 16 rows
@@ -699,8 +694,7 @@ struct WideLds {
   static constexpr int kValueRow = 2 * D;
   static constexpr int kValues = kWideStep * kKeyRow;  // where the values start
   static constexpr int kBuffer = kValues + kWideStep * kValueRow;
-  static constexpr int kBuffers = WBUF;
-  static constexpr int kBytes = kBuffers * kBuffer;
+  static constexpr int kBytes = 2 * kBuffer;
   __device__ static constexpr int swizzle(int row) {
     return D == 64 ? ((row >> 1) & 3) + 4 * ((row >> 1) & 1) : 5 * (row & 3);
   }
@@ -922,8 +916,11 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_w
         for (int e = 0; e < 4; ++e) *reinterpret_cast<v8bf*>(dst + 16 * ((4 * my_chunk + pair_order(e)) ^ mix)) = part8(x, e);
       }
       if (tid < kWideStep) {
-        scale_s[buf][0][tid] = scales[0] * scale2;
-        scale_s[buf][1][tid] = seen ? scales[1] : 0.0f;
+        // a value scale that is not finite makes the key's score NaN and is
+        // itself kept from the rows that do not see the key
+        const bool fine = fabsf(scales[1]) < __builtin_huge_valf();
+        scale_s[buf][0][tid] = fine ? scales[0] * scale2 : __builtin_nanf("");
+        scale_s[buf][1][tid] = fine ? scales[1] : 0.0f;
         seen_s[buf][tid] = seen;
       }
     };
@@ -935,7 +932,7 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_w
       store_step(0);
     }
     int buf = 0;
-    for (int j0 = lo; j0 < hi; j0 += kWideStep, buf ^= L::kBuffers - 1) {
+    for (int j0 = lo; j0 < hi; j0 += kWideStep, buf ^= 1) {
       __syncthreads();
       const bool more = j0 + kWideStep < hi;
       if (more) {
@@ -959,14 +956,12 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_w
             for (int p = 0; p < N; ++p) x[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k8, q[i][p], x[kb], 0, 0, 0);
           }
         }
-        v4f sv[2][4];
         const float ref = m == -INFINITY ? 0.0f : m;
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const v4f sk = *reinterpret_cast<const v4f*>(&scale_s[buf][0][32 * kb + 8 * e + 4 * h]);
-            sv[kb][e] = *reinterpret_cast<const v4f*>(&scale_s[buf][1][32 * kb + 8 * e + 4 * h]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[kb][4 * e + i] = fmaf(x[kb][4 * e + i], sk[i], -ref);
           }
@@ -984,6 +979,18 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_w
             }
         };
         load_values(0);
+        // the values' scales: read here where registers allow
+        constexpr bool kEarly = D != 64;
+        v4f sv[kEarly ? 2 : 1][4];
+        auto load_value_scales = [&](int kb) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            sv[kEarly ? kb : 0][e] = *reinterpret_cast<const v4f*>(&scale_s[buf][1][32 * kb + 8 * e + 4 * h]);
+        };
+        if constexpr (kEarly) {
+          load_value_scales(0);
+          load_value_scales(1);
+        }
         if (!whole) {
           keep_branch();
 #pragma unroll
@@ -994,8 +1001,7 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_w
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               const bool on = bits & (1u << (8 * (e >> 2) + (e & 3)));
-              x[kb][e] = on ? x[kb][e] : -INFINITY;
-              sv[kb][e >> 2][e & 3] = on ? sv[kb][e >> 2][e & 3] : 0.0f;
+              x[kb][e] = on ? x[kb][e] : -INFINITY;  // probability 0
             }
           }
         }
@@ -1018,12 +1024,13 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_w
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
           v8bf pr[2][N];
+          if constexpr (!kEarly) load_value_scales(kb);
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const float p = __builtin_amdgcn_exp2f(x[kb][e]);
             l += p;
             __bf16 part[N];
-            split_bf16<N>(p * sv[kb][e >> 2][e & 3], part);
+            split_bf16<N>(p * sv[kEarly ? kb : 0][e >> 2][e & 3], part);
 #pragma unroll
             for (int i = 0; i < N; ++i) pr[e >> 3][i][e & 7] = part[i];
           }
@@ -1037,8 +1044,7 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_w
           if (kb == 0) load_values(1);
         }
       }
-      if (L::kBuffers == 1) __syncthreads();
-      if (more) store_step(buf ^ (L::kBuffers - 1));
+      if (more) store_step(buf ^ 1);
     }
 
     // the wave's rows: lane n, h holds channels 32 c + 8 b + 4 h + i of row n
@@ -1184,6 +1190,7 @@ hipError_t launch_combine(const AttnArgs& a, int rows, int step, int blocks, hip
 template <int D, bool PRECISE>
 hipError_t launch_narrow(const AttnArgs& a, hipStream_t st) {
   const int64_t most = steps_max(a, kNarrowRows, kNarrowStep);
+  static_assert(kNarrowBlocks<D, PRECISE> <= kNarrowBlocksMost, "borders and partial results have no room");
   const int full = kCUs * kNarrowBlocks<D, PRECISE>;
   const int blocks = most < full ? int(most) : full;
   hipLaunchKernelGGL((kv_attention_narrow_kernel<D, PRECISE>), dim3(blocks), dim3(256), 0, st, a);
@@ -1194,6 +1201,7 @@ hipError_t launch_narrow(const AttnArgs& a, hipStream_t st) {
 template <int D, bool PRECISE>
 hipError_t launch_wide(const AttnArgs& a, hipStream_t st) {
   const int64_t most = steps_max(a, kWideRows, kWideStep), units = units_max(a, kWideRows);
+  static_assert(kWideBlocks<D, PRECISE> <= kWideBlocksMost, "borders and partial results have no room");
   const int full = kCUs * kWideBlocks<D, PRECISE>;
   const int blocks = most < full ? int(most) : full;
   const Cut cut{kWideRows, kWideStep, 2 * full};
@@ -1218,7 +1226,8 @@ hipError_t launch_head(const AttnArgs& a, hipStream_t st) {
 }  // namespace
 
 int64_t kv_attention_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t head_dim) {
-  const int64_t narrow = int64_t(kCUs) * 3 * kNarrowRows, wide = int64_t(kCUs) * 3 * 128;
+  const int64_t narrow = int64_t(kCUs) * kNarrowBlocksMost * kNarrowRows;
+  const int64_t wide = int64_t(kCUs) * kWideBlocksMost * kWideRows;
   return kMaxBlocks * int64_t(sizeof(Border)) +
          2 * (narrow > wide ? narrow : wide) * (head_dim + 2) * int64_t(sizeof(float));
 }

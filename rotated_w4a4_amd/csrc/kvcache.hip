@@ -108,7 +108,7 @@ __global__ __launch_bounds__(kSlotsThreads) void kv_slots_kernel(SlotsArgs a, bo
     run[2] += r.back;
     if (run[1] <= count) most = int32_t(run[1]);
   }
-  if (b1 == B && b0 < B) {
+  if (b1 == B && (b0 < B || (B == 0 && tid == 0))) {
     tok0[B] = sat32(run[0]);
     need0[B] = sat32(run[1]);
     back0[B] = sat32(run[2]);

@@ -134,9 +134,10 @@ class KVCache:
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.pages, self.kv_heads, self.page_size, half = k.shape
         self.head_dim, self.device = 2 * half, k.device
+        # the stride of a dimension of one entry is not used
+        cs, ss = ([x if n > 1 else 0 for x, n in zip(s, k.shape[:3])] for s in (cs, ss))
         self._struct = _CacheStruct(k.data_ptr(), k_scale.data_ptr(), v.data_ptr(), v_scale.data_ptr(), self.pages,
-                                    self.page_size, self.kv_heads, self.head_dim, cs[0], cs[1], cs[2], ss[0], ss[1],
-                                    ss[2])
+                                    self.page_size, self.kv_heads, self.head_dim, *cs, *ss)
         self._ptr = ctypes.addressof(self._struct)
 
     @classmethod

@@ -520,3 +520,96 @@ def test_prepared_calls_and_streams():
     for c, w in zip(calls, want):
         assert torch.equal(c.result, w)
     assert got is calls[1].result
+
+
+def test_slots_without_requests():
+    e = torch.empty(0, dtype=torch.int32, device=ku.DEV)
+    state = ku.dev(np.array([3, 4], np.int32))
+    got = rw4.kv_slots(e, e, torch.empty((0, 5), dtype=torch.int32, device=ku.DEV), ku.dev(np.arange(8, dtype=np.int32)),
+                       state, 16, 7)
+    torch.cuda.synchronize()
+    assert got.cu_new.tolist() == [0] and got.free_state.tolist() == [3, 4]
+    assert got.slot_map.tolist() == [-1] * 7 and got.positions.tolist() == [-1] * 7
+
+
+def test_captured_chunk_replays():
+    # the kernel for many rows under capture; lengths change between the replays
+    rng = np.random.default_rng(13)
+    D, page = 64, 16
+    ck, sk = ku.pool(rng, 80, 2, page, D)
+    cv, sv = ku.pool(rng, 80, 2, page, D)
+    cache = ku.cache_of(ck, sk, cv, sv)
+    table = ku.dev(rng.permutation(80).reshape(2, 40).astype(np.int32))
+    kv, cu = ku.dev(np.array([500, 640], np.int32)), ku.dev(np.array([0, 70, 150], np.int32))
+    q = ku.dev(rng.standard_normal((150, 8, D)).astype(np.float32), BF16)
+    out = torch.zeros_like(q)
+    args = dict(max_q_len=80, out=out, workspace=torch.empty(
+        rw4.kv_attention_workspace_bytes(150, 2, 8, 2, D), dtype=torch.uint8, device=ku.DEV))
+    rw4.kv_attention(q, cache, table, kv, cu, **args)
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        rw4.kv_attention(q, cache, table, kv, cu, **args)
+    for lens in ([500, 640], [90, 80], [640, 81], [1, 333]):
+        kv.copy_(ku.dev(np.array(lens, np.int32)))
+        out.fill_(9.0)
+        g.replay()
+        junk = torch.randn(1000, device=ku.DEV).sum()
+        torch.cuda.synchronize()
+        want = rw4.kv_attention(q, cache, table, kv, cu, max_q_len=80)
+        assert torch.equal(out, want) and torch.isfinite(junk)
+
+
+def test_cache_beyond_32_bit_offsets():
+    # pages of 32 KiB up to byte 5.4e9 of each half; the same rows in a small cache give the same bits
+    D, hk, page, pages = 128, 8, 64, 165000
+    cache = rw4.KVCache(*(torch.empty(s, dtype=d, device=ku.DEV) for s, d in
+                          (((pages, hk, page, D // 2), torch.uint8),) * 2 + (((pages, hk, page), F32),) * 2))
+    small = rw4.KVCache.empty(4, page, hk, D)
+    T = 150
+    k, v, q = _rows(1, T, hk, D, BF16), _rows(2, T, hk, D, BF16), _rows(3, T, 16, D, BF16)
+    high = np.array([[pages - 1, 131072, 164001]], np.int32)
+    for c, ids in ((cache, high), (small, np.array([[2, 0, 3]], np.int32))):
+        j = np.arange(T)
+        rw4.kv_append(c, k, v, ku.dev(ids[0, j // page].astype(np.int64) * page + j % page))
+    kv, cu = ku.dev(np.array([T], np.int32)), ku.dev(np.array([0, T], np.int32))
+    for rows, hint in ((T, T), (1, 1)):
+        cu = ku.dev(np.array([0, rows], np.int32))
+        got = rw4.kv_attention(q[:rows], cache, ku.dev(high), kv, cu, max_q_len=hint)
+        want = rw4.kv_attention(q[:rows], small, ku.dev(np.array([[2, 0, 3]], np.int32)), kv, cu, max_q_len=hint)
+        assert torch.equal(got, want) and torch.isfinite(got).all()
+
+
+@pytest.mark.parametrize("D,dtype", [(64, BF16), (128, BF16), (256, BF16), (64, F32), (128, F32)])
+def test_attention_large_batches_match_a_row_at_a_time(D, dtype):
+    # many units (whole ones, cut ones) against single-request calls on the same cache
+    rng = np.random.default_rng(14)
+    hk, group, page, B = 2, 4, 16, 24
+    q_lens = rng.integers(0, 260, B).tolist()
+    kv_lens = [int(n + rng.integers(0, 900)) for n in q_lens]
+    pages = sum(-(-n // page) for n in kv_lens) + 1
+    table = ku.page_table(rng, kv_lens, page, max(-(-n // page) for n in kv_lens), pages)
+    ck, sk = ku.pool(rng, pages, hk, page, D)
+    cv, sv = ku.pool(rng, pages, hk, page, D)
+    cache = ku.cache_of(ck, sk, cv, sv)
+    cu = np.concatenate([[0], np.cumsum(q_lens)]).astype(np.int32)
+    q = ku.dev(rng.standard_normal((int(cu[-1]), hk * group, D)).astype(np.float32), dtype)
+    td, kd = ku.dev(table), ku.dev(np.array(kv_lens, np.int32))
+    full, lse = rw4.kv_attention(q, cache, td, kd, ku.dev(cu), max_q_len=260, return_lse=True)
+    few, lse2 = rw4.kv_attention(q, cache, td, kd, ku.dev(cu), max_q_len=1, return_lse=True)  # the other kernel
+    # what a relative error of the probabilities acts on: sum_j p_j |v_j|, from the magnitudes of the values; twice
+    # the tolerance against the definition, since both sides have it, and 1 % for the bound's own rounding
+    mags = rw4.kv_attention(q, ku.cache_of(ck, sk, np.abs(cv), sv), td, kd, ku.dev(cu), max_q_len=1, unrotate=False,
+                            out_dtype=F32)
+    reach = 1.01 * ku.np64(mags).sum(-1) / D ** 0.5
+    size = D ** -0.5 * 7 * float(sk.max()) * ku.np64(q.float().abs().sum(-1))
+    tol = 2 * ku.attention_tolerance(ku.np64(few), reach, size, dtype, D, max(kv_lens))
+    ku.close(ku.np64(full), ku.np64(few), tol, "kernels")
+    lt = 2 * ((D + 8) * ku.U24 * size + (64 + max(kv_lens)) * ku.U24 + 4 * ku.U24 * np.abs(ku.np64(lse)))
+    ku.close(ku.np64(lse), ku.np64(lse2), lt, "lse")
+    for b in (0, 5, 11, 23):
+        a0, a1 = int(cu[b]), int(cu[b + 1])
+        if a0 < a1:
+            one = rw4.kv_attention(q[a0:a1], cache, td[b:b + 1].contiguous(), kd[b:b + 1],
+                                   ku.dev(np.array([0, a1 - a0], np.int32)))
+            ku.close(ku.np64(one), ku.np64(full)[a0:a1], tol[a0:a1], f"request {b}")
