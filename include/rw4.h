@@ -594,8 +594,9 @@ int64_t rw4_kv_attention_workspace_bytes(int64_t T, int64_t B, int32_t heads, in
  * lse or leaves it as it is.  Queries are in
  * the rotated domain when the cache is (kv_append's or qk_norm_rope's rotate,
  * or rw4_rotate_act).  causal = 0 is attention to another sequence's states.
- * Scores, softmax and sums are fp32; bf16 output: probabilities enter the
- * product rounded to bf16, fp32 output: as three bf16 parts (exact).
+ * Scores, softmax and sums are fp32.  Probabilities enter the product with
+ * the values as bf16 parts: three (exact) when the queries or the output are
+ * fp32, else one (2^-8 of each) or, for few rows a request, two (2^-16).
  *   q, out [T, heads, head_dim] of q_dtype / out_dtype, strides in elements
  *   (*_token, *_head), 16-byte aligned heads; lse fp32 [T, heads] or NULL;
  *   block_table int32 [B][table_width]; kv_len int32 [B]; cu_q int32 [B+1].

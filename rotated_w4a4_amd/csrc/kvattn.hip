@@ -9,9 +9,12 @@
 //   o' = o 2^(m - m') + sum 2^(s_j - m') sv_j cv_j.
 // The codes are exact in bf16 and the scales stay outside the products (sk
 // multiplies the score, sv the probability), so scores of bf16 queries are
-// exact up to the fp32 accumulation; probabilities enter the second product
-// as bf16 (bf16 output) or as three bf16 parts (fp32 output, PRECISE, where
-// fp32 queries are split the same way).
+// exact up to the fp32 accumulation.  Probabilities enter the second product as
+// bf16 parts: three where anything is fp32 (PRECISE; fp32 queries are split the
+// same way), else two in the kernel for few rows, which is bound by memory
+// (2^-16, no loss against the output's own rounding), and one in the kernel for
+// many rows, where a second product would cost time (2^-8 of each probability,
+// as much as the output's own rounding).
 //
 // Work.  A unit is a tile of query rows (row = query token x query head of one
 // KV head) of one request and KV head.  The keys of all units, in steps of 64
@@ -408,7 +411,8 @@ constexpr int kNarrowBlocks = D == 256 ? (PRECISE ? 1 : 2) : (PRECISE ? 2 : 3);
 
 template <int D, bool PRECISE>
 __global__ __launch_bounds__(256, (kNarrowBlocks<D, PRECISE>)) void kv_attention_narrow_kernel(AttnArgs a) {
-  constexpr int N = PRECISE ? 3 : 1;
+  constexpr int N = PRECISE ? 3 : 1;        // parts of the queries
+  constexpr int NP = PRECISE ? 3 : 2;       // parts of the probabilities
   constexpr int NL = D / 64;                 // 16-byte loads a lane makes for 32 rows of codes
   constexpr int NK = D == 64 ? 4 : D / 32;   // query operands
   using L = NarrowLds<D>;
@@ -598,15 +602,15 @@ __global__ __launch_bounds__(256, (kNarrowBlocks<D, PRECISE>)) void kv_attention
           for (int e = 0; e < 8; ++e) x[e] -= top;
         }
       }
-      v8bf pr[N];
+      v8bf pr[NP];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float p = __builtin_amdgcn_exp2f(x[e]);
         l += p;
-        __bf16 part[N];
-        split_bf16<N>(p * sv[e >> 2][e & 3], part);
+        __bf16 part[NP];
+        split_bf16<NP>(p * sv[e >> 2][e & 3], part);
 #pragma unroll
-        for (int i = 0; i < N; ++i) pr[i][e] = part[i];
+        for (int i = 0; i < NP; ++i) pr[i][e] = part[i];
       }
       if (more) load_scales(kv.v_scales, sv);
       // output: keys of lane group g: 4 g + 0..3 and 16 + 4 g + 0..3
@@ -616,7 +620,7 @@ __global__ __launch_bounds__(256, (kNarrowBlocks<D, PRECISE>)) void kv_attention
       for (int c = 0; c < D / 16; ++c) {
         const v8bf vt = lds_transposed(vsrc + 32 * c, vsrc + 32 * c + 16 * L::kRow);
 #pragma unroll
-        for (int i = 0; i < N; ++i) o[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vt, pr[i], o[c], 0, 0, 0);
+        for (int i = 0; i < NP; ++i) o[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vt, pr[i], o[c], 0, 0, 0);
       }
       wave_lds_order();
     }
