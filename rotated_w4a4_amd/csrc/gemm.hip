@@ -58,6 +58,14 @@ constexpr int kF6 = 2;             // MFMA operand format FP6 E2M3
 // 6-register FP6 operand (the last two registers of the vector are not
 // read by an FP6 MFMA).  Four instructions per pair: X[0:32] = a & A,
 // X[64:96] = b & C, X[32:64] = (a & ~A) | (b & ~C).
+template <bool SIGNED>
+__device__ __forceinline__ void open_pair(uint32_t a, uint32_t b, uint32_t& d0, uint32_t& d1, uint32_t& d2) {
+  constexpr uint32_t kA = SIGNED ? kSgnA : kUnsA, kC = SIGNED ? kSgnC : kUnsC;
+  const uint32_t t = b & ~kC;
+  asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(d1) : "v"(a), "s"(~kA), "v"(t));  // (a & ~A) | t
+  d0 = a & kA;
+  d2 = b & kC;
+}
 template <bool SIGNED = true, class W>
 __device__ __forceinline__ v8i f6_operand(const W& w) {
   uint32_t d[6];

@@ -281,15 +281,6 @@ __device__ __forceinline__ void pair_fields(uint32_t w, uint32_t p, bool role, u
     hi = mid & 0xFFFFu;
   }
 }
-// A word pair (a, b) opened into the dense FP6 string of its 16 codes.
-template <bool SIGNED>
-__device__ __forceinline__ void open_pair(uint32_t a, uint32_t b, uint32_t& d0, uint32_t& d1, uint32_t& d2) {
-  constexpr uint32_t kA = SIGNED ? kSgnA : kUnsA, kC = SIGNED ? kSgnC : kUnsC;
-  const uint32_t t = b & ~kC;
-  asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(d1) : "v"(a), "s"(~kA), "v"(t));  // (a & ~A) | t
-  d0 = a & kA;
-  d2 = b & kC;
-}
 // field k (0-7) of a 48-bit field string
 __device__ __forceinline__ uint32_t field6(uint32_t lo, uint32_t hi, int k) {
   return k < 5 ? (lo >> (6 * k)) & 63u : k == 5 ? (lo >> 30) | ((hi & 15u) << 2) : (hi >> (6 * k - 32)) & 63u;

@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import collections
 import ctypes
+import functools
 
 import numpy as np
 
@@ -329,7 +330,9 @@ def _append(cache, k, v, slot_map, q, q_weight, k_weight, cos_sin, positions, ep
             (cache, k, v, slot_map, q, q_weight, k_weight, cos_sin, positions), q_out)
 
 
+@functools.lru_cache(maxsize=256)
 def kv_attention_workspace_bytes(tokens: int, requests: int, heads: int, kv_heads: int, head_dim: int) -> int:
+    """Bytes of workspace kv_attention needs; 0 for invalid sizes."""
     return int(lib.rw4_kv_attention_workspace_bytes(tokens, requests, heads, kv_heads, head_dim))
 
 
@@ -377,7 +380,7 @@ def _attention(q, cache, block_table, kv_len, cu_q, max_q_len, scale, causal, wi
         _out("lse", lse, (T, heads), torch.float32, dev)
     elif return_lse:
         lse = torch.empty((T, heads), dtype=torch.float32, device=q.device)
-    nbytes = lib.rw4_kv_attention_workspace_bytes(T, B, heads, kv_heads, D)
+    nbytes = kv_attention_workspace_bytes(T, B, heads, kv_heads, D)
     if workspace is None:
         wbytes = nbytes if nbytes > 16 else 16
         workspace = torch.empty((wbytes,), dtype=torch.uint8, device=q.device)
