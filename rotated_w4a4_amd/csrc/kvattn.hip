@@ -795,12 +795,98 @@ __device__ __forceinline__ void wide_store(const AttnArgs& a, const It& it, cons
   }
 }
 
+// The keys of a piece that any of the unit's rows sees, [lo, hi) with lo on a
+// step, what the rows of a wave (32 from row0) see, and what all of them see.
+struct Reach {
+  int lo, hi, wave_hi, full_lo, full_hi;
+};
+// Also cuts the lane's own [begin, end) to the piece.
+__device__ __forceinline__ Reach wide_reach(const AttnArgs& a, const Piece& it, bool by_units, int steps, int row0,
+                                            int& begin, int& end) {
+  const int rows = it.r.qn * a.group;
+  Reach u{0, 0, 0, 0, 0};
+  int skip;
+  const int last = (it.tile + 1) * kWideRows < rows ? (it.tile + 1) * kWideRows - 1 : rows - 1;
+  row_range(a, it.r, it.tile * kWideRows / a.group, u.lo, skip);
+  row_range(a, it.r, last / a.group, skip, u.hi);
+  if (row0 < rows) {
+    const int wave_last = row0 + 32 < rows ? row0 + 31 : rows - 1;
+    row_range(a, it.r, row0 / a.group, skip, u.full_hi);
+    row_range(a, it.r, wave_last / a.group, u.full_lo, u.wave_hi);
+  }
+  const int chunk0 = it.r.lo + (by_units ? 0 : it.at * kWideStep);
+  const int64_t stop = by_units ? it.r.kv : int64_t(chunk0) + int64_t(steps) * kWideStep;
+  const int chunk1 = stop < it.r.kv ? int(stop) : it.r.kv;
+  u.lo = u.lo > chunk0 ? u.lo : chunk0;
+  u.hi = u.hi < chunk1 ? u.hi : chunk1;
+  u.wave_hi = u.wave_hi < chunk1 ? u.wave_hi : chunk1;
+  u.full_hi = u.full_hi < chunk1 ? u.full_hi : chunk1;
+  u.lo = chunk0 + ((u.lo - chunk0) & ~(kWideStep - 1));
+  begin = begin > chunk0 ? begin : chunk0;
+  end = end < chunk1 ? end : chunk1;
+  return u;
+}
+
+// A wave's rows after their last key: lane n, h holds channels 32 c + 8 b + 4 h
+// + i of row n.  Written out, or left in the workspace for the combine kernel.
+template <int D>
+__device__ __forceinline__ void wide_finish(const AttnArgs& a, const Piece& it, v16f (&o)[D / 32], float m, float l,
+                                            bool complete, int64_t slot, int wave, int n, int h) {
+  l += __shfl_xor(l, 32);
+  const int at = wave * 32 + n, row = it.tile * kWideRows + at, rows = it.r.qn * a.group;
+  if (complete) {
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) o[c] *= a.unrotate ? inv * kHeadPost<D> : inv;
+    if (a.unrotate) wide_hadamard<D>(o);
+    wide_store<D>(a, it, o, row, row < rows, h);
+    if (a.lse && h == 0 && row < rows)
+      a.lse[(it.r.q0 + row / a.group) * int64_t(a.heads) + it.head * a.group + row % a.group] =
+          l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+  } else if (row < rows) {
+    float* part = partials(a) + slot * (kWideRows * (D + 2));
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        *reinterpret_cast<v4f*>(part + at * D + 32 * c + 8 * b + 4 * h) =
+            v4f{o[c][4 * b], o[c][4 * b + 1], o[c][4 * b + 2], o[c][4 * b + 3]};
+    if (h == 0) {
+      part[kWideRows * D + at] = m;
+      part[kWideRows * (D + 1) + at] = l;
+    }
+  }
+}
+
+// Products whose operands are read from LDS kAhead ahead (left to itself the
+// compiler reads each right before its product); `meanwhile` is work in the
+// shadow of the matrix unit.  The wave goes first meanwhile, so that the
+// others of its SIMD do their softmax behind its products and not beside its.
+constexpr int kAhead = 4;
+template <int COUNT, class Load, class Product, class Meanwhile>
+__device__ __forceinline__ void products(Load load, Product product, Meanwhile meanwhile) {
+  v8bf operand[kAhead];
+  __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+  for (int at = 0; at < kAhead; ++at) operand[at] = load(at);
+#pragma unroll
+  for (int at = 0; at < COUNT; ++at) {
+    __builtin_amdgcn_sched_barrier(0);
+    product(at, operand[at % kAhead]);
+    if (at + kAhead < COUNT) operand[at % kAhead] = load(at + kAhead);
+    meanwhile(at);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_setprio(0);
+}
+
 template <int D, bool PRECISE>
 __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_wide_kernel(AttnArgs a, Cut cut, int blocks) {
   constexpr int N = PRECISE ? 3 : 1;
   constexpr int CH = D / 32;                          // chunks of a row
   constexpr int NS = (2 * kWideStep * CH) / 256;      // chunks a thread opens a step (1: keys or values)
   constexpr int NH = NS > 1 ? NS / 2 : 1;             // of one kind
+  constexpr int kPer = D == 64 ? 2 : 1;               // scales read a product
   using L = WideLds<D>;
   extern __shared__ __align__(16) char lds[];
   __shared__ float scale_s[2][2][kWideStep];
@@ -837,28 +923,8 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_w
       for (int i = 0; i < D / 16; ++i) query_operand<N>(a, base + 16 * i + 8 * h, live, q[i]);
       row_range(a, it.r, tok, begin, end);
     }
-    // keys of the unit's rows and of the wave's: all that any row sees, and those that every row sees
-    int lo, hi, wave_hi = 0, full_lo = 0, full_hi = 0, skip;
-    {
-      const int last = (it.tile + 1) * kWideRows < rows ? (it.tile + 1) * kWideRows - 1 : rows - 1;
-      row_range(a, it.r, it.tile * kWideRows / a.group, lo, skip);
-      row_range(a, it.r, last / a.group, skip, hi);
-      if (row0 < rows) {
-        const int wave_last = row0 + 32 < rows ? row0 + 31 : rows - 1;
-        row_range(a, it.r, row0 / a.group, skip, full_hi);
-        row_range(a, it.r, wave_last / a.group, full_lo, wave_hi);
-      }
-    }
-    const int chunk0 = it.r.lo + (by_units ? 0 : it.at * kWideStep);
-    const int64_t stop = by_units ? it.r.kv : int64_t(chunk0) + int64_t(steps) * kWideStep;
-    const int chunk1 = stop < it.r.kv ? int(stop) : it.r.kv;
-    lo = lo > chunk0 ? lo : chunk0;
-    hi = hi < chunk1 ? hi : chunk1;
-    wave_hi = wave_hi < chunk1 ? wave_hi : chunk1;
-    full_hi = full_hi < chunk1 ? full_hi : chunk1;
-    lo = chunk0 + ((lo - chunk0) & ~(kWideStep - 1));
-    begin = begin > chunk0 ? begin : chunk0;
-    end = end < chunk1 ? end : chunk1;
+    const Reach reach = wide_reach(a, it, by_units, steps, row0, begin, end);
+    const int lo = reach.lo, hi = reach.hi, wave_hi = reach.wave_hi;
 
     v16f o[D / 32];
 #pragma unroll
@@ -870,22 +936,17 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_w
     const bool half_v = NS == 1 && tid >= 128;  // D = 64: one half of the threads takes keys, the other values
     const int my_row = NS == 1 ? (tid & 127) / CH : tid / CH, my_chunk = tid % CH;
     const float scale2 = a.scale * kLog2e;
-    int ids[NH], scale_id;
+    // page ids as they are read, checked where they are used: a check here would wait for them
+    const uint32_t pages = kv.pages < 0x7FFFFFFF ? uint32_t(kv.pages) : 0x7FFFFFFFu;
+    const int* table = a.block_table + it.b * a.table_width;
+    int ids[NH], scale_id = 0;
     auto load_ids = [&](int j0) {
 #pragma unroll
       for (int i = 0; i < NH; ++i) {
         const int j = j0 + my_row + i * kApart;
-        ids[i] = -1;
-        if (j < hi) {
-          const int id = a.block_table[it.b * a.table_width + (j >> kv.log2_page)];
-          ids[i] = id < kv.pages ? id : -1;
-        }
+        ids[i] = table[(j < hi ? j : hi - 1) >> kv.log2_page];
       }
-      scale_id = -1;
-      if (tid < kWideStep && j0 + tid < hi) {
-        const int id = a.block_table[it.b * a.table_width + ((j0 + tid) >> kv.log2_page)];
-        scale_id = id < kv.pages ? id : -1;
-      }
+      if (tid < kWideStep) scale_id = table[(j0 + tid < hi ? j0 + tid : hi - 1) >> kv.log2_page];
     };
     v4u raw[NS];
     float scales[2];
@@ -895,7 +956,7 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_w
 #pragma unroll
       for (int i = 0; i < NH; ++i) {
         const int j = j0 + my_row + i * kApart, at = j & ((1 << kv.log2_page) - 1);
-        const int64_t off = head_codes + row_at(ids[i], kv.code_page, at, kv.code_slot) + 16 * my_chunk;
+        const int64_t off = head_codes + row_at(uint32_t(ids[i]) < pages ? ids[i] : 0, kv.code_page, at, kv.code_slot) + 16 * my_chunk;
         if constexpr (NS == 1) {
           raw[0] = *reinterpret_cast<const v4u*>((half_v ? kv.v_codes : kv.k_codes) + off);
         } else {
@@ -905,8 +966,9 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_w
       }
       if (tid < kWideStep) {  // the keys' scales, from the first wave
         const int at = (j0 + tid) & ((1 << kv.log2_page) - 1);
-        seen = scale_id >= 0;
-        const int64_t off = head_scales + row_at(scale_id, kv.scale_page, at, kv.scale_slot);
+        const bool known = uint32_t(scale_id) < pages;
+        seen = known && j0 + tid < hi;
+        const int64_t off = head_scales + row_at(known ? scale_id : 0, kv.scale_page, at, kv.scale_slot);
         scales[0] = kv.k_scales[off];
         scales[1] = kv.v_scales[off];
       }
@@ -951,54 +1013,34 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_w
         const char* kbase = lds + buf * L::kBuffer;
         const char* vbase = kbase + L::kValues;
         const uint64_t vis = __ballot(seen_s[buf][lane] != 0);
-        const bool whole = vis == ~uint64_t(0) && j0 >= full_lo && j0 + kWideStep <= full_hi;
+        const bool whole = vis == ~uint64_t(0) && j0 >= reach.full_lo && j0 + kWideStep <= reach.full_hi;
         // scores of the step's two 32-key halves
         v16f x[2] = {v16f{}, v16f{}};
         const char* krow = kbase + n * L::kKeyRow + 16 * h;
+        v4f scale[8];
+        products<D / 8>(
+            [&](int at) { return *reinterpret_cast<const v8bf*>(krow + 32 * (at & 1) * L::kKeyRow + 32 * (at >> 1)); },
+            [&](int at, const v8bf& k8) {
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
+              for (int p = 0; p < N; ++p)
+                x[at & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k8, q[at >> 1][p], x[at & 1], 0, 0, 0);
+            },
+            [&](int at) {  // the keys' scales
+              if (at >= D / 8 - 8 / kPer) {
 #pragma unroll
-          for (int kb = 0; kb < 2; ++kb) {
-            const v8bf k8 = *reinterpret_cast<const v8bf*>(krow + 32 * kb * L::kKeyRow + 32 * i);
-#pragma unroll
-            for (int p = 0; p < N; ++p) x[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k8, q[i][p], x[kb], 0, 0, 0);
-          }
-        }
+                for (int e = 0; e < kPer; ++e) {
+                  const int k = (at - (D / 8 - 8 / kPer)) * kPer + e;
+                  scale[k] = *reinterpret_cast<const v4f*>(&scale_s[buf][0][8 * k + 4 * h]);
+                }
+              }
+            });
         const float ref = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
+        for (int e = 0; e < 32; ++e) x[e >> 4][e & 15] = fmaf(x[e >> 4][e & 15], scale[e >> 2][e & 3], -ref);
+        // the values' scales
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const v4f sk = *reinterpret_cast<const v4f*>(&scale_s[buf][0][32 * kb + 8 * e + 4 * h]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[kb][4 * e + i] = fmaf(x[kb][4 * e + i], sk[i], -ref);
-          }
-        // values: 8 bytes of row 32 kb + 16 b + 4 h + (l % 16) / 4 (and 8 rows on), 32-channel tile c
-        const int vr = 4 * h + ((lane & 15) >> 2), vu = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-        const char* vrow = vbase + vr * L::kValueRow + 8 * (lane & 1);
-        v8bf vt[2][D / 32];
-        auto load_values = [&](int kb) {
-#pragma unroll
-          for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              const char* v0 = vrow + (32 * kb + 16 * b) * L::kValueRow + 16 * ((4 * c + vu) ^ L::swizzle(vr));
-              vt[b][c] = lds_transposed(v0, v0 + 8 * L::kValueRow);
-            }
-        };
-        load_values(0);
-        // the values' scales: read here where registers allow
-        constexpr bool kEarly = D != 64;
-        v4f sv[kEarly ? 2 : 1][4];
-        auto load_value_scales = [&](int kb) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            sv[kEarly ? kb : 0][e] = *reinterpret_cast<const v4f*>(&scale_s[buf][1][32 * kb + 8 * e + 4 * h]);
-        };
-        if constexpr (kEarly) {
-          load_value_scales(0);
-          load_value_scales(1);
-        }
+        for (int e = 0; e < 8; ++e) scale[e] = *reinterpret_cast<const v4f*>(&scale_s[buf][1][8 * e + 4 * h]);
+        __builtin_amdgcn_sched_barrier(0);
         if (!whole) {
           keep_branch();
 #pragma unroll
@@ -1029,58 +1071,41 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_w
             for (int e = 0; e < 32; ++e) x[e >> 4][e & 15] -= top;
           }
         }
+        v8bf pr[4][N];
+        auto probability = [&](int e) {
+          const float p = __builtin_amdgcn_exp2f(x[e >> 4][e & 15]);
+          l += p;
+          __bf16 part[N];
+          split_bf16<N>(p * scale[e >> 2][e & 3], part);
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-          v8bf pr[2][N];
-          if constexpr (!kEarly) load_value_scales(kb);
+          for (int i = 0; i < N; ++i) pr[e >> 3][i][e & 7] = part[i];
+        };
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float p = __builtin_amdgcn_exp2f(x[kb][e]);
-            l += p;
-            __bf16 part[N];
-            split_bf16<N>(p * sv[kEarly ? kb : 0][e >> 2][e & 3], part);
-#pragma unroll
-            for (int i = 0; i < N; ++i) pr[e >> 3][i][e & 7] = part[i];
-          }
-#pragma unroll
-          for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c)
+        for (int e = 0; e < 16; ++e) probability(e);
+        // values: 8 bytes of row 32 kb + 16 b + 4 h + (l % 16) / 4 (and 8 rows on), 32-channel tile c
+        const int vr = 4 * h + ((lane & 15) >> 2), vu = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+        const char* vrow = vbase + vr * L::kValueRow + 8 * (lane & 1);
+        products<4 * CH>(
+            [&](int at) {
+              const char* v0 = vrow + 16 * (at / CH) * L::kValueRow + 16 * ((4 * (at % CH) + vu) ^ L::swizzle(vr));
+              return lds_transposed(v0, v0 + 8 * L::kValueRow);
+            },
+            [&](int at, const v8bf& v8) {
 #pragma unroll
               for (int i = 0; i < N; ++i)
-                o[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vt[b][c], pr[b][i], o[c], 0, 0, 0);
-          if (kb == 0) load_values(1);
-        }
+                o[at % CH] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v8, pr[at / CH][i], o[at % CH], 0, 0, 0);
+            },
+            [&](int at) {  // the second half's probabilities
+              if (at < 2 * CH) {
+#pragma unroll
+                for (int e = 0; e < 8 / CH; ++e) probability(16 + at * (8 / CH) + e);
+              }
+            });
       }
       if (more) store_step(buf ^ 1);
     }
 
-    // the wave's rows: lane n, h holds channels 32 c + 8 b + 4 h + i of row n
-    l += __shfl_xor(l, 32);
-    const int row = row0 + n;
-    if (complete) {
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) o[c] *= a.unrotate ? inv * kHeadPost<D> : inv;
-      if (a.unrotate) wide_hadamard<D>(o);
-      wide_store<D>(a, it, o, row, row < rows, h);
-      if (a.lse && h == 0 && row < rows)
-        a.lse[(it.r.q0 + row / a.group) * int64_t(a.heads) + it.head * a.group + row % a.group] =
-            l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
-    } else if (row < rows) {
-      float* part = partials(a) + slot * (kWideRows * (D + 2));
-      const int at = wave * 32 + n;
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c)
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-          *reinterpret_cast<v4f*>(part + at * D + 32 * c + 8 * b + 4 * h) =
-              v4f{o[c][4 * b], o[c][4 * b + 1], o[c][4 * b + 2], o[c][4 * b + 3]};
-      if (h == 0) {
-        part[kWideRows * D + at] = m;
-        part[kWideRows * (D + 1) + at] = l;
-      }
-    }
+    wide_finish<D>(a, it, o, m, l, complete, slot, wave, n, h);
     __syncthreads();  // the buffers are free for the next piece
   }
 }
