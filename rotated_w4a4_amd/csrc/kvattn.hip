@@ -51,10 +51,11 @@ constexpr int kNarrowBlocksMost = 3, kWideBlocksMost = 3;
 constexpr int kMaxBlocks = kCUs * (kNarrowBlocksMost > kWideBlocksMost ? kNarrowBlocksMost : kWideBlocksMost);
 // Up to this many rows of a request the kernel for few rows is used.  Measured
 // on 32 requests of 4000 keys and 8 KV heads (few / many rows, us): D = 128 bf16
-// 48 rows 81 / 99, 64 rows 116 / 99; D = 64 48 rows 63 / 66, 64 rows 93 / 65;
-// D = 256 64 rows 197 / 244, 96 rows 284 / 247; fp32 96 rows 217 / 220.
+// 48 rows 82 / 87, 64 rows 120 / 88; D = 64 16 rows 38 / 52, 32 rows 56 / 53, 48
+// rows 63 / 60; D = 256 48 rows 178 / 200, 64 rows 202 / 198, 96 rows 289 / 204;
+// fp32 64 rows 149 / 188, 96 rows 215 / 192.
 template <int D, bool PRECISE>
-constexpr int kNarrowMost = D == 256 || PRECISE ? 96 : 48;
+constexpr int kNarrowMost = D == 256 || PRECISE ? 64 : D == 128 ? 48 : 32;
 
 // ---------------------------------------------------------------------------
 // The line of work.
@@ -1224,12 +1225,15 @@ int64_t steps_max(const AttnArgs& a, int rows, int step) {
 }
 
 template <int D, bool SPLIT>
-hipError_t launch_combine(const AttnArgs& a, int rows, int step, int blocks, hipStream_t st) {
+hipError_t launch_combine(const AttnArgs& a, int rows, int step, int blocks, int64_t whole, hipStream_t st) {
   if (blocks < 2 || (a.table_width << a.cache.log2_page) <= step) return hipSuccess;  // no unit can be cut
   // blocks for the rows that max_q_len lets expect (they go on to the others if it is wrong)
   constexpr int kBlockRows = kWave / (D / 8) * (SPLIT ? 1 : 4);
   const int64_t live = a.max_q_len < rows ? a.max_q_len * a.group : rows;
-  const int parts = int((live < 1 ? 1 : live < rows ? live : rows) + kBlockRows - 1) / kBlockRows;
+  // With `whole` units or more (0: never) none is cut, which the device lengths
+  // decide; if the tokens are enough for that, blocks are left to find nothing.
+  const bool few = whole > 0 && a.cache.heads * (a.T * a.group / rows) >= whole;
+  const int parts = few ? 1 : int((live < 1 ? 1 : live < rows ? live : rows) + kBlockRows - 1) / kBlockRows;
   hipLaunchKernelGGL((kv_attention_combine_kernel<D, SPLIT>), dim3((blocks - 1) * parts), dim3(256), 0, st, a, rows,
                      parts);
   return hipGetLastError();
@@ -1243,7 +1247,7 @@ hipError_t launch_narrow(const AttnArgs& a, hipStream_t st) {
   const int blocks = most < full ? int(most) : full;
   hipLaunchKernelGGL((kv_attention_narrow_kernel<D, PRECISE>), dim3(blocks), dim3(256), 0, st, a);
   const hipError_t e = hipGetLastError();
-  return e != hipSuccess ? e : launch_combine<D, true>(a, kNarrowRows, kNarrowStep, blocks, st);
+  return e != hipSuccess ? e : launch_combine<D, true>(a, kNarrowRows, kNarrowStep, blocks, 0, st);
 }
 
 template <int D, bool PRECISE>
@@ -1260,7 +1264,7 @@ hipError_t launch_wide(const AttnArgs& a, hipStream_t st) {
   hipLaunchKernelGGL(kernel, dim3(unsigned(units > blocks ? units : blocks)), dim3(256), WideLds<D>::kBytes, st, a, cut,
                      blocks);
   const hipError_t e = hipGetLastError();
-  return e != hipSuccess ? e : launch_combine<D, false>(a, kWideRows, kWideStep, blocks, st);
+  return e != hipSuccess ? e : launch_combine<D, false>(a, kWideRows, kWideStep, blocks, cut.whole, st);
 }
 
 template <int D>
