@@ -613,3 +613,25 @@ def test_attention_large_batches_match_a_row_at_a_time(D, dtype):
             one = rw4.kv_attention(q[a0:a1], cache, td[b:b + 1].contiguous(), kd[b:b + 1],
                                    ku.dev(np.array([0, a1 - a0], np.int32)))
             ku.close(ku.np64(one), ku.np64(full)[a0:a1], tol[a0:a1], f"request {b}")
+
+
+@pytest.mark.parametrize("D,dtype", [(64, BF16), (128, BF16), (256, BF16), (128, F32)])
+def test_attention_many_rows_hide_bad_pages_and_clamp_bad_lengths(D, dtype):
+    # pages out of range in the middle of steps and as whole steps; a length beyond the table
+    rng = np.random.default_rng(17)
+    page, pages, lens, q_lens = 16, 24, [190, 10 ** 9], [70, 80]
+    ck, sk = ku.pool(rng, pages, 2, page, D)
+    cv, sv = ku.pool(rng, pages, 2, page, D)
+    cache = ku.cache_of(ck, sk, cv, sv)
+    table = rng.permutation(pages).reshape(2, 12).astype(np.int32)
+    table[0, 1], table[0, 4:8] = -1, (pages, -2 ** 31, 2 ** 31 - 1, pages + 3)
+    table[1, 0], table[1, 11] = -5, pages
+    cu = np.array([0, 70, 150], np.int32)
+    q = ku.dev((1.5 * rng.standard_normal((150, 4, D))).astype(np.float32), dtype)
+    out, lse = rw4.kv_attention(q, cache, ku.dev(table), ku.dev(np.array(lens, np.int32)), ku.dev(cu),
+                                max_q_len=max(q_lens), return_lse=True)
+    kv = [190, 12 * page]
+    want, wl, reach, size = okv.kv_attention(ku.np64(q), ck, sk, cv, sv, pages, table, kv, cu, D ** -0.5, True, 0, True)
+    ku.close(ku.np64(out), want, ku.attention_tolerance(want, reach, size, dtype, D, 192), "out")
+    lt = (D + 8) * ku.U24 * size + (64 + 192) * ku.U24 + 4 * ku.U24 * np.abs(wl)
+    ku.close(ku.np64(lse), wl, lt, "lse")
