@@ -635,3 +635,27 @@ def test_attention_many_rows_hide_bad_pages_and_clamp_bad_lengths(D, dtype):
     ku.close(ku.np64(out), want, ku.attention_tolerance(want, reach, size, dtype, D, 192), "out")
     lt = (D + 8) * ku.U24 * size + (64 + 192) * ku.U24 + 4 * ku.U24 * np.abs(wl)
     ku.close(ku.np64(lse), wl, lt, "lse")
+
+
+def test_attention_cut_units_behind_a_long_padding():
+    # tokens for far more units than the requests have: units are cut all the same, and merged by few blocks
+    rng = np.random.default_rng(23)
+    D, page, kv_lens, q_lens, padded = 128, 64, [6000, 5801], [60, 75], 17000
+    pages = sum(-(-n // page) for n in kv_lens)
+    table = ku.dev(ku.page_table(rng, kv_lens, page, -(-6000 // page), pages))
+    ck, sk = ku.pool(rng, pages, 2, page, D)
+    cv, sv = ku.pool(rng, pages, 2, page, D)
+    cache = ku.cache_of(ck, sk, cv, sv)
+    kv, cu, n = ku.dev(np.array(kv_lens, np.int32)), ku.dev(np.array([0, 60, 135], np.int32)), 135
+    q = torch.zeros((padded, 8, D), dtype=BF16, device=ku.DEV)
+    q[:n] = ku.dev(rng.standard_normal((n, 8, D)).astype(np.float32), BF16)
+    out = torch.full_like(q, 3.0)
+    _, lse = rw4.kv_attention(q, cache, table, kv, cu, max_q_len=75, out=out, return_lse=True)
+    want, wl = rw4.kv_attention(q[:n], cache, table, kv, cu, max_q_len=75, return_lse=True)
+    assert torch.equal(out[:n], want) and torch.equal(lse[:n], wl)
+    assert (out[n:] == 3.0).all()
+    for b, (a0, a1) in enumerate(((0, 60), (60, 135))):  # and alone, against the oracle
+        o, _, reach, size = okv.kv_attention(ku.np64(q[a0:a1]), ck, sk, cv, sv, pages, table[b:b + 1].cpu().numpy(),
+                                             kv_lens[b:b + 1], [0, a1 - a0], D ** -0.5, True, 0, True)
+        tol = ku.attention_tolerance(o, reach, size, BF16, D, kv_lens[b])
+        ku.close(ku.np64(out[a0:a1]), o, tol, f"request {b}")
