@@ -604,8 +604,8 @@ int64_t rw4_kv_attention_workspace_bytes(int64_t T, int64_t B, int32_t heads, in
  *   kernel, and with it the roundings above, nothing else.  window > 0 needs causal.
  *   B <= 65535; heads a multiple of the cache heads, at most 64 query heads
  *   per KV head; T * heads <= 2^30; scale finite.
- * Checked in the kernel: kv_len is clamped to [0, table_width * page_size],
- * cu_q to [0, T] and rising order; a token whose page is outside [0, pages)
+ * Checked in the kernel: kv_len is clamped to [0, table_width * page_size]
+ * and to 2^31 - 8192, cu_q to [0, T] and rising order; a token whose page is outside [0, pages)
  * is not visible.  Query tokens of no request are left as they were.  out
  * must not overlap q.
  *   workspace: rw4_kv_attention_workspace_bytes bytes, 16-byte aligned,

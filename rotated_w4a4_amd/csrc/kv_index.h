@@ -1,0 +1,25 @@
+// Index bounds of the KV cache kernels: constants and arithmetic without any
+// device code, so that host compilers can check them too.
+#pragma once
+
+#include <stdint.h>
+
+namespace rw4 {
+
+// Keys of one request that kv_attention works on, at most (longer lengths are
+// clamped).  The kernels hold key indexes in 32 bits and look up to two steps, or
+// 32 tiles of page ids, ahead of the last key.
+constexpr int kMostKeys = 0x7FFFFFFF - 8191;
+
+constexpr int clamp_keys(int64_t len, int64_t room) {
+  const int64_t most = room < kMostKeys ? room : int64_t(kMostKeys);
+  return int(len < 0 ? 0 : len > most ? most : len);
+}
+
+// The kernel for few rows fetches the page ids of 32 tiles at a time, one a
+// lane: lane n has the half n & 1 (16 keys) of tile n / 2, the tiles of a wave
+// 128 keys apart.  The lane's first key lies this far behind the first tile's.
+constexpr int ids_ahead(int lane) { return 128 * (lane >> 1) + 16 * (lane & 1); }
+static_assert(kMostKeys <= 0x7FFFFFFF - ids_ahead(63) - 128, "key indexes stay in 32 bits");
+
+}  // namespace rw4

@@ -26,6 +26,7 @@
 // combine kernel.  Every block works the line out by itself from kv_len and
 // cu_q: no plan, no copy to the host, and a captured graph follows its lengths.
 #include "kv_device.h"
+#include "kv_index.h"
 #include "kv_internal.h"
 
 namespace rw4 {
@@ -73,8 +74,7 @@ __device__ __forceinline__ Req request(const AttnArgs& a, int b, int rows) {
   const int q1 = clamp_int(a.cu_q[b + 1], a.T);
   r.q0 = clamp_int(a.cu_q[b], a.T);
   r.qn = q1 > r.q0 ? q1 - r.q0 : 0;
-  const int64_t room = a.table_width << a.cache.log2_page;
-  r.kv = clamp_int(a.kv_len[b], room < 0x7FFFFF00 ? room : 0x7FFFFF00);
+  r.kv = clamp_keys(a.kv_len[b], a.table_width << a.cache.log2_page);
   r.tiles = (r.qn * a.group + rows - 1) / rows;  // T * heads < 2^31
   r.lo = 0;
   if (a.window > 0) {
@@ -491,7 +491,7 @@ __global__ __launch_bounds__(256, (kNarrowBlocks<D, PRECISE>)) void kv_attention
     // Page ids of 32 tiles at a time (two 16-key halves each), one per lane; -1: no key of the half is visible.
     int ids = -1;
     auto load_ids = [&](int j) {
-      j += 128 * (lane >> 1) + 16 * (lane & 1);
+      j += ids_ahead(lane);  // j < hi <= kMostKeys: the sum stays in 32 bits
       ids = -1;
       if (j < hi) {
         ids = a.block_table[it.b * a.table_width + (j >> kv.log2_page)];

@@ -1,0 +1,47 @@
+"""Index arithmetic of the KV cache kernels, compiled for the host (no GPU
+needed): evaluated in constant expressions, where an overflow is an error."""
+import os
+import shutil
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def _compile(tmp_path, body):
+    src = tmp_path / "check.cpp"
+    src.write_text('#include "kv_index.h"\nusing namespace rw4;\n' + body)
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        pytest.skip("no host compiler")
+    r = subprocess.run([cxx, "-std=c++17", "-Wall", "-fsyntax-only", "-I", os.path.join(ROOT, "rotated_w4a4_amd", "csrc"),
+                        str(src)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+
+
+def test_page_ids_of_the_longest_requests_stay_in_the_table(tmp_path):
+    # every length a table can hold and more: a lane reads entry j / page_size only for j in [0, keys), for the first
+    # tile of every group that starts in front of the last key
+    _compile(tmp_path, """
+constexpr bool lanes_fit(int64_t len, int64_t room) {
+  const int hi = clamp_keys(len, room);
+  if (hi < 0 || hi > room) return false;
+  for (int back = 1; back <= 4500; back += back < 200 ? 1 : 61) {
+    const int j = hi - back;
+    if (j < 0) break;
+    for (int lane = 0; lane < 64; ++lane) {
+      const int key = j + ids_ahead(lane);
+      if (key < j) return false;
+    }
+    const int next = j + 128 + 64 + 127;  // two steps ahead of the kernel for many rows, rows of a step behind
+    if (next < j) return false;
+  }
+  return true;
+}
+static_assert(lanes_fit(0x7FFFFFFF, int64_t(2048) << 20));
+static_assert(lanes_fit(0x7FFFFFFF, int64_t(0x7FFFFFFF) << 20));
+static_assert(lanes_fit(0x7FFFFF00, int64_t(2048) << 20));
+static_assert(lanes_fit(-5, 64) && lanes_fit(100, 64) && lanes_fit(1 << 20, 0));
+static_assert(clamp_keys(-1, 64) == 0 && clamp_keys(100, 64) == 64 && clamp_keys(63, 64) == 63);
+""")
