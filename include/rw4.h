@@ -556,7 +556,7 @@ rw4_status rw4_qk_norm_rope(const void* q, int64_t q_token, int64_t q_head, cons
  * stored in row slot_map[t] of the cache (page slot / page_size, slot
  * slot % page_size).  Codes are those of the exact quotients, ties to even (u
  * in fp64 where that matters; the norm's factor does not enter them), scales
- * are fp32.  A row with an infinity or NaN gets the
+ * are fp32 (infinite where the value lies beyond its range).  A row with an infinity or NaN gets the
  * scale NaN and codes 0 (rotate = 0 as well), a row of zeros scale 0 and
  * codes 0.  Queries (optional, q NULL: none): as rw4_qk_norm_rope with the
  * same rotate, into q_out.

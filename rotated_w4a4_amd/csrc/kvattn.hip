@@ -583,10 +583,12 @@ __global__ __launch_bounds__(256, (kNarrowBlocks<D, PRECISE>)) void kv_attention
       // softmax
       float x[8];
       const bool whole = seen[0] && seen[1] && j0 >= full_lo && j0 + 32 <= full_hi && j0 + 32 <= hi;
-      // relative to the running maximum
+      // relative to the running maximum; 0 sk makes NaN of a key whose scale is
+      // infinite, which could otherwise have a score of -infinity and be lost
       float ref = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = fmaf(sc[e >> 2][e & 3], sk[e >> 2][e & 3] * scale2, -ref);
+      for (int e = 0; e < 8; ++e)
+        x[e] = fmaf(sc[e >> 2][e & 3], sk[e >> 2][e & 3] * scale2, fmaf(sk[e >> 2][e & 3], 0.0f, -ref));
       if (more) load_scales(kv.k_scales, sk);
       if (!whole) {
         keep_branch();
@@ -1002,9 +1004,10 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_w
         for (int e = 0; e < 4; ++e) *reinterpret_cast<v8bf*>(dst + 16 * ((4 * my_chunk + pair_order(e)) ^ mix)) = part8(x, e);
       }
       if (tid < kWideStep) {
-        // a value scale that is not finite makes the key's score NaN and is
-        // itself kept from the rows that do not see the key
-        const bool fine = fabsf(scales[1]) < __builtin_huge_valf();
+        // a scale that is not finite makes the key's score NaN (an infinite one
+        // could otherwise make it -infinity, and the key would be lost); that of a
+        // value is itself kept from the rows that do not see the key
+        const bool fine = fabsf(scales[0]) < __builtin_huge_valf() && fabsf(scales[1]) < __builtin_huge_valf();
         scale_s[buf][0][tid] = fine ? scales[0] * scale2 : __builtin_nanf("");
         scale_s[buf][1][tid] = fine ? scales[1] : 0.0f;
         seen_s[buf][tid] = seen;
