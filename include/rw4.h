@@ -595,8 +595,8 @@ int64_t rw4_kv_attention_workspace_bytes(int64_t T, int64_t B, int32_t heads, in
  * the rotated domain when the cache is (kv_append's or qk_norm_rope's rotate,
  * or rw4_rotate_act).  causal = 0 is attention to another sequence's states.
  * Scores, softmax and sums are fp32.  Probabilities enter the product with
- * the values as bf16 parts: three (exact) when the queries or the output are
- * fp32, else one (2^-8 of each) or, for few rows a request, two (2^-16).
+ * the values as three bf16 parts (exact) when the queries or the output are
+ * fp32, else as one fp16 number (2^-11 of each) or two bf16 parts (2^-16).
  *   q, out [T, heads, head_dim] of q_dtype / out_dtype, strides in elements
  *   (*_token, *_head), 16-byte aligned heads; lse fp32 [T, heads] or NULL;
  *   block_table int32 [B][table_width]; kv_len int32 [B]; cu_q int32 [B+1].

@@ -10,11 +10,10 @@
 // The codes are exact in bf16 and the scales stay outside the products (sk
 // multiplies the score, sv the probability), so scores of bf16 queries are
 // exact up to the fp32 accumulation.  Probabilities enter the second product as
-// bf16 parts: three where anything is fp32 (PRECISE; fp32 queries are split the
-// same way), else two in the kernel for few rows, which is bound by memory
-// (2^-16, no loss against the output's own rounding), and one in the kernel for
-// many rows, where a second product would cost time (2^-8 of each probability,
-// as much as the output's own rounding).
+// three bf16 parts where anything is fp32 (PRECISE; fp32 queries are split the same
+// way), else as two (2^-16) in the kernel for few rows, which is bound by memory,
+// and as one fp16 number (2^-11) in the kernel for many rows, where a second product
+// would cost time: little against the output's own rounding, 2^-8.
 //
 // Work.  A unit is a tile of query rows (row = query token x query head of one
 // KV head) of one request and KV head.  The keys of all units, in steps of 64
@@ -29,6 +28,8 @@
 #include "kv_index.h"
 #include "kv_internal.h"
 
+#include <type_traits>
+
 namespace rw4 {
 
 namespace {
@@ -39,10 +40,14 @@ typedef int v6i __attribute__((ext_vector_type(6)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef __bf16 v32bf __attribute__((ext_vector_type(32)));
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef _Float16 v32h __attribute__((ext_vector_type(32)));
 typedef unsigned int v4u __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kSlack = 8.0f;  // probabilities may reach 2^kSlack before the maximum is raised
+// Probabilities may reach 2^kSlack before the maximum is raised (2^kHalfSlack where
+// they enter products as fp16).
+constexpr float kSlack = 8.0f, kHalfSlack = 7.0f;
 constexpr int kCUs = 256;
 constexpr int kNarrowRows = 16;
 constexpr int kNarrowStep = 128;  // keys of a step: 32 for each of a block's 4 waves
@@ -283,13 +288,18 @@ __device__ __forceinline__ void row_range(const AttnArgs& a, const Req& r, int i
 // ---------------------------------------------------------------------------
 // Operands.
 // ---------------------------------------------------------------------------
-// A 16-byte chunk's 32 codes as bf16, in the order of the stored pairs:
+// A 16-byte chunk's 32 codes as bf16 or fp16, in the order of the stored pairs:
 // elements 8 i .. 8 i + 7 are channels 8 pair_order(i) .. of the chunk.
-__device__ __forceinline__ v32bf open_chunk(const v4u& w) {
+__device__ __forceinline__ v6i chunk_pairs(const v4u& w) {
   // a pair (a, b) opens into X[0:32] = a & A, X[32:64] = (a & ~A) | (b & ~C), X[64:96] = b & C
-  const v6i p = {int(w[0] & kSgnA), int((w[0] & ~kSgnA) | (w[3] & ~kSgnC)), int(w[3] & kSgnC),
-                 int(w[1] & kSgnA), int((w[1] & ~kSgnA) | (w[2] & ~kSgnC)), int(w[2] & kSgnC)};
-  return __builtin_amdgcn_cvt_scalef32_pk32_bf16_fp6(p, 8.0f);  // E2M3 c / 8 times 8
+  return v6i{int(w[0] & kSgnA), int((w[0] & ~kSgnA) | (w[3] & ~kSgnC)), int(w[3] & kSgnC),
+             int(w[1] & kSgnA), int((w[1] & ~kSgnA) | (w[2] & ~kSgnC)), int(w[2] & kSgnC)};
+}
+__device__ __forceinline__ v32bf open_chunk(const v4u& w) {
+  return __builtin_amdgcn_cvt_scalef32_pk32_bf16_fp6(chunk_pairs(w), 8.0f);  // E2M3 c / 8 times 8
+}
+__device__ __forceinline__ v32h open_chunk_half(const v4u& w) {
+  return __builtin_amdgcn_cvt_scalef32_pk32_f16_fp6(chunk_pairs(w), 8.0f);
 }
 __device__ __forceinline__ int pair_order(int i) { return i == 0 ? 0 : i == 1 ? 3 : i == 2 ? 1 : 2; }
 
@@ -298,6 +308,14 @@ __device__ __forceinline__ v8bf part8(const v32bf& x, int i) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) r[e] = x[8 * i + e];
   return r;
+}
+
+// The same 8 of an fp16 chunk, as the 16 bytes that are stored.
+__device__ __forceinline__ v8bf part8(const v32h& x, int i) {
+  v8h r;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) r[e] = x[8 * i + e];
+  return __builtin_bit_cast(v8bf, r);
 }
 
 // x = sum of N bf16 parts (N = 3: exact up to the smallest exponents).
@@ -845,23 +863,34 @@ __device__ __forceinline__ Reach wide_reach(const AttnArgs& a, const Piece& it, 
   return u;
 }
 
+// o 2^unit.
+template <int D>
+__device__ __forceinline__ void wide_unit(v16f (&o)[D / 32], int unit) {
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[c][e] = ldexpf(o[c][e], unit);
+}
+
 // A wave's rows after their last key: lane n, h holds channels 32 c + 8 b + 4 h
 // + i of row n.  Written out, or left in the workspace for the combine kernel.
-template <int D>
+template <int D, bool HALF>
 __device__ __forceinline__ void wide_finish(const AttnArgs& a, const Piece& it, v16f (&o)[D / 32], float m, float l,
-                                            bool complete, int64_t slot, int wave, int n, int h) {
+                                            int unit, bool complete, int64_t slot, int wave, int n, int h) {
   l += __shfl_xor(l, 32);
   const int at = wave * 32 + n, row = it.tile * kWideRows + at, rows = it.r.qn * a.group;
   if (complete) {
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) o[c] *= a.unrotate ? inv * kHeadPost<D> : inv;
+    if constexpr (HALF) wide_unit<D>(o, unit);
     if (a.unrotate) wide_hadamard<D>(o);
     wide_store<D>(a, it, o, row, row < rows, h);
     if (a.lse && h == 0 && row < rows)
       a.lse[(it.r.q0 + row / a.group) * int64_t(a.heads) + it.head * a.group + row % a.group] =
           l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
   } else if (row < rows) {
+    if constexpr (HALF) wide_unit<D>(o, unit);
     float* part = partials(a) + slot * (kWideRows * (D + 2));
 #pragma unroll
     for (int c = 0; c < D / 32; ++c)
@@ -874,6 +903,39 @@ __device__ __forceinline__ void wide_finish(const AttnArgs& a, const Piece& it, 
       part[kWideRows * (D + 1) + at] = l;
     }
   }
+}
+
+// ---------------------------------------------------------------------------
+// Weights of the kernel for many rows.  Where queries and output are bf16, a
+// probability times its value's scale, w = p sv, enters the product as one fp16
+// number: half a step is 2^-11, an eighth of the output's.  (One bf16 part, 2^-8,
+// makes the output's error 1.4 times as large as its own rounding; two take a
+// quarter more time, 182 us for 147 on the prompt case, where fp16 takes 152.)
+//   fp16 has 11 bits from 2^-14 to 2^16 and loses at most 2^-25 of what is smaller,
+// so a piece's scales are multiplied by a power of two, which is exact: 2^-unit puts
+// the largest of its first step into [2^5, 2^6).  If all of the piece's n keys then
+// have a scale in [n 2^-16, 2^8), no weight passes 2^15 (p <= 2^kHalfSlack), each
+// row has one of n 2^-16 or more (its largest p is at least 1), and what n keys
+// lose, 2^-25 each, is at most 2^-9 of that, and that only if all lie below fp16's
+// normal range.  At the first step with a key outside of the range (a value of
+// zeros, say) the piece starts again with weights of two bf16 parts, which need
+// none; a prompt of such keys alone takes 194 us.
+// ---------------------------------------------------------------------------
+struct Unit {
+  int exp;
+  float least;  // n 2^-16
+};
+
+// The largest v >= 0 of a wave's lanes.
+__device__ __forceinline__ float wave_max(float v) {
+  for (int d = 1; d < kWave; d <<= 1) v = fmaxf(v, __shfl_xor(v, d));
+  return v;
+}
+
+// The power of two of a piece whose first step has this scale in the lane (0: none).
+__device__ __forceinline__ int unit_exponent(float sv) {
+  const float most = wave_max(fabsf(sv));
+  return most > 0.0f ? uniform(__builtin_amdgcn_frexp_expf(most)) - 6 : 0;
 }
 
 // Products whose operands are read from LDS kAhead ahead (left to itself the
@@ -900,7 +962,8 @@ __device__ __forceinline__ void products(Load load, Product product, Meanwhile m
 
 template <int D, bool PRECISE>
 __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_wide_kernel(AttnArgs a, Cut cut, int blocks) {
-  constexpr int N = PRECISE ? 3 : 1;
+  constexpr int N = PRECISE ? 3 : 1;                  // parts of the queries
+  constexpr int NP = PRECISE ? 3 : 2;                 // bf16 parts of the weights
   constexpr int CH = D / 32;                          // chunks of a row
   constexpr int NS = (2 * kWideStep * CH) / 256;      // chunks a thread opens a step (1: keys or values)
   constexpr int NH = NS > 1 ? NS / 2 : 1;             // of one kind
@@ -908,11 +971,10 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_w
   using L = WideLds<D>;
   extern __shared__ __align__(16) char lds[];
   __shared__ float scale_s[2][2][kWideStep];
-  __shared__ int seen_s[2][kWideStep];
+  __shared__ int unit_s;                // the piece's power of two
+  __shared__ int seen_s[2][kWideStep];  // bit 0: the key is visible; bit 1: fp16 weights do not do for the piece
   __shared__ Line line;
 
-  const int tid = threadIdx.x, lane = tid & (kWave - 1), n = lane & 31, h = lane >> 5;
-  const int wave = uniform(tid / kWave);
   const KvCache& kv = a.cache;
   line_build(a, cut, line);
   const int64_t total = line_total(line);
@@ -921,13 +983,21 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_w
   const int64_t begin_pos = share * blockIdx.x;
   const int64_t end_pos = begin_pos + share < total ? begin_pos + share : total;
   if (begin_pos >= end_pos && int(blockIdx.x) < blocks) write_border(a, blockIdx.x, false, Piece{}, share);
-  for (int64_t pos = begin_pos; pos < end_pos;) {
+  // The piece at pos, with weights in fp16 (false: they do not do for it) or in NP
+  // bf16 parts; moves pos on.
+  auto run = [&](auto half_weights, int64_t& pos) {
+    constexpr bool HALF = decltype(half_weights)::value;
+    // lane numbers of its own for each form, or the compiler computes both forms'
+    // addresses ahead of the loop over pieces and spills them
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));
+    const int lane = tid & (kWave - 1), n = lane & 31, h = lane >> 5;
+    const int wave = uniform(tid / kWave);
     const Piece it = line_find(a, cut, line, pos);
     const int steps = end_pos - pos < it.steps - it.at ? int(end_pos - pos) : it.steps - it.at;
     const bool complete = steps == it.steps;
     const int64_t slot = piece_slot(blockIdx.x, pos == begin_pos);
     if (pos == begin_pos && int(blockIdx.x) < blocks) write_border(a, blockIdx.x, true, it, share);
-    pos += steps;
 
     const int rows = it.r.qn * a.group, row0 = it.tile * kWideRows + wave * 32;
     v8bf q[D / 16][N];
@@ -944,14 +1014,9 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_w
     const Reach reach = wide_reach(a, it, by_units, steps, row0, begin, end);
     const int lo = reach.lo, hi = reach.hi, wave_hi = reach.wave_hi;
 
-    v16f o[D / 32];
-#pragma unroll
-    for (int c = 0; c < D / 32; ++c) o[c] = v16f{};
-    float m = -INFINITY, l = 0.0f;
-
     // staging: the thread's chunks of a step (row my_row + i * rows_apart, chunk my_chunk)
     constexpr int kApart = 256 / CH;
-    const bool half_v = NS == 1 && tid >= 128;  // D = 64: one half of the threads takes keys, the other values
+    const bool half_v = NS == 1 && wave >= 2;  // D = 64: one half of the threads takes keys, the other values
     const int my_row = NS == 1 ? (tid & 127) / CH : tid / CH, my_chunk = tid % CH;
     const float scale2 = a.scale * kLog2e;
     // page ids as they are read, checked where they are used: a check here would wait for them
@@ -991,17 +1056,26 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_w
         scales[1] = kv.v_scales[off];
       }
     };
-    auto store_step = [&](int buf) {
+    v16f o[D / 32];
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) o[c] = v16f{};
+    float m = -INFINITY, l = 0.0f;
+
+    Unit unit{0, float(hi - lo) * 0x1p-16f};
+    auto store_step = [&](int buf, bool first) {
       char* base = lds + buf * L::kBuffer;
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
-        const v32bf x = open_chunk(raw[i]);
         const bool v = NS == 1 ? half_v : i >= NH;
         const int row = my_row + (i % NH) * kApart;
         char* dst = base + (v ? L::kValues + row * L::kValueRow : row * L::kKeyRow);
         const int mix = v ? L::swizzle(row) : 0;
+        auto store_chunk = [&](const auto& x) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) *reinterpret_cast<v8bf*>(dst + 16 * ((4 * my_chunk + pair_order(e)) ^ mix)) = part8(x, e);
+          for (int e = 0; e < 4; ++e) *reinterpret_cast<v8bf*>(dst + 16 * ((4 * my_chunk + pair_order(e)) ^ mix)) = part8(x, e);
+        };
+        if (HALF && v) store_chunk(open_chunk_half(raw[i]));
+        else store_chunk(open_chunk(raw[i]));
       }
       if (tid < kWideStep) {
         // a scale that is not finite makes the key's score NaN (an infinite one
@@ -1009,8 +1083,18 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_w
         // value is itself kept from the rows that do not see the key
         const bool fine = fabsf(scales[0]) < __builtin_huge_valf() && fabsf(scales[1]) < __builtin_huge_valf();
         scale_s[buf][0][tid] = fine ? scales[0] * scale2 : __builtin_nanf("");
-        scale_s[buf][1][tid] = fine ? scales[1] : 0.0f;
-        seen_s[buf][tid] = seen;
+        float sv = fine ? scales[1] : 0.0f;
+        int word = seen;
+        if constexpr (HALF) {
+          if (first) {
+            unit.exp = unit_exponent(seen ? sv : 0.0f);
+            if (tid == 0) unit_s = unit.exp;
+          }
+          sv = seen ? ldexpf(sv, -unit.exp) : 0.0f;
+          if (__ballot(seen && fine && !(fabsf(sv) >= unit.least && fabsf(sv) < 0x1p8f))) word |= 2;
+        }
+        scale_s[buf][1][tid] = sv;
+        seen_s[buf][tid] = word;
       }
     };
 
@@ -1018,7 +1102,7 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_w
       load_ids(lo);
       load_step(lo);
       load_ids(lo + kWideStep);
-      store_step(0);
+      store_step(0, true);
     }
     int buf = 0;
     for (int j0 = lo; j0 < hi; j0 += kWideStep, buf ^= 1) {
@@ -1028,10 +1112,11 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_w
         load_step(j0 + kWideStep);
         load_ids(j0 + 2 * kWideStep);
       }
+      const int word = seen_s[buf][lane];
       if (j0 < wave_hi) {
         const char* kbase = lds + buf * L::kBuffer;
         const char* vbase = kbase + L::kValues;
-        const uint64_t vis = __ballot(seen_s[buf][lane] != 0);
+        const uint64_t vis = __ballot((word & 1) != 0);
         const bool whole = vis == ~uint64_t(0) && j0 >= reach.full_lo && j0 + kWideStep <= reach.full_hi;
         // scores of the step's two 32-key halves
         v16f x[2] = {v16f{}, v16f{}};
@@ -1077,7 +1162,7 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_w
         float top = x[0][0];
 #pragma unroll
         for (int e = 1; e < 32; ++e) top = fmaxf(top, x[e >> 4][e & 15]);
-        const float limit = m == -INFINITY ? -INFINITY : kSlack;
+        const float limit = m == -INFINITY ? -INFINITY : HALF ? kHalfSlack : kSlack;
         if (__ballot(top > limit)) {
           top = fmaxf(top, __shfl_xor(top, 32));
           if (top > limit) {
@@ -1090,14 +1175,19 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_w
             for (int e = 0; e < 32; ++e) x[e >> 4][e & 15] -= top;
           }
         }
-        v8bf pr[4][N];
+        v8bf pr[4][NP];
+        v8h half[4];
         auto probability = [&](int e) {
           const float p = __builtin_amdgcn_exp2f(x[e >> 4][e & 15]);
           l += p;
-          __bf16 part[N];
-          split_bf16<N>(p * scale[e >> 2][e & 3], part);
+          if constexpr (HALF) {
+            half[e >> 3][e & 7] = static_cast<_Float16>(p * scale[e >> 2][e & 3]);  // round to nearest even
+          } else {
+            __bf16 part[NP];
+            split_bf16<NP>(p * scale[e >> 2][e & 3], part);
 #pragma unroll
-          for (int i = 0; i < N; ++i) pr[e >> 3][i][e & 7] = part[i];
+            for (int i = 0; i < NP; ++i) pr[e >> 3][i][e & 7] = part[i];
+          }
         };
 #pragma unroll
         for (int e = 0; e < 16; ++e) probability(e);
@@ -1110,9 +1200,14 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_w
               return lds_transposed(v0, v0 + 8 * L::kValueRow);
             },
             [&](int at, const v8bf& v8) {
+              if constexpr (HALF) {
+                o[at % CH] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, v8), half[at / CH], o[at % CH],
+                                                                    0, 0, 0);
+              } else {
 #pragma unroll
-              for (int i = 0; i < N; ++i)
-                o[at % CH] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v8, pr[at / CH][i], o[at % CH], 0, 0, 0);
+                for (int i = 0; i < NP; ++i)
+                  o[at % CH] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v8, pr[at / CH][i], o[at % CH], 0, 0, 0);
+              }
             },
             [&](int at) {  // the second half's probabilities
               if (at < 2 * CH) {
@@ -1121,10 +1216,24 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_w
               }
             });
       }
-      if (more) store_step(buf ^ 1);
+      if (HALF && (uniform(word) & 2)) return false;
+      if (more) store_step(buf ^ 1, false);
     }
 
-    wide_finish<D>(a, it, o, m, l, complete, slot, wave, n, h);
+    wide_finish<D, HALF>(a, it, o, m, l, HALF ? unit_s : 0, complete, slot, wave, n, h);
+    pos += steps;
+    return true;
+  };
+  bool half = true;
+  for (int64_t pos = begin_pos; pos < end_pos;) {
+    if constexpr (PRECISE) {
+      run(std::false_type{}, pos);
+    } else if (half) {
+      half = run(std::true_type{}, pos);
+    } else {
+      run(std::false_type{}, pos);
+      half = true;
+    }
     __syncthreads();  // the buffers are free for the next piece
   }
 }

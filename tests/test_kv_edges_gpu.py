@@ -74,3 +74,79 @@ def test_attention_scales_that_are_not_finite(D, dtype, rows):
         y, lse2 = y.cpu(), lse2.cpu()
         assert torch.isnan(y[see]).all(), (k_scale, v_scale)
         assert torch.equal(y[~see], x.cpu()[~see]) and torch.equal(lse2[~see], lse.cpu()[~see]), (k_scale, v_scale)
+
+
+def _weights_case(D, sv_of, score_of=None, n=300, q_len=90, unrotate=False, seed=33):
+    """Attention of q_len rows on n keys with the value scales sv_of(rng, n) (and scores steered by score_of), in the
+    kernel for many rows, against the oracle.  Allowed: 2^-11 of each weight (fp16; two bf16 parts are finer), the fp32
+    terms of ku.attention_tolerance and the output's rounding.  What fp16 loses of small weights, 2^-25 a key, is less
+    than 2^-14 of the largest weight in the cases that stay in it (n <= 20000, largest 2^4 or more)."""
+    rng = np.random.default_rng(seed)
+    page = 16
+    pages = -(-n // page)
+    ck, sk = ku.pool(rng, pages, 1, page, D)
+    cv, sv = ku.pool(rng, pages, 1, page, D)
+    sv = sv_of(rng, pages * page).astype(np.float32).reshape(pages, 1, page)
+    if score_of is not None:
+        ck[:] = np.where(rng.random(ck.shape) < 0.5, -1, 1)
+        ck[..., 0] = 7
+        sk[:] = score_of(pages * page).astype(np.float32).reshape(pages, 1, page) / 7
+    q = rng.standard_normal((q_len, 2, D))
+    if score_of is not None:
+        q[:] = 0
+        q[..., 0] = 1  # the score of a key is its score_of
+    q = ku.dev(q.astype(np.float32), BF16)
+    table, cu = np.arange(pages, dtype=np.int32)[None], [0, q_len]
+    scale = 1.0 if score_of is not None else D ** -0.5
+    out, lse = rw4.kv_attention(q, ku.cache_of(ck, sk, cv, sv), ku.dev(table), ku.dev(np.array([n], np.int32)),
+                                ku.dev(np.array(cu, np.int32)), max_q_len=q_len, unrotate=unrotate, scale=scale,
+                                return_lse=True)
+    want, wl, reach, size = okv.kv_attention(ku.np64(q), ck, sk, cv, sv, pages, table, [n], cu, scale, True, 0, unrotate)
+    rel = 2.0 ** -11 + 2 * (D + 8) * ku.U24 * size + (n + 24) * ku.U24
+    tol = rel[..., None] * reach[..., None] + ku.half_step(BF16) * np.abs(want)
+    ku.close(ku.np64(out), want, tol, "out")
+    ku.close(ku.np64(lse), wl, (D + 8) * ku.U24 * size + (64 + n) * ku.U24 + 4 * ku.U24 * np.abs(wl), "lse")
+
+
+@pytest.mark.parametrize("unrotate", [False, True])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_many_rows_keep_their_weights(D, unrotate):
+    _weights_case(D, lambda rng, n: np.exp(0.3 * rng.standard_normal(n)), unrotate=unrotate)
+
+
+def _at(x, where, value):
+    x[where] = value
+    return x
+
+
+VALUE_SCALES = {
+    "tiny": lambda rng, n: 1e-30 * np.exp(0.3 * rng.standard_normal(n)),
+    "huge": lambda rng, n: 1e30 * np.exp(0.3 * rng.standard_normal(n)),
+    "far_apart": lambda rng, n: np.exp(6 * rng.standard_normal(n)),
+    "further_apart": lambda rng, n: np.exp(np.clip(20 * rng.standard_normal(n), -50, 50)),
+    "zeros": lambda rng, n: np.zeros(n),
+    "some_zeros": lambda rng, n: np.exp(0.3 * rng.standard_normal(n)) * (rng.random(n) < 0.7),
+    "first_step_zero": lambda rng, n: _at(np.exp(0.3 * rng.standard_normal(n)), slice(0, 64), 0.0),
+    "first_small": lambda rng, n: _at(np.exp(0.3 * rng.standard_normal(n)), 0, 1e-9),
+    "late_large": lambda rng, n: _at(np.exp(0.3 * rng.standard_normal(n)), n - 90, 3e7),
+    "late_small": lambda rng, n: _at(np.exp(0.3 * rng.standard_normal(n)), n - 60, 1e-12),
+    "rising": lambda rng, n: 2.0 ** (np.arange(n) / 8.0),
+    "falling": lambda rng, n: 2.0 ** (-np.arange(n) / 8.0),
+    "negative": lambda rng, n: np.exp(0.3 * rng.standard_normal(n)) * rng.choice([-1, 1], n),
+}
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("name", VALUE_SCALES)
+def test_attention_many_rows_value_scales_of_any_range(name, D):
+    _weights_case(D, VALUE_SCALES[name])
+
+
+@pytest.mark.parametrize("D,n", [(64, 2000), (128, 2000), (128, 20000)])
+@pytest.mark.parametrize("low", [-8.0, -14.0, -20.0])
+@pytest.mark.parametrize("sink", [1.0, 1e-3, 0.0])
+def test_attention_many_rows_tails_of_small_weights(D, n, low, sink):
+    # one key takes the maximum, the others share what is left of the softmax, e^low each; the first key's value may be
+    # small or zero, so that the tail makes the output
+    _weights_case(D, lambda rng, k: _at(np.exp(0.1 * rng.standard_normal(k)), 0, sink),
+                  lambda k: _at(low + 0.1 * np.sin(np.arange(k)), 0, 0.0), n=n, q_len=66)
