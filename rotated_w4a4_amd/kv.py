@@ -129,14 +129,13 @@ class KVCache:
                 or k_scale.shape != k.shape[:3] or v_scale.shape != k.shape[:3]:
             raise ValueError("k and v must be uint8 [pages, kv_heads, page_size, head_dim / 2] and their scales "
                              "float32 [pages, kv_heads, page_size]")
-        cs, ss = k.stride(), k_scale.stride()
-        if v.stride() != cs or v_scale.stride() != ss or cs[3] != 1:
+        # the stride of a dimension of one entry is not used
+        cs, cv, ss, sv = ([x if n > 1 else 0 for x, n in zip(t.stride(), k.shape[:3])] for t in (k, v, k_scale, v_scale))
+        if cv != cs or sv != ss or k.stride(3) != 1 or v.stride(3) != 1:
             raise ValueError("k and v must have the same strides, with unit stride in a row (their scales likewise)")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.pages, self.kv_heads, self.page_size, half = k.shape
         self.head_dim, self.device = 2 * half, k.device
-        # the stride of a dimension of one entry is not used
-        cs, ss = ([x if n > 1 else 0 for x, n in zip(s, k.shape[:3])] for s in (cs, ss))
         self._struct = _CacheStruct(k.data_ptr(), k_scale.data_ptr(), v.data_ptr(), v_scale.data_ptr(), self.pages,
                                     self.page_size, self.kv_heads, self.head_dim, *cs, *ss)
         self._ptr = ctypes.addressof(self._struct)

@@ -150,3 +150,21 @@ def test_attention_many_rows_tails_of_small_weights(D, n, low, sink):
     # small or zero, so that the tail makes the output
     _weights_case(D, lambda rng, k: _at(np.exp(0.1 * rng.standard_normal(k)), 0, sink),
                   lambda k: _at(low + 0.1 * np.sin(np.arange(k)), 0, 0.0), n=n, q_len=66)
+
+
+def test_cache_of_one_head_or_page_with_other_strides():
+    # the stride of a dimension of one entry says nothing: tensors that differ in it alone are a cache
+    D, page, pages = 64, 16, 3
+    k, v = (torch.zeros((pages, 1, page, D // 2), dtype=torch.uint8, device=ku.DEV) for _ in range(2))
+    ks, vs = torch.zeros((pages, 1, page), device=ku.DEV), torch.zeros((pages, page), device=ku.DEV).unsqueeze(1)
+    v2 = v.squeeze(1).as_strided((pages, 1, page, D // 2), (page * D // 2, 5, D // 2, 1))
+    vs2 = vs.as_strided((pages, 1, page), (page, 77, 1))
+    x = ku.dev(np.random.default_rng(0).standard_normal((pages * page, 1, D)).astype(np.float32))
+    slots = torch.arange(pages * page, device=ku.DEV)
+    for a, b in ((v, vs), (v2, vs2)):
+        cache = rw4.KVCache(k, a, ks, b)
+        rw4.kv_append(cache, x, x, slots)
+        assert torch.equal(cache.k, cache.v) and torch.equal(cache.k_scale, cache.v_scale) and (ks > 0).all()
+        a.zero_()
+    with pytest.raises(ValueError, match="strides"):
+        rw4.KVCache(k, v, ks, torch.zeros((page, pages), device=ku.DEV).t().unsqueeze(1))
