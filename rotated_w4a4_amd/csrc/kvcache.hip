@@ -349,20 +349,62 @@ __device__ __forceinline__ void fast_hadamard(float (&v)[8], const QuantLane& ql
   }
 }
 
+// Whether a row's mean square + eps can be formed from this fp32 sum of squares.
+__device__ __forceinline__ bool squares_fit(float ss, float eps) {
+  return ss <= 0x1p120f && (ss >= 0x1p-100f || eps >= 0x1p-90f);
+}
+
+// The power of two 2^-k that brings a row's largest magnitude into [1/2, 1) (k >=
+// -100, so that eps 4^-k stays in range where squares_fit fails); 0 for rows of
+// zeros, with infinities or NaN.
+template <int L>
+__device__ __forceinline__ int row_exponent(const float (&v)[8]) {
+  float most = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) most = fabsf(v[e]) < __builtin_huge_valf() ? fmaxf(most, fabsf(v[e])) : __builtin_huge_valf();
+  most = row_max<L>(most);
+  const int k = __builtin_amdgcn_frexp_expf(most);
+  return most > 0.0f && most < __builtin_huge_valf() ? (k > -100 ? k : -100) : 0;
+}
+
+// 1 / sqrt(mean square + eps) of a row, times 2^k, from its values times 2^-k.
+template <int L>
+__device__ __forceinline__ float norm_factor(float ss, float eps, int k) {
+  const float x = ss * (1.0f / (8 * L)) + ldexpf(ldexpf(eps, -k), -k);
+  const bool tiny = x < 0x1p-100f;  // below the normal numbers the hardware's estimate is infinite
+  const float y = inv_root(tiny ? x * 0x1p120f : x);
+  return tiny ? y * 0x1p60f : y;
+}
+
 // One dense row (queries; keys without a cache).  The norm's factor is common to
-// the row and enters at the end.
-template <int D, bool BF16>
-__device__ __forceinline__ void dense_row(const RowsArgs& a, const DenseRows& r, const float* weight, int64_t t, int h,
+// the row and enters at the end.  A row whose squares, or sums under the Hadamard,
+// leave fp32's range is left to the RESCALED form, which takes its values times a
+// power of two: returns whether the lane's row is one.
+template <int D, bool BF16, bool RESCALED = false>
+__device__ __forceinline__ bool dense_row(const RowsArgs& a, const DenseRows& r, const float* weight, int64_t t, int h,
                                           bool live, const RopeLane& rope, const QuantLane& ql, int lane, int l) {
   constexpr int L = D / 8;
   float v[8];
   load_row8<BF16>(r.in, t * r.in_token + h * r.in_head + 8 * l, v);
   float post = 1.0f;
+  bool fits = true;
+  int k = 0;
+  if constexpr (RESCALED) {
+    k = row_exponent<L>(v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = ldexpf(v[e], -k);
+  }
   if (weight) {
     float ss = 0.0f, w[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
-    post = inv_root(row_sum<L>(ss) * (1.0f / D) + a.eps);
+    ss = row_sum<L>(ss);
+    if constexpr (RESCALED) {
+      post = norm_factor<L>(ss, a.eps, k);
+    } else {
+      fits = squares_fit(ss, a.eps);
+      post = inv_root(ss * (1.0f / D) + a.eps);
+    }
     load_row8<false>(weight, 8 * l, w);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] *= w[e];
@@ -371,12 +413,25 @@ __device__ __forceinline__ void dense_row(const RowsArgs& a, const DenseRows& r,
   int word = l;
   if (a.rotate) {
     fast_hadamard<D>(v, ql, lane);
+    if (!RESCALED && !weight) {
+      float most = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(v[e]));
+      fits = row_max<L>(most) < __builtin_huge_valf();
+    }
     post *= kHeadPost<D> * ql.sign;
     word = ql.word;
   }
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] *= post;
-  if (live) store_row8(r.out, a.out_bf16, t * r.out_token + h * r.out_head + 8 * word, v);
+  if constexpr (RESCALED) {
+    if (!weight) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = ldexpf(v[e], k);
+    }
+  }
+  if (live && fits) store_row8(r.out, a.out_bf16, t * r.out_token + h * r.out_head + 8 * word, v);
+  return live && !fits;
 }
 
 // The exact codes of one row, in fp64, by the whole wave: lane n has channels
@@ -446,8 +501,10 @@ __device__ __forceinline__ double exact_row(const RowsArgs& a, const void* in, i
 }
 
 // One quantized row into the cache.
-template <int D, bool BF16, bool KEY>
-__device__ __forceinline__ void cache_row(const RowsArgs& a, int64_t t, int h, bool live, int64_t slot, int64_t pos,
+//   A key whose squares leave fp32's range is left to the RESCALED form, which takes
+// its values times a power of two: returns whether the lane's row is one.
+template <int D, bool BF16, bool KEY, bool RESCALED = false>
+__device__ __forceinline__ bool cache_row(const RowsArgs& a, int64_t t, int h, bool live, int64_t slot, int64_t pos,
                                           const RopeLane& rope, const QuantLane& ql, int lane, int l) {
   constexpr int L = D / 8;
   const void* in = KEY ? a.k.in : a.v;
@@ -455,14 +512,27 @@ __device__ __forceinline__ void cache_row(const RowsArgs& a, int64_t t, int h, b
   const float* weight = KEY ? a.k_weight : nullptr;
   const bool roped = KEY && a.cos_sin;
   float v[8], inv = 1.0f;
+  bool fits = true;
+  int k = 0;
   load_row8<BF16>(in, at, v);
+  if constexpr (RESCALED) {
+    k = row_exponent<L>(v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = ldexpf(v[e], -k);
+  }
   if (KEY && weight) {
     // the norm's factor is common to the row: it does not move the codes, so
     // it enters the scale alone
     float ss = 0.0f, w[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
-    inv = inv_root(row_sum<L>(ss) * (1.0f / D) + a.eps);
+    ss = row_sum<L>(ss);
+    if constexpr (RESCALED) {
+      inv = norm_factor<L>(ss, a.eps, k);
+    } else {
+      fits = squares_fit(ss, a.eps);
+      inv = inv_root(ss * (1.0f / D) + a.eps);
+    }
     load_row8<false>(weight, 8 * l, w);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] *= w[e];
@@ -498,7 +568,7 @@ __device__ __forceinline__ void cache_row(const RowsArgs& a, int64_t t, int h, b
   // 2 n 2^-24 with n = 8 additions, 3 products and some room for S itself: 2^-20 (values), 2^-19 (keys)
   const float margin = fmaf(size * r7, KEY ? 0x1p-19f : 0x1p-20f, 0x1p-18f);
   // also where the range of the fp32 steps does not do (zeros are fine), for infinities and NaN
-  uint64_t near = __ballot(!(far < 0.5f - margin) || !(size < 0x1p120f) || (size > 0.0f && m < kTinyMax));
+  uint64_t near = __ballot(!(far < 0.5f - margin) || !(size < 0x1p120f) || (size > 0.0f && (RESCALED || m < kTinyMax)));
   while (near) {  // a row at a time
     constexpr int E = D / 64;
     const int first = (__builtin_ctzll(near) / L) * L;
@@ -520,24 +590,26 @@ __device__ __forceinline__ void cache_row(const RowsArgs& a, int64_t t, int h, b
 #pragma unroll
       for (int e = 0; e < 8; ++e) b[e] = kRoundMagicBits + uint32_t(int(int8_t(got[e / E] >> (8 * (e % E)))));
       word = l;
-      scale = !(top < __builtin_huge_val()) ? __int_as_float(0x7FC00000) : top > 0.0 ? float(top * double(post)) : 0.0f;
+      scale = !(top < __builtin_huge_val()) ? __int_as_float(0x7FC00000) : top > 0.0 ? float(ldexp(top * double(post), -k)) : 0.0f;
     }
   }
   const uint32_t bits = pack8_bits(b, (word & 2) != 0);
-  if (!live) return;
+  if (!live || !fits) return live;
   const KvCache& c = a.cache;
   const int64_t page = slot >> c.log2_page, off = slot & ((int64_t(1) << c.log2_page) - 1);
   *reinterpret_cast<uint32_t*>((KEY ? c.k_codes : c.v_codes) + page * c.code_page + h * c.code_head + off * c.code_slot +
                                4 * word) = bits;
   if (l == 0)
     (KEY ? c.k_scales : c.v_scales)[page * c.scale_page + h * c.scale_head + off * c.scale_slot] = scale;
+  return false;
 }
 
 // A wave takes one token's head groups (64 / L heads of one kind: queries,
 // keys, values) part, part + parts, ...; the rotary factors stay in registers
-// across them.
+// across them.  Five blocks a CU for appends (96 registers): left to itself the
+// compiler takes 103 for the rare paths, and 8191 tokens 51 us for 45.
 template <int D, bool BF16, bool APPEND>
-__global__ __launch_bounds__(256) void kv_rows_kernel(RowsArgs a, int parts) {
+__global__ __launch_bounds__(256, APPEND && D != 256 ? 5 : 1) void kv_rows_kernel(RowsArgs a, int parts) {
   constexpr int L = D / 8, R = kWave / L;
   const int lane = threadIdx.x & (kWave - 1), l = lane & (L - 1);
   const int64_t w =
@@ -564,16 +636,21 @@ __global__ __launch_bounds__(256) void kv_rows_kernel(RowsArgs a, int parts) {
     int h = (kind == 0 ? g : kind == 1 ? g - gq : g - gq - gk) * R + lane / L;
     const bool live = h < heads;
     h = live ? h : heads - 1;
+    auto dense = [&](const DenseRows& r, const float* weight) {
+      const bool left = dense_row<D, BF16>(a, r, weight, t, h, live, rope, ql, lane, l);
+      if (__ballot(left)) dense_row<D, BF16, true>(a, r, weight, t, h, left, rope, ql, lane, l);
+    };
     if (kind == 0) {
-      dense_row<D, BF16>(a, a.q, a.q_weight, t, h, live, rope, ql, lane, l);
-    } else if constexpr (APPEND) {
-      if (!stored) continue;
-      if (kind == 1)
-        cache_row<D, BF16, true>(a, t, h, live, slot, pos, rope, ql, lane, l);
-      else
-        cache_row<D, BF16, false>(a, t, h, live, slot, pos, rope, ql, lane, l);
+      dense(a.q, a.q_weight);
+    } else if (!APPEND) {
+      dense(a.k, a.k_weight);
+    } else if (!stored) {
+      continue;
+    } else if (kind == 1) {
+      const bool left = cache_row<D, BF16, true>(a, t, h, live, slot, pos, rope, ql, lane, l);
+      if (__ballot(left)) cache_row<D, BF16, true, true>(a, t, h, left, slot, pos, rope, ql, lane, l);
     } else {
-      dense_row<D, BF16>(a, a.k, a.k_weight, t, h, live, rope, ql, lane, l);
+      cache_row<D, BF16, false>(a, t, h, live, slot, pos, rope, ql, lane, l);
     }
   }
 }

@@ -168,3 +168,87 @@ def test_cache_of_one_head_or_page_with_other_strides():
         a.zero_()
     with pytest.raises(ValueError, match="strides"):
         rw4.KVCache(k, v, ks, torch.zeros((page, pages), device=ku.DEV).t().unsqueeze(1))
+
+
+# magnitudes of rows, and eps: squares that leave fp32's range at either end
+MAGNITUDES = [(1e19, 1e-6), (3e25, 1e-6), (2e36, 1e-6), (1e-17, 0.0), (1e-25, 0.0), (1e-36, 0.0), (1e-25, 1e-30),
+              (1e-20, 1e-38), (1e-30, 1e-6), (1e18, 1e30)]
+
+
+def _rows_of(seed, T, heads, D, dtype, big):
+    """Rows of magnitude `big`, every third of 1 and one of zeros."""
+    rng = np.random.default_rng(seed)
+    x = rng.standard_normal((T, heads, D)) * np.where(np.arange(T) % 3 == 1, 1.0, big)[:, None, None]
+    x[4] = 0
+    return ku.dev(x.astype(np.float32), dtype)
+
+
+@pytest.mark.parametrize("rotate", [False, True])
+@pytest.mark.parametrize("D,dtype,inter", [(64, BF16, False), (128, F32, False), (128, BF16, True), (256, F32, True)])
+@pytest.mark.parametrize("big,eps", MAGNITUDES)
+def test_norm_of_any_magnitude(big, eps, D, dtype, inter, rotate):
+    # queries and keys through qk_norm_rope (also in place) and kv_append, against the oracle
+    T, hq, hk, page = 11, 6, 3, 16
+    rng = np.random.default_rng(34)
+    q, k = _rows_of(1, T, hq, D, dtype, big), _rows_of(2, T, hk, D, dtype, big)
+    v = _rows_of(3, T, hk, D, dtype, 1.0)
+    w = (1 + 0.3 * rng.standard_normal((2, D))).astype(np.float32)
+    wd = [ku.dev(x) for x in w]
+    cs, pos = rw4.rope_table(50, D // 2), rng.integers(0, 50, T).astype(np.int32)
+    kw = dict(eps=eps, interleaved=inter, rotate=rotate)
+    got = rw4.qk_norm_rope(q, k, wd[0], wd[1], cs, ku.dev(pos), **kw)
+    rows = [t for t in range(T) if eps > 0 or t != 4]  # 0 / 0 otherwise
+    exact = []
+    for x, y, wt in ((q, got[0], w[0]), (k, got[1], w[1])):
+        z, f = okv.norm_rope(ku.np64(x)[rows], wt, float(np.float32(eps)), ku.np64(cs), pos[rows], inter)
+        exact.append((z, f))
+        want = okv.rotate_heads(z * f) if rotate else z * f
+        # as for rows of ordinary size (32 roundings of the row's length and the output's own); below fp32's normal range
+        # the roundings are of 2^-149
+        tol = 32 * ku.U24 * np.linalg.norm(z * f, axis=-1, keepdims=True) + ku.half_step(dtype) * np.abs(want) + 2.0 ** -140
+        ku.close(ku.np64(y)[rows], want, tol, "rows")
+    q2, k2 = q.clone(), k.clone()
+    rw4.qk_norm_rope(q2, k2, wd[0], wd[1], cs, ku.dev(pos), q_out=q2, k_out=k2, **kw)
+    assert torch.equal(q2[rows], got[0][rows]) and torch.equal(k2[rows], got[1][rows])
+    cache = rw4.KVCache.empty(1, page, hk, D)
+    q3 = rw4.kv_append(cache, k, v, torch.arange(T, device=ku.DEV), q, wd[0], wd[1], cs, ku.dev(pos), **kw)
+    assert torch.equal(q3[rows], got[0][rows])
+    z, f = exact[1]
+    c, s = okv.quantize_heads(z, f, rotate)
+    assert np.array_equal(ku.opened(cache.k)[0].transpose(1, 0, 2)[rows], c)
+    ku.close(ku.np64(cache.k_scale)[0].T[rows], s, np.abs(s) * 18 * ku.U24 + 2.0 ** -140, "scale")
+    assert (cache.k_scale[0, :, 4] == 0).all() and (ku.opened(cache.k)[0, :, 4] == 0).all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_rotated_rows_at_the_end_of_the_range(D):
+    # sums under the Hadamard pass fp32's range where the result does not; infinities and NaN stay in their rows
+    T = 6
+    rng = np.random.default_rng(35)
+    x = rng.uniform(0.2, 0.5, (T, 3, D)) * 3e38
+    x[0] = rng.standard_normal((3, D))
+    q = ku.dev(x.astype(np.float32))
+    got = rw4.qk_norm_rope(q, rotate=True)[0]
+    want = okv.rotate_heads(ku.np64(q))
+    fits = np.abs(want) < 3.4e38
+    ku.close(ku.np64(got)[fits], want[fits], (32 * ku.U24 * np.linalg.norm(ku.np64(q), axis=-1, keepdims=True)
+                                              * np.ones(D))[fits], "rows")
+    assert np.isinf(ku.np64(got)[np.abs(want) > 3.42e38]).all()
+    q[2, 1, 3], q[3, 0, 7] = float("inf"), float("nan")
+    bad = rw4.qk_norm_rope(q, rotate=True)[0]
+    assert not torch.isfinite(bad[2, 1]).any() and torch.isnan(bad[3, 0]).all()
+    bad[2, 1], bad[3, 0] = got[2, 1], got[3, 0]
+    assert torch.equal(bad, got)
+
+
+def test_append_special_rows_under_a_norm():
+    D = 128
+    x = np.random.default_rng(36).standard_normal((5, 1, D)).astype(np.float32)
+    x[1, 0, 3], x[2, 0, 9], x[3] = np.inf, np.nan, 0
+    t, w = ku.dev(x), torch.ones(D, device=ku.DEV)
+    for rotate in (False, True):
+        cache = rw4.KVCache.empty(1, 16, 1, D)
+        rw4.kv_append(cache, t, t, torch.arange(5, device=ku.DEV), k_weight=w, rotate=rotate)
+        codes, scale = ku.opened(cache.k)[0, 0], cache.k_scale[0, 0].tolist()
+        assert np.isnan(scale[1]) and np.isnan(scale[2]) and scale[3] == 0 and scale[0] > 0 and scale[4] > 0
+        assert (codes[1:4] == 0).all() and (codes[[0, 4]] != 0).any(-1).all()
