@@ -638,7 +638,7 @@ __global__ __launch_bounds__(256, APPEND && D != 256 ? 5 : 1) void kv_rows_kerne
     h = live ? h : heads - 1;
     auto dense = [&](const DenseRows& r, const float* weight) {
       const bool left = dense_row<D, BF16>(a, r, weight, t, h, live, rope, ql, lane, l);
-      if (__ballot(left)) dense_row<D, BF16, true>(a, r, weight, t, h, left, rope, ql, lane, l);
+      if (__builtin_expect(__ballot(left) != 0, 0)) dense_row<D, BF16, true>(a, r, weight, t, h, left, rope, ql, lane, l);
     };
     if (kind == 0) {
       dense(a.q, a.q_weight);
@@ -648,7 +648,7 @@ __global__ __launch_bounds__(256, APPEND && D != 256 ? 5 : 1) void kv_rows_kerne
       continue;
     } else if (kind == 1) {
       const bool left = cache_row<D, BF16, true>(a, t, h, live, slot, pos, rope, ql, lane, l);
-      if (__ballot(left)) cache_row<D, BF16, true, true>(a, t, h, left, slot, pos, rope, ql, lane, l);
+      if (__builtin_expect(__ballot(left) != 0, 0)) cache_row<D, BF16, true, true>(a, t, h, left, slot, pos, rope, ql, lane, l);
     } else {
       cache_row<D, BF16, false>(a, t, h, live, slot, pos, rope, ql, lane, l);
     }
