@@ -22,4 +22,12 @@ constexpr int clamp_keys(int64_t len, int64_t room) {
 constexpr int ids_ahead(int lane) { return 128 * (lane >> 1) + 16 * (lane & 1); }
 static_assert(kMostKeys <= 0x7FFFFFFF - ids_ahead(63) - 128, "key indexes stay in 32 bits");
 
+// Whether the kernel for many rows gives every block a whole unit instead of
+// cutting the line of all units' steps into equal shares.  That needs `whole` units
+// or more (0: never), so that the grid is full for a while, and no unit that is
+// longer than a share: the last block to start would else run on alone.
+constexpr bool whole_units(int64_t units, int64_t whole, int64_t longest, int64_t steps, int blocks) {
+  return whole > 0 && units >= whole && longest * blocks <= steps;
+}
+
 }  // namespace rw4

@@ -132,10 +132,10 @@ __device__ __forceinline__ void wave_lds_order() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// How a kernel cuts the work: query rows of a unit, keys of a step, and with
-// how many units or more (0: never) every block takes whole units instead.
+// How a kernel cuts the work: query rows of a unit, keys of a step, blocks that
+// share the line, and what whole_units goes by.
 struct Cut {
-  int rows, step, whole;
+  int rows, step, blocks, whole;
 };
 
 // Steps before each thread's requests (256 threads take consecutive ones), and
@@ -143,8 +143,8 @@ struct Cut {
 struct Line {
   long long before[257];
   Req reqs[256];
-  long long wave_sum[4];
-  long long wave_units[4];
+  long long wave_sum[4], wave_units[4];
+  int wave_longest[4];
   bool by_units;  // a step for each unit
 };
 
@@ -157,12 +157,17 @@ __device__ __forceinline__ bool line_build_wave(const AttnArgs& a, const Cut& cu
   if (lane < int(a.B)) r = request(a, lane, cut.rows);
   const int units = r.tiles * a.cache.heads, steps = req_steps(r, cut.step);
   if (__ballot(float(units) * float(steps) > 0x1p24f)) return false;  // sums below 2^30
-  int upto = wave_prefix_dpp(units);
-  const bool by_units = cut.whole > 0 && __builtin_amdgcn_readlane(upto, kWave - 1) >= cut.whole;
-  int own = units;
-  if (!by_units) {
-    own = units * steps;
-    upto = wave_prefix_dpp(own);
+  int own = units * steps, upto = wave_prefix_dpp(own);
+  bool by_units = false;
+  if (cut.whole > 0) {
+    const int upto_units = wave_prefix_dpp(units);
+    // of every lane's request in the place of the longest
+    by_units = !__ballot(!whole_units(__builtin_amdgcn_readlane(upto_units, kWave - 1), cut.whole, units > 0 ? steps : 0,
+                                      __builtin_amdgcn_readlane(upto, kWave - 1), cut.blocks));
+    if (by_units) {
+      own = units;
+      upto = upto_units;
+    }
   }
   line.before[lane] = upto - own;
   line.reqs[lane] = r;
@@ -178,26 +183,40 @@ __device__ __forceinline__ void line_build(const AttnArgs& a, const Cut& cut, Li
   if (B <= kWave && line_build_wave(a, cut, line)) return;
   const int b0 = tid * per < B ? tid * per : B, b1 = b0 + per < B ? b0 + per : B;
   long long sum = 0, units = 0;
+  int longest = 0;
   for (int b = b0; b < b1; ++b) {
     const Req r = request(a, b, cut.rows);
-    sum += (long long)(r.tiles) * a.cache.heads * req_steps(r, cut.step);
+    const int steps = req_steps(r, cut.step);
+    sum += (long long)(r.tiles) * a.cache.heads * steps;
     units += (long long)(r.tiles) * a.cache.heads;
+    if (r.tiles > 0) longest = max(longest, steps);
     if (per == 1) line.reqs[tid] = r;
   }
+  long long upto = wave_prefix(sum, lane), upto_units = 0;
+  if (lane == kWave - 1) line.wave_sum[wave] = upto;
+  if (cut.whole > 0) {
+    upto_units = wave_prefix(units, lane);
+    for (int d = 1; d < kWave; d <<= 1) longest = max(longest, __shfl_xor(longest, d));
+    if (lane == kWave - 1) {
+      line.wave_units[wave] = upto_units;
+      line.wave_longest[wave] = longest;
+    }
+  }
+  __syncthreads();
   bool by_units = false;
   if (cut.whole > 0) {
-    const long long upto_units = wave_prefix(units, lane);
-    if (lane == kWave - 1) line.wave_units[wave] = upto_units;
-    __syncthreads();
-    by_units = line.wave_units[0] + line.wave_units[1] + line.wave_units[2] + line.wave_units[3] >= cut.whole;
-    if (by_units) sum = units;
+    const long long all = line.wave_sum[0] + line.wave_sum[1] + line.wave_sum[2] + line.wave_sum[3];
+    const long long all_units = line.wave_units[0] + line.wave_units[1] + line.wave_units[2] + line.wave_units[3];
+    longest = max(max(line.wave_longest[0], line.wave_longest[1]), max(line.wave_longest[2], line.wave_longest[3]));
+    by_units = whole_units(all_units, cut.whole, longest, all, cut.blocks);
+    if (by_units) {
+      sum = units;
+      upto = upto_units;
+    }
   }
   if (tid == 0) line.by_units = by_units;
-  const long long upto = wave_prefix(sum, lane);
-  if (lane == kWave - 1) line.wave_sum[wave] = upto;
-  __syncthreads();
   long long before = upto - sum;
-  for (int w = 0; w < wave; ++w) before += line.wave_sum[w];
+  for (int w = 0; w < wave; ++w) before += by_units ? line.wave_units[w] : line.wave_sum[w];
   line.before[tid] = before;
   if (tid == 255) line.before[256] = before + sum;
   __syncthreads();
@@ -453,9 +472,9 @@ __global__ __launch_bounds__(256, (kNarrowBlocks<D, PRECISE>)) void kv_attention
   char* vbuf = lds + wave * L::kWaveBytes;
   const KvCache& kv = a.cache;
   __shared__ Line line;
-  constexpr Cut cut{kNarrowRows, kNarrowStep, 0};
+  const Cut cut{kNarrowRows, kNarrowStep, int(gridDim.x), 0};
   line_build(a, cut, line);
-  const int64_t total = line_total(line), share = line_share(total, gridDim.x);
+  const int64_t total = line_total(line), share = line_share(total, cut.blocks);
   const int64_t begin_pos = share * blockIdx.x;
   const int64_t end_pos = begin_pos + share < total ? begin_pos + share : total;
   if (begin_pos >= end_pos) write_border(a, blockIdx.x, false, Piece{}, share);
@@ -724,9 +743,11 @@ __global__ __launch_bounds__(256, (kNarrowBlocks<D, PRECISE>)) void kv_attention
 // ---------------------------------------------------------------------------
 typedef float v16f __attribute__((ext_vector_type(16)));
 
-// Blocks of the grid for each CU.
+// Blocks of the grid for each CU, and with how many units whole ones are taken.
 template <int D, bool PRECISE>
 constexpr int kWideBlocks = (D == 256 || PRECISE) ? 1 : D == 64 ? 3 : 2;
+template <int D, bool PRECISE>
+constexpr int kWhole = 2 * kCUs * kWideBlocks<D, PRECISE>;
 
 template <int D>
 struct WideLds {
@@ -961,7 +982,7 @@ __device__ __forceinline__ void products(Load load, Product product, Meanwhile m
 }
 
 template <int D, bool PRECISE>
-__global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_wide_kernel(AttnArgs a, Cut cut, int blocks) {
+__global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_wide_kernel(AttnArgs a, int blocks) {
   constexpr int N = PRECISE ? 3 : 1;                  // parts of the queries
   constexpr int NP = PRECISE ? 3 : 2;                 // bf16 parts of the weights
   constexpr int CH = D / 32;                          // chunks of a row
@@ -976,13 +997,14 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_w
   __shared__ Line line;
 
   const KvCache& kv = a.cache;
+  const Cut cut{kWideRows, kWideStep, blocks, kWhole<D, PRECISE>};
   line_build(a, cut, line);
   const int64_t total = line_total(line);
   const bool by_units = uniform(int(line.by_units));
-  const int64_t share = by_units ? 1 : line_share(total, blocks);
+  const int64_t share = by_units ? 1 : line_share(total, cut.blocks);
   const int64_t begin_pos = share * blockIdx.x;
   const int64_t end_pos = begin_pos + share < total ? begin_pos + share : total;
-  if (begin_pos >= end_pos && int(blockIdx.x) < blocks) write_border(a, blockIdx.x, false, Piece{}, share);
+  if (begin_pos >= end_pos && int(blockIdx.x) < cut.blocks) write_border(a, blockIdx.x, false, Piece{}, share);
   // The piece at pos, with weights in fp16 (false: they do not do for it) or in NP
   // bf16 parts; moves pos on.
   auto run = [&](auto half_weights, int64_t& pos) {
@@ -997,7 +1019,7 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_w
     const int steps = end_pos - pos < it.steps - it.at ? int(end_pos - pos) : it.steps - it.at;
     const bool complete = steps == it.steps;
     const int64_t slot = piece_slot(blockIdx.x, pos == begin_pos);
-    if (pos == begin_pos && int(blockIdx.x) < blocks) write_border(a, blockIdx.x, true, it, share);
+    if (pos == begin_pos && int(blockIdx.x) < cut.blocks) write_border(a, blockIdx.x, true, it, share);
 
     const int rows = it.r.qn * a.group, row0 = it.tile * kWideRows + wave * 32;
     v8bf q[D / 16][N];
@@ -1368,15 +1390,14 @@ hipError_t launch_wide(const AttnArgs& a, hipStream_t st) {
   static_assert(kWideBlocks<D, PRECISE> <= kWideBlocksMost, "borders and partial results have no room");
   const int full = kCUs * kWideBlocks<D, PRECISE>;
   const int blocks = most < full ? int(most) : full;
-  const Cut cut{kWideRows, kWideStep, 2 * full};
   const auto kernel = kv_attention_wide_kernel<D, PRECISE>;
   const hipError_t set = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, WideLds<D>::kBytes);
   if (set != hipSuccess) return set;
-  hipLaunchKernelGGL(kernel, dim3(unsigned(units > blocks ? units : blocks)), dim3(256), WideLds<D>::kBytes, st, a, cut,
+  hipLaunchKernelGGL(kernel, dim3(unsigned(units > blocks ? units : blocks)), dim3(256), WideLds<D>::kBytes, st, a,
                      blocks);
   const hipError_t e = hipGetLastError();
-  return e != hipSuccess ? e : launch_combine<D, false>(a, kWideRows, kWideStep, blocks, cut.whole, st);
+  return e != hipSuccess ? e : launch_combine<D, false>(a, kWideRows, kWideStep, blocks, kWhole<D, PRECISE>, st);
 }
 
 template <int D>

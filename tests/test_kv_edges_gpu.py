@@ -252,3 +252,38 @@ def test_append_special_rows_under_a_norm():
         codes, scale = ku.opened(cache.k)[0, 0], cache.k_scale[0, 0].tolist()
         assert np.isnan(scale[1]) and np.isnan(scale[2]) and scale[3] == 0 and scale[0] > 0 and scale[4] > 0
         assert (codes[1:4] == 0).all() and (codes[[0, 4]] != 0).any(-1).all()
+
+
+@pytest.mark.parametrize("D,dtype,B", [(64, BF16, 40), (128, BF16, 40), (128, F32, 90), (256, BF16, 40), (256, F32, 40)])
+def test_attention_one_long_request_beside_many_short(D, dtype, B):
+    # units enough for whole ones, but one request far longer than the others: its units are cut
+    rng = np.random.default_rng(37)
+    hk, group, page = 4, 8, 64
+    q_lens = [40] + rng.integers(130, 200, B - 1).tolist()
+    kv_lens = [9000] + q_lens[1:]
+    if B > 64:
+        q_lens[50], kv_lens[50] = 0, 7000  # a long request without queries
+    pages = sum(-(-n // page) for n in kv_lens)
+    table = ku.page_table(rng, kv_lens, page, -(-9000 // page), pages)
+    ck, sk = ku.pool(rng, pages, hk, page, D)
+    cv, sv = ku.pool(rng, pages, hk, page, D)
+    cache = ku.cache_of(ck, sk, cv, sv)
+    cu = np.concatenate([[0], np.cumsum(q_lens)]).astype(np.int32)
+    q = ku.dev(rng.standard_normal((int(cu[-1]), hk * group, D)).astype(np.float32), dtype)
+    td, kd, cd = ku.dev(table), ku.dev(np.array(kv_lens, np.int32)), ku.dev(cu)
+    out, lse = rw4.kv_attention(q, cache, td, kd, cd, max_q_len=max(q_lens), return_lse=True)
+    few, lse2 = rw4.kv_attention(q, cache, td, kd, cd, max_q_len=1, return_lse=True)  # the other kernel
+    mags = rw4.kv_attention(q, ku.cache_of(ck, sk, np.abs(cv), sv), td, kd, cd, max_q_len=1, unrotate=False,
+                            out_dtype=F32)
+    reach = 1.01 * ku.np64(mags).sum(-1) / D ** 0.5
+    size = D ** -0.5 * 7 * float(sk.max()) * ku.np64(q.float().abs().sum(-1))
+    # both sides have the tolerance against the definition
+    tol = 2 * ku.attention_tolerance(ku.np64(few), reach, size, dtype, D, 9000)
+    ku.close(ku.np64(out), ku.np64(few), tol, "kernels")
+    lt = 2 * ((D + 8) * ku.U24 * size + (64 + 4096) * ku.U24 + 4 * ku.U24 * np.abs(ku.np64(lse2)))
+    ku.close(ku.np64(lse), ku.np64(lse2), lt, "lse")
+    for b in (0, B - 1):
+        rows = slice(int(cu[b]), int(cu[b]) + 6)
+        want, wl, reach1, size1 = okv.kv_attention(ku.np64(q[rows]), ck, sk, cv, sv, pages, table[b:b + 1],
+                                                   [kv_lens[b] - q_lens[b] + 6], [0, 6], D ** -0.5, True, 0, True)
+        ku.close(ku.np64(out[rows]), want, ku.attention_tolerance(want, reach1, size1, dtype, D, kv_lens[b]), f"request {b}")

@@ -45,3 +45,16 @@ static_assert(lanes_fit(0x7FFFFF00, int64_t(2048) << 20));
 static_assert(lanes_fit(-5, 64) && lanes_fit(100, 64) && lanes_fit(1 << 20, 0));
 static_assert(clamp_keys(-1, 64) == 0 && clamp_keys(100, 64) == 64 && clamp_keys(63, 64) == 63);
 """)
+
+
+def test_whole_units_only_where_none_outlasts_a_share(tmp_path):
+    _compile(tmp_path, """
+// 4 prompts of 1500..2048 tokens (8 heads, group 4): 1800 units of 24..32 steps on 512 blocks
+static_assert(whole_units(1800, 1024, 32, 1800 * 28, 512));
+static_assert(whole_units(1024, 1024, 32, 1024 * 32, 512));
+static_assert(!whole_units(1023, 1024, 32, 1023 * 32, 512) && !whole_units(1 << 20, 0, 1, 1 << 20, 512));
+// one chunk of 256 tokens on 65536 keys (64 units of 1024 steps) beside 63 prompts of 128 (2016 units of 2): a share
+// is 136 steps, whole units would take 1024
+static_assert(!whole_units(64 + 2016, 1024, 1024, 64 * 1024 + 2016 * 2, 512));
+static_assert(whole_units(int64_t(1) << 40, 1024, 1 << 24, int64_t(1) << 62, 768));
+""")
