@@ -493,8 +493,9 @@ typedef struct {
  *   new_len[b] >= 0  adds that many tokens: the pages it lacks are taken off
  *                    the free list, in request order, and written behind its
  *                    pages in block_table; kv_len[b] = ctx_len + new_len.
- *                    A request whose pages do not fit in table_width is
- *                    refused and takes none; from the first request that
+ *                    A request whose pages do not fit in table_width, or
+ *                    with more than 2^31 - 8192 tokens, is refused and takes
+ *                    none; from the first request that
  *                    the free list cannot give all its pages, every request
  *                    that needs a page is refused.  Refused: kv_len[b] =
  *                    ctx_len[b], its tokens get slot and position -1.
@@ -507,7 +508,7 @@ typedef struct {
  * tail.  The new state goes to free_state_out.
  *   served [B] int32: 1, or 0 where refused; cu_new [B + 1] int32: the
  *   starts of the requests' tokens, cu_new[b + 1] - cu_new[b] =
- *   max(new_len[b], 0), refused requests included;
+ *   max(new_len[b], 0), refused requests included (sums stop at 2^31 - 1);
  *   slot_map [tokens] int64: page * page_size + offset of each new token in
  *   that order; positions [tokens] int32: its place in its request.  Tokens
  *   beyond cu_new[B] get -1 in both, tokens beyond `tokens` are not written.

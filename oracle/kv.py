@@ -35,7 +35,7 @@ def kv_slots(ctx_len, new_len, table, ring, state, page, tokens):
             continue
         want = -(-(ctx + add) // page)
         need = want - have
-        if want > width:
+        if want > width or ctx + add > 2 ** 31 - 8192:
             served[b], kv_len[b] = 0, ctx
             continue
         wanted += need

@@ -6,8 +6,8 @@
 
 namespace rw4 {
 
-// Keys of one request that kv_attention works on, at most (longer lengths are
-// clamped).  The kernels hold key indexes in 32 bits and look up to two steps, or
+// Tokens of one request, at most: kv_slots refuses more, kv_attention clamps longer
+// lengths.  The kernels hold key indexes in 32 bits and look up to two steps, or
 // 32 tiles of page ids, ahead of the last key.
 constexpr int kMostKeys = 0x7FFFFFFF - 8191;
 

@@ -3,6 +3,7 @@
 // norm, rotary positions, Hadamard rotation, INT4 quantization and the store
 // into the cache's pages (qk_norm_rope, kv_append).
 #include "kv_device.h"
+#include "kv_index.h"
 #include "kv_internal.h"
 
 namespace rw4 {
@@ -35,8 +36,8 @@ __device__ __forceinline__ SlotsLens slots_lens(const SlotsArgs& a, int64_t b) {
   r.ctx = a.ctx_len[b] > 0 ? a.ctx_len[b] : 0;
   r.add = a.new_len[b];
   r.have = (r.ctx + page - 1) >> a.log2_page;
-  const int64_t want = (r.ctx + (r.add > 0 ? r.add : 0) + page - 1) >> a.log2_page;
-  r.fits = want <= a.table_width;
+  const int64_t all = r.ctx + (r.add > 0 ? r.add : 0), want = (all + page - 1) >> a.log2_page;
+  r.fits = want <= a.table_width && all <= kMostKeys;
   r.need = r.add >= 0 && r.fits ? want - r.have : 0;
   r.back = r.add >= 0 ? 0 : r.have < a.table_width ? r.have : a.table_width;
   return r;

@@ -287,3 +287,26 @@ def test_attention_one_long_request_beside_many_short(D, dtype, B):
         want, wl, reach1, size1 = okv.kv_attention(ku.np64(q[rows]), ck, sk, cv, sv, pages, table[b:b + 1],
                                                    [kv_lens[b] - q_lens[b] + 6], [0, 6], D ** -0.5, True, 0, True)
         ku.close(ku.np64(out[rows]), want, ku.attention_tolerance(want, reach1, size1, dtype, D, kv_lens[b]), f"request {b}")
+
+
+@pytest.mark.parametrize("new", [3, 4, 5000, 2 ** 31 - 1])
+def test_slots_of_the_longest_requests(new):
+    # requests end at 2^31 - 8192 tokens, what attention works on: more are refused, places stay in 32 bits
+    page, width, most = 1 << 20, 4096, 2 ** 31 - 8192
+    ctx = np.array([most - 3, 5, most - 2 ** 20], np.int32)
+    add = np.array([new, 2, 1], np.int32)
+    table = np.arange(3 * width, dtype=np.int32).reshape(3, width)
+    ring, state = np.arange(20000, 20008, dtype=np.int32), np.array([3, 8], np.int32)
+    tokens = min(new, 5000) + 5
+    want = okv.kv_slots(ctx, add, table, ring, state, page, tokens) if new < 10 ** 6 else None
+    d = [ku.dev(x) for x in (ctx, add, table, ring, state)]
+    got = rw4.kv_slots(*d, page, tokens)
+    torch.cuda.synchronize()
+    assert got.served.tolist() == [int(new == 3), 1, 1]
+    assert got.kv_len.tolist() == [most if new == 3 else most - 3, 7, most - 2 ** 20 + 1]
+    if want is not None:
+        have = [got.kv_len, got.cu_new, got.served, got.slot_map, got.positions, d[2], d[3], got.free_state]
+        for x, y in zip(have, want):
+            assert np.array_equal(x.cpu().numpy(), y)
+    else:
+        assert (got.slot_map == -1).all() and (got.positions == -1).all()
