@@ -6,6 +6,8 @@
 #include "kv_index.h"
 #include "kv_internal.h"
 
+#include <type_traits>
+
 namespace rw4 {
 
 // ---------------------------------------------------------------------------
@@ -656,6 +658,28 @@ __global__ __launch_bounds__(256, APPEND && D != 256 ? 5 : 1) void kv_rows_kerne
   }
 }
 
+// Tokens of one launch, at most: a grid has fewer than 2^32 threads.
+constexpr int64_t kMostTokens = int64_t(1) << 25;
+
+// n tokens from token t on.
+template <bool BF16>
+static RowsArgs rows_from(const RowsArgs& a, int64_t t, int64_t n) {
+  const int64_t in = BF16 ? 2 : 4, out = a.out_bf16 ? 2 : 4;
+  RowsArgs r = a;
+  auto on = [](auto*& p, int64_t bytes) {
+    if (p) p = reinterpret_cast<std::remove_reference_t<decltype(p)>>(reinterpret_cast<uintptr_t>(p) + bytes);
+  };
+  on(r.q.in, t * a.q.in_token * in);
+  on(r.q.out, t * a.q.out_token * out);
+  on(r.k.in, t * a.k.in_token * in);
+  on(r.k.out, t * a.k.out_token * out);
+  on(r.v, t * a.v_token * in);
+  on(r.slot_map, t * int64_t(sizeof(*r.slot_map)));
+  on(r.positions, t * int64_t(sizeof(*r.positions)));
+  r.T = n;
+  return r;
+}
+
 template <int D, bool BF16, bool APPEND>
 static hipError_t launch_rows(const RowsArgs& a, hipStream_t st) {
   constexpr int R = kWave / (D / 8);
@@ -665,10 +689,14 @@ static hipError_t launch_rows(const RowsArgs& a, hipStream_t st) {
   // factors for several groups, with at least 16384 waves in the grid
   int64_t parts = (16384 + a.T - 1) / a.T;
   parts = parts < 1 ? 1 : parts > groups ? groups : parts;
-  const int64_t waves = a.T * parts, blocks = (waves + 3) / 4;
-  if (blocks > 0x1FFFFFFF) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((kv_rows_kernel<D, BF16, APPEND>), dim3(unsigned(blocks)), dim3(256), 0, st, a, int(parts));
-  return hipGetLastError();
+  for (int64_t t = 0; t < a.T; t += kMostTokens) {
+    const RowsArgs some = rows_from<BF16>(a, t, a.T - t < kMostTokens ? a.T - t : kMostTokens);
+    const int64_t blocks = (some.T * parts + 3) / 4;
+    hipLaunchKernelGGL((kv_rows_kernel<D, BF16, APPEND>), dim3(unsigned(blocks)), dim3(256), 0, st, some, int(parts));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <bool APPEND>

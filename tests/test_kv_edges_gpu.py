@@ -310,3 +310,20 @@ def test_slots_of_the_longest_requests(new):
             assert np.array_equal(x.cpu().numpy(), y)
     else:
         assert (got.slot_map == -1).all() and (got.positions == -1).all()
+
+
+def test_append_of_more_tokens_than_a_grid_has_threads():
+    # 2^26 + 70000 tokens, one key and value for all of them; all but a few store nothing
+    D, T, page = 64, 2 ** 26 + 70000, 16
+    rng = np.random.default_rng(38)
+    x = ku.dev(rng.standard_normal((2, 1, D)).astype(np.float32), BF16)
+    k, v = x[:1].expand(T, 1, D), x[1:].expand(T, 1, D)
+    cache, small = rw4.KVCache.empty(2, page, 1, D), rw4.KVCache.empty(2, page, 1, D)
+    slots = torch.full((T,), -1, dtype=torch.int64, device=ku.DEV)
+    for s, t in enumerate((0, 2 ** 25 - 1, 2 ** 25, 2 ** 26, T - 1)):
+        slots[t] = 5 * s
+    rw4.kv_append(cache, k, v, slots)
+    rw4.kv_append(small, k[:5], v[:5], torch.arange(5, device=ku.DEV) * 5)
+    for n in ("k", "v", "k_scale", "v_scale"):
+        assert torch.equal(getattr(cache, n), getattr(small, n)), n
+    assert (cache.k_scale > 0).sum() == 5
