@@ -24,10 +24,17 @@ static_assert(kMostKeys <= 0x7FFFFFFF - ids_ahead(63) - 128, "key indexes stay i
 
 // Whether the kernel for many rows gives every block a whole unit instead of
 // cutting the line of all units' steps into equal shares.  That needs `whole` units
-// or more (0: never), so that the grid is full for a while, and no unit that is
-// longer than a share: the last block to start would else run on alone.
-constexpr bool whole_units(int64_t units, int64_t whole, int64_t longest, int64_t steps, int blocks) {
-  return whole > 0 && units >= whole && longest * blocks <= steps;
+// or more (0: never), so that the grid is full for a while, a grid with a block for
+// each, and no unit that is longer than a share: the last block to start would else
+// run on alone.
+constexpr bool whole_units(int64_t units, int64_t whole, int64_t grid, int64_t longest, int64_t steps, int blocks) {
+  return whole > 0 && units >= whole && units <= grid && longest * blocks <= steps;
+}
+
+// Blocks of the kernel for many rows, for so many units at most: a block for each,
+// or those that share the line where a grid (fewer than 2^32 threads) has no room.
+constexpr int64_t wide_grid(int64_t units, int64_t blocks) {
+  return units > blocks && units < (int64_t(1) << 24) ? units : blocks;
 }
 
 }  // namespace rw4

@@ -162,8 +162,8 @@ __device__ __forceinline__ bool line_build_wave(const AttnArgs& a, const Cut& cu
   if (cut.whole > 0) {
     const int upto_units = wave_prefix_dpp(units);
     // of every lane's request in the place of the longest
-    by_units = !__ballot(!whole_units(__builtin_amdgcn_readlane(upto_units, kWave - 1), cut.whole, units > 0 ? steps : 0,
-                                      __builtin_amdgcn_readlane(upto, kWave - 1), cut.blocks));
+    by_units = !__ballot(!whole_units(__builtin_amdgcn_readlane(upto_units, kWave - 1), cut.whole, gridDim.x,
+                                      units > 0 ? steps : 0, __builtin_amdgcn_readlane(upto, kWave - 1), cut.blocks));
     if (by_units) {
       own = units;
       upto = upto_units;
@@ -208,7 +208,7 @@ __device__ __forceinline__ void line_build(const AttnArgs& a, const Cut& cut, Li
     const long long all = line.wave_sum[0] + line.wave_sum[1] + line.wave_sum[2] + line.wave_sum[3];
     const long long all_units = line.wave_units[0] + line.wave_units[1] + line.wave_units[2] + line.wave_units[3];
     longest = max(max(line.wave_longest[0], line.wave_longest[1]), max(line.wave_longest[2], line.wave_longest[3]));
-    by_units = whole_units(all_units, cut.whole, longest, all, cut.blocks);
+    by_units = whole_units(all_units, cut.whole, gridDim.x, longest, all, cut.blocks);
     if (by_units) {
       sum = units;
       upto = upto_units;
@@ -1394,7 +1394,7 @@ hipError_t launch_wide(const AttnArgs& a, hipStream_t st) {
   const hipError_t set = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, WideLds<D>::kBytes);
   if (set != hipSuccess) return set;
-  hipLaunchKernelGGL(kernel, dim3(unsigned(units > blocks ? units : blocks)), dim3(256), WideLds<D>::kBytes, st, a,
+  hipLaunchKernelGGL(kernel, dim3(unsigned(wide_grid(units, blocks))), dim3(256), WideLds<D>::kBytes, st, a,
                      blocks);
   const hipError_t e = hipGetLastError();
   return e != hipSuccess ? e : launch_combine<D, false>(a, kWideRows, kWideStep, blocks, kWhole<D, PRECISE>, st);

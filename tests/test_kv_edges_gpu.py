@@ -327,3 +327,22 @@ def test_append_of_more_tokens_than_a_grid_has_threads():
     for n in ("k", "v", "k_scale", "v_scale"):
         assert torch.equal(getattr(cache, n), getattr(small, n)), n
     assert (cache.k_scale > 0).sum() == 5
+
+
+def test_attention_of_more_units_than_a_grid_has_blocks():
+    # 16400 requests of a token and 1024 heads each: 2^24 units and more in the kernel for many rows
+    D, heads, page, B = 64, 1024, 16, 16400
+    rng = np.random.default_rng(39)
+    ck, sk = ku.pool(rng, 1, heads, page, D)
+    cv, sv = ku.pool(rng, 1, heads, page, D)
+    cache = ku.cache_of(ck, sk, cv, sv)
+    one = ku.dev(rng.standard_normal((1, heads, D)).astype(np.float32), BF16)
+    lens = np.arange(B) % page + 1
+    args = [ku.dev(np.zeros((B, 1), np.int32)), ku.dev(lens.astype(np.int32)), ku.dev(np.arange(B + 1, dtype=np.int32))]
+    out = rw4.kv_attention(one.expand(B, heads, D), cache, *args, max_q_len=B)
+    some = out[:page]
+    assert torch.equal(out, some.repeat(B // page, 1, 1))
+    q = ku.np64(one.expand(page, heads, D))[:, :8]
+    want, _, reach, size = okv.kv_attention(q, ck[:, :8], sk[:, :8], cv[:, :8], sv[:, :8], 1, np.zeros((page, 1), np.int32),
+                                            lens[:page], np.arange(page + 1), D ** -0.5, True, 0, True)
+    ku.close(ku.np64(some)[:, :8], want, ku.attention_tolerance(want, reach, size, BF16, D, page), "out")

@@ -50,11 +50,15 @@ static_assert(clamp_keys(-1, 64) == 0 && clamp_keys(100, 64) == 64 && clamp_keys
 def test_whole_units_only_where_none_outlasts_a_share(tmp_path):
     _compile(tmp_path, """
 // 4 prompts of 1500..2048 tokens (8 heads, group 4): 1800 units of 24..32 steps on 512 blocks
-static_assert(whole_units(1800, 1024, 32, 1800 * 28, 512));
-static_assert(whole_units(1024, 1024, 32, 1024 * 32, 512));
-static_assert(!whole_units(1023, 1024, 32, 1023 * 32, 512) && !whole_units(1 << 20, 0, 1, 1 << 20, 512));
+static_assert(whole_units(1800, 1024, 1800, 32, 1800 * 28, 512));
+static_assert(whole_units(1024, 1024, 2000, 32, 1024 * 32, 512));
+static_assert(!whole_units(1023, 1024, 2000, 32, 1023 * 32, 512) && !whole_units(1 << 20, 0, 1 << 20, 1, 1 << 20, 512));
 // one chunk of 256 tokens on 65536 keys (64 units of 1024 steps) beside 63 prompts of 128 (2016 units of 2): a share
 // is 136 steps, whole units would take 1024
-static_assert(!whole_units(64 + 2016, 1024, 1024, 64 * 1024 + 2016 * 2, 512));
-static_assert(whole_units(int64_t(1) << 40, 1024, 1 << 24, int64_t(1) << 62, 768));
+static_assert(!whole_units(64 + 2016, 1024, 3000, 1024, 64 * 1024 + 2016 * 2, 512));
+static_assert(whole_units(int64_t(1) << 23, 1024, int64_t(1) << 23, 1 << 24, int64_t(1) << 47, 768));
+// no block for every unit: equal shares; and no grid of 2^32 threads
+static_assert(!whole_units(1801, 1024, 1800, 32, 1801 * 28, 512));
+static_assert(wide_grid(1800, 512) == 1800 && wide_grid(100, 512) == 512 && wide_grid(int64_t(1) << 24, 768) == 768);
+static_assert(256 * wide_grid((int64_t(1) << 24) - 1, 768) < int64_t(1) << 32);
 """)
