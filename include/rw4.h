@@ -574,9 +574,11 @@ rw4_status rw4_kv_append(const rw4_kv_cache* cache_host, const void* k, int64_t 
                          int32_t interleaved, const int32_t* positions, int32_t rotate, void* q_out, int64_t qo_token,
                          int64_t qo_head, rw4_dtype out_dtype, void* stream);
 
-/* Bytes of device workspace rw4_kv_attention needs for T query tokens of B
- * requests (partial results where a long request is split); 0 for invalid
- * sizes. */
+/* Bytes of device workspace rw4_kv_attention needs for up to T query tokens
+ * of B requests (partial results where a long request is split); 0 for
+ * invalid sizes.  It goes by the device, not by the lengths: 7, 13 or 17 MB
+ * at head_dim 64, 128 or 256 for few tokens, 52, 68 or 68 MB where T times
+ * the query heads of a KV head passes 32, 48 or 64. */
 int64_t rw4_kv_attention_workspace_bytes(int64_t T, int64_t B, int32_t heads, int32_t kv_heads, int32_t head_dim);
 
 /* kv_attention: softmax attention of query tokens over the cache.  Request b
@@ -611,7 +613,7 @@ int64_t rw4_kv_attention_workspace_bytes(int64_t T, int64_t B, int32_t heads, in
  * must not overlap q.
  *   workspace: rw4_kv_attention_workspace_bytes bytes, 16-byte aligned,
  *   owned by the caller, overwritten; calls that may overlap in time need
- *   one each. */
+ *   one each, calls in stream order (a model's layers) can share one. */
 rw4_status rw4_kv_attention(const rw4_kv_cache* cache_host, const void* q, rw4_dtype q_dtype, int64_t q_token,
                             int64_t q_head, int64_t T, int32_t heads, const int32_t* block_table, int64_t table_width,
                             const int32_t* kv_len, const int32_t* cu_q, int64_t B, int64_t max_q_len, float scale,

@@ -795,7 +795,7 @@ static bool attention_sizes_ok(int64_t T, int64_t B, int32_t heads, int32_t kv_h
 
 int64_t rw4_kv_attention_workspace_bytes(int64_t T, int64_t B, int32_t heads, int32_t kv_heads, int32_t head_dim) {
   if (!attention_sizes_ok(T, B, heads, kv_heads, head_dim)) return 0;
-  return rw4::kv_attention_workspace_bytes(T, B, heads, kv_heads, head_dim);
+  return rw4::kv_attention_workspace_bytes(T, heads, kv_heads, head_dim);
 }
 
 rw4_status rw4_kv_attention(const rw4_kv_cache* cache_host, const void* q, rw4_dtype q_dtype, int64_t q_token,
@@ -820,7 +820,7 @@ rw4_status rw4_kv_attention(const rw4_kv_cache* cache_host, const void* q, rw4_d
   if (!kv_len || !cu_q || (table_width > 0 && !block_table)) return RW4_ERR_ARG;
   if (!workspace || !aligned16(workspace) ||
       workspace_bytes <
-          rw4::kv_attention_workspace_bytes(T, B, heads, cache_host->heads, cache_host->head_dim))
+          rw4::kv_attention_workspace_bytes(T, heads, cache_host->heads, cache_host->head_dim))
     return RW4_ERR_ARG;
   a.q = q;
   a.q_token = q_token;

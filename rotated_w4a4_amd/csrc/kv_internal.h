@@ -88,7 +88,7 @@ hipError_t launch_kv_slots(const SlotsArgs& a, hipStream_t st);
 hipError_t launch_qk_norm_rope(const RowsArgs& a, bool x_bf16, hipStream_t st);
 hipError_t launch_kv_append(const RowsArgs& a, bool x_bf16, hipStream_t st);
 
-int64_t kv_attention_workspace_bytes(int64_t T, int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim);
+int64_t kv_attention_workspace_bytes(int64_t T, int64_t heads, int64_t kv_heads, int64_t head_dim);
 hipError_t launch_kv_attention(const AttnArgs& a, hipStream_t st);
 
 }  // namespace rw4

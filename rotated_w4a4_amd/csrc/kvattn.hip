@@ -52,7 +52,7 @@ constexpr int kCUs = 256;
 constexpr int kNarrowRows = 16;
 constexpr int kNarrowStep = 128;  // keys of a step: 32 for each of a block's 4 waves
 constexpr int kWideRows = 128, kWideStep = 64;
-// Blocks of a grid for each CU, at most: the workspace has room for these.
+// Blocks of a grid for each CU, at most: the workspace has room for the borders of these.
 constexpr int kNarrowBlocksMost = 3, kWideBlocksMost = 3;
 constexpr int kMaxBlocks = kCUs * (kNarrowBlocksMost > kWideBlocksMost ? kNarrowBlocksMost : kWideBlocksMost);
 // Up to this many rows of a request the kernel for few rows is used.  Measured
@@ -1348,6 +1348,8 @@ __global__ __launch_bounds__(256) void kv_attention_combine_kernel(AttnArgs a, i
   }
 }
 
+constexpr int most_of(int a, int b) { return a > b ? a : b; }
+
 // Units and steps a call can have at most, as far as the host knows.
 int64_t units_max(const AttnArgs& a, int rows) {
   return a.cache.heads * (a.T * a.group / rows + (a.B < a.T ? a.B : a.T));
@@ -1411,11 +1413,25 @@ hipError_t launch_head(const AttnArgs& a, hipStream_t st) {
 
 }  // namespace
 
-int64_t kv_attention_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t head_dim) {
-  const int64_t narrow = int64_t(kCUs) * kNarrowBlocksMost * kNarrowRows;
-  const int64_t wide = int64_t(kCUs) * kWideBlocksMost * kWideRows;
+namespace {
+
+// Borders, and two partial results for each block of the largest grid that such a
+// call can get: launch_head takes the kernel for few rows whatever the types where a
+// call has that few.
+template <int D>
+int64_t workspace_bytes(int64_t rows) {
+  const int64_t narrow = int64_t(kCUs) * most_of(kNarrowBlocks<D, false>, kNarrowBlocks<D, true>) * kNarrowRows;
+  const int64_t wide = int64_t(kCUs) * most_of(kWideBlocks<D, false>, kWideBlocks<D, true>) * kWideRows;
+  const bool few = rows <= kNarrowMost<D, false> && rows <= kNarrowMost<D, true>;
   return kMaxBlocks * int64_t(sizeof(Border)) +
-         2 * (narrow > wide ? narrow : wide) * (head_dim + 2) * int64_t(sizeof(float));
+         2 * (few || narrow > wide ? narrow : wide) * (D + 2) * int64_t(sizeof(float));
+}
+
+}  // namespace
+
+int64_t kv_attention_workspace_bytes(int64_t T, int64_t heads, int64_t kv_heads, int64_t head_dim) {
+  const int64_t rows = T * (heads / kv_heads);
+  return head_dim == 64 ? workspace_bytes<64>(rows) : head_dim == 128 ? workspace_bytes<128>(rows) : workspace_bytes<256>(rows);
 }
 
 hipError_t launch_kv_attention(const AttnArgs& a, hipStream_t st) {

@@ -354,7 +354,10 @@ def kv_attention(q, cache: KVCache, block_table, kv_len, cu_q, *, max_q_len=None
 def prepare_kv_attention(q, cache: KVCache, block_table, kv_len, cu_q, *, max_q_len=None, scale=None,
                          causal: bool = True, window: int = 0, unrotate: bool = True, out=None, out_dtype=None,
                          return_lse: bool = False, lse=None, workspace=None) -> Call:
-    """kv_attention checked and marshalled once, with a workspace of its own; calling the result runs it."""
+    """kv_attention checked and marshalled once; calling the result runs it.
+
+    Without `workspace` it has one of its own (7 to 68 MB, kv_attention_workspace_bytes), so do not let two runs of it
+    overlap in time (two streams, two graphs); prepared calls that run one after the other can be given one together."""
     return KVCall(*_attention(q, cache, block_table, kv_len, cu_q, max_q_len, scale, causal, window, unrotate, out,
                               out_dtype, return_lse, lse, workspace))
 

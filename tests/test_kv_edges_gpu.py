@@ -346,3 +346,30 @@ def test_attention_of_more_units_than_a_grid_has_blocks():
     want, _, reach, size = okv.kv_attention(q, ck[:, :8], sk[:, :8], cv[:, :8], sv[:, :8], 1, np.zeros((page, 1), np.int32),
                                             lens[:page], np.arange(page + 1), D ** -0.5, True, 0, True)
     ku.close(ku.np64(some)[:, :8], want, ku.attention_tolerance(want, reach, size, BF16, D, page), "out")
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("q_lens,hint", [([1], 1), ([8], 8), ([1] * 40, 1), ([1] * 40, 40), ([70, 9, 200], 200),
+                                         ([70, 9, 200], 1)])
+def test_attention_stays_in_its_workspace(D, dtype, q_lens, hint):
+    # cut units in a workspace of exactly the bytes asked for: what lies behind it stays
+    rng = np.random.default_rng(40)
+    hk, group, page, n = 2, 4, 64, 8000
+    pages, B, T = n // page, len(q_lens), sum(q_lens)
+    ck, sk = ku.pool(rng, pages, hk, page, D)
+    cv, sv = ku.pool(rng, pages, hk, page, D)
+    table = ku.dev(np.stack([rng.permutation(pages) for _ in range(B)]).astype(np.int32))
+    lens = ku.dev((n - rng.integers(0, 500, B)).astype(np.int32))
+    cu = ku.dev(np.concatenate([[0], np.cumsum(q_lens)]).astype(np.int32))
+    q = ku.dev(rng.standard_normal((T, hk * group, D)).astype(np.float32), dtype)
+    nbytes = rw4.kv_attention_workspace_bytes(T, B, hk * group, hk, D)
+    room = torch.full((nbytes + 4096,), 0xA5, dtype=torch.uint8, device=ku.DEV)
+    cache = ku.cache_of(ck, sk, cv, sv)
+    got = rw4.kv_attention(q, cache, table, lens, cu, max_q_len=hint, workspace=room[:nbytes])
+    assert (room[nbytes:] == 0xA5).all() and (room[:nbytes] != 0xA5).any()
+    room.fill_(0xFF)  # and nothing in it is read before it is written
+    assert torch.equal(rw4.kv_attention(q, cache, table, lens, cu, max_q_len=hint, workspace=room[:nbytes]), got)
+    assert torch.isfinite(got).all() and (room[nbytes:] == 0xFF).all()
+    with pytest.raises(ValueError, match="workspace"):
+        rw4.kv_attention(q, cache, table, lens, cu, workspace=room[:nbytes - 16])
