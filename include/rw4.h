@@ -578,7 +578,7 @@ rw4_status rw4_kv_append(const rw4_kv_cache* cache_host, const void* k, int64_t 
  * of B requests (partial results where a long request is split); 0 for
  * invalid sizes.  It goes by the device, not by the lengths: 7, 13 or 17 MB
  * at head_dim 64, 128 or 256 for few tokens, 52, 68 or 68 MB where T times
- * the query heads of a KV head passes 32, 48 or 64. */
+ * the query heads of a KV head passes 32, 48 or 48. */
 int64_t rw4_kv_attention_workspace_bytes(int64_t T, int64_t B, int32_t heads, int32_t kv_heads, int32_t head_dim);
 
 /* kv_attention: softmax attention of query tokens over the cache.  Request b

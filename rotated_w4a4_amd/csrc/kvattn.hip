@@ -55,13 +55,18 @@ constexpr int kWideRows = 128, kWideStep = 64;
 // Blocks of a grid for each CU, at most: the workspace has room for the borders of these.
 constexpr int kNarrowBlocksMost = 3, kWideBlocksMost = 3;
 constexpr int kMaxBlocks = kCUs * (kNarrowBlocksMost > kWideBlocksMost ? kNarrowBlocksMost : kWideBlocksMost);
-// Up to this many rows of a request the kernel for few rows is used.  Measured
-// on 32 requests of 4000 keys and 8 KV heads (few / many rows, us): D = 128 bf16
-// 48 rows 82 / 87, 64 rows 120 / 88; D = 64 16 rows 38 / 52, 32 rows 56 / 53, 48
-// rows 63 / 60; D = 256 48 rows 178 / 200, 64 rows 202 / 198, 96 rows 289 / 204;
-// fp32 64 rows 149 / 188, 96 rows 215 / 192.
+// Up to this many rows of a request the kernel for few rows is used.  Measured on
+// requests of 4000 keys and 8 KV heads, few / many rows, us:
+//               batch of 32                          batch of 4
+//   D = 128     32 rows 71 / 80, 48 82 / 90,         31 / 29, 31 / 32,
+//               64 118 / 89                          36 / 33
+//   D = 64      32 rows 55 / 56, 48 63 / 61          23 / 25, 25 / 27
+//   D = 256     48 rows 173 / 182, 64 191 / 175      52 / 43, 51 / 44
+//   fp32, 128   64 rows 144 / 176, 96 210 / 179      37 / 45, 50 / 47
+//   fp32, 64    64 rows 118 / 125, 96 174 / 126      29 / 32, 40 / 33
+//   fp32, 256   48 rows 258 / 297, 64 335 / 297      57 / 69, 59 / 69
 template <int D, bool PRECISE>
-constexpr int kNarrowMost = D == 256 || PRECISE ? 64 : D == 128 ? 48 : 32;
+constexpr int kNarrowMost = PRECISE ? 64 : D == 64 ? 32 : 48;
 
 // ---------------------------------------------------------------------------
 // The line of work.

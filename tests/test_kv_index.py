@@ -67,7 +67,7 @@ static_assert(256 * wide_grid((int64_t(1) << 24) - 1, 768) < int64_t(1) << 32);
 def test_workspace_goes_by_the_kernels_a_call_can_get():
     rw4 = pytest.importorskip("rotated_w4a4_amd", reason="librw4.so not built")
     ws = rw4.lib.rw4_kv_attention_workspace_bytes
-    for D, few, few_mb, mb in ((64, 32, 7, 52), (128, 48, 13, 69), (256, 64, 17, 68)):
+    for D, few, few_mb, mb in ((64, 32, 7, 52), (128, 48, 13, 69), (256, 48, 17, 68)):
         rows = few // 4
         assert ws(1, 1, 32, 8, D) == ws(rows, rows, 32, 8, D) <= few_mb * 10 ** 6
         assert ws(1, 1, 32, 8, D) < ws(rows + 1, 1, 32, 8, D) == ws(10 ** 6, 9, 32, 8, D) <= mb * 10 ** 6
