@@ -604,7 +604,9 @@ int64_t rw4_kv_attention_workspace_bytes(int64_t T, int64_t B, int32_t heads, in
  *   (*_token, *_head), 16-byte aligned heads; lse fp32 [T, heads] or NULL;
  *   block_table int32 [B][table_width]; kv_len int32 [B]; cu_q int32 [B+1].
  *   max_q_len: the largest number of query tokens of a request; chooses the
- *   kernel, and with it the roundings above, nothing else.  window > 0 needs causal.
+ *   kernel (for few rows a request or for many, for the whole call), and with
+ *   it the roundings above, nothing else.  Both are right for any lengths; the
+ *   one for many rows takes 2 to 4 times as long on single tokens.  window > 0 needs causal.
  *   B <= 65535; heads a multiple of the cache heads, at most 64 query heads
  *   per KV head; T * heads <= 2^30; scale finite.
  * Checked in the kernel: kv_len is clamped to [0, table_width * page_size]

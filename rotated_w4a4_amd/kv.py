@@ -3,7 +3,13 @@
     cache = KVCache.empty(pages, page_size, kv_heads, head_dim, "cuda")
     step = kv_slots(ctx_len, new_len, block_table, free_pages, free_state, page_size, tokens)
     q = kv_append(cache, k, v, step.slot_map, q, q_weight, k_weight, cos_sin, step.positions)
-    o = kv_attention(q, cache, block_table, step.kv_len, step.cu_new)
+    o = kv_attention(q, cache, block_table, step.kv_len, step.cu_new, max_q_len=largest)
+
+where `largest` is the largest number of new tokens of a request (1 in a decode step), which chooses the kernel.
+
+Rows that a call skips (padding of a batch: no position, no slot, no request) are left as they were.  In an output
+that the binding allocates that is whatever the memory held before, so where such rows go on into a call that mixes
+tokens (the Rotated Runtime Smooth quantizer's maxima), pass an output that was filled (`q_out`, `out`).
 
 Marshalling and argument checks only, like the rest of the package; every
 call has a prepare_ form that checks once and launches again on each call.
@@ -236,7 +242,8 @@ def qk_norm_rope(q, k=None, q_weight=None, k_weight=None, cos_sin=None, position
     """Per-head RMS norm (weights fp32 [D], None: no norm) and rotary positions (cos_sin [max_pos, rot], None: none)
     of queries [T, heads, D] and keys [T, kv_heads, D] in one pass, then the head's Hadamard when `rotate`.
 
-    Returns (q_out, k_out); with q_out = q and k_out = k in place.  k may be None."""
+    Returns (q_out, k_out); with q_out = q and k_out = k in place.  k may be None.  Rows of tokens without a position are
+    not written."""
     fn, args, dev, what, _, result = _norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved, rotate,
                                                 q_out, k_out, out_dtype)
     _launch(fn, args, dev, what)
@@ -283,7 +290,8 @@ def kv_append(cache: KVCache, k, v, slot_map, q=None, q_weight=None, k_weight=No
               eps: float = 1e-6, interleaved: bool = False, rotate: bool = True, q_out=None, out_dtype=None):
     """New tokens into the cache: keys [T, kv_heads, D] normed and given their positions (as qk_norm_rope), keys and
     values rotated by the head's Hadamard (`rotate`) and stored as INT4 in rows slot_map (int64 [T]).  Queries, if
-    given, go through qk_norm_rope in the same launch; returns q_out (None without q)."""
+    given, go through qk_norm_rope in the same launch; returns q_out (None without q; rows of tokens without a position
+    are not written)."""
     fn, args, dev, what, _, result = _append(cache, k, v, slot_map, q, q_weight, k_weight, cos_sin, positions, eps,
                                              interleaved, rotate, q_out, out_dtype)
     _launch(fn, args, dev, what)
@@ -342,9 +350,13 @@ def kv_attention(q, cache: KVCache, block_table, kv_len, cu_q, *, max_q_len=None
     first kv_len[b] cached tokens, in the pages block_table[b].
 
     causal: a request's queries are its last tokens; window > 0: the last `window` keys only.  scale defaults to
-    1 / sqrt(D); unrotate applies the head's Hadamard to the output (for a cache of rotated values).  max_q_len (the
-    largest number of query tokens of a request, default all) only chooses the kernel.  Returns out [T, heads, D],
-    with return_lse (out, lse fp32 [T, heads]).  A row that sees no key gives 0 and -inf."""
+    1 / sqrt(D); unrotate applies the head's Hadamard to the output (for a cache of rotated values).  Returns out [T,
+    heads, D], with return_lse (out, lse fp32 [T, heads]).  A row that sees no key gives 0 and -inf, one of no request is
+    not written.
+
+    max_q_len is the largest number of query tokens of a request (default: all tokens).  It chooses the kernel for the
+    whole call and nothing else, but say it: a decode step of 32 requests without it takes the kernel for many rows, 2 to
+    4 times as long, and so do single tokens in one call with a prompt's chunk; two calls can be the faster way there."""
     fn, args, dev, what, _, result = _attention(q, cache, block_table, kv_len, cu_q, max_q_len, scale, causal, window,
                                                 unrotate, out, out_dtype, return_lse, lse, workspace)
     _launch(fn, args, dev, what)
