@@ -609,10 +609,11 @@ __device__ __forceinline__ bool cache_row(const RowsArgs& a, int64_t t, int h, b
 
 // A wave takes one token's head groups (64 / L heads of one kind: queries,
 // keys, values) part, part + parts, ...; the rotary factors stay in registers
-// across them.  Five blocks a CU for appends (96 registers): left to itself the
-// compiler takes 103 for the rare paths, and 8191 tokens 51 us for 45.
+// across them.  Registers for 8 blocks a CU for dense rows, 5 for appends of 128: left
+// to itself the compiler takes more for the rare paths, and 8191 tokens into a cache
+// 68 us for 60, dense rows of 12001 tokens 58 for 54.
 template <int D, bool BF16, bool APPEND>
-__global__ __launch_bounds__(256, APPEND && D != 256 ? 5 : 1) void kv_rows_kernel(RowsArgs a, int parts) {
+__global__ __launch_bounds__(256, APPEND ? (D == 128 ? 5 : 1) : 8) void kv_rows_kernel(RowsArgs a, int parts) {
   constexpr int L = D / 8, R = kWave / L;
   const int lane = threadIdx.x & (kWave - 1), l = lane & (L - 1);
   const int64_t w =
@@ -641,7 +642,12 @@ __global__ __launch_bounds__(256, APPEND && D != 256 ? 5 : 1) void kv_rows_kerne
     h = live ? h : heads - 1;
     auto dense = [&](const DenseRows& r, const float* weight) {
       const bool left = dense_row<D, BF16>(a, r, weight, t, h, live, rope, ql, lane, l);
-      if (__builtin_expect(__ballot(left) != 0, 0)) dense_row<D, BF16, true>(a, r, weight, t, h, left, rope, ql, lane, l);
+      if (__builtin_expect(__ballot(left) != 0, 0)) {
+        int lane2 = lane;
+        asm volatile("" : "+v"(lane2));  // keeps the rare form's lane constants out of the common one's registers
+        const int l2 = lane2 & (L - 1);
+        dense_row<D, BF16, true>(a, r, weight, t, h, left, rope, quant_lane<D>(l2), lane2, l2);
+      }
     };
     if (kind == 0) {
       dense(a.q, a.q_weight);
