@@ -597,7 +597,9 @@ int64_t rw4_kv_attention_workspace_bytes(int64_t T, int64_t B, int32_t heads, in
  * lse or leaves it as it is.  Queries are in
  * the rotated domain when the cache is (kv_append's or qk_norm_rope's rotate,
  * or rw4_rotate_act).  causal = 0 is attention to another sequence's states.
- * Scores, softmax and sums are fp32.  Probabilities enter the product with
+ * Scores, softmax and sums are fp32, and have to stay in its range: the
+ * scores, and 2^11 kv_len times the largest value scale (sums before their
+ * division by the softmax's).  Probabilities enter the product with
  * the values as three bf16 parts (exact) when the queries or the output are
  * fp32, else as one fp16 number (2^-11 of each) or two bf16 parts (2^-16).
  *   q, out [T, heads, head_dim] of q_dtype / out_dtype, strides in elements

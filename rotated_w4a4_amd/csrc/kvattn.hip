@@ -445,7 +445,7 @@ __device__ __forceinline__ void finish_row(const AttnArgs& a, int q0, int qn, in
 // the exchange across lanes that finds the maximum) is left out.
 //
 // Bound by memory: 64 requests of up to 16384 keys (8 KV heads of 128, 571 MB)
-// take 130-136 us, 4.2-4.4 TB/s; the same loads without any arithmetic 114 us.
+// take 132-147 us on different cards, 3.9-4.3 TB/s; the same loads without any arithmetic 114 us.
 // 128-key steps with each wave's own 32 keys need no barrier, so loads of the
 // next tile fly over all of a tile's work; 3 blocks a CU by registers and LDS (4
 // spill: 275 us).
@@ -740,9 +740,10 @@ __global__ __launch_bounds__(256, (kNarrowBlocks<D, PRECISE>)) void kv_attention
 // Bound by the softmax's vector work beside the products (a step of 32 x 64
 // scores at D = 128: 32 products of 32 cycles, 32 exponentials of 16 and about
 // 200 other vector instructions of 4) and by the start and end of units: 4
-// prompts of 1500-2048 tokens (32 heads of 128) 154 us, 670 TFLOP/s of what is
-// visible; at D = 64, 6 chunks on up to 12000 keys, 70 us, 450 TFLOP/s.  64 rows
-// a wave (1 wave a SIMD) took 287 us where this took 205; blocks of 8 waves
+// prompts of 1500-2048 tokens (32 heads of 128) 154 us, 668 TFLOP/s of what is
+// visible; at D = 64, 6 chunks on up to 12000 keys, 73 us, 424 TFLOP/s (3 blocks a
+// CU spill 35 registers, hardly in the loop; 2, without, 91 us where 3 take 85).  64
+// rows a wave (1 wave a SIMD) took 287 us where this took 205; blocks of 8 waves
 // whose halves take turns at products and softmax 157 us against 154, as one
 // block a CU leaves the starts and ends of its units uncovered.
 // ---------------------------------------------------------------------------

@@ -199,8 +199,9 @@ hipError_t launch_kv_slots(const SlotsArgs& a, hipStream_t st) {
 // own (of at most 7).  Where a quotient lies that close to a half (1 % of the
 // rows of 128 Gaussian values), the wave evaluates its rows again in fp64, in
 // which the sums of bf16 values are exact.  8191 tokens (32 + 8 + 8 heads of 128)
-// take 58 us, bound by vector arithmetic (68 % busy, about 170 instructions for
-// a lane's 8 channels); 80 us with every row in fp64.  Dense rows of 12001 tokens
+// take 60 us, bound by vector arithmetic (71 % busy, about 170 instructions for
+// a lane's 8 channels) and the waits for a group of heads that is loaded when the
+// one before is stored; 80 us with every row in fp64.  Dense rows of 12001 tokens
 // take 45 us, 5.6 TB/s.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ float lane_get(float v, int src) {
