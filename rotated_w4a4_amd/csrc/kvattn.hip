@@ -941,16 +941,16 @@ __device__ __forceinline__ void wide_finish(const AttnArgs& a, const Piece& it, 
 //   fp16 has 11 bits from 2^-14 to 2^16 and loses at most 2^-25 of what is smaller,
 // so a piece's scales are multiplied by a power of two, which is exact: 2^-unit puts
 // the largest of its first step into [2^5, 2^6).  If all of the piece's n keys then
-// have a scale in [n 2^-16, 2^8), no weight passes 2^15 (p <= 2^kHalfSlack), each
-// row has one of n 2^-16 or more (its largest p is at least 1), and what n keys
-// lose, 2^-25 each, is at most 2^-9 of that, and that only if all lie below fp16's
-// normal range.  At the first step with a key outside of the range (a value of
+// have a scale in [max(n 2^-16, 2^-14), 2^8), no weight passes 2^15 (p <=
+// 2^kHalfSlack), each row has one of that much or more (its largest p is at least
+// 1), and what n keys lose, 2^-25 each, is at most 2^-9 of it, and that only if all
+// others lie below fp16's normal range.  At the first step with a key outside of the range (a value of
 // zeros, say) the piece starts again with weights of two bf16 parts, which need
 // none; a prompt of such keys alone takes 194 us.
 // ---------------------------------------------------------------------------
 struct Unit {
   int exp;
-  float least;  // n 2^-16
+  float least;  // n 2^-16, 2^-14 at least
 };
 
 // The largest v >= 0 of a wave's lanes.
@@ -1089,7 +1089,7 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_w
     for (int c = 0; c < D / 32; ++c) o[c] = v16f{};
     float m = -INFINITY, l = 0.0f;
 
-    Unit unit{0, float(hi - lo) * 0x1p-16f};
+    Unit unit{0, fmaxf(float(hi - lo) * 0x1p-16f, 0x1p-14f)};
     auto store_step = [&](int buf, bool first) {
       char* base = lds + buf * L::kBuffer;
 #pragma unroll

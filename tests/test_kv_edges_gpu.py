@@ -373,3 +373,23 @@ def test_attention_stays_in_its_workspace(D, dtype, q_lens, hint):
     assert torch.isfinite(got).all() and (room[nbytes:] == 0xFF).all()
     with pytest.raises(ValueError, match="workspace"):
         rw4.kv_attention(q, cache, table, lens, cu, workspace=room[:nbytes - 16])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("ratio", range(17, 24))
+def test_attention_many_rows_first_row_of_a_small_value(D, ratio):
+    # two keys, the first row sees the one with a value 2^ratio times smaller alone: 11 bits of it all the same
+    rng = np.random.default_rng(41)
+    page, heads, seeds = 16, 64, 40
+    pages = seeds
+    ck, sk = ku.pool(rng, pages, 1, page, D)
+    cv, sv = ku.pool(rng, pages, 1, page, D)
+    sv[:, 0, 0] = 2.0 ** -ratio * rng.uniform(1, 2, seeds)
+    sv[:, 0, 1] = rng.uniform(1, 2, seeds)
+    q = ku.dev(rng.standard_normal((2 * seeds, heads, D)).astype(np.float32), BF16)
+    table, lens, cu = np.arange(pages, dtype=np.int32)[:, None], np.full(seeds, 2, np.int32), 2 * np.arange(seeds + 1)
+    out = ku.np64(rw4.kv_attention(q, ku.cache_of(ck, sk, cv, sv), ku.dev(table), ku.dev(lens),
+                                   ku.dev(cu.astype(np.int32)), max_q_len=2, unrotate=False))[::2]
+    want = (cv[:, 0, 0].astype(np.float64) * sv[:, 0, 0].astype(np.float64)[:, None])[:, None, :]
+    tol = (2.0 ** -11 + 2 * ku.U24) * np.abs(want).max(-1, keepdims=True) + ku.half_step(BF16) * np.abs(want)
+    ku.close(out, np.broadcast_to(want, out.shape), np.broadcast_to(tol, out.shape), "first rows")
