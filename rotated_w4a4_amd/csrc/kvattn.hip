@@ -445,7 +445,8 @@ __device__ __forceinline__ void finish_row(const AttnArgs& a, int q0, int qn, in
 // the exchange across lanes that finds the maximum) is left out.
 //
 // Bound by memory: 64 requests of up to 16384 keys (8 KV heads of 128, 571 MB)
-// take 132-147 us on different cards, 3.9-4.3 TB/s; the same loads without any arithmetic 114 us.
+// take 132-147 us on different cards, 3.9-4.3 TB/s; the same loads without any
+// arithmetic 114 us.
 // 128-key steps with each wave's own 32 keys need no barrier, so loads of the
 // next tile fly over all of a tile's work; 3 blocks a CU by registers and LDS (4
 // spill: 275 us).
@@ -944,9 +945,9 @@ __device__ __forceinline__ void wide_finish(const AttnArgs& a, const Piece& it, 
 // have a scale in [max(n 2^-16, 2^-14), 2^8), no weight passes 2^15 (p <=
 // 2^kHalfSlack), each row has one of that much or more (its largest p is at least
 // 1), and what n keys lose, 2^-25 each, is at most 2^-9 of it, and that only if all
-// others lie below fp16's normal range.  At the first step with a key outside of the range (a value of
-// zeros, say) the piece starts again with weights of two bf16 parts, which need
-// none; a prompt of such keys alone takes 194 us.
+// others lie below fp16's normal range.  At the first step with a key outside of the
+// range (a value of zeros, say) the piece starts again with weights of two bf16
+// parts, which need none; a prompt of such keys alone takes 194 us.
 // ---------------------------------------------------------------------------
 struct Unit {
   int exp;
