@@ -42,7 +42,7 @@ def listed():
         {"name": "quantize_down", "op": "quantize", "rows": 4096, "K": 14336, "block": 128, "signed": False,
          "dtype": BF16, "layout": "rows"},
         # fp32 activations, an odd number of tokens, wider blocks with random signs
-        {"name": "quantize_f32", "op": "quantize", "rows": 1333, "K": 11008, "block": 256, "signed": True, "dtype": F32,
+        {"name": "quantize_f32", "op": "quantize", "rows": 1333, "K": 8192, "block": 256, "signed": True, "dtype": F32,
          "layout": "rows"},
         # a layer's weights [K, N] packed
         {"name": "pack_weight", "op": "quantize", "rows": 4096, "K": 4096, "block": 128, "signed": False, "dtype": F32,
@@ -77,8 +77,7 @@ def draw(rng):
     dtype = rng.choice([BF16, BF16, F32])
     if op == "quantize":
         block = rng.choice([1, 128, 128, 256, 512])
-        K = 128 * _spread(rng, 1, 112)
-        K = max(1, K // block) * block if block > 128 else K
+        K = rng.choice([512, 1024, 2048, 4096, 8192]) if block > 128 else 128 * _spread(rng, 1, 112)
         return {"op": op, "rows": _spread(rng, 1, max(1, min(16384, 4096 * 14336 // K))), "K": K, "block": block,
                 "signed": block > 1 and rng.random() < 0.3, "dtype": dtype,
                 "layout": rng.choice(["rows", "rows", "rows", "kn", "nk"])}
