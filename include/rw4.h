@@ -443,6 +443,50 @@ rw4_status rw4_w4a4_gemm_g(const uint8_t* qa, const float* sa, const uint8_t* qw
 rw4_status rw4_dequantize_g(const uint8_t* q, const float* s, int64_t M, int64_t K, int32_t group, void* out,
                             rw4_dtype out_dtype, int64_t ldo, void* stream);
 
+/* ---- MXFP4: 4-bit floating point with a power-of-two scale for 32 channels ----
+ * The microscaled FP4 format that the gfx950 matrix cores multiply as it is stored
+ * (the scales too), beside the INT4 groups above: the same rotations and layers,
+ * and a product that needs no rescaling of partial sums.
+ *   codes q [rows, K/2] bytes, rows contiguous: FP4 E2M1, channel 2j in the low
+ *   four bits of byte j, channel 2j+1 in the high four; bit 3 of a code is its
+ *   sign, bits 0-2 are the index into 0, 0.5, 1, 1.5, 2, 3, 4, 6;
+ *   scales s [K/128, rows, 4] bytes: byte i of (g, r) is the exponent plus 127
+ *   (E8M0) of channels 128g + 32i .. of row r; 255 is NaN.  So the scales of one
+ *   128-channel group lie side by side for all rows.
+ * K is a multiple of 128 and at most 2^23, rows at most 2^31.
+ *
+ * rw4_mx_quantize_act: x [M, K] (ldx elements a row, 16-byte rows) through the
+ * transform t, then per 32 channels
+ *   E = clamp(floor(log2 max |y|) - 2, -127, 127)   (-127 for a block of zeros),
+ *   code = y 2^-E to the nearest of the values above, ties to the even index,
+ *   beyond 6 to 6; a code keeps the sign of a value that rounds to zero.
+ * Codes and scales are those of the exact y (evaluated in 32 bits with a bound of
+ * the error, in 64 bits where the bound does not decide).  A block whose largest y
+ * is infinite or NaN gets the scale 255 and codes 0; a Hadamard spreads one such
+ * value over its whole block.
+ * t: block Hadamards of 128, 256 or 512 channels, plain or signed; NULL for no
+ * transform.  Larger blocks and Givens transforms give RW4_ERR_UNSUPPORTED: call
+ * rw4_rotate_act with an fp32 output and quantize that with t NULL (codes are then
+ * those of the rounded values).
+ *
+ * rw4_mx_pack_weight: the same for the output channels of w (element (k, n) at
+ * w[k stride_k + n stride_n], strides positive), qw [N, K/2], sw [K/128, N, 4].
+ *
+ * rw4_mx_dequantize: the values, exact in fp32 and in bf16 (ldo elements a row,
+ * 16-byte rows).
+ *
+ * rw4_mx_gemm: Y [M, N] = sum over 32-channel blocks of the scales' product times
+ * the codes' products, fp32 sums, y_dtype output (ldy elements a row).
+ * Outputs must not overlap inputs. */
+rw4_status rw4_mx_quantize_act(const rw4_transform* t, const void* x, rw4_dtype x_dtype, int64_t M, int64_t K,
+                               int64_t ldx, uint8_t* q, uint8_t* s, void* stream);
+rw4_status rw4_mx_pack_weight(const rw4_transform* t, const void* w, rw4_dtype w_dtype, int64_t N, int64_t K,
+                              int64_t stride_k, int64_t stride_n, uint8_t* qw, uint8_t* sw, void* stream);
+rw4_status rw4_mx_dequantize(const uint8_t* q, const uint8_t* s, int64_t M, int64_t K, void* out, rw4_dtype out_dtype,
+                             int64_t ldo, void* stream);
+rw4_status rw4_mx_gemm(const uint8_t* qa, const uint8_t* sa, const uint8_t* qw, const uint8_t* sw, int64_t M, int64_t N,
+                       int64_t K, void* y, rw4_dtype y_dtype, int64_t ldy, void* stream);
+
 /* ---- Serving with an INT4 KV cache ---------------------------------------
  * The Rotated Runtime Smooth page's experimental setup quantizes the KV
  * cache symmetrically (round to nearest) in groups of the head's channels,

@@ -30,6 +30,8 @@ __all__ = [
     "dequantize_asym", "mixed_tables", "quantize_act_mixed", "prepare_quantize_act_mixed", "extend_weight_groups",
     "KVCache", "KVSlots", "kv_slots", "prepare_kv_slots", "rope_table", "qk_norm_rope", "prepare_qk_norm_rope",
     "kv_append", "prepare_kv_append", "kv_attention", "prepare_kv_attention", "kv_attention_workspace_bytes",
+    "mx_quantize_act", "prepare_mx_quantize_act", "mx_pack_weight", "mx_dequantize", "prepare_mx_dequantize", "mx_gemm",
+    "prepare_mx_gemm", "mx_scale_rows",
     "status_str", "version", "EXPORTED_SYMBOLS",
 ]
 
@@ -48,7 +50,8 @@ EXPORTED_SYMBOLS = (
     "rw4_version", "rw4_rrs_reorder_workspace_bytes", "rw4_quantize_act_rrs_reorder", "rw4_pack_weight_per_channel",
     "rw4_permute_codes", "rw4_decode_fused", "rw4_quantize_act_asym", "rw4_weight_code_sums", "rw4_w4a4_gemm_asym",
     "rw4_dequantize_asym", "rw4_quantize_act_mixed", "rw4_extend_weight_groups", "rw4_kv_slots", "rw4_qk_norm_rope",
-    "rw4_kv_append", "rw4_kv_attention_workspace_bytes", "rw4_kv_attention",
+    "rw4_kv_append", "rw4_kv_attention_workspace_bytes", "rw4_kv_attention", "rw4_mx_quantize_act",
+    "rw4_mx_pack_weight", "rw4_mx_dequantize", "rw4_mx_gemm",
 )
 
 
@@ -737,3 +740,6 @@ def prepare_w4a4_gemm(qa, sa, qw, sw, out_dtype=None, out=None) -> Call:
 from .kv import (  # noqa: E402  (the binding of the kv calls builds on the names above)
     KVCache, KVSlots, kv_append, kv_attention, kv_attention_workspace_bytes, kv_slots, prepare_kv_append,
     prepare_kv_attention, prepare_kv_slots, prepare_qk_norm_rope, qk_norm_rope, rope_table)
+from .mx import (  # noqa: E402
+    mx_dequantize, mx_gemm, mx_pack_weight, mx_quantize_act, mx_scale_rows, prepare_mx_dequantize, prepare_mx_gemm,
+    prepare_mx_quantize_act)

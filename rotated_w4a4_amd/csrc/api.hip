@@ -14,6 +14,7 @@
 
 #include "../../include/rw4.h"
 #include "kv_internal.h"
+#include "mx_internal.h"
 #include "rw4_internal.h"
 
 struct rw4_transform {
@@ -610,6 +611,91 @@ rw4_status rw4_w4a4_gemm(const uint8_t* qa, const float* sa, const uint8_t* qw, 
                          int64_t M, int64_t N, int64_t K, void* y, rw4_dtype y_dtype, int64_t ldy,
                          void* stream) {
   return rw4_w4a4_gemm_g(qa, sa, qw, sw, M, N, K, 128, y, y_dtype, ldy, stream);
+}
+
+// ---- MXFP4 ----
+
+// Channels of an MXFP4 row, at most: a tile of 256 rows stays below 2^31 bytes.
+constexpr int64_t kMostMxK = int64_t(1) << 23;
+// Rows of an operand, at most: row numbers and scale offsets of a tile stay in 32 bits.
+constexpr int64_t kMostMxRows = int64_t(1) << 31;
+constexpr int64_t kMostMxStride = int64_t(1) << 40;
+
+static rw4_status mx_sizes(int64_t rows, int64_t K) {
+  return rows < 0 || rows > kMostMxRows || K <= 0 || K % kGroup || K > kMostMxK ? RW4_ERR_SHAPE : RW4_OK;
+}
+
+// The transform's part of the arguments (t NULL: none).
+static rw4_status mx_transform(const rw4_transform* t, int64_t K, rw4::MxRows* a) {
+  a->block = 1;
+  a->sign_mask = nullptr;
+  if (!t) return RW4_OK;
+  if (t->dev.K != K) return RW4_ERR_SHAPE;
+  if (t->dev.kind != rw4::TransformKind::Hadamard || t->dev.block > 512) return RW4_ERR_UNSUPPORTED;
+  if (!on_home_device(t)) return RW4_ERR_ARG;
+  a->block = int(t->dev.block);
+  a->sign_mask = t->dev.sign_mask;
+  return RW4_OK;
+}
+
+rw4_status rw4_mx_quantize_act(const rw4_transform* t, const void* x, rw4_dtype x_dtype, int64_t M, int64_t K,
+                               int64_t ldx, uint8_t* q, uint8_t* s, void* stream) {
+  if (x_dtype != RW4_F32 && x_dtype != RW4_BF16) return RW4_ERR_ARG;
+  rw4_status st = mx_sizes(M, K);
+  if (st != RW4_OK) return st;
+  rw4::MxRows a{x, x_dtype == RW4_BF16, M, K, ldx, 1, 1, nullptr, q, s};
+  st = mx_transform(t, K, &a);
+  if (st != RW4_OK) return st;
+  if (M == 0) return RW4_OK;
+  if (!x || !q || !s) return RW4_ERR_ARG;
+  const int64_t esz = x_dtype == RW4_BF16 ? 2 : 4;
+  if (ldx < K || ldx >= kMostMxStride || (ldx * esz) % 16 || !aligned16(x) || !aligned16(q) || !aligned16(s))
+    return RW4_ERR_ARG;
+  return from_hip(rw4::launch_mx_quantize(a, static_cast<hipStream_t>(stream)));
+}
+
+rw4_status rw4_mx_pack_weight(const rw4_transform* t, const void* w, rw4_dtype w_dtype, int64_t N, int64_t K,
+                              int64_t stride_k, int64_t stride_n, uint8_t* qw, uint8_t* sw, void* stream) {
+  if (w_dtype != RW4_F32 && w_dtype != RW4_BF16) return RW4_ERR_ARG;
+  rw4_status st = mx_sizes(N, K);
+  if (st != RW4_OK) return st;
+  rw4::MxRows a{w, w_dtype == RW4_BF16, N, K, stride_n, stride_k, 1, nullptr, qw, sw};
+  st = mx_transform(t, K, &a);
+  if (st != RW4_OK) return st;
+  if (N == 0) return RW4_OK;
+  if (!w || !qw || !sw) return RW4_ERR_ARG;
+  if (stride_k <= 0 || stride_n <= 0 || stride_k >= kMostMxStride || stride_n >= kMostMxStride) return RW4_ERR_ARG;
+  const int64_t esz = w_dtype == RW4_BF16 ? 2 : 4;
+  if ((reinterpret_cast<uintptr_t>(w) % esz) || !aligned16(qw) || !aligned16(sw)) return RW4_ERR_ARG;
+  hipStream_t to = static_cast<hipStream_t>(stream);
+  const bool rows = stride_k == 1 && stride_n >= K && aligned16(w) && (stride_n * esz) % 16 == 0;
+  return from_hip(rows ? rw4::launch_mx_quantize(a, to) : rw4::launch_mx_pack(a, to));
+}
+
+rw4_status rw4_mx_dequantize(const uint8_t* q, const uint8_t* s, int64_t M, int64_t K, void* out, rw4_dtype out_dtype,
+                             int64_t ldo, void* stream) {
+  if (out_dtype != RW4_F32 && out_dtype != RW4_BF16) return RW4_ERR_ARG;
+  const rw4_status st = mx_sizes(M, K);
+  if (st != RW4_OK) return st;
+  if (M == 0) return RW4_OK;
+  if (!q || !s || !out) return RW4_ERR_ARG;
+  const int64_t esz = out_dtype == RW4_BF16 ? 2 : 4;
+  if (ldo < K || ldo >= kMostMxStride || (ldo * esz) % 16 || !aligned16(q) || !aligned16(s) || !aligned16(out))
+    return RW4_ERR_ARG;
+  return from_hip(rw4::launch_mx_dequantize(q, s, M, K, out, out_dtype == RW4_BF16, ldo, static_cast<hipStream_t>(stream)));
+}
+
+rw4_status rw4_mx_gemm(const uint8_t* qa, const uint8_t* sa, const uint8_t* qw, const uint8_t* sw, int64_t M, int64_t N,
+                       int64_t K, void* y, rw4_dtype y_dtype, int64_t ldy, void* stream) {
+  if (y_dtype != RW4_F32 && y_dtype != RW4_BF16) return RW4_ERR_ARG;
+  rw4_status st = mx_sizes(M, K);
+  if (st == RW4_OK) st = mx_sizes(N, K);
+  if (st != RW4_OK) return st;
+  if (M == 0 || N == 0) return RW4_OK;
+  if (!qa || !sa || !qw || !sw || !y) return RW4_ERR_ARG;
+  if (ldy < N || ldy >= kMostMxStride || !aligned16(qa) || !aligned16(qw) || !aligned16(sa) || !aligned16(sw) || !aligned16(y))
+    return RW4_ERR_ARG;
+  return from_hip(rw4::launch_mx_gemm(qa, sa, qw, sw, M, N, K, y, y_dtype == RW4_BF16, ldy, static_cast<hipStream_t>(stream)));
 }
 
 // ---- Serving with an INT4 KV cache ----
