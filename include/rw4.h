@@ -669,6 +669,18 @@ rw4_status rw4_kv_attention(const rw4_kv_cache* cache_host, const void* q, rw4_d
                             int64_t out_token, int64_t out_head, float* lse, void* workspace, int64_t workspace_bytes,
                             void* stream);
 
+/* rw4_kv_attention with sinks: besides the keys of its window a query also sees the
+ * request's first `sinks` keys (those up to its own place).  Keys that no query of
+ * the request sees are not read, so a long request costs its sinks and its window.
+ * Without a window (0) every earlier key is visible and sinks changes nothing;
+ * sinks >= 0.  Everything else as above, the workspace included. */
+rw4_status rw4_kv_attention_sinks(const rw4_kv_cache* cache_host, const void* q, rw4_dtype q_dtype, int64_t q_token,
+                                  int64_t q_head, int64_t T, int32_t heads, const int32_t* block_table,
+                                  int64_t table_width, const int32_t* kv_len, const int32_t* cu_q, int64_t B,
+                                  int64_t max_q_len, float scale, int32_t causal, int64_t window, int64_t sinks,
+                                  int32_t unrotate, void* out, rw4_dtype out_dtype, int64_t out_token, int64_t out_head,
+                                  float* lse, void* workspace, int64_t workspace_bytes, void* stream);
+
 /* Static description of a status code. */
 const char* rw4_status_str(rw4_status s);
 

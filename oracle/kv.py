@@ -96,7 +96,7 @@ def quantize_heads(x, factor, rotate):
     return codes.astype(np.int8), (m * factor / (7.0 * (math.sqrt(D) if rotate else 1.0)))[..., 0]
 
 
-def kv_attention(q, ck, sk, cv, sv, pages, table, kv_len, cu_q, scale, causal, window, unrotate):
+def kv_attention(q, ck, sk, cv, sv, pages, table, kv_len, cu_q, scale, causal, window, unrotate, sinks=0):
     """Attention over cached codes ck, cv [pages, heads, page, D] with scales [pages, heads, page].
 
     Returns out [T, Hq, D], lse [T, Hq], reach [T, Hq]: sum over channels of sum_j p_j |v_j|, over sqrt(D) when
@@ -123,7 +123,7 @@ def kv_attention(q, ck, sk, cv, sv, pages, table, kv_len, cu_q, scale, causal, w
             if causal:
                 see &= j <= place
             if window:
-                see &= j > place - window
+                see &= (j > place - window) | (j < sinks)
             for h in range(Hq):
                 kh = h // G
                 if not see.any():

@@ -50,8 +50,8 @@ EXPORTED_SYMBOLS = (
     "rw4_version", "rw4_rrs_reorder_workspace_bytes", "rw4_quantize_act_rrs_reorder", "rw4_pack_weight_per_channel",
     "rw4_permute_codes", "rw4_decode_fused", "rw4_quantize_act_asym", "rw4_weight_code_sums", "rw4_w4a4_gemm_asym",
     "rw4_dequantize_asym", "rw4_quantize_act_mixed", "rw4_extend_weight_groups", "rw4_kv_slots", "rw4_qk_norm_rope",
-    "rw4_kv_append", "rw4_kv_attention_workspace_bytes", "rw4_kv_attention", "rw4_mx_quantize_act",
-    "rw4_mx_pack_weight", "rw4_mx_dequantize", "rw4_mx_gemm",
+    "rw4_kv_append", "rw4_kv_attention_workspace_bytes", "rw4_kv_attention", "rw4_kv_attention_sinks",
+    "rw4_mx_quantize_act", "rw4_mx_pack_weight", "rw4_mx_dequantize", "rw4_mx_gemm",
 )
 
 

@@ -13,6 +13,7 @@
 #include <hip/hip_runtime.h>
 
 #include "../../include/rw4.h"
+#include "kv_index.h"
 #include "kv_internal.h"
 #include "mx_internal.h"
 #include "rw4_internal.h"
@@ -890,12 +891,23 @@ rw4_status rw4_kv_attention(const rw4_kv_cache* cache_host, const void* q, rw4_d
                             int32_t causal, int64_t window, int32_t unrotate, void* out, rw4_dtype out_dtype,
                             int64_t out_token, int64_t out_head, float* lse, void* workspace, int64_t workspace_bytes,
                             void* stream) {
+  return rw4_kv_attention_sinks(cache_host, q, q_dtype, q_token, q_head, T, heads, block_table, table_width, kv_len, cu_q,
+                                B, max_q_len, scale, causal, window, 0, unrotate, out, out_dtype, out_token, out_head, lse,
+                                workspace, workspace_bytes, stream);
+}
+
+rw4_status rw4_kv_attention_sinks(const rw4_kv_cache* cache_host, const void* q, rw4_dtype q_dtype, int64_t q_token,
+                                  int64_t q_head, int64_t T, int32_t heads, const int32_t* block_table,
+                                  int64_t table_width, const int32_t* kv_len, const int32_t* cu_q, int64_t B,
+                                  int64_t max_q_len, float scale, int32_t causal, int64_t window, int64_t sinks,
+                                  int32_t unrotate, void* out, rw4_dtype out_dtype, int64_t out_token, int64_t out_head,
+                                  float* lse, void* workspace, int64_t workspace_bytes, void* stream) {
   if (!dtype_known(q_dtype) || !dtype_known(out_dtype) || !std::isfinite(scale)) return RW4_ERR_ARG;
   rw4::AttnArgs a{};
   const rw4_status st = kv_cache_of(cache_host, &a.cache);
   if (st != RW4_OK) return st;
   if (!attention_sizes_ok(T, B, heads, cache_host->heads, cache_host->head_dim) || table_width < 0 ||
-      table_width > 0x7FFFFFFF || max_q_len < 0 || window < 0)
+      table_width > 0x7FFFFFFF || max_q_len < 0 || window < 0 || sinks < 0)
     return RW4_ERR_SHAPE;
   if (window > 0 && !causal) return RW4_ERR_UNSUPPORTED;
   if (T == 0 || B == 0) return RW4_OK;
@@ -927,6 +939,7 @@ rw4_status rw4_kv_attention(const rw4_kv_cache* cache_host, const void* q, rw4_d
   a.causal = causal != 0;
   a.unrotate = unrotate != 0;
   a.window = window < kMaxStride ? window : kMaxStride;  // longer than any request
+  a.sinks = window > 0 ? int(sinks < rw4::kMostKeys ? sinks : rw4::kMostKeys) : 0;
   a.out = out;
   a.out_token = out_token;
   a.out_head = out_head;

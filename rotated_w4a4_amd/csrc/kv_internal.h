@@ -78,6 +78,7 @@ struct AttnArgs {
   float scale;
   int causal, unrotate;
   int64_t window;
+  int sinks;  // first keys that stay visible; 0 where window is 0
   void* out;
   int64_t out_token, out_head;
   float* lse;

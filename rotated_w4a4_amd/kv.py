@@ -47,7 +47,9 @@ lib.rw4_kv_attention_workspace_bytes.argtypes = [_i64, _i64, _i32, _i32, _i32]
 lib.rw4_kv_attention_workspace_bytes.restype = _i64
 lib.rw4_kv_attention.argtypes = [_p, _p, ctypes.c_int, _i64, _i64, _i64, _i32, _p, _i64, _p, _p, _i64, _i64, _f32, _i32,
                                  _i64, _i32, _p, ctypes.c_int, _i64, _i64, _p, _p, _i64, _p]
-for _name in ("rw4_kv_slots", "rw4_qk_norm_rope", "rw4_kv_append", "rw4_kv_attention"):
+lib.rw4_kv_attention_sinks.argtypes = [_p, _p, ctypes.c_int, _i64, _i64, _i64, _i32, _p, _i64, _p, _p, _i64, _i64, _f32,
+                                       _i32, _i64, _i64, _i32, _p, ctypes.c_int, _i64, _i64, _p, _p, _i64, _p]
+for _name in ("rw4_kv_slots", "rw4_qk_norm_rope", "rw4_kv_append", "rw4_kv_attention", "rw4_kv_attention_sinks"):
     getattr(lib, _name).restype = ctypes.c_int
 
 
@@ -344,12 +346,13 @@ def kv_attention_workspace_bytes(tokens: int, requests: int, heads: int, kv_head
 
 
 def kv_attention(q, cache: KVCache, block_table, kv_len, cu_q, *, max_q_len=None, scale=None, causal: bool = True,
-                 window: int = 0, unrotate: bool = True, out=None, out_dtype=None, return_lse: bool = False, lse=None,
-                 workspace=None):
+                 window: int = 0, sinks: int = 0, unrotate: bool = True, out=None, out_dtype=None,
+                 return_lse: bool = False, lse=None, workspace=None):
     """Softmax attention of q [T, heads, D] over the cache: request b owns query tokens cu_q[b]:cu_q[b + 1] and the
     first kv_len[b] cached tokens, in the pages block_table[b].
 
-    causal: a request's queries are its last tokens; window > 0: the last `window` keys only.  scale defaults to
+    causal: a request's queries are its last tokens; window > 0: the last `window` keys only, and the first `sinks` keys
+    (those up to the query's own place), whose cost is that of a request of sinks + window keys.  scale defaults to
     1 / sqrt(D); unrotate applies the head's Hadamard to the output (for a cache of rotated values).  Returns out [T,
     heads, D], with return_lse (out, lse fp32 [T, heads]).  A row that sees no key gives 0 and -inf, one of no request is
     not written.
@@ -358,23 +361,23 @@ def kv_attention(q, cache: KVCache, block_table, kv_len, cu_q, *, max_q_len=None
     whole call and nothing else, but say it: a decode step of 32 requests without it takes the kernel for many rows, 2 to
     4 times as long, and so do single tokens in one call with a prompt's chunk; two calls can be the faster way there."""
     fn, args, dev, what, _, result = _attention(q, cache, block_table, kv_len, cu_q, max_q_len, scale, causal, window,
-                                                unrotate, out, out_dtype, return_lse, lse, workspace)
+                                                sinks, unrotate, out, out_dtype, return_lse, lse, workspace)
     _launch(fn, args, dev, what)
     return result
 
 
 def prepare_kv_attention(q, cache: KVCache, block_table, kv_len, cu_q, *, max_q_len=None, scale=None,
-                         causal: bool = True, window: int = 0, unrotate: bool = True, out=None, out_dtype=None,
-                         return_lse: bool = False, lse=None, workspace=None) -> Call:
+                         causal: bool = True, window: int = 0, sinks: int = 0, unrotate: bool = True, out=None,
+                         out_dtype=None, return_lse: bool = False, lse=None, workspace=None) -> Call:
     """kv_attention checked and marshalled once; calling the result runs it.
 
     Without `workspace` it has one of its own (7 to 68 MB, kv_attention_workspace_bytes), so do not let two runs of it
     overlap in time (two streams, two graphs); prepared calls that run one after the other can be given one together."""
-    return KVCall(*_attention(q, cache, block_table, kv_len, cu_q, max_q_len, scale, causal, window, unrotate, out,
-                              out_dtype, return_lse, lse, workspace))
+    return KVCall(*_attention(q, cache, block_table, kv_len, cu_q, max_q_len, scale, causal, window, sinks, unrotate,
+                              out, out_dtype, return_lse, lse, workspace))
 
 
-def _attention(q, cache, block_table, kv_len, cu_q, max_q_len, scale, causal, window, unrotate, out, out_dtype,
+def _attention(q, cache, block_table, kv_len, cu_q, max_q_len, scale, causal, window, sinks, unrotate, out, out_dtype,
                return_lse, lse, workspace):
     i32, dev, D, kv_heads = torch.int32, cache._dev, cache.head_dim, cache.kv_heads
     qp, qt, qh = _rows("q", q, dev)
@@ -405,7 +408,7 @@ def _attention(q, cache, block_table, kv_len, cu_q, max_q_len, scale, causal, wi
             raise ValueError(f"workspace must be a contiguous tensor of at least {nbytes} bytes")
     args = (cache._ptr, qp, _code(q.dtype), qt, qh, T, heads, table, width, _vec("kv_len", kv_len, i32, B, dev),
             _vec("cu_q", cu_q, i32, B + 1, dev), B, T if max_q_len is None else int(max_q_len),
-            D ** -0.5 if scale is None else scale, int(causal), int(window), int(unrotate), op, _code(out.dtype), ot, oh,
-            None if lse is None else lse.data_ptr(), workspace.data_ptr(), wbytes)
-    return (lib.rw4_kv_attention, args, dev, "rw4_kv_attention",
+            D ** -0.5 if scale is None else scale, int(causal), int(window), int(sinks), int(unrotate), op,
+            _code(out.dtype), ot, oh, None if lse is None else lse.data_ptr(), workspace.data_ptr(), wbytes)
+    return (lib.rw4_kv_attention_sinks, args, dev, "rw4_kv_attention",
             (q, cache, block_table, kv_len, cu_q, workspace, lse), (out, lse) if return_lse else out)
