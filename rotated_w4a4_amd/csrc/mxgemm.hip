@@ -58,42 +58,68 @@ __device__ __forceinline__ void store_one(void* y, int64_t at, float v) {
 }
 
 // ---------------------------------------------------------------------------
-// Many rows: BM tokens x BN channels a block, WM x WN waves.  K goes in stages of
-// 256 channels, which the DMA brings from memory into one of two LDS buffers while
-// the other is computed on (one barrier a stage).  A row of a stage is 128 bytes,
-// eight 16-byte chunks, chunk c at place c ^ (row & 7), so that 8 lanes reading one
-// chunk of 8 rows hit all banks; the DMA writes LDS in lane order, so the exchange is
-// in the addresses it reads from.  The scales of a stage go straight into registers
-// (4 bytes for 128 channels of a row, rows side by side), a stage ahead.
+// Many rows: BM tokens x BN channels a block, WM x WN waves of TM x TN tiles.  K goes
+// in stages of 256 channels (whole 128-byte lines of the rows) through LDS buffers that the DMA fills (RING of them where the
+// tiles are small and a stage's products take less than the memory's latency).  A stage is four steps of 64 channels; the operands of a step are
+// read from LDS during the products of the step before, also across stages.  So the
+// last reads of a buffer are over when its stage's last step begins: there the wait
+// for the next stage's arrival, the barrier, and the start of the DMA of the stage
+// after that into the buffer just read, which has RING - 1 stages' time to arrive; the
+// matrix unit has the last step's products meanwhile.
+//   A row of a stage is eight 16-byte chunks, chunk c at place c ^ (row & 7), so that 8
+// lanes reading one chunk of 8 rows hit all banks; the DMA writes LDS in lane order,
+// so the exchange is in the addresses it reads from.
 // ---------------------------------------------------------------------------
-constexpr int kStageK = 256, kStageRow = kStageK / 2;
+constexpr int kStageRow = kGroup;  // bytes of 256 channels
+constexpr int kSteps = 4;
 
 template <int BM, int BN, int WM, int WN>
 struct Tile {
   static constexpr int waves = WM * WN, threads = 64 * waves;
   static constexpr int TM = BM / WM / 32, TN = BN / WN / 32;  // 32 x 32 tiles of a wave
-  static constexpr int bytes = (BM + BN) * kStageRow;
-  static constexpr int loads = (BM + BN) / 8 / waves;  // DMA instructions of a wave, 8 rows each
-  static_assert((BM + BN) % (8 * waves) == 0 && BM % (8 * waves) == 0, "whole DMA instructions of one operand");
+  // a stage in LDS: codes, then the scale words of its two groups of 128 channels
+  static constexpr int codes = (BM + BN) * kStageRow, words = (BM + BN) * 4, bytes = codes + 2 * words;
+  // DMA instructions of a wave for a stage: 8 rows' codes, and 64 rows' words of a group each
+  static constexpr int LA = BM / 8 / waves, LW = BN / 8 / waves, pieces = 2 * (BM + BN) / 64;
+  static constexpr int LX = (pieces + waves - 1) / waves, loads = LA + LW + LX;
+  static_assert(BM % (8 * waves) == 0 && BN % (8 * waves) == 0 && BM % 64 == 0 && BN % 64 == 0, "whole DMA instructions");
 };
 
-template <int BM, int BN, int WM, int WN, bool BF16>
-__global__ __launch_bounds__(64 * WM * WN) void mx_gemm_kernel(
+// Until at most n vector-memory instructions of the wave are in flight; LDS reads go on.
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 0xF) | (0x7 << 4) | (0xF << 8) | ((N >> 4) << 14));
+}
+// The same, and all LDS reads of the wave are done.
+template <int N>
+__device__ __forceinline__ void wait_vm_lds() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 0xF) | (0x7 << 4) | (0x0 << 8) | ((N >> 4) << 14));
+}
+__device__ __forceinline__ void block_barrier() { asm volatile("s_barrier" ::: "memory"); }
+
+template <int BM, int BN, int WM, int WN, int RING, bool BF16>
+__global__ __launch_bounds__(64 * WM * WN, 1) void mx_gemm_kernel(
     const uint8_t* __restrict__ qa, const uint32_t* __restrict__ sa, const uint8_t* __restrict__ qw,
     const uint32_t* __restrict__ sw, int64_t M, int64_t N, int64_t K, void* __restrict__ y, int64_t ldy,
     int64_t tiles_m) {
   using T = Tile<BM, BN, WM, WN>;
   constexpr int TM = T::TM, TN = T::TN;
-  // two objects: the compiler sees that the DMA into one never writes what is read from the other
+  // objects of their own: the compiler sees that the DMA into one never writes what is read from another
+  static_assert(RING >= 2 && RING <= 4, "buffers of the ring");
   __shared__ __align__(16) uint8_t buf0[T::bytes];
   __shared__ __align__(16) uint8_t buf1[T::bytes];
+  __shared__ __align__(16) uint8_t buf2[RING > 2 ? T::bytes : 16];
+  __shared__ __align__(16) uint8_t buf3[RING > 3 ? T::bytes : 16];
 
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
   int64_t mt, nt;
   mx_tile(blockIdx.x, gridDim.x, tiles_m, mt, nt);
-  const int64_t m0 = mt * BM, n0 = nt * BN, row_bytes = K / 2, G = K / kGroup;
+  const int64_t m0 = mt * BM, n0 = nt * BN, row_bytes = K / 2;
+  const int G = int(K / kGroup);
   const int rows_a = int(M - m0 < BM ? M - m0 : BM), rows_w = int(N - n0 < BN ? N - n0 : BN);
 
   // rows beyond the last one read that again; what they give is not stored
@@ -101,56 +127,46 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_kernel(
                                                                       int(rows_a * row_bytes), 0x00020000);
   const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(qw + n0 * row_bytes), 0,
                                                                       int(rows_w * row_bytes), 0x00020000);
-  constexpr int LA = BM / 8 / T::waves, LW = T::loads - LA;
-  uint32_t from_a[LA], from_w[LW];
+  uint32_t from_a[T::LA], from_w[T::LW];
   const int sub = lane >> 3, chunk = ((lane & 7) ^ sub) * 16;
 #pragma unroll
-  for (int i = 0; i < LA; ++i) {
-    const int r = (wave * LA + i) * 8 + sub;
+  for (int i = 0; i < T::LA; ++i) {
+    const int r = (wave * T::LA + i) * 8 + sub;
     from_a[i] = uint32_t((r < rows_a ? r : rows_a - 1) * row_bytes + chunk);
   }
 #pragma unroll
-  for (int i = 0; i < LW; ++i) {
-    const int r = (wave * LW + i) * 8 + sub;
+  for (int i = 0; i < T::LW; ++i) {
+    const int r = (wave * T::LW + i) * 8 + sub;
     from_w[i] = uint32_t((r < rows_w ? r : rows_w - 1) * row_bytes + chunk);
   }
-  auto bring = [&](uint8_t* to, int64_t stage) {  // behind the last channel: other rows' codes or zeros, not used
-    const int at = int(stage * kStageRow);
-#pragma unroll
-    for (int i = 0; i < LA; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void_t*)(to + (wave * LA + i) * 1024), 16, int(from_a[i]), at, 0, 0);
-#pragma unroll
-    for (int i = 0; i < LW; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void_t*)(to + BM * kStageRow + (wave * LW + i) * 1024), 16,
-                                               int(from_w[i]), at, 0, 0);
-  };
-
-  // scales: word g of a row holds the bytes of its channels 128 g ..; shifted so that
-  // byte 0 and byte 2 are the lane half's blocks of the two products of 64 channels
-  int row_a[TM], row_w[TN];
-#pragma unroll
-  for (int i = 0; i < TM; ++i) {
-    const int r = (wm * TM + i) * 32 + n;
-    row_a[i] = r < rows_a ? r : rows_a - 1;
-  }
-#pragma unroll
-  for (int i = 0; i < TN; ++i) {
-    const int r = (wn * TN + i) * 32 + n;
-    row_w[i] = r < rows_w ? r : rows_w - 1;
-  }
-  struct Scales {
-    uint32_t a[2][TM], w[2][TN];
-  };
-  auto load_scales = [&](int64_t stage, Scales& to) {
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      const int64_t g = 2 * stage + p < G ? 2 * stage + p : G - 1;
-      const uint32_t* pa = sa + g * M + m0;
-      const uint32_t* pw = sw + g * N + n0;
-#pragma unroll
-      for (int i = 0; i < TM; ++i) to.a[p][i] = pa[row_a[i]];
-#pragma unroll
-      for (int i = 0; i < TN; ++i) to.w[p][i] = pw[row_w[i]];
+  const int stages = (G + 1) / 2;
+  // One of the wave's T::loads DMA instructions of a stage (behind the last stage: that
+  // again, not used; behind the last channel: the next row's codes or zeros).
+  auto bring = [&](uint8_t* to, int stage, int i) {
+    const int s = stage < stages ? stage : stages - 1;
+    if (i < T::LA) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void_t*)(to + (wave * T::LA + i) * 1024), 16, int(from_a[i]),
+                                               s * kStageRow, 0, 0);
+    } else if (i < T::LA + T::LW) {
+      i -= T::LA;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void_t*)(to + BM * kStageRow + (wave * T::LW + i) * 1024), 16,
+                                               int(from_w[i]), s * kStageRow, 0, 0);
+    } else {
+      // 64 rows' words of a group; zeros behind the tile's last row, and for a last stage's
+      // second half that has no channels: whatever the codes there are, products of two
+      // operands of scale 2^-127 are below the smallest fp32 number, so they add nothing.
+      // Where there are fewer pieces than waves, the last one again.
+      int p = wave * T::LX + i - T::LA - T::LW;
+      p = p < T::pieces ? p : T::pieces - 1;
+      constexpr int kHalf = T::pieces / 2;
+      const int half = p >= kHalf ? 1 : 0, row = 64 * (p - half * kHalf);  // of the tokens, then the channels
+      const int g = 2 * s + half;
+      const bool a = row < BM;
+      const uint32_t* from = a ? sa + g * M + m0 : sw + g * N + n0;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          __builtin_amdgcn_make_buffer_rsrc(const_cast<uint32_t*>(from), 0, g < G ? (a ? rows_a : rows_w) * 4 : 0,
+                                            0x00020000),
+          (lds_void_t*)(to + T::codes + p * 256), 4, ((a ? row : row - BM) + lane) * 4, 0, 0, 0);
     }
   };
 
@@ -160,72 +176,126 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_kernel(
 #pragma unroll
     for (int j = 0; j < TM; ++j) acc[i][j] = v16f{};
 
-  int off[4];  // of the lane's chunk of each product in a tile of 32 rows
+  int off[kSteps];  // of the lane's chunk of a step in a tile of 32 rows
 #pragma unroll
-  for (int k = 0; k < 4; ++k) off[k] = n * kStageRow + (((2 * k + h) ^ (n & 7)) * 16);
+  for (int k = 0; k < kSteps; ++k) off[k] = n * kStageRow + (((2 * k + h) ^ (n & 7)) * 16);
   const int base_a = wm * TM * 32 * kStageRow, base_w = (BM + wn * TN * 32) * kStageRow;
+  const int base_xa = T::codes + (wm * TM * 32 + n) * 4, base_xw = T::codes + (BM + wn * TN * 32 + n) * 4;
 
   struct Operands {
-    v4u a[TM], w[TN];
+    v4u v[TN + TM];  // weights, then activations
   };
-  auto read = [&](const uint8_t* from, int k, Operands& to) {
-#pragma unroll
-    for (int i = 0; i < TN; ++i) to.w[i] = *reinterpret_cast<const v4u*>(from + base_w + off[k] + i * 32 * kStageRow);
-#pragma unroll
-    for (int i = 0; i < TM; ++i) to.a[i] = *reinterpret_cast<const v4u*>(from + base_a + off[k] + i * 32 * kStageRow);
+  struct Scales {
+    uint32_t v[TN + TM];
   };
-  auto multiply = [&](const Operands& o, const uint32_t (&xa)[TM], const uint32_t (&xw)[TN], auto second) {
+  auto read_one = [&](const uint8_t* from, int k, int i, Operands& to) {
+    to.v[i] = *reinterpret_cast<const v4u*>(from + off[k] + (i < TN ? base_w + i * 32 * kStageRow
+                                                                    : base_a + (i - TN) * 32 * kStageRow));
+  };
+  auto read_scale = [&](const uint8_t* from, int half, int i, Scales& to) {
+    to.v[i] = *reinterpret_cast<const uint32_t*>(from + half * T::words + (i < TN ? base_xw + i * 128 : base_xa + (i - TN) * 128));
+  };
+  // The products of a step, `meanwhile` between them.  Scale words are shifted so that
+  // bytes 0 and 2 are the lane half's blocks of the two steps.
+  auto multiply = [&](const Operands& o, const Scales& x, auto second, auto meanwhile) {
     constexpr int kByte = decltype(second)::value ? 2 : 0;
 #pragma unroll
-    for (int i = 0; i < TN; ++i)
-#pragma unroll
-      for (int j = 0; j < TM; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fp4_operand(o.w[i]), fp4_operand(o.a[j]), acc[i][j],
-                                                                    kFp4, kFp4, kByte, int(xw[i]), kByte, int(xa[j]));
+    for (int at = 0; at < TN * TM; ++at) {
+      const int i = at / TM, j = at % TM;
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fp4_operand(o.v[i]), fp4_operand(o.v[TN + j]), acc[i][j],
+                                                                  kFp4, kFp4, kByte, int(x.v[i]), kByte, int(x.v[TN + j]));
+      meanwhile(at);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   };
 
-  Scales next;
-  const int64_t stages = (G + 1) / 2;
-  bring(buf0, 0);
-  load_scales(0, next);
-  auto stage = [&](const uint8_t* from, uint8_t* to, int64_t s) {
-    __syncthreads();  // this stage has arrived, the other buffer is read
-    Scales x;
+  Operands o0, o1;
+  Scales x, now;
+  constexpr int P = TN * TM, R = TN + TM;
+  // f(i) for i < COUNT, spread over the P products of a step from the first one on
+  auto spread = [&](int at, auto count, auto f) {
+    constexpr int kCount = decltype(count)::value, kEach = (kCount + P - 1) / P;
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-#pragma unroll
-      for (int i = 0; i < TM; ++i) x.a[p][i] = next.a[p][i] >> (8 * h);
-#pragma unroll
-      for (int i = 0; i < TN; ++i) x.w[p][i] = next.w[p][i] >> (8 * h);
-    }
-    if (s + 1 < stages) {
-      bring(to, s + 1);
-      load_scales(s + 1, next);
-    }
-    Operands o[2];
-    read(from, 0, o[0]);
-    read(from, 1, o[1]);
-    multiply(o[0], x.a[0], x.w[0], std::false_type{});
-    const bool two = 2 * s + 1 < G;
-    if (two) read(from, 2, o[0]);
-    multiply(o[1], x.a[0], x.w[0], std::true_type{});
-    if (two) {
-      read(from, 3, o[1]);
-      multiply(o[0], x.a[1], x.w[1], std::false_type{});
-      multiply(o[1], x.a[1], x.w[1], std::true_type{});
-    }
+    for (int e = 0; e < kEach; ++e)
+      if (at * kEach + e < kCount) f(at * kEach + e);
   };
-  for (int64_t s = 0; s < stages; s += 2) {
-    stage(buf0, buf1, s);
-    if (s + 1 < stages) stage(buf1, buf0, s + 1);
+  using Reads = std::integral_constant<int, R>;
+  using Loads = std::integral_constant<int, T::loads>;
+  auto shift = [&]() {
+#pragma unroll
+    for (int i = 0; i < R; ++i) now.v[i] = x.v[i] >> (8 * h);
+  };
+#pragma unroll
+  for (int i = 0; i < T::loads; ++i) bring(buf0, 0, i);
+#pragma unroll
+  for (int i = 0; i < T::loads; ++i) bring(buf1, 1, i);
+  if constexpr (RING > 2) {
+#pragma unroll
+    for (int i = 0; i < T::loads; ++i) bring(buf2, 2, i);
   }
-  __syncthreads();
+  if constexpr (RING > 3) {
+#pragma unroll
+    for (int i = 0; i < T::loads; ++i) bring(buf3, 3, i);
+  }
+  wait_vm<(RING - 1) * T::loads>();
+  block_barrier();
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    read_one(buf0, 0, i, o0);
+    read_scale(buf0, 0, i, x);
+  }
+  using First = std::false_type;
+  using Second = std::true_type;
+  // Stage s in `cur`, whose first operands and scales are read; reads those of the next one.
+  auto stage = [&](uint8_t* cur, const uint8_t* next, int s) {
+    shift();
+    multiply(o0, now, First{}, [&](int at) { spread(at, Reads{}, [&](int i) { read_one(cur, 1, i, o1); }); });
+    multiply(o1, now, Second{}, [&](int at) {
+      spread(at, Reads{}, [&](int i) {
+        read_one(cur, 2, i, o0);
+        read_scale(cur, 1, i, x);
+      });
+    });
+    shift();
+    multiply(o0, now, First{}, [&](int at) { spread(at, Reads{}, [&](int i) { read_one(cur, 3, i, o1); }); });
+    wait_vm_lds<(RING - 2) * T::loads>();  // the next stage has arrived, this wave has read the last of this one
+    block_barrier();                       // for all waves
+    multiply(o1, now, Second{}, [&](int at) {
+      spread(at, Reads{}, [&](int i) {
+        read_one(next, 0, i, o0);
+        read_scale(next, 0, i, x);
+      });
+      spread(at, Loads{}, [&](int i) { bring(cur, s + RING, i); });
+    });
+  };
+  int s = 0;
+  for (; s + RING <= stages; s += RING) {
+    stage(buf0, buf1, s);
+    if constexpr (RING == 2) {
+      stage(buf1, buf0, s + 1);
+    } else if constexpr (RING == 3) {
+      stage(buf1, buf2, s + 1);
+      stage(buf2, buf0, s + 2);
+    } else {
+      stage(buf1, buf2, s + 1);
+      stage(buf2, buf3, s + 2);
+      stage(buf3, buf0, s + 3);
+    }
+  }
+  if (s < stages) stage(buf0, buf1, s);
+  if constexpr (RING > 2) {
+    if (s + 1 < stages) stage(buf1, buf2, s + 1);
+  }
+  if constexpr (RING > 3) {
+    if (s + 2 < stages) stage(buf2, buf3, s + 2);
+  }
+  __syncthreads();  // the DMA behind the last stage included
 
   // Output: 32 tokens at a time through the wave's own part of LDS into rows of 16-byte chunks.
   constexpr int E = BF16 ? 2 : 4, kCols = TN * 32, kOut = kCols * E + 16, kChunks = kCols * E / 16;
-  constexpr int kWaveBytes = 32 * kOut;
-  static_assert((T::waves / 2) * kWaveBytes <= T::bytes, "output rows of half of the waves in each buffer");
-  uint8_t* out = (wave < T::waves / 2 ? buf0 : buf1) + (wave % (T::waves / 2)) * kWaveBytes;
+  constexpr int kWaveBytes = 32 * kOut, kEach = T::waves / 2;
+  static_assert(kEach * kWaveBytes <= T::bytes, "output rows of half of the waves in each buffer");
+  uint8_t* out = (wave < kEach ? buf0 : buf1) + (wave % kEach) * kWaveBytes;
   const bool aligned = (ldy * E) % 16 == 0 && (reinterpret_cast<uintptr_t>(y) & 15) == 0;
   const int64_t c0 = n0 + wn * kCols;
 #pragma unroll
@@ -247,21 +317,33 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_kernel(
       }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
+    const int64_t first = m0 + (wm * TM + j) * 32;
+    if (aligned && c0 + kCols <= N) {
 #pragma unroll
-    for (int it = 0; it < 32 * kChunks / 64; ++it) {
-      const int idx = it * 64 + lane, r = idx / kChunks, c = idx % kChunks;
-      const int64_t m = m0 + (wm * TM + j) * 32 + r, col = c0 + c * (16 / E);
-      const v4u v = *reinterpret_cast<const v4u*>(out + r * kOut + c * 16);
-      if (m < M && col < N) {
-        if (aligned && col + 16 / E <= N) {
-          *reinterpret_cast<v4u*>(reinterpret_cast<uint8_t*>(y) + (m * ldy + col) * E) = v;
-        } else {
+      for (int it = 0; it < 32 * kChunks / 64; ++it) {
+        const int idx = it * 64 + lane, r = idx / kChunks, c = idx % kChunks;
+        const v4u v = *reinterpret_cast<const v4u*>(out + r * kOut + c * 16);
+        if (first + r < M)  // nothing in the kernel reads y back
+          __builtin_nontemporal_store(v, reinterpret_cast<v4u*>(reinterpret_cast<uint8_t*>(y) + ((first + r) * ldy + c0) * E + c * 16));
+      }
+    } else {  // rows that are not 16-byte aligned, or end in the tile: neighbouring lanes store neighbouring values
+      typedef typename std::conditional<BF16, uint16_t, uint32_t>::type Word;
+      constexpr int kRows = kCols < 64 ? 64 / kCols : 1, kPasses = kCols < 64 ? 1 : kCols / 64;  // of an instruction
+      const int r0 = kCols < 64 ? lane / kCols : 0, c1 = kCols < 64 ? lane % kCols : lane;
 #pragma unroll
-          for (int e = 0; e < 16 / E; ++e)
-            if (col + e < N) {
-              if constexpr (BF16) reinterpret_cast<uint16_t*>(y)[m * ldy + col + e] = uint16_t(v[e / 2] >> (16 * (e & 1)));
-              else reinterpret_cast<uint32_t*>(y)[m * ldy + col + e] = v[e];
-            }
+      for (int i = 0; i < 32; i += 8 * kRows) {
+        Word v[8][kPasses];  // read together: the stores below wait for them once
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+#pragma unroll
+          for (int p = 0; p < kPasses; ++p)
+            v[e][p] = *reinterpret_cast<const Word*>(out + (i + e * kRows + r0) * kOut + (c1 + 64 * p) * E);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int64_t m = first + i + e * kRows + r0;
+#pragma unroll
+          for (int p = 0; p < kPasses; ++p)
+            if (m < M && c0 + c1 + 64 * p < N) reinterpret_cast<Word*>(y)[m * ldy + c0 + c1 + 64 * p] = v[e][p];
         }
       }
     }
@@ -271,46 +353,53 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_kernel(
 }
 
 // ---------------------------------------------------------------------------
-// Few rows: a block takes 16 channels and up to 16 MT tokens (grid y: chunks of
+// Few rows: a block takes 16 CT channels and up to 16 MT tokens (grid y: chunks of
 // them), its 8 waves split K in slices of 128 channels, two consecutive ones at a
-// time, so that a wave reads whole 128-byte lines of the weights.  Weights go
-// straight to registers, the next slices are loaded before the current ones are
-// multiplied, the waves' sums meet in LDS.
+// time, so that a wave reads whole 128-byte lines of the rows.  Operands go straight
+// to registers, the next slices are loaded before the current ones are multiplied,
+// the waves' sums meet in LDS.
 // ---------------------------------------------------------------------------
 constexpr int kFewWaves = 8, kFewPair = 2;
 
-template <int MT, bool BF16>
+template <int MT, int CT, bool BF16>
 __global__ __launch_bounds__(64 * kFewWaves) void mx_gemm_few_kernel(
     const uint8_t* __restrict__ qa, const uint32_t* __restrict__ sa, const uint8_t* __restrict__ qw,
     const uint32_t* __restrict__ sw, int64_t M, int64_t N, int64_t K, void* __restrict__ y, int64_t ldy) {
-  __shared__ __align__(16) float sums[kFewWaves][MT * 16][20];  // 16 channels of a token, +4: fewer bank conflicts
+  constexpr int kCols = 16 * CT, kRow = kCols + 4;  // floats of a token's sums; +4: fewer bank conflicts
+  __shared__ __align__(16) float sums[kFewWaves][16][kRow];
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, g4 = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int64_t n0 = int64_t(blockIdx.x) * 16, m0 = int64_t(blockIdx.y) * (16 * MT), row_bytes = K / 2;
+  const int64_t n0 = int64_t(blockIdx.x) * kCols, m0 = int64_t(blockIdx.y) * (16 * MT), row_bytes = K / 2;
   const int G = int(K / kGroup);
-  const int64_t row_w = n0 + n < N ? n0 + n : N - 1;  // rows beyond the last one read that again
-  const uint8_t* pw = qw + row_w * row_bytes + 16 * g4;
-  int64_t row_a[MT];
+  int64_t row_a[MT], row_w[CT];  // rows beyond the last one read that again; what they give is not stored
 #pragma unroll
   for (int i = 0; i < MT; ++i) row_a[i] = m0 + 16 * i + n < M ? m0 + 16 * i + n : M - 1;
+#pragma unroll
+  for (int i = 0; i < CT; ++i) row_w[i] = n0 + 16 * i + n < N ? n0 + 16 * i + n : N - 1;
 
   struct Slice {
-    v4u w, a[MT];
-    uint32_t xw, xa[MT];
+    v4u w[CT], a[MT];
+    uint32_t xw[CT], xa[MT];
   };
   auto load = [&](int g, Slice& s) {
     g = g < G ? g : G - 1;
-    s.w = *reinterpret_cast<const v4u*>(pw + int64_t(g) * 64);
-    s.xw = sw[g * N + row_w];
+    const int64_t at = int64_t(g) * 64 + 16 * g4;
+#pragma unroll
+    for (int i = 0; i < CT; ++i) {
+      s.w[i] = *reinterpret_cast<const v4u*>(qw + row_w[i] * row_bytes + at);
+      s.xw[i] = sw[g * N + row_w[i]];
+    }
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-      s.a[i] = *reinterpret_cast<const v4u*>(qa + row_a[i] * row_bytes + int64_t(g) * 64 + 16 * g4);
+      s.a[i] = *reinterpret_cast<const v4u*>(qa + row_a[i] * row_bytes + at);
       s.xa[i] = sa[g * M + row_a[i]];
     }
   };
-  v4f acc[MT];
+  v4f acc[MT][CT];
 #pragma unroll
-  for (int i = 0; i < MT; ++i) acc[i] = v4f{};
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < CT; ++j) acc[i][j] = v4f{};
   constexpr int kStep = kFewWaves * kFewPair;
   Slice cur[kFewPair], next[kFewPair];
   int g = wave * kFewPair;
@@ -328,23 +417,33 @@ __global__ __launch_bounds__(64 * kFewWaves) void mx_gemm_few_kernel(
       if (g + p < G) {
 #pragma unroll
         for (int i = 0; i < MT; ++i)
-          acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fp4_operand(cur[p].w), fp4_operand(cur[p].a[i]), acc[i],
-                                                                    kFp4, kFp4, 0, int(cur[p].xw >> (8 * g4)), 0,
-                                                                    int(cur[p].xa[i] >> (8 * g4)));
+#pragma unroll
+          for (int j = 0; j < CT; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                fp4_operand(cur[p].w[j]), fp4_operand(cur[p].a[i]), acc[i][j], kFp4, kFp4, 0,
+                int(cur[p].xw[j] >> (8 * g4)), 0, int(cur[p].xa[i] >> (8 * g4)));
       }
     }
 #pragma unroll
     for (int p = 0; p < kFewPair; ++p) cur[p] = next[p];
   }
 #pragma unroll
-  for (int i = 0; i < MT; ++i) *reinterpret_cast<v4f*>(&sums[wave][16 * i + n][4 * g4]) = acc[i];
-  __syncthreads();
-  for (int at = tid; at < MT * 256; at += 64 * kFewWaves) {
-    const int t = at >> 4, c = at & 15;
-    float v = 0.0f;
+  for (int i = 0; i < MT; ++i) {
+    if (i > 0) {
+      if (m0 + 16 * i >= M) return;  // the whole block
+      __syncthreads();
+    }
 #pragma unroll
-    for (int w = 0; w < kFewWaves; ++w) v += sums[w][t][c];
-    if (m0 + t < M && n0 + c < N) store_one<BF16>(y, (m0 + t) * ldy + n0 + c, v);
+    for (int j = 0; j < CT; ++j) *reinterpret_cast<v4f*>(&sums[wave][n][16 * j + 4 * g4]) = acc[i][j];
+    __syncthreads();
+    for (int at = tid; at < 16 * kCols; at += 64 * kFewWaves) {
+      const int t = at / kCols, c = at % kCols;
+      float v = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kFewWaves; ++w) v += sums[w][t][c];
+      const int64_t m = m0 + 16 * i + t;
+      if (m < M && n0 + c < N) store_one<BF16>(y, m * ldy + n0 + c, v);
+    }
   }
 }
 
@@ -354,36 +453,59 @@ hipError_t launch_mx_gemm(const uint8_t* qa, const uint8_t* sa, const uint8_t* q
                           int64_t N, int64_t K, void* y, bool y_bf16, int64_t ldy, hipStream_t st) {
   const uint32_t* xa = reinterpret_cast<const uint32_t*>(sa);
   const uint32_t* xw = reinterpret_cast<const uint32_t*>(sw);
-  auto few = [&](auto mt) {
-    constexpr int MT = decltype(mt)::value;
-    const int64_t blocks = (N + 15) / 16, chunks = (M + 16 * MT - 1) / (16 * MT);
-    if (blocks > (int64_t(1) << 22)) return hipErrorInvalidValue;
+  auto few = [&](auto mt, auto ct) {
+    constexpr int MT = decltype(mt)::value, CT = decltype(ct)::value;
+    const int64_t blocks = (N + 16 * CT - 1) / (16 * CT), chunks = (M + 16 * MT - 1) / (16 * MT);
+    if (blocks > (int64_t(1) << 22) || chunks > 65535) return hipErrorInvalidValue;
     const dim3 grid{unsigned(blocks), unsigned(chunks), 1u};
     if (y_bf16)
-      hipLaunchKernelGGL((mx_gemm_few_kernel<MT, true>), grid, dim3(64 * kFewWaves), 0, st, qa, xa, qw, xw, M, N, K, y, ldy);
+      hipLaunchKernelGGL((mx_gemm_few_kernel<MT, CT, true>), grid, dim3(64 * kFewWaves), 0, st, qa, xa, qw, xw, M, N, K, y, ldy);
     else
-      hipLaunchKernelGGL((mx_gemm_few_kernel<MT, false>), grid, dim3(64 * kFewWaves), 0, st, qa, xa, qw, xw, M, N, K, y, ldy);
+      hipLaunchKernelGGL((mx_gemm_few_kernel<MT, CT, false>), grid, dim3(64 * kFewWaves), 0, st, qa, xa, qw, xw, M, N, K, y, ldy);
     return hipGetLastError();
   };
-  auto many = [&](auto bm, auto bn, auto wm, auto wn) {
-    constexpr int BM = decltype(bm)::value, BN = decltype(bn)::value, WM = decltype(wm)::value, WN = decltype(wn)::value;
+  auto many = [&](auto bm, auto bn, auto wm, auto wn, auto ring) {
+    constexpr int BM = decltype(bm)::value, BN = decltype(bn)::value, WM = decltype(wm)::value, WN = decltype(wn)::value,
+                  R = decltype(ring)::value;
     const int64_t tiles_m = (M + BM - 1) / BM, blocks = tiles_m * ((N + BN - 1) / BN);
     if (blocks > (int64_t(1) << 22)) return hipErrorInvalidValue;
     const dim3 grid{unsigned(blocks)}, threads{64 * WM * WN};
     if (y_bf16)
-      hipLaunchKernelGGL((mx_gemm_kernel<BM, BN, WM, WN, true>), grid, threads, 0, st, qa, xa, qw, xw, M, N, K, y, ldy,
+      hipLaunchKernelGGL((mx_gemm_kernel<BM, BN, WM, WN, R, true>), grid, threads, 0, st, qa, xa, qw, xw, M, N, K, y, ldy,
                          tiles_m);
     else
-      hipLaunchKernelGGL((mx_gemm_kernel<BM, BN, WM, WN, false>), grid, threads, 0, st, qa, xa, qw, xw, M, N, K, y, ldy,
+      hipLaunchKernelGGL((mx_gemm_kernel<BM, BN, WM, WN, R, false>), grid, threads, 0, st, qa, xa, qw, xw, M, N, K, y, ldy,
                          tiles_m);
     return hipGetLastError();
   };
   using std::integral_constant;
-  if (M <= 16) return few(integral_constant<int, 1>{});
-  if (M <= 64) return few(integral_constant<int, 4>{});
-  const integral_constant<int, 128> k128{};
+  const integral_constant<int, 1> k1{};
   const integral_constant<int, 2> k2{};
-  return many(k128, k128, k2, k2);
+  const integral_constant<int, 4> k4{};
+  const integral_constant<int, 128> k128{};
+  const integral_constant<int, 256> k256{};
+  const integral_constant<int, 64> k64{};
+  const integral_constant<int, 3> k3{};
+  // Measured with K = 4096 (times in us, launch included).  The kernel for few rows reads
+  // all of its tokens for every 16 or 32 channels, the tiles wait for the memory once a
+  // stage whatever their number, so the former is for small M N, or few tokens:
+  //   M x N         few / 64 x 64 tiles       M x N         few / 64 x 64 tiles
+  //   1 x 4096      3.8 / 7.1                 61 x 4096     6.6 / 7.1
+  //   1 x 14336     7.6 / 7.3                 61 x 6144     10.0 / 7.1
+  //   16 x 8192     6.2 / 7.0                 61 x 11008    14.0 / 7.4
+  //   16 x 14336    9.9 / 7.1                 100 x 2048    6.4 / 7.1
+  if (M <= 8 || (N <= 8192 && M * N <= (int64_t(1) << 18))) return M <= 16 ? few(k1, k1) : few(k2, k2);
+  // 64 x 64, 128 x 128: up to 2 1/2 of the small tiles for each CU
+  //   512 x 4096 (512 small tiles) 10.0 / 13.2, 256 x 11008 (688) 13.6 / 13.5,
+  //   384 x 8192 (768) 14.1 / 13.6, 1024 x 4096 (1024) 18.3 / 14.5
+  const int64_t small = ((M + 63) / 64) * ((N + 63) / 64);
+  if (small <= 640) return many(k64, k64, k2, k2, k3);
+  // 128 x 128, 256 x 256: the large tiles where they fill 7/8 of the rounds of a block for
+  // each CU that they take
+  //   2048 x 4096 (128 large tiles) 22 / 29, 2048 x 6144 (192) 32 / 33, 2048 x 8192 (256) 41 / 37,
+  //   3000 x 6144 (288) 49 / 58, 2048 x 14336 (448) 70 / 65; 4096 x 14336 x 4096 127 / 105
+  const int64_t large = ((M + 255) / 256) * ((N + 255) / 256), rounds = (large + 255) / 256;
+  return 8 * large >= 7 * 256 * rounds ? many(k256, k256, k4, k2, k2) : many(k128, k128, k2, k2, k2);
 }
 
 }  // namespace rw4
