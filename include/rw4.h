@@ -453,7 +453,7 @@ rw4_status rw4_dequantize_g(const uint8_t* q, const float* s, int64_t M, int64_t
  *   scales s [K/128, rows, 4] bytes: byte i of (g, r) is the exponent plus 127
  *   (E8M0) of channels 128g + 32i .. of row r; 255 is NaN.  So the scales of one
  *   128-channel group lie side by side for all rows.
- * K is a multiple of 128 and at most 2^23, rows at most 2^31.
+ * K is a multiple of 128 and at most 2^23, rows at most 2^28.
  *
  * rw4_mx_quantize_act: x [M, K] (ldx elements a row, 16-byte rows) through the
  * transform t, then per 32 channels

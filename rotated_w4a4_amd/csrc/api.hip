@@ -618,8 +618,8 @@ rw4_status rw4_w4a4_gemm(const uint8_t* qa, const float* sa, const uint8_t* qw, 
 
 // Channels of an MXFP4 row, at most: a tile of 256 rows stays below 2^31 bytes.
 constexpr int64_t kMostMxK = int64_t(1) << 23;
-// Rows of an operand, at most: row numbers and scale offsets of a tile stay in 32 bits.
-constexpr int64_t kMostMxRows = int64_t(1) << 31;
+// Rows of an operand, at most: the offsets of 4 groups' scales stay in 32 bits.
+constexpr int64_t kMostMxRows = int64_t(1) << 28;
 constexpr int64_t kMostMxStride = int64_t(1) << 40;
 
 static rw4_status mx_sizes(int64_t rows, int64_t K) {

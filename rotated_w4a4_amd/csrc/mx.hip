@@ -199,10 +199,10 @@ __device__ __forceinline__ MxWord encode(float (&v)[8], Load load, int lane) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = butterfly_x<32>(v[e], lane);
     }
-    uint32_t top = 0;
+    float most8 = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7FFFFFFFu);
-    top = block_max<BLOCK>(top);
+    for (int e = 0; e < 8; ++e) most8 = fmaxf(most8, fabsf(v[e]));  // NaN is seen in S
+    const uint32_t top = block_max<BLOCK>(__float_as_uint(most8));
     const float err = S * (kPost32<BLOCK> * float(n + 5) * 0x1p-24f);
     const float most = __uint_as_float(top) * kPost32<BLOCK>;
     const uint32_t at = __float_as_uint(most + err) >> 23;
@@ -224,140 +224,231 @@ __device__ __forceinline__ MxWord encode(float (&v)[8], Load load, int lane) {
   }
 }
 
-__device__ __forceinline__ void store_word(const MxRows& a, int64_t row, int64_t k0, int lane, const MxWord& r) {
-  // k0: first channel of the wave's span
-  const int64_t g = (k0 >> 7) + (lane >> 4);
-  *reinterpret_cast<uint32_t*>(a.q + row * (a.K >> 1) + 64 * g + 4 * r.word) = r.codes;
-  if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(a.s + (g * a.rows + row) * 4) = r.scales;
+// Stores the lane's word of the wave's span (first channel k0, `channels` of them in
+// the row).  Lanes without anything to store do so out of range, where the hardware
+// drops it: a branch would make the compiler wait for everything in flight, the next
+// row's loads among it.  Rows are at most 2^28, so offsets stay in 32 bits.
+__device__ __forceinline__ void store_word(const MxRows& a, int64_t row, int64_t k0, int channels, int lane, const MxWord& r) {
+  const int g = lane >> 4;
+  __builtin_amdgcn_raw_buffer_store_b32(
+      r.codes, __builtin_amdgcn_make_buffer_rsrc(a.q + row * (a.K >> 1) + (k0 >> 1), 0, channels >> 1, 0x00020000),
+      64 * g + 4 * r.word, 0, 0);
+  const uint32_t group = uint32_t(a.rows) * 4;  // bytes from one group's scales to the next
+  __builtin_amdgcn_raw_buffer_store_b32(
+      r.scales,
+      __builtin_amdgcn_make_buffer_rsrc(a.s + ((k0 >> 7) * a.rows + row) * 4, 0, int(group * ((channels >> 7) - 1) + 4),
+                                        0x00020000),
+      (lane & 15) == 0 ? int(g * group) : -1, 0, 0);
 }
 
 // ---------------------------------------------------------------------------
-// Rows with unit stride: a wave takes 512 channels of a row, the grid walks the
-// spans of all rows in order; the next span is loaded before the current one is
-// computed.
+// Rows with unit stride: a wave keeps one span of 512 channels and walks rows, the
+// waves of a block side by side along a row.  The next row's values are on their way
+// while the current ones are computed.
 // ---------------------------------------------------------------------------
 template <bool BF16, int BLOCK, bool SIGNED>
-__global__ __launch_bounds__(256) void mx_quantize_kernel(MxRows a) {
+__global__ __launch_bounds__(256) void mx_quantize_kernel(MxRows a, uint32_t spans, uint32_t rows_apart) {
+  typedef unsigned int v4u __attribute__((ext_vector_type(4)));
+  constexpr int kSize = BF16 ? 2 : 4, kLoads = BF16 ? 1 : 2;
   const int lane = threadIdx.x & 63;
-  const int64_t spans = (a.K + kSpan - 1) / kSpan;
-  const int64_t waves = int64_t(gridDim.x) * 4, first = int64_t(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t step_row = waves / spans, step_span = waves % spans;
-  int64_t row = first / spans, span = first % spans;
-  auto load = [&](int64_t r, int64_t sp, float (&v)[8]) {
-    const int64_t k = sp * kSpan + 8 * lane;
-    if (k < a.K) {
-      RowSrc<BF16> src{a.x, a.stride_row};
-      if constexpr (SIGNED) SignedSrc<RowSrc<BF16>>{src, a.sign_mask}.load8(r, k, v);
-      else src.load8(r, k, v);
-    } else {
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
+  const uint32_t span = wave % spans;
+  int64_t row = wave / spans;
+  if (row >= rows_apart || row >= a.rows) return;
+  const int64_t k0 = int64_t(span) * kSpan;
+  const int channels = int(a.K - k0 < kSpan ? a.K - k0 : kSpan);  // behind them loads give zeros
+  const char* const x = reinterpret_cast<const char*>(a.x) + k0 * kSize;
+  struct Raw {
+    v4u v[kLoads];
+  };
+  auto load = [&](int64_t r) {
+    const __amdgpu_buffer_rsrc_t from = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(x + r * a.stride_row * kSize), 0,
+                                                                          channels * kSize, 0x00020000);
+    Raw raw;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+    for (int i = 0; i < kLoads; ++i) raw.v[i] = __builtin_amdgcn_raw_buffer_load_b128(from, lane * (8 * kSize) + 16 * i, 0, 0);
+    return raw;
+  };
+  uint32_t sign[8] = {};
+  if constexpr (SIGNED) {
+    const __amdgpu_buffer_rsrc_t from =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint32_t*>(a.sign_mask + k0), 0, channels * 4, 0x00020000);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const v4u m = __builtin_amdgcn_raw_buffer_load_b128(from, lane * 32 + 16 * i, 0, 0);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sign[4 * i + e] = m[e];
+    }
+  }
+  auto open = [&](const Raw& raw, float(&v)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if constexpr (BF16) v[e] = (e & 1) ? bf16_hi(raw.v[0][e >> 1]) : bf16_lo(raw.v[0][e >> 1]);
+      else v[e] = __uint_as_float(raw.v[(e >> 2) % kLoads][e & 3]);
+      if constexpr (SIGNED) v[e] = __uint_as_float(__float_as_uint(v[e]) ^ sign[e]);
     }
   };
-  float next[8];
-  if (row < a.rows) load(row, span, next);
+  Raw next = load(row);
   while (row < a.rows) {
+    const Raw raw = next;
+    const int64_t row2 = row + rows_apart;
+    next = load(row2 < a.rows ? row2 : row);
     float v[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = next[e];
-    int64_t row2 = row + step_row, span2 = span + step_span;
-    if (span2 >= spans) {
-      span2 -= spans;
-      ++row2;
-    }
-    if (row2 < a.rows) load(row2, span2, next);
-    const MxWord r = encode<BLOCK>(v, [&](float(&w)[8]) { load(row, span, w); }, lane);
-    if (span * kSpan + 8 * lane < a.K) store_word(a, row, span * kSpan, lane, r);
+    open(raw, v);
+    const MxWord r = encode<BLOCK>(v, [&](float(&w)[8]) { open(raw, w); }, lane);
+    store_word(a, row, k0, channels, lane, r);
     row = row2;
-    span = span2;
   }
 }
 
 // ---------------------------------------------------------------------------
-// Rows of any strides (weights [K, N]): a block brings 32 rows x 512 channels
-// into LDS, its lanes along whichever stride is 1, then encodes them from there.
-// Channel k of a row lies at k + k / 8, so that 64 lanes reading every ninth
-// word hit all banks; rows are an odd number of words apart for the writes.
+// Rows of any strides (weights [K, N]): a block brings some rows of one Hadamard block
+// (128 channels at least) into LDS, then encodes them from there, 16 lanes or more a
+// row.  VECTOR: rows lie side by side (stride_row 1) and 16-byte loads fit; otherwise
+// single values, the lanes along whichever stride is the smaller.  Channel k of a row
+// lies at k + k / 8, so that lanes reading every ninth word hit all banks; rows are an
+// odd number of words apart for the writes.
 // ---------------------------------------------------------------------------
-constexpr int kPackRows = 32;
-constexpr int kPackRow = kSpan + kSpan / 8 + 1;
+template <int BLOCK>
+struct Pack {
+  static constexpr int span = BLOCK < 128 ? 128 : BLOCK, rows = BLOCK < 512 ? 64 : 32;
+  static constexpr int row = span + span / 8 + 1, lanes = span / 8;
+};
 
-template <bool BF16, int BLOCK, bool SIGNED>
+template <bool BF16, int BLOCK, bool SIGNED, bool VECTOR>
 __global__ __launch_bounds__(256) void mx_pack_kernel(MxRows a, int64_t spans) {
-  __shared__ float tile[kPackRows * kPackRow];
+  using P = Pack<BLOCK>;
+  __shared__ float tile[P::rows * P::row];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int64_t row0 = (blockIdx.x / spans) * kPackRows, k0 = (blockIdx.x % spans) * kSpan;
-  const int64_t rows = a.rows - row0 < kPackRows ? a.rows - row0 : kPackRows;
-  const int64_t channels = a.K - k0 < kSpan ? a.K - k0 : kSpan;
-  const bool along_rows = a.stride_row <= a.stride_k;
-  const StridedSrc<BF16> src{a.x, a.stride_k, a.stride_row};
-#pragma unroll 8
-  for (int i = 0; i < kPackRows * kSpan / 256; ++i) {
-    const int at = i * 256 + tid;
-    const int r = along_rows ? at % kPackRows : at / kSpan, k = along_rows ? at / kPackRows : at % kSpan;
-    float v = 0.0f;
-    if (r < rows && k < channels) {
-      v = src.at(row0 + r, k0 + k);
-      if constexpr (SIGNED) v = __uint_as_float(__float_as_uint(v) ^ a.sign_mask[k0 + k]);
+  const int64_t row0 = (blockIdx.x / spans) * P::rows, k0 = (blockIdx.x % spans) * P::span;  // spans are whole
+  const int rows = int(a.rows - row0 < P::rows ? a.rows - row0 : P::rows);
+  auto put = [&](int r, int k, float v) {
+    if constexpr (SIGNED) v = __uint_as_float(__float_as_uint(v) ^ a.sign_mask[k0 + k]);
+    tile[r * P::row + k + (k >> 3)] = v;
+  };
+  if constexpr (VECTOR) {
+    constexpr int E = BF16 ? 8 : 4, kAcross = P::rows / E, kPasses = P::span * kAcross / 256;
+    const int r = (tid % kAcross) * E;
+    const char* from = reinterpret_cast<const char*>(a.x) + (row0 + (r < rows ? r : 0)) * (BF16 ? 2 : 4);
+#pragma unroll
+    for (int i0 = 0; i0 < kPasses; i0 += 8) {
+      uint4 w[8];
+#pragma unroll
+      for (int i = 0; i < 8 && i0 + i < kPasses; ++i) {
+        const int k = (i0 + i) * (256 / kAcross) + tid / kAcross;
+        w[i] = *reinterpret_cast<const uint4*>(from + (k0 + k) * a.stride_k * (BF16 ? 2 : 4));  // rows is a multiple of E
+      }
+#pragma unroll
+      for (int i = 0; i < 8 && i0 + i < kPasses; ++i) {
+        const int k = (i0 + i) * (256 / kAcross) + tid / kAcross;
+        const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          put(r + e, k, BF16 ? ((e & 1) ? bf16_hi(u[e >> 1]) : bf16_lo(u[e >> 1])) : __uint_as_float(u[e & 3]));
+      }
     }
-    tile[r * kPackRow + k + (k >> 3)] = v;
+  } else {
+    const bool along_rows = a.stride_row <= a.stride_k;
+    const StridedSrc<BF16> src{a.x, a.stride_k, a.stride_row};
+#pragma unroll 8
+    for (int i = 0; i < P::rows * P::span / 256; ++i) {
+      const int at = i * 256 + tid;
+      const int r = along_rows ? at % P::rows : at / P::span, k = along_rows ? at / P::rows : at % P::span;
+      put(r, k, src.at(row0 + (r < rows ? r : 0), k0 + k));
+    }
   }
   __syncthreads();
-  for (int r = wave; r < rows; r += 4) {
+  constexpr int kTogether = 64 / P::lanes;  // rows of a wave
+  const int l = lane % P::lanes;
+  for (int r0 = wave * kTogether; r0 < rows; r0 += 4 * kTogether) {
+    const int r = r0 + lane / P::lanes;
     auto load = [&](float(&v)[8]) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = tile[r * kPackRow + 9 * lane + e];
+      for (int e = 0; e < 8; ++e) v[e] = tile[r * P::row + 9 * l + e];
     };
     float v[8];
     load(v);
     const MxWord w = encode<BLOCK>(v, load, lane);
-    if (8 * lane < channels) store_word(a, row0 + r, k0, lane, w);
+    if (r < rows) {
+      const int64_t g = (k0 >> 7) + (l >> 4);
+      *reinterpret_cast<uint32_t*>(a.q + (row0 + r) * (a.K >> 1) + 64 * g + 4 * w.word) = w.codes;
+      if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(a.s + (g * a.rows + row0 + r) * 4) = w.scales;
+    }
   }
 }
 
 // ---------------------------------------------------------------------------
-// Reading back: 8 codes a lane.  Values are exact in bf16 and fp32.
+// Reading back: a wave keeps one span of 512 channels, 8 a lane, and walks rows, four at
+// a time, the next four on their way.  Values are exact in bf16 and fp32.  Lanes
+// behind the last channel load zeros and store out of range, where it is dropped.
 // ---------------------------------------------------------------------------
+constexpr int kBackRows = 4;
+
 template <bool BF16>
-__global__ __launch_bounds__(256) void mx_dequantize_kernel(const uint8_t* q, const uint8_t* s, int64_t M, int64_t K,
-                                                            void* out, int64_t ldo) {
+__global__ __launch_bounds__(256) void mx_dequantize_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ s,
+                                                            int64_t M, int64_t K, void* __restrict__ out, int64_t ldo,
+                                                            uint32_t spans, uint32_t walkers) {
   typedef float v2f __attribute__((ext_vector_type(2)));
-  const int64_t words = K >> 3, step = int64_t(gridDim.x) * 256, all = M * words;
-  int64_t at = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  int64_t row = at / words, word = at % words;
-  const int64_t step_row = step / words, step_word = step % words;
-  for (; at < all; at += step) {
-    const uint32_t w = reinterpret_cast<const uint32_t*>(q)[at];
-    const uint32_t e = s[((word >> 4) * M + row) * 4 + ((word >> 2) & 3)];
-    v2f p[4];
-    p[0] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0);
-    p[1] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1);
-    p[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2);
-    p[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
-    float v[8];
+  typedef unsigned int v4u __attribute__((ext_vector_type(4)));
+  constexpr int kSize = BF16 ? 2 : 4;
+  const int lane = threadIdx.x & 63;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
+  const int64_t k0 = int64_t(wave % spans) * kSpan;
+  int64_t row = int64_t(wave / spans) * kBackRows;
+  if (wave / spans >= walkers) return;
+  const int channels = int(K - k0 < kSpan ? K - k0 : kSpan);
+  // the lane's scale byte in its group's words of the rows, rows at most 2^28
+  const uint32_t group = uint32_t(M) * 4, at = uint32_t(lane >> 4) * group;
+  const int shift = 8 * ((lane >> 2) & 3);
+  struct Raw {
+    uint32_t codes[kBackRows], scales[kBackRows];
+  };
+  auto load = [&](int64_t r, Raw& raw) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float x = ldexpf(p[i >> 1][i & 1], int(e) - 127);
-      v[i] = e == 255 ? __builtin_nanf("") : x;
+    for (int i = 0; i < kBackRows; ++i) {
+      const int64_t n = r + i < M ? r + i : M - 1;
+      raw.codes[i] = __builtin_amdgcn_raw_buffer_load_b32(
+          __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(q + n * (K >> 1) + (k0 >> 1)), 0, channels >> 1, 0x00020000),
+          lane * 4, 0, 0);
+      raw.scales[i] = __builtin_amdgcn_raw_buffer_load_b32(
+          __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(s + ((k0 >> 7) * M + n) * 4), 0,
+                                            int(group * ((channels >> 7) - 1) + 4), 0x00020000),
+          int(at), 0, 0);
     }
-    const int64_t o = row * ldo + 8 * word;
-    if constexpr (BF16) {
-      uint32_t b[4];
+  };
+  Raw next;
+  load(row, next);
+  while (row < M) {
+    const Raw raw = next;
+    const int64_t row2 = row + int64_t(walkers) * kBackRows;
+    load(row2 < M ? row2 : row, next);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)  // exact: the lower halves are zero (NaN: its upper half is NaN)
-        b[i] = (__float_as_uint(v[2 * i]) >> 16) | (__float_as_uint(v[2 * i + 1]) & 0xFFFF0000u);
-      *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(out) + o) = make_uint4(b[0], b[1], b[2], b[3]);
-    } else {
-      float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + o);
-      dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-      dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+    for (int i = 0; i < kBackRows; ++i) {
+      const uint32_t w = raw.codes[i], e = (raw.scales[i] >> shift) & 255u;
+      const v2f p[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0), __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1),
+                        __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2), __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3)};
+      uint32_t v[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const float x = ldexpf(p[c >> 1][c & 1], int(e) - 127);
+        v[c] = __float_as_uint(e == 255u ? __builtin_nanf("") : x);
+      }
+      // rows behind the last one: an empty range
+      const int64_t n = row + i;
+      const __amdgpu_buffer_rsrc_t to = __builtin_amdgcn_make_buffer_rsrc(
+          reinterpret_cast<char*>(out) + (n < M ? n * ldo + k0 : 0) * kSize, 0, n < M ? channels * kSize : 0, 0x00020000);
+      if constexpr (BF16) {
+        v4u b;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)  // exact: the lower halves are zero (NaN: its upper half is NaN)
+          b[c] = (v[2 * c] >> 16) | (v[2 * c + 1] & 0xFFFF0000u);
+        __builtin_amdgcn_raw_buffer_store_b128(b, to, lane * 16, 0, 0);
+      } else {
+        __builtin_amdgcn_raw_buffer_store_b128(v4u{v[0], v[1], v[2], v[3]}, to, lane * 32, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(v4u{v[4], v[5], v[6], v[7]}, to, lane * 32 + 16, 0, 0);
+      }
     }
-    row += step_row;
-    word += step_word;
-    if (word >= words) {
-      word -= words;
-      ++row;
-    }
+    row = row2;
   }
 }
 
@@ -381,33 +472,48 @@ hipError_t by_kind(const MxRows& a, F f) {
 }  // namespace
 
 hipError_t launch_mx_quantize(const MxRows& a, hipStream_t st) {
-  const int64_t spans = (a.K + kSpan - 1) / kSpan, items = a.rows * spans;
-  const int64_t full = 256 * 8;  // 8 blocks of 4 waves a CU
-  const int64_t need = (items + 3) / 4, blocks = need < full ? need : full;
+  const int64_t spans = (a.K + kSpan - 1) / kSpan;  // at most 2^14
+  const int64_t full = 256 * 32;                    // waves the card holds
+  int64_t apart = full / spans > 1 ? full / spans : 1;
+  apart = apart < a.rows ? apart : a.rows;
+  const int64_t blocks = (spans * apart + 3) / 4;
   return by_kind(a, [&](auto bf16, auto block, auto sign) {
     hipLaunchKernelGGL((mx_quantize_kernel<decltype(bf16)::value, decltype(block)::value, decltype(sign)::value>),
-                       dim3(unsigned(blocks)), dim3(256), 0, st, a);
+                       dim3(unsigned(blocks)), dim3(256), 0, st, a, uint32_t(spans), uint32_t(apart));
     return hipGetLastError();
   });
 }
 
 hipError_t launch_mx_pack(const MxRows& a, hipStream_t st) {
-  const int64_t spans = (a.K + kSpan - 1) / kSpan, blocks = (a.rows + kPackRows - 1) / kPackRows * spans;
-  if (blocks > (int64_t(1) << 23)) return hipErrorInvalidValue;  // a grid has fewer than 2^32 threads
+  const int64_t size = a.bf16 ? 2 : 4;
+  const bool vector = a.stride_row == 1 && (a.stride_k * size) % 16 == 0 && (a.rows * size) % 16 == 0 &&
+                      (reinterpret_cast<uintptr_t>(a.x) & 15) == 0;
   return by_kind(a, [&](auto bf16, auto block, auto sign) {
-    hipLaunchKernelGGL((mx_pack_kernel<decltype(bf16)::value, decltype(block)::value, decltype(sign)::value>),
-                       dim3(unsigned(blocks)), dim3(256), 0, st, a, spans);
+    using P = Pack<decltype(block)::value>;
+    const int64_t spans = a.K / P::span, blocks = (a.rows + P::rows - 1) / P::rows * spans;
+    if (blocks > (int64_t(1) << 23)) return hipErrorInvalidValue;  // a grid has fewer than 2^32 threads
+    if (vector)
+      hipLaunchKernelGGL((mx_pack_kernel<decltype(bf16)::value, decltype(block)::value, decltype(sign)::value, true>),
+                         dim3(unsigned(blocks)), dim3(256), 0, st, a, spans);
+    else
+      hipLaunchKernelGGL((mx_pack_kernel<decltype(bf16)::value, decltype(block)::value, decltype(sign)::value, false>),
+                         dim3(unsigned(blocks)), dim3(256), 0, st, a, spans);
     return hipGetLastError();
   });
 }
 
 hipError_t launch_mx_dequantize(const uint8_t* q, const uint8_t* s, int64_t M, int64_t K, void* out, bool out_bf16,
                                 int64_t ldo, hipStream_t st) {
-  const int64_t need = (M * (K >> 3) + 255) / 256, full = 256 * 16, blocks = need < full ? need : full;
+  const int64_t spans = (K + kSpan - 1) / kSpan, most = (M + kBackRows - 1) / kBackRows;
+  int64_t walkers = 256 * 32 / spans > 1 ? 256 * 32 / spans : 1;  // as many waves as the card holds
+  walkers = walkers < most ? walkers : most;
+  const dim3 grid{unsigned((spans * walkers + 3) / 4)};
   if (out_bf16)
-    hipLaunchKernelGGL((mx_dequantize_kernel<true>), dim3(unsigned(blocks)), dim3(256), 0, st, q, s, M, K, out, ldo);
+    hipLaunchKernelGGL((mx_dequantize_kernel<true>), grid, dim3(256), 0, st, q, s, M, K, out, ldo, uint32_t(spans),
+                       uint32_t(walkers));
   else
-    hipLaunchKernelGGL((mx_dequantize_kernel<false>), dim3(unsigned(blocks)), dim3(256), 0, st, q, s, M, K, out, ldo);
+    hipLaunchKernelGGL((mx_dequantize_kernel<false>), grid, dim3(256), 0, st, q, s, M, K, out, ldo, uint32_t(spans),
+                       uint32_t(walkers));
   return hipGetLastError();
 }
 

@@ -27,7 +27,7 @@ SIZES = [(dict(K=0), SHAPE), (dict(K=-128), SHAPE), (dict(K=100), SHAPE), (dict(
 
 
 @pytest.mark.parametrize("change,want", SIZES + [
-    (dict(M=-1), SHAPE), (dict(M=(1 << 31) + 1), SHAPE), (dict(x=None), ARG), (dict(x=P + 2), ARG), (dict(ldx=255), ARG),
+    (dict(M=-1), SHAPE), (dict(M=(1 << 28) + 1), SHAPE), (dict(x=None), ARG), (dict(x=P + 2), ARG), (dict(ldx=255), ARG),
     (dict(ldx=260), ARG), (dict(ldx=1 << 40), ARG), (dict(dt=0, ldx=258), ARG), (dict(M=0, x=None, q=None, s=None), OK)])
 def test_quantize_refusals(change, want):
     assert _call(lib.rw4_mx_quantize_act, ACT, ACT_OK, **change) == want
