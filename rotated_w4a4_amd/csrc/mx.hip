@@ -10,18 +10,17 @@
 //
 // Exactness.  Codes and exponents are those of the exact y.  The butterflies run
 // in fp32 and keep a bound of their error: each of the n stages rounds every
-// intermediate once, all intermediates of an output are at most S = sum |x| over
-// the Hadamard block, so |u - exact| <= n 2^-24 S (1 + tiny); forming y = u c 2^-E
-// and the two values below costs 3 roundings of at most S more, and the sum S
-// itself is short of the exact one by less than 2^-19 of it, so
-//   d = (n + 5) 2^-24 S c 2^-E
-// covers everything.  A lane converts y - d and y + d: where the codes of both
-// are the same they are the code of the exact value.  Otherwise, or where the
-// maximum could lie on either side of a power of two, the wave evaluates its rows
-// again in fp64 (about one wave of 512 values in 50 for Gaussian values in blocks
-// of 128).  fp64 for every row would take several times as long, fp32 alone would
-// decide ties by the order of its additions: with blocks of 256 and bf16 values,
-// exact ties are common.
+// intermediate once, and the intermediates of a stage that an output depends on add
+// up to at most S = sum |x| over the Hadamard block, so |u - exact| <= n 2^-24 S (1 +
+// tiny).  Forming y = u c 2^-E costs the roundings of c 2^-E and of the result, 2^-24 of
+// |y| < 8 each.  With
+//   d = (n + 1/8) 2^-24 S c 2^-E + 2^-20
+// (the eighth for S's own roundings, below 2^-19 of it) a lane converts y - d and y + d:
+// where the codes of both are the same they are the code of the exact value.  Otherwise,
+// or where the maximum could lie on either side of a power of two, the wave evaluates
+// its rows again in fp64 (about one wave of 512 Gaussian values in 60 in blocks of 128).
+// fp64 for every row would take several times as long, fp32 alone would decide ties by
+// the order of its additions: with blocks of 256 and bf16 values, exact ties are common.
 #include <type_traits>
 
 #include "mx_internal.h"
@@ -91,6 +90,30 @@ __device__ __forceinline__ float block_sum(float s) {
   return s;
 }
 
+// A lane's value and that of lane ^ M (16 or 32): of the lane whose bit M is clear, and
+// of the other.  Exchanging the upper halves (odd rows of 16) of a register with the
+// lower ones (even rows) of its copy leaves just that.
+struct Both {
+  uint32_t clear, set;
+};
+template <int M>
+__device__ __forceinline__ Both both(uint32_t v) {
+  static_assert(M == 16 || M == 32, "lane masks of the swaps");
+  if constexpr (M == 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return Both{r[0], r[1]};
+  } else {
+    const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return Both{r[0], r[1]};
+  }
+}
+// The butterfly over lane bit M.
+template <int M>
+__device__ __forceinline__ float lane_stage_swap(float v, int lane) {
+  const Both b = both<M>(__float_as_uint(v));
+  return fmaf((lane & M) ? -1.0f : 1.0f, __uint_as_float(b.set), __uint_as_float(b.clear));
+}
+
 // The four scale bytes of 128 channels from the lanes that hold them: byte b in
 // its place, or-ed over lanes with different b.
 template <int BLOCK>
@@ -111,65 +134,97 @@ struct MxWord {
   int word;
 };
 
-__device__ __forceinline__ double shfl_xor64(double v, int mask) { return __shfl_xor(v, mask); }
+// v of lane ^ 1, 2, 7 or 8 (CTRL a DPP control), in 64 bits.
+template <int CTRL>
+__device__ __forceinline__ double dpp64(double v) {
+  const long long b = __double_as_longlong(v);
+  const uint32_t lo = uint32_t(__builtin_amdgcn_mov_dpp(int(b), CTRL, 0xF, 0xF, true));
+  const uint32_t hi = uint32_t(__builtin_amdgcn_mov_dpp(int(b >> 32), CTRL, 0xF, 0xF, true));
+  return __longlong_as_double((long long)((uint64_t(hi) << 32) | lo));
+}
+template <int CTRL>
+__device__ __forceinline__ void lane_stage64(double (&u)[8], bool negative) {
+  const double c = negative ? -1.0 : 1.0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) u[e] = fma(dpp64<CTRL>(u[e]), c, u[e]);
+}
 
-// The rows of the wave in fp64, in channel order (rarely called).
-template <int BLOCK, class Load>
-__device__ __forceinline__ MxWord encode64(Load load, int lane) {
-  float v[8];
-  load(v);
+template <int M>
+__device__ __forceinline__ void lane_stage64_swap(double (&u)[8], int lane) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const uint64_t b = uint64_t(__double_as_longlong(u[e]));
+    const Both lo = both<M>(uint32_t(b)), hi = both<M>(uint32_t(b >> 32));
+    const double clear = __longlong_as_double((long long)((uint64_t(hi.clear) << 32) | lo.clear));
+    const double set = __longlong_as_double((long long)((uint64_t(hi.set) << 32) | lo.set));
+    u[e] = fma((lane & M) ? -1.0 : 1.0, set, clear);
+  }
+}
+
+// |x| as an fp32 number on the same side of every number of few bits: where x lies
+// between two fp32 numbers, the one whose last bit is 1.
+__device__ __forceinline__ float to_odd(double x) {
+  const float f = float(x);
+  const double rest = x - double(f);
+  const uint32_t bits = __float_as_uint(f);
+  const uint32_t odd = bits + (rest > 0.0 ? 1u : rest < 0.0 ? ~0u : 0u);
+  return __uint_as_float((bits & 1u) ? bits : odd);
+}
+
+// The wave's rows in fp64, in the lanes' order of the stages of encode (rarely called).
+template <int BLOCK>
+__device__ __forceinline__ MxWord encode64(const float (&v)[8], int lane) {
+  const int l = lane & 15;
   double u[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) u[e] = v[e];
-  if constexpr (BLOCK > 1) {
 #pragma unroll
-    for (int h = 1; h < 8; h <<= 1)
+  for (int h = 1; h < 8; h <<= 1)
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if ((e & h) == 0) {
-          const double a = u[e], b = u[e | h];
-          u[e] = a + b;
-          u[e | h] = a - b;
-        }
-#pragma unroll 1
-    for (int m = 1; m < BLOCK / 8; m <<= 1)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const double o = shfl_xor64(u[e], m);
-        u[e] = (lane & m) ? o - u[e] : u[e] + o;
+    for (int e = 0; e < 8; ++e)
+      if ((e & h) == 0) {
+        const double a = u[e], b = u[e | h];
+        u[e] = a + b;
+        u[e | h] = a - b;
       }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) u[e] *= kPost64<BLOCK>;
-  }
-  unsigned long long top = 0;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) top = max(top, (unsigned long long)(__double_as_longlong(u[e])) & 0x7FFFFFFFFFFFFFFFull);
-  top = max(top, (unsigned long long)(__shfl_xor((long long)(top), 1)));
-  top = max(top, (unsigned long long)(__shfl_xor((long long)(top), 2)));
-  const bool finite = top < 0x7FF0000000000000ull;
-  int E = int(top >> 52) - 1023 - 2;  // a zero or a subnormal lies below -127
-  E = E < -127 ? -127 : E > 127 ? 127 : E;
-  MxWord r;
-  r.codes = 0;
-  r.word = lane & 15;
-  const double inv = ldexp(1.0, -E);
+  lane_stage64<0xB1>(u, __builtin_popcount(l & 5) & 1);   // lane ^ 1
+  lane_stage64<0x4E>(u, __builtin_popcount(l & 6) & 1);   // lane ^ 2
+  lane_stage64<0x141>(u, (l & 4) != 0);                   // lane ^ 7
+  lane_stage64<0x128>(u, (l & 8) != 0);                   // lane ^ 8
+  if constexpr (BLOCK >= 256) lane_stage64_swap<16>(u, lane);
+  if constexpr (BLOCK >= 512) lane_stage64_swap<32>(u, lane);
+  const double c = kPost64<BLOCK> * double(parity_sign(l));
+  double most = 0.0;
+  bool finite = true;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const double a = fabs(u[e]) * inv;
-    // ties between codes i and i + 1 go to the even one
-    const uint32_t n = uint32_t(a > 0.25) + uint32_t(a >= 0.75) + uint32_t(a > 1.25) + uint32_t(a >= 1.75) +
-                       uint32_t(a > 2.5) + uint32_t(a >= 3.5) + uint32_t(a > 5.0);
-    r.codes |= (n | (u[e] < 0.0 ? 8u : 0u)) << (4 * e);
+    u[e] *= c;
+    finite = finite && fabs(u[e]) < __builtin_huge_val();
+    most = fmax(most, fabs(u[e]));
   }
-  if (!finite) r.codes = 0;
-  r.scales = gather_scales<1>(finite ? uint32_t(E + 127) : 255u, lane & 15);
-  return r;
+  // over the lanes of the block (as block_max): the upper half of a number that is not finite above all others
+  uint32_t top = finite ? uint32_t(uint64_t(__double_as_longlong(most)) >> 32) : 0x7FF00000u;
+  top = block_max<BLOCK>(top);
+  finite = top < 0x7FF00000u;
+  int E = int(top >> 20) - 1023 - 2;  // a zero or a subnormal lies below -127
+  E = E < -127 ? -127 : E > 127 ? 127 : E;
+  const double inv = __longlong_as_double((long long)(1023 - E) << 52);
+  float f[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float a = finite ? to_odd(fabs(u[e]) * inv) : 0.0f;
+    f[e] = finite && u[e] < 0.0 ? -a : a;
+  }
+  return MxWord{fp4_word(f), gather_scales<BLOCK>(finite ? uint32_t(E + 127) : 255u, l), h128_lane_word(l)};
 }
 
 // The lane's 8 channels of a row (16 lanes hold 128, the wave 512), encoded.
-// load gives the values again; every lane of the wave takes part.
-template <int BLOCK, class Load>
-__device__ __forceinline__ MxWord encode(float (&v)[8], Load load, int lane) {
+// Every lane of the wave takes part.
+template <int BLOCK>
+__device__ __forceinline__ MxWord encode(const float (&x)[8], int lane) {
+  float v[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = x[e];
   const int l = lane & 15;
   if constexpr (BLOCK == 1) {
     uint32_t top = 0;
@@ -193,21 +248,21 @@ __device__ __forceinline__ MxWord encode(float (&v)[8], Load load, int lane) {
                     (l & 4) ? -1.0f : 1.0f, (l & 8) ? -1.0f : 1.0f);
     if constexpr (BLOCK >= 256) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = butterfly_x<16>(v[e], lane);
+      for (int e = 0; e < 8; ++e) v[e] = lane_stage_swap<16>(v[e], lane);
     }
     if constexpr (BLOCK >= 512) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = butterfly_x<32>(v[e], lane);
+      for (int e = 0; e < 8; ++e) v[e] = lane_stage_swap<32>(v[e], lane);
     }
     float most8 = 0.0f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) most8 = fmaxf(most8, fabsf(v[e]));  // NaN is seen in S
     const uint32_t top = block_max<BLOCK>(__float_as_uint(most8));
-    const float err = S * (kPost32<BLOCK> * float(n + 5) * 0x1p-24f);
+    const float err = S * (kPost32<BLOCK> * (n + 0.125f) * 0x1p-24f), most_err = S * (kPost32<BLOCK> * (n + 3) * 0x1p-24f);
     const float most = __uint_as_float(top) * kPost32<BLOCK>;
-    const uint32_t at = __float_as_uint(most + err) >> 23;
+    const uint32_t at = __float_as_uint(most + most_err) >> 23;
     const int E = max(int(at) - 127 - 2, -127);
-    const float inv = two_to(-E), d = err * inv;
+    const float inv = two_to(-E), d = fmaf(err, inv, 0x1p-20f);
     const float c = kPost32<BLOCK> * parity_sign(l) * inv;
     float lo[8], hi[8];
 #pragma unroll
@@ -215,48 +270,36 @@ __device__ __forceinline__ MxWord encode(float (&v)[8], Load load, int lane) {
       lo[e] = fmaf(v[e], c, -d);
       hi[e] = fmaf(v[e], c, d);
     }
-    const uint32_t w = fp4_word(hi);  // v c + 0 is not -0
+    const uint32_t w = S != 0.0f ? fp4_word(hi) : 0u;
     // Sums beyond 2^100 (and what is not finite) could leave fp32; below 2^-90 the
     // products above could lose bits; without any value all is zero.
-    const bool sure = w == fp4_word(lo) && at == __float_as_uint(most - err) >> 23 && S < 0x1p100f && S > 0x1p-90f;
-    if (__builtin_amdgcn_ballot_w64(!sure && S != 0.0f) != 0) return encode64<BLOCK>(load, lane);
+    const bool sure = w == fp4_word(lo) && at == __float_as_uint(most - most_err) >> 23 && S < 0x1p100f && S > 0x1p-90f;
+    if (__builtin_amdgcn_ballot_w64(!sure && S != 0.0f) != 0) return encode64<BLOCK>(x, lane);
     return MxWord{w, gather_scales<BLOCK>(uint32_t(E + 127), l), h128_lane_word(l)};
   }
-}
-
-// Stores the lane's word of the wave's span (first channel k0, `channels` of them in
-// the row).  Lanes without anything to store do so out of range, where the hardware
-// drops it: a branch would make the compiler wait for everything in flight, the next
-// row's loads among it.  Rows are at most 2^28, so offsets stay in 32 bits.
-__device__ __forceinline__ void store_word(const MxRows& a, int64_t row, int64_t k0, int channels, int lane, const MxWord& r) {
-  const int g = lane >> 4;
-  __builtin_amdgcn_raw_buffer_store_b32(
-      r.codes, __builtin_amdgcn_make_buffer_rsrc(a.q + row * (a.K >> 1) + (k0 >> 1), 0, channels >> 1, 0x00020000),
-      64 * g + 4 * r.word, 0, 0);
-  const uint32_t group = uint32_t(a.rows) * 4;  // bytes from one group's scales to the next
-  __builtin_amdgcn_raw_buffer_store_b32(
-      r.scales,
-      __builtin_amdgcn_make_buffer_rsrc(a.s + ((k0 >> 7) * a.rows + row) * 4, 0, int(group * ((channels >> 7) - 1) + 4),
-                                        0x00020000),
-      (lane & 15) == 0 ? int(g * group) : -1, 0, 0);
 }
 
 // ---------------------------------------------------------------------------
 // Rows with unit stride: a wave keeps one span of 512 channels and walks rows, the
 // waves of a block side by side along a row.  The next row's values are on their way
-// while the current ones are computed.
+// while the current ones are computed.  QUAD: 4 consecutive rows at a time, whose
+// scales go out together, 16 bytes a group (where there are rows enough for every
+// wave: at 4096 x 14336 single words took 5 us more).
+//   Lanes behind the last channel load zeros and store out of range, where the hardware
+// drops it: a branch around a store would make the compiler wait for everything in
+// flight, the next row's values among it.  Rows are at most 2^28, so the offsets of
+// four groups' scales stay in 32 bits.
 // ---------------------------------------------------------------------------
-template <bool BF16, int BLOCK, bool SIGNED>
-__global__ __launch_bounds__(256) void mx_quantize_kernel(MxRows a, uint32_t spans, uint32_t rows_apart) {
+template <bool BF16, int BLOCK, bool SIGNED, bool QUAD>
+__global__ __launch_bounds__(256) void mx_quantize_kernel(MxRows a, uint32_t spans, uint32_t walkers) {
   typedef unsigned int v4u __attribute__((ext_vector_type(4)));
-  constexpr int kSize = BF16 ? 2 : 4, kLoads = BF16 ? 1 : 2;
-  const int lane = threadIdx.x & 63;
+  constexpr int kSize = BF16 ? 2 : 4, kLoads = BF16 ? 1 : 2, kRows = QUAD ? 4 : 1;
+  const int lane = threadIdx.x & 63, g = lane >> 4;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
-  const uint32_t span = wave % spans;
-  int64_t row = wave / spans;
-  if (row >= rows_apart || row >= a.rows) return;
-  const int64_t k0 = int64_t(span) * kSpan;
-  const int channels = int(a.K - k0 < kSpan ? a.K - k0 : kSpan);  // behind them loads give zeros
+  const int64_t k0 = int64_t(wave % spans) * kSpan;
+  int64_t row = int64_t(wave / spans) * kRows;
+  if (wave / spans >= walkers || row >= a.rows) return;
+  const int channels = int(a.K - k0 < kSpan ? a.K - k0 : kSpan);
   const char* const x = reinterpret_cast<const char*>(a.x) + k0 * kSize;
   struct Raw {
     v4u v[kLoads];
@@ -280,23 +323,52 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(MxRows a, uint32_t spa
       for (int e = 0; e < 4; ++e) sign[4 * i + e] = m[e];
     }
   }
-  auto open = [&](const Raw& raw, float(&v)[8]) {
+  const uint32_t group = uint32_t(a.rows) * 4;  // bytes from one group's scales to the next
+  const int scale_range = int(group * ((channels >> 7) - 1) + 4 * kRows);
+  const int scale_at = (lane & 15) == 0 && 128 * g < channels ? int(g * group) : -1;
+  v4u scales{};
+  Raw next = load(row);
+  for (int i = 0;;) {
+    const Raw raw = next;
+    int64_t row2 = row + 1;
+    if (!QUAD || i == kRows - 1) row2 = row + int64_t(walkers) * kRows - (kRows - 1);
+    const bool last = row2 >= a.rows && (!QUAD || i == kRows - 1 || row + 1 >= a.rows);
+    next = load(row2 < a.rows ? row2 : row);
+    float v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       if constexpr (BF16) v[e] = (e & 1) ? bf16_hi(raw.v[0][e >> 1]) : bf16_lo(raw.v[0][e >> 1]);
       else v[e] = __uint_as_float(raw.v[(e >> 2) % kLoads][e & 3]);
       if constexpr (SIGNED) v[e] = __uint_as_float(__float_as_uint(v[e]) ^ sign[e]);
     }
-  };
-  Raw next = load(row);
-  while (row < a.rows) {
-    const Raw raw = next;
-    const int64_t row2 = row + rows_apart;
-    next = load(row2 < a.rows ? row2 : row);
-    float v[8];
-    open(raw, v);
-    const MxWord r = encode<BLOCK>(v, [&](float(&w)[8]) { open(raw, w); }, lane);
-    store_word(a, row, k0, channels, lane, r);
+    const MxWord r = encode<BLOCK>(v, lane);
+    __builtin_amdgcn_raw_buffer_store_b32(
+        r.codes, __builtin_amdgcn_make_buffer_rsrc(a.q + row * (a.K >> 1) + (k0 >> 1), 0, channels >> 1, 0x00020000),
+        64 * g + 4 * r.word, 0, 0);
+    if constexpr (QUAD) {
+      scales = v4u{scales[1], scales[2], scales[3], r.scales};
+      if (i == kRows - 1) {
+        __builtin_amdgcn_raw_buffer_store_b128(
+            scales, __builtin_amdgcn_make_buffer_rsrc(a.s + ((k0 >> 7) * a.rows + row - 3) * 4, 0, scale_range, 0x00020000),
+            scale_at, 0, 0);
+      } else if (row + 1 >= a.rows) {  // the last rows, fewer than 4
+        const int first = 3 - i;       // of their words in `scales`
+#pragma unroll
+        for (int e = 1; e < 4; ++e)
+          if (e >= first)
+            __builtin_amdgcn_raw_buffer_store_b32(
+                scales[e],
+                __builtin_amdgcn_make_buffer_rsrc(a.s + ((k0 >> 7) * a.rows + row - 3 + e) * 4, 0,
+                                                  int(group * ((channels >> 7) - 1) + 4), 0x00020000),
+                scale_at, 0, 0);
+      }
+      i = (i + 1) & 3;
+    } else {
+      __builtin_amdgcn_raw_buffer_store_b32(
+          r.scales, __builtin_amdgcn_make_buffer_rsrc(a.s + ((k0 >> 7) * a.rows + row) * 4, 0, scale_range, 0x00020000),
+          scale_at, 0, 0);
+    }
+    if (last) return;
     row = row2;
   }
 }
@@ -362,13 +434,10 @@ __global__ __launch_bounds__(256) void mx_pack_kernel(MxRows a, int64_t spans) {
   const int l = lane % P::lanes;
   for (int r0 = wave * kTogether; r0 < rows; r0 += 4 * kTogether) {
     const int r = r0 + lane / P::lanes;
-    auto load = [&](float(&v)[8]) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = tile[r * P::row + 9 * l + e];
-    };
     float v[8];
-    load(v);
-    const MxWord w = encode<BLOCK>(v, load, lane);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = tile[r * P::row + 9 * l + e];
+    const MxWord w = encode<BLOCK>(v, lane);
     if (r < rows) {
       const int64_t g = (k0 >> 7) + (l >> 4);
       *reinterpret_cast<uint32_t*>(a.q + (row0 + r) * (a.K >> 1) + 64 * g + 4 * w.word) = w.codes;
@@ -474,12 +543,18 @@ hipError_t by_kind(const MxRows& a, F f) {
 hipError_t launch_mx_quantize(const MxRows& a, hipStream_t st) {
   const int64_t spans = (a.K + kSpan - 1) / kSpan;  // at most 2^14
   const int64_t full = 256 * 32;                    // waves the card holds
-  int64_t apart = full / spans > 1 ? full / spans : 1;
-  apart = apart < a.rows ? apart : a.rows;
-  const int64_t blocks = (spans * apart + 3) / 4;
+  const bool quad = a.rows * spans >= 4 * full;
+  const int64_t most = quad ? (a.rows + 3) / 4 : a.rows;
+  int64_t walkers = full / spans > 1 ? full / spans : 1;
+  walkers = walkers < most ? walkers : most;
+  const dim3 grid{unsigned((spans * walkers + 3) / 4)};
   return by_kind(a, [&](auto bf16, auto block, auto sign) {
-    hipLaunchKernelGGL((mx_quantize_kernel<decltype(bf16)::value, decltype(block)::value, decltype(sign)::value>),
-                       dim3(unsigned(blocks)), dim3(256), 0, st, a, uint32_t(spans), uint32_t(apart));
+    constexpr bool B = decltype(bf16)::value, S = decltype(sign)::value;
+    constexpr int L = decltype(block)::value;
+    if (quad)
+      hipLaunchKernelGGL((mx_quantize_kernel<B, L, S, true>), grid, dim3(256), 0, st, a, uint32_t(spans), uint32_t(walkers));
+    else
+      hipLaunchKernelGGL((mx_quantize_kernel<B, L, S, false>), grid, dim3(256), 0, st, a, uint32_t(spans), uint32_t(walkers));
     return hipGetLastError();
   });
 }
