@@ -74,10 +74,10 @@ constexpr int kNarrowMost = PRECISE ? 64 : D == 64 ? 32 : 48;
 struct Req {
   int q0, qn, kv;   // first query token, query tokens, keys
   int tiles;        // row tiles
-  int lo, span;     // first key of any row's window (a multiple of 64), keys on the line: from there on, and the sinks
+  int lo, span;     // first key any row sees (a multiple of 64) and keys from there on; with sinks 0, and a tile's positions
 };
 
-__device__ __forceinline__ int round64(int n) { return (n + 63) & ~63; }
+__device__ __forceinline__ int round16(int n) { return (n + 15) & ~15; }
 
 __device__ __forceinline__ int clamp_int(int64_t v, int64_t hi) { return int(v < 0 ? 0 : v > hi ? hi : v); }
 
@@ -93,29 +93,34 @@ __device__ __forceinline__ Req request(const AttnArgs& a, int b, int rows) {
     const int64_t first = int64_t(r.kv) - r.qn + 1 - a.window;
     r.lo = first > 0 ? int(first) & ~63 : 0;
   }
-  int head = 0;  // keys of the sinks' steps in front of a gap
-  if (a.sinks > 0) {
-    if (r.lo > round64(a.sinks)) head = round64(a.sinks);
-    else r.lo = 0;
+  r.span = r.kv - r.lo;
+  if (a.sinks > 0) {  // positions of a tile (Places), at most: its rows' windows start at most qn - 1 or a tile's tokens apart
+    const int tokens = (rows + a.group - 2) / a.group + 1;
+    const int64_t most = int64_t(round16(a.sinks)) + a.window + (r.qn < tokens ? r.qn : tokens) + 15;
+    r.lo = 0;
+    r.span = most < r.kv ? int(most) : r.kv;
   }
-  r.span = head + r.kv - r.lo;
   return r;
 }
 
-// With sinks the positions of a request's part of the line are its keys without those
-// between the sinks' last step of 64 and the first key of any row's window: position w
-// is key w up to `head`, key w + gap from there on (both multiples of 64, gap 0 where
-// nothing lies between, so 64 positions from a multiple of 64 are consecutive keys).
-template <bool SINKS>
+// With sinks a unit works on positions instead of keys: the sinks, then the keys from
+// the first one of its rows' windows on, without those between.  Position w is key w in
+// front of `head` and key w + gap from there on (gap 0 where nothing lies between);
+// GRAIN: keys that stay side by side, from a multiple of GRAIN on.
+template <bool SINKS, int GRAIN>
 struct Places {
   int head, gap;
-  __device__ __forceinline__ explicit Places(const Req& r) : head(SINKS ? r.span - (r.kv - r.lo) : 0), gap(SINKS ? r.lo - head : 0) {}
+  // lo: first key of the windows of the unit's rows
+  __device__ __forceinline__ Places(const AttnArgs& a, int lo) : head(0), gap(0) {
+    if constexpr (SINKS) {
+      head = (a.sinks + GRAIN - 1) & ~(GRAIN - 1);
+      lo &= ~(GRAIN - 1);
+      gap = lo > head ? lo - head : 0;
+    }
+  }
   __device__ __forceinline__ int key(int w) const { return SINKS && w >= head ? w + gap : w; }
-  // of a key behind the gap
+  // of a key of the windows
   __device__ __forceinline__ int place(int j) const { return SINKS ? j - gap : j; }
-  // first position of a unit's step `at`
-  __device__ __forceinline__ int start(const Req& r, int at, int step) const { return (SINKS ? 0 : r.lo) + at * step; }
-  __device__ __forceinline__ int last(const Req& r) const { return SINKS ? r.span : r.kv; }
 };
 
 template <typename T>
@@ -540,16 +545,19 @@ __global__ __launch_bounds__(256, (kNarrowBlocks<D, PRECISE>)) void kv_attention
     int full_lo, full_hi;  // keys that every row sees
     row_range(a, it.r, first_tok, lo, full_hi);
     row_range(a, it.r, last_tok, full_lo, hi);
-    // lo and hi from here on: positions (keys, without sinks) of the piece's tiles
-    const Places<SINKS> places(it.r);
-    const int chunk0 = places.start(it.r, it.at, kNarrowStep);
+    // from here on positions (keys, without sinks)
+    const Places<SINKS, 16> places(a, lo);
+    const int chunk0 = it.r.lo + it.at * kNarrowStep;
     const int64_t stop = int64_t(chunk0) + int64_t(steps) * kNarrowStep;
-    const int chunk1 = stop < places.last(it.r) ? int(stop) : places.last(it.r);
     if constexpr (SINKS) {
-      // few rows, whose windows start within a step or two of each other: no more is left out
       lo = chunk0;
-      hi = places.place(hi) < chunk1 ? places.place(hi) : chunk1;
+      hi = places.place(hi) < stop ? places.place(hi) : int(stop);
+      begin = places.place(begin);
+      end = places.place(end);
+      full_lo = places.place(full_lo);
+      full_hi = places.place(full_hi);
     } else {
+      const int chunk1 = stop < it.r.kv ? int(stop) : it.r.kv;
       lo = lo > chunk0 ? lo : chunk0;
       hi = hi < chunk1 ? hi : chunk1;
       begin = begin > chunk0 ? begin : chunk0;
@@ -584,7 +592,7 @@ __global__ __launch_bounds__(256, (kNarrowBlocks<D, PRECISE>)) void kv_attention
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int id = __builtin_amdgcn_readlane(ids, 2 * (tile & 31) + h);
-        const int slot = (places.key(j) + 16 * h) & ((1 << kv.log2_page) - 1);
+        const int slot = places.key(j + 16 * h) & ((1 << kv.log2_page) - 1);
         next_seen[h] = id >= 0;
         const int64_t page = id >= 0 ? id : 0;  // a half without keys reads page 0, unused
         code_at[h] = page * kv.code_page + it.head * kv.code_head + slot * kv.code_slot;
@@ -656,9 +664,8 @@ __global__ __launch_bounds__(256, (kNarrowBlocks<D, PRECISE>)) void kv_attention
       if (more) load_codes(kv.v_codes, vraw);
       // softmax
       float x[8];
-      const int k0 = places.key(j0);  // the tile's first key
-      const bool whole = seen[0] && seen[1] && (k0 >= full_lo || (SINKS && k0 + 32 <= a.sinks)) && k0 + 32 <= full_hi &&
-                         j0 + 32 <= hi;
+      const bool whole = seen[0] && seen[1] && (j0 >= full_lo || (SINKS && (full_lo <= a.sinks || j0 + 32 <= a.sinks))) &&
+                         j0 + 32 <= full_hi && j0 + 32 <= hi;
       // relative to the running maximum; 0 sk makes NaN of a key whose scale is
       // infinite, which could otherwise have a score of -infinity and be lost
       float ref = m == -INFINITY ? 0.0f : m;
@@ -670,7 +677,7 @@ __global__ __launch_bounds__(256, (kNarrowBlocks<D, PRECISE>)) void kv_attention
         keep_branch();
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const int j = k0 + 16 * (e >> 2) + 4 * g + (e & 3);
+          const int j = j0 + 16 * (e >> 2) + 4 * g + (e & 3);
           const bool vis = seen[e >> 2] && (j >= begin || (SINKS && j < a.sinks)) && j < end;
           x[e] = vis ? x[e] : -INFINITY;  // probability 0
           sv[e >> 2][e & 3] = vis ? sv[e >> 2][e & 3] : 0.0f;  // whatever lies behind the last key
@@ -892,18 +899,17 @@ __device__ __forceinline__ void wide_store(const AttnArgs& a, const It& it, cons
   }
 }
 
-// The positions of a piece whose keys any of the unit's rows sees, [lo, hi) with lo
-// on a step (with sinks: without those from `head` up to `skip`), what the rows of a
-// wave (32 from row0) see, and the keys that all of them see.
+// The keys (positions, with sinks) of a piece that any of the unit's rows sees, [lo, hi)
+// with lo on a step, what the rows of a wave (32 from row0) see, and what all of them see.
 struct Reach {
-  int lo, hi, wave_hi, full_lo, full_hi, head, skip;
+  int lo, hi, wave_hi, full_lo, full_hi;
 };
-// Also cuts the lane's own [begin, end) to the piece.
+// Also cuts the lane's own [begin, end) to the piece (makes them positions).
 template <bool SINKS>
-__device__ __forceinline__ Reach wide_reach(const AttnArgs& a, const Piece& it, const Places<SINKS>& places, bool by_units,
-                                            int steps, int row0, int& begin, int& end) {
+__device__ __forceinline__ Reach wide_reach(const AttnArgs& a, const Piece& it, bool by_units, int steps, int row0, int& begin,
+                                            int& end, Places<SINKS, 1>& places) {
   const int rows = it.r.qn * a.group;
-  Reach u{0, 0, 0, 0, 0, 0, 0};
+  Reach u{0, 0, 0, 0, 0};
   int skip;
   const int last = (it.tile + 1) * kWideRows < rows ? (it.tile + 1) * kWideRows - 1 : rows - 1;
   row_range(a, it.r, it.tile * kWideRows / a.group, u.lo, skip);
@@ -913,17 +919,20 @@ __device__ __forceinline__ Reach wide_reach(const AttnArgs& a, const Piece& it, 
     row_range(a, it.r, row0 / a.group, skip, u.full_hi);
     row_range(a, it.r, wave_last / a.group, u.full_lo, u.wave_hi);
   }
-  const int chunk0 = places.start(it.r, by_units ? 0 : it.at, kWideStep), last_place = places.last(it.r);
-  const int64_t stop = by_units ? last_place : int64_t(chunk0) + int64_t(steps) * kWideStep;
-  const int chunk1 = stop < last_place ? int(stop) : last_place;
+  const int chunk0 = it.r.lo + (by_units ? 0 : it.at * kWideStep);
+  const int64_t stop = by_units ? it.r.kv : int64_t(chunk0) + int64_t(steps) * kWideStep;
   if constexpr (SINKS) {
-    u.head = round64(a.sinks);  // positions are keys up to there
-    u.skip = places.place(u.lo) & ~(kWideStep - 1);
-    u.lo = chunk0 >= u.head && chunk0 < u.skip ? u.skip : chunk0;
-    u.hi = places.place(u.hi) < chunk1 ? places.place(u.hi) : chunk1;
+    places = Places<SINKS, 1>(a, u.lo);
+    u.lo = chunk0;
+    u.hi = places.place(u.hi) < stop ? places.place(u.hi) : int(stop);
     u.wave_hi = row0 < rows ? places.place(u.wave_hi) : 0;
+    u.full_lo = places.place(u.full_lo);
+    u.full_hi = places.place(u.full_hi);
+    begin = places.place(begin);
+    end = places.place(end);
     return u;
   }
+  const int chunk1 = stop < it.r.kv ? int(stop) : it.r.kv;
   u.lo = u.lo > chunk0 ? u.lo : chunk0;
   u.hi = u.hi < chunk1 ? u.hi : chunk1;
   u.wave_hi = u.wave_hi < chunk1 ? u.wave_hi : chunk1;
@@ -1083,13 +1092,9 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_w
       for (int i = 0; i < D / 16; ++i) query_operand<N>(a, base + 16 * i + 8 * h, live, q[i]);
       row_range(a, it.r, tok, begin, end);
     }
-    const Places<SINKS> places(it.r);
-    const Reach reach = wide_reach<SINKS>(a, it, places, by_units, steps, row0, begin, end);
+    Places<SINKS, 1> places(a, 0);
+    const Reach reach = wide_reach<SINKS>(a, it, by_units, steps, row0, begin, end, places);
     const int lo = reach.lo, hi = reach.hi, wave_hi = reach.wave_hi;
-    auto next_step = [&](int w) {
-      w += kWideStep;
-      return SINKS && w >= reach.head && w < reach.skip ? reach.skip : w;
-    };
 
     // staging: the thread's chunks of a step (row my_row + i * rows_apart, chunk my_chunk)
     constexpr int kApart = 256 / CH;
@@ -1115,7 +1120,7 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_w
     auto load_step = [&](int j0) {
 #pragma unroll
       for (int i = 0; i < NH; ++i) {
-        const int j = places.key(j0) + my_row + i * kApart, at = j & ((1 << kv.log2_page) - 1);
+        const int j = places.key(j0 + my_row + i * kApart), at = j & ((1 << kv.log2_page) - 1);
         const int64_t off = head_codes + row_at(uint32_t(ids[i]) < pages ? ids[i] : 0, kv.code_page, at, kv.code_slot) + 16 * my_chunk;
         if constexpr (NS == 1) {
           raw[0] = *reinterpret_cast<const v4u*>((half_v ? kv.v_codes : kv.k_codes) + off);
@@ -1125,7 +1130,7 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_w
         }
       }
       if (tid < kWideStep) {  // the keys' scales, from the first wave
-        const int at = (places.key(j0) + tid) & ((1 << kv.log2_page) - 1);
+        const int at = places.key(j0 + tid) & ((1 << kv.log2_page) - 1);
         const bool known = uint32_t(scale_id) < pages;
         seen = known && j0 + tid < hi;
         const int64_t off = head_scales + row_at(known ? scale_id : 0, kv.scale_page, at, kv.scale_slot);
@@ -1178,26 +1183,25 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_w
     if (lo < hi) {
       load_ids(lo);
       load_step(lo);
-      load_ids(next_step(lo));
+      load_ids(lo + kWideStep);
       store_step(0, true);
     }
     int buf = 0;
-    for (int j0 = lo; j0 < hi; j0 = next_step(j0), buf ^= 1) {
+    for (int j0 = lo; j0 < hi; j0 += kWideStep, buf ^= 1) {
       __syncthreads();
-      const int j1 = next_step(j0);
-      const bool more = j1 < hi;
+      const bool more = j0 + kWideStep < hi;
       if (more) {
-        load_step(j1);
-        load_ids(next_step(j1));
+        load_step(j0 + kWideStep);
+        load_ids(j0 + 2 * kWideStep);
       }
       const int word = seen_s[buf][lane];
       if (j0 < wave_hi) {
         const char* kbase = lds + buf * L::kBuffer;
         const char* vbase = kbase + L::kValues;
         const uint64_t vis = __ballot((word & 1) != 0);
-        const int k0 = places.key(j0);  // the step's first key
-        const bool whole = vis == ~uint64_t(0) && (k0 >= reach.full_lo || (SINKS && k0 + kWideStep <= a.sinks)) &&
-                           k0 + kWideStep <= reach.full_hi;
+        const bool whole = vis == ~uint64_t(0) &&
+                           (j0 >= reach.full_lo || (SINKS && (reach.full_lo <= a.sinks || j0 + kWideStep <= a.sinks))) &&
+                           j0 + kWideStep <= reach.full_hi;
         // scores of the step's two 32-key halves
         v16f x[2] = {v16f{}, v16f{}};
         const char* krow = kbase + n * L::kKeyRow + 16 * h;
@@ -1230,7 +1234,7 @@ __global__ __launch_bounds__(256, (kWideBlocks<D, PRECISE>)) void kv_attention_w
 #pragma unroll
           for (int kb = 0; kb < 2; ++kb) {
             // bit 8 b + i: key 32 kb + 8 b + 4 h + i of the step
-            const int j = k0 + 32 * kb + 4 * h;
+            const int j = j0 + 32 * kb + 4 * h;
             uint32_t bits = ~bits_below(begin - j);
             if constexpr (SINKS) bits |= bits_below(a.sinks - j);
             bits &= (uint32_t(vis >> (32 * kb)) >> (4 * h)) & bits_below(end - j);

@@ -452,6 +452,7 @@ __global__ __launch_bounds__(256) void mx_pack_kernel(MxRows a, int64_t spans) {
 // behind the last channel load zeros and store out of range, where it is dropped.
 // ---------------------------------------------------------------------------
 constexpr int kBackRows = 4;
+constexpr int kStream = 2;  // stores as non-temporal: 4096 x 14336 takes 24.7 us, 34.9 through the caches
 
 template <bool BF16>
 __global__ __launch_bounds__(256) void mx_dequantize_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ s,
@@ -511,10 +512,10 @@ __global__ __launch_bounds__(256) void mx_dequantize_kernel(const uint8_t* __res
 #pragma unroll
         for (int c = 0; c < 4; ++c)  // exact: the lower halves are zero (NaN: its upper half is NaN)
           b[c] = (v[2 * c] >> 16) | (v[2 * c + 1] & 0xFFFF0000u);
-        __builtin_amdgcn_raw_buffer_store_b128(b, to, lane * 16, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(b, to, lane * 16, 0, kStream);
       } else {
-        __builtin_amdgcn_raw_buffer_store_b128(v4u{v[0], v[1], v[2], v[3]}, to, lane * 32, 0, 0);
-        __builtin_amdgcn_raw_buffer_store_b128(v4u{v[4], v[5], v[6], v[7]}, to, lane * 32 + 16, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(v4u{v[0], v[1], v[2], v[3]}, to, lane * 32, 0, kStream);
+        __builtin_amdgcn_raw_buffer_store_b128(v4u{v[4], v[5], v[6], v[7]}, to, lane * 32 + 16, 0, kStream);
       }
     }
     row = row2;
