@@ -31,6 +31,21 @@ constexpr bool whole_units(int64_t units, int64_t whole, int64_t grid, int64_t l
   return whole > 0 && units >= whole && units <= grid && longest * blocks <= steps;
 }
 
+// The same for the kernel for few rows where a unit's keys are bounded (a window with
+// sinks): whole units for `whole` units or more that the grid has blocks for, while the
+// longest is at most two shares and 8 steps.  A share cut anywhere starts and merges
+// two units or more, so whole ones take less time even where they are less even.  Equal
+// shares / whole units, us, 8 KV heads of 128, single tokens:
+//   64 requests, window 2048                     54.9 / 43.5 (17 steps, share 12)
+//   64 of 1 to 3000 keys, window 2048            55.1 / 38.5 (17, 9)
+//   64 requests, window 512                      27.7 / 21.0 (5, 4)
+//   64 requests, window 8192                     135 / 134 (65, 43)
+//   32 requests, window 2048 (256 units)         32.6 / 33.9 (17, 6)
+//   32 requests, window 8192                     77.9 / 104 (65, 22): shares
+constexpr bool whole_few(int64_t units, int64_t whole, int64_t grid, int64_t longest, int64_t steps, int blocks) {
+  return whole > 0 && units >= whole && units <= grid && longest <= 2 * ((steps + blocks - 1) / blocks) + 8;
+}
+
 // Blocks of the kernel for many rows, for so many units at most: a block for each,
 // or those that share the line where a grid (fewer than 2^32 threads) has no room.
 constexpr int64_t wide_grid(int64_t units, int64_t blocks) {

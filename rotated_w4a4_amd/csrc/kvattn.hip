@@ -166,9 +166,14 @@ __device__ __forceinline__ void wave_lds_order() {
 }
 
 // How a kernel cuts the work: query rows of a unit, keys of a step, blocks that
-// share the line, and what whole_units goes by.
+// share the line, what whole_units goes by, and whether whole_few does instead.
 struct Cut {
   int rows, step, blocks, whole;
+  bool few = false;
+  __device__ __forceinline__ bool take_whole(int64_t units, int64_t longest, int64_t steps) const {
+    return few ? whole_few(units, whole, gridDim.x, longest, steps, blocks)
+               : whole_units(units, whole, gridDim.x, longest, steps, blocks);
+  }
 };
 
 // Steps before each thread's requests (256 threads take consecutive ones), and
@@ -195,8 +200,8 @@ __device__ __forceinline__ bool line_build_wave(const AttnArgs& a, const Cut& cu
   if (cut.whole > 0) {
     const int upto_units = wave_prefix_dpp(units);
     // of every lane's request in the place of the longest
-    by_units = !__ballot(!whole_units(__builtin_amdgcn_readlane(upto_units, kWave - 1), cut.whole, gridDim.x,
-                                      units > 0 ? steps : 0, __builtin_amdgcn_readlane(upto, kWave - 1), cut.blocks));
+    by_units = !__ballot(!cut.take_whole(__builtin_amdgcn_readlane(upto_units, kWave - 1), units > 0 ? steps : 0,
+                                         __builtin_amdgcn_readlane(upto, kWave - 1)));
     if (by_units) {
       own = units;
       upto = upto_units;
@@ -241,7 +246,7 @@ __device__ __forceinline__ void line_build(const AttnArgs& a, const Cut& cut, Li
     const long long all = line.wave_sum[0] + line.wave_sum[1] + line.wave_sum[2] + line.wave_sum[3];
     const long long all_units = line.wave_units[0] + line.wave_units[1] + line.wave_units[2] + line.wave_units[3];
     longest = max(max(line.wave_longest[0], line.wave_longest[1]), max(line.wave_longest[2], line.wave_longest[3]));
-    by_units = whole_units(all_units, cut.whole, gridDim.x, longest, all, cut.blocks);
+    by_units = cut.take_whole(all_units, longest, all);
     if (by_units) {
       sum = units;
       upto = upto_units;
@@ -491,6 +496,9 @@ struct NarrowLds {
 template <int D, bool PRECISE>
 constexpr int kNarrowBlocks = D == 256 ? (PRECISE ? 1 : 2) : (PRECISE ? 2 : 3);
 
+// Units from which on whole ones are considered with sinks (whole_few): one a CU.
+constexpr int kWholeFew = kCUs;
+
 template <int D, bool PRECISE, bool SINKS>
 __global__ __launch_bounds__(256, (kNarrowBlocks<D, PRECISE>)) void kv_attention_narrow_kernel(AttnArgs a) {
   constexpr int N = PRECISE ? 3 : 1;        // parts of the queries
@@ -506,9 +514,10 @@ __global__ __launch_bounds__(256, (kNarrowBlocks<D, PRECISE>)) void kv_attention
   char* vbuf = lds + wave * L::kWaveBytes;
   const KvCache& kv = a.cache;
   __shared__ Line line;
-  const Cut cut{kNarrowRows, kNarrowStep, int(gridDim.x), 0};
+  const Cut cut{kNarrowRows, kNarrowStep, int(gridDim.x), SINKS ? kWholeFew : 0, SINKS};
   line_build(a, cut, line);
-  const int64_t total = line_total(line), share = line_share(total, cut.blocks);
+  const bool by_units = SINKS && uniform(int(line.by_units));
+  const int64_t total = line_total(line), share = by_units ? 1 : line_share(total, cut.blocks);
   const int64_t begin_pos = share * blockIdx.x;
   const int64_t end_pos = begin_pos + share < total ? begin_pos + share : total;
   if (begin_pos >= end_pos) write_border(a, blockIdx.x, false, Piece{}, share);
@@ -547,8 +556,8 @@ __global__ __launch_bounds__(256, (kNarrowBlocks<D, PRECISE>)) void kv_attention
     row_range(a, it.r, last_tok, full_lo, hi);
     // from here on positions (keys, without sinks)
     const Places<SINKS, 16> places(a, lo);
-    const int chunk0 = it.r.lo + it.at * kNarrowStep;
-    const int64_t stop = int64_t(chunk0) + int64_t(steps) * kNarrowStep;
+    const int chunk0 = it.r.lo + it.at * kNarrowStep;  // whole units: at is 0
+    const int64_t stop = by_units ? it.r.kv : int64_t(chunk0) + int64_t(steps) * kNarrowStep;
     if constexpr (SINKS) {
       lo = chunk0;
       hi = places.place(hi) < stop ? places.place(hi) : int(stop);

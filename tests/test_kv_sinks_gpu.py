@@ -116,6 +116,17 @@ def test_many_requests(hint):
     _check(64, BF16, [1] * 300, kv, 50, 30, hint=hint)
 
 
+@pytest.mark.parametrize("D,dtype", [(64, BF16), (128, BF16), (256, F32)])
+@pytest.mark.parametrize("name,kv,window", [("even", 700, 300), ("ragged", None, 500), ("long_beside_short", -1, 4000)])
+def test_whole_and_cut_units_of_few_rows(name, kv, window, D, dtype):
+    # 70 requests of 4 KV heads: 280 units, each a block's (even, ragged), or cut (one request of 30 times the others' keys)
+    rng = np.random.default_rng(8)
+    kv = [kv] * 70 if kv and kv > 0 else [int(x) for x in rng.integers(1, 700 if kv is None else 130, 70)]
+    if name == "long_beside_short":
+        kv[33] = 3900
+    _check(D, dtype, [1 + i % 2 for i in range(70)], kv, window, 21, hk=4, group=2)
+
+
 def test_a_sink_on_a_bad_page_is_hidden():
     rng = np.random.default_rng(4)
     page, D = 16, 128
