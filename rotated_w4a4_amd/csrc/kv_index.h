@@ -31,19 +31,20 @@ constexpr bool whole_units(int64_t units, int64_t whole, int64_t grid, int64_t l
   return whole > 0 && units >= whole && units <= grid && longest * blocks <= steps;
 }
 
-// The same for the kernel for few rows where a unit's keys are bounded (a window with
-// sinks): whole units for `whole` units or more that the grid has blocks for, while the
-// longest is at most two shares and 8 steps.  A share cut anywhere starts and merges
-// two units or more, so whole ones take less time even where they are less even.  Equal
-// shares / whole units, us, 8 KV heads of 128, single tokens:
-//   64 requests, window 2048                     54.9 / 43.5 (17 steps, share 12)
-//   64 of 1 to 3000 keys, window 2048            55.1 / 38.5 (17, 9)
-//   64 requests, window 512                      27.7 / 21.0 (5, 4)
-//   64 requests, window 8192                     135 / 134 (65, 43)
-//   32 requests, window 2048 (256 units)         32.6 / 33.9 (17, 6)
-//   32 requests, window 8192                     77.9 / 104 (65, 22): shares
+// The kernel for few rows where a unit's keys are bounded (a window with sinks): units
+// take whole shares, so that no block works on two of them.  A share cut anywhere
+// starts and merges two units or more, which costs as much as 8 steps, so even shares
+// may be up to twice as long and 8 steps longer than equal ones.  Steps a share and us,
+// equal / even, 8 KV heads of 128, single tokens:
+//   64 requests, window 2048            12, 54.9 / 17, 43.5
+//   64 of 1 to 3000 keys, window 2048   9, 55.1 / 17, 38.5
+//   64 requests, window 512             4, 27.7 / 5, 21.0
+//   64 requests, window 8192            43, 135 / 65, 134
+constexpr int even_most(int equal) { return 2 * equal + 8; }
+// With more than 64 requests the even share is a whole unit, where there are `whole` of
+// them or more and the grid has blocks for all.
 constexpr bool whole_few(int64_t units, int64_t whole, int64_t grid, int64_t longest, int64_t steps, int blocks) {
-  return whole > 0 && units >= whole && units <= grid && longest <= 2 * ((steps + blocks - 1) / blocks) + 8;
+  return whole > 0 && units >= whole && units <= grid && longest <= even_most(int((steps + blocks - 1) / blocks));
 }
 
 // Blocks of the kernel for many rows, for so many units at most: a block for each,

@@ -142,6 +142,16 @@ __device__ __forceinline__ int wave_prefix_dpp(int v) {
   v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // lane 31 to rows 2 and 3
   return v;
 }
+// The largest of the lanes up to each one, of values from 0 on, the same way.
+__device__ __forceinline__ int wave_upmost_dpp(int v) {
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false));
+  return v;
+}
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ __forceinline__ int64_t uniform(int64_t v) {
   return int64_t(uint32_t(uniform(int(v)))) | (int64_t(uniform(int(v >> 32))) << 32);
@@ -166,7 +176,7 @@ __device__ __forceinline__ void wave_lds_order() {
 }
 
 // How a kernel cuts the work: query rows of a unit, keys of a step, blocks that
-// share the line, what whole_units goes by, and whether whole_few does instead.
+// share the line, what whole_units goes by, and whether even_share and whole_few do instead.
 struct Cut {
   int rows, step, blocks, whole;
   bool few = false;
@@ -184,7 +194,28 @@ struct Line {
   long long wave_sum[4], wave_units[4];
   int wave_longest[4];
   bool by_units;  // a step for each unit
+  int even;       // > 0: units take whole shares of so many steps (even_share), their last one may be cut short
 };
+
+// Steps with the room that a unit takes on the line.
+__device__ __forceinline__ int even_steps(int steps, int even) { return even > 0 ? (steps + even - 1) / even * even : steps; }
+
+// A share of which every unit can have whole ones of its own within the grid's blocks:
+// the longest unit in as many equal parts as fit (tried in steps of a sixteenth: a
+// few tries at most); 0: none up to even_most.  A lane's
+// request has `units` of `steps`, all together `total` steps.  Every lane of the wave
+// takes part.
+__device__ __forceinline__ int even_share(int units, int steps, int total, int blocks) {
+  const int longest = __builtin_amdgcn_readlane(wave_upmost_dpp(units > 0 ? steps : 0), kWave - 1);
+  const int equal = total > blocks ? (total + blocks - 1) / blocks : 1, most = even_most(equal);
+  for (int parts = (longest + equal - 1) / equal; parts > 0; parts -= 1 + (parts >> 4)) {
+    const int share = (longest + parts - 1) / parts;
+    if (share > most) break;
+    const int need = wave_prefix_dpp(units * ((steps + share - 1) / share));
+    if (__builtin_amdgcn_readlane(need, kWave - 1) <= blocks) return share;
+  }
+  return 0;
+}
 
 // Up to 64 requests, and 32 bits for their steps: a lane each, every wave by
 // itself and with the same results, so no barrier (they write the same values).
@@ -197,7 +228,12 @@ __device__ __forceinline__ bool line_build_wave(const AttnArgs& a, const Cut& cu
   if (__ballot(float(units) * float(steps) > 0x1p24f)) return false;  // sums below 2^30
   int own = units * steps, upto = wave_prefix_dpp(own);
   bool by_units = false;
-  if (cut.whole > 0) {
+  int even = 0;
+  if (cut.few) {
+    even = even_share(units, steps, __builtin_amdgcn_readlane(upto, kWave - 1), cut.blocks);
+    own = units * even_steps(steps, even);
+    upto = wave_prefix_dpp(own);
+  } else if (cut.whole > 0) {
     const int upto_units = wave_prefix_dpp(units);
     // of every lane's request in the place of the longest
     by_units = !__ballot(!cut.take_whole(__builtin_amdgcn_readlane(upto_units, kWave - 1), units > 0 ? steps : 0,
@@ -210,7 +246,10 @@ __device__ __forceinline__ bool line_build_wave(const AttnArgs& a, const Cut& cu
   line.before[lane] = upto - own;
   line.reqs[lane] = r;
   if (lane == kWave - 1) line.before[256] = upto;
-  if (lane == 0) line.by_units = by_units;
+  if (lane == 0) {
+    line.by_units = by_units;
+    line.even = even;
+  }
   wave_lds_order();
   return true;
 }
@@ -252,7 +291,10 @@ __device__ __forceinline__ void line_build(const AttnArgs& a, const Cut& cut, Li
       upto = upto_units;
     }
   }
-  if (tid == 0) line.by_units = by_units;
+  if (tid == 0) {
+    line.by_units = by_units;
+    line.even = 0;
+  }
   long long before = upto - sum;
   for (int w = 0; w < wave; ++w) before += by_units ? line.wave_units[w] : line.wave_sum[w];
   line.before[tid] = before;
@@ -277,23 +319,26 @@ __device__ __forceinline__ Piece line_find(const AttnArgs& a, const Cut& cut, co
   for (int i = 0; i < blocks64; ++i) seg += __popcll(__ballot(line.before[kWave * i + lane] <= pos));
   Piece p;
   const bool by_units = uniform(int(line.by_units));
+  const int even = uniform(line.even);
+  int room;
   p.b = seg * per;
   int64_t local = pos - uniform(int64_t(line.before[seg]));
   for (;; ++p.b) {  // ends at the last request at the latest: pos lies on the line
     const Req r = per == 1 ? line.reqs[p.b] : request(a, p.b, cut.rows);
     p.r = Req{uniform(r.q0), uniform(r.qn), uniform(r.kv), uniform(r.tiles), uniform(r.lo), uniform(r.span)};
     p.steps = by_units ? 1 : req_steps(p.r, cut.step);
-    const int64_t all = int64_t(p.r.tiles) * a.cache.heads * p.steps;
+    room = even_steps(p.steps, even);
+    const int64_t all = int64_t(p.r.tiles) * a.cache.heads * room;
     if (local < all || p.b + 1 >= int(a.B)) break;
     local -= all;
   }
   int unit;
   if (local >> 31) {
-    unit = int(local / p.steps);
-    p.at = int(local % p.steps);
+    unit = int(local / room);
+    p.at = int(local % room);
   } else {
-    unit = int(local) / p.steps;
-    p.at = int(local) % p.steps;
+    unit = int(local) / room;
+    p.at = int(local) % room;
   }
   p.head = unit % a.cache.heads;
   p.tile = p.r.tiles - 1 - unit / a.cache.heads;  // the rows that see most first
@@ -496,7 +541,8 @@ struct NarrowLds {
 template <int D, bool PRECISE>
 constexpr int kNarrowBlocks = D == 256 ? (PRECISE ? 1 : 2) : (PRECISE ? 2 : 3);
 
-// Units from which on whole ones are considered with sinks (whole_few): one a CU.
+// Units from which on whole ones are considered with sinks and more than 64 requests
+// (whole_few): one a CU.
 constexpr int kWholeFew = kCUs;
 
 template <int D, bool PRECISE, bool SINKS>
@@ -517,7 +563,8 @@ __global__ __launch_bounds__(256, (kNarrowBlocks<D, PRECISE>)) void kv_attention
   const Cut cut{kNarrowRows, kNarrowStep, int(gridDim.x), SINKS ? kWholeFew : 0, SINKS};
   line_build(a, cut, line);
   const bool by_units = SINKS && uniform(int(line.by_units));
-  const int64_t total = line_total(line), share = by_units ? 1 : line_share(total, cut.blocks);
+  const int even = SINKS ? uniform(line.even) : 0;
+  const int64_t total = line_total(line), share = by_units ? 1 : even > 0 ? even : line_share(total, cut.blocks);
   const int64_t begin_pos = share * blockIdx.x;
   const int64_t end_pos = begin_pos + share < total ? begin_pos + share : total;
   if (begin_pos >= end_pos) write_border(a, blockIdx.x, false, Piece{}, share);
@@ -527,7 +574,7 @@ __global__ __launch_bounds__(256, (kNarrowBlocks<D, PRECISE>)) void kv_attention
     const bool complete = steps == it.steps;
     const int64_t slot = piece_slot(blockIdx.x, pos == begin_pos);
     if (pos == begin_pos) write_border(a, blockIdx.x, true, it, share);
-    pos += steps;
+    pos += even > 0 ? share : steps;  // even shares are of one unit
 
     const int row = it.tile * kNarrowRows + n;
     const bool live = row < it.r.qn * a.group;
