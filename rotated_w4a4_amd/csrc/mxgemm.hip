@@ -8,11 +8,12 @@
 // block, and that block's scale byte.  Sums are fp32.  A scale of 255 makes its
 // products NaN.
 //
-// Operand layout: for 32 x 32 x 64, lane l supplies row l % 32, channels 32 (l / 32)
-// .. + 32; for 16 x 16 x 128, row l % 16, channels 32 (l / 16) .. + 32.  The weights
-// are the row operand and the tokens the column operand, so that a lane ends with
-// one token and 4 consecutive channels at a time: D[8 (r / 4) + 4 (l / 32) + r % 4]
-// [l % 32], r = 0..15, and D[4 (l / 16) + r][l % 16], r = 0..3.
+// Every kernel uses v_mfma_scale_f32_16x16x128_f8f6f4: lane l supplies row l % 16,
+// channels 32 (l / 16) .. + 32.  (With random codes, where the card's power limits the
+// matrix units, it reaches 6.85 PFLOP/s in a loop of nothing else; 32 x 32 x 64, which
+// reads and writes twice the accumulators for each product, 5.4-6.15; on zeros both
+// 9.4.)  The weights are the row operand and the tokens the column operand, so that a
+// lane ends with one token and 4 consecutive channels: D[4 (l / 16) + r][l % 16].
 #include <type_traits>
 
 #include "mx_internal.h"
@@ -23,7 +24,6 @@ namespace rw4 {
 namespace {
 
 typedef int v8i __attribute__((ext_vector_type(8)));
-typedef float v16f __attribute__((ext_vector_type(16)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef unsigned int v4u __attribute__((ext_vector_type(4)));
 typedef unsigned int v2u __attribute__((ext_vector_type(2)));
@@ -58,25 +58,28 @@ __device__ __forceinline__ void store_one(void* y, int64_t at, float v) {
 }
 
 // ---------------------------------------------------------------------------
-// Many rows: BM tokens x BN channels a block, WM x WN waves of TM x TN tiles.  K goes
-// in stages of 256 channels (whole 128-byte lines of the rows) through LDS buffers that the DMA fills (RING of them where the
-// tiles are small and a stage's products take less than the memory's latency).  A stage is four steps of 64 channels; the operands of a step are
-// read from LDS during the products of the step before, also across stages.  So the
-// last reads of a buffer are over when its stage's last step begins: there the wait
-// for the next stage's arrival, the barrier, and the start of the DMA of the stage
-// after that into the buffer just read, which has RING - 1 stages' time to arrive; the
-// matrix unit has the last step's products meanwhile.
+// Many rows: BM tokens x BN channels a block, WM x WN waves of TM x TN tiles of 16 x 16.
+// K goes in stages of 256 channels (whole 128-byte lines of the rows) through a ring of
+// LDS buffers that the DMA fills (RING more than 2 where the tiles are small and a
+// stage's products take less than the memory's latency).  A stage is two steps of 128
+// channels; the operands of a step are read from LDS during the products of the step
+// before, also across stages.  So the reads of a buffer are over when its stage's second
+// step begins: there the wait for the next stage's arrival, the barrier, and the start
+// of the DMA into the buffer just read, which has RING - 1 stages' time to arrive.
+//   Operands: a second set of registers takes the next step's where there is room
+// (TWICE); the 256 x 256 tile reads each one into the registers of the same one as soon
+// as its last product of the step is issued.
 //   A row of a stage is eight 16-byte chunks, chunk c at place c ^ (row & 7), so that 8
 // lanes reading one chunk of 8 rows hit all banks; the DMA writes LDS in lane order,
 // so the exchange is in the addresses it reads from.
 // ---------------------------------------------------------------------------
 constexpr int kStageRow = kGroup;  // bytes of 256 channels
-constexpr int kSteps = 4;
 
 template <int BM, int BN, int WM, int WN>
 struct Tile {
   static constexpr int waves = WM * WN, threads = 64 * waves;
-  static constexpr int TM = BM / WM / 32, TN = BN / WN / 32;  // 32 x 32 tiles of a wave
+  static constexpr int TM = BM / WM / 16, TN = BN / WN / 16;  // 16 x 16 tiles of a wave
+  static constexpr bool twice = TM * TN <= 16;               // two sets of operands
   // a stage in LDS: codes, then the scale words of its two groups of 128 channels
   static constexpr int codes = (BM + BN) * kStageRow, words = (BM + BN) * 4, bytes = codes + 2 * words;
   // DMA instructions of a wave for a stage: 8 rows' codes, and 64 rows' words of a group each
@@ -85,7 +88,7 @@ struct Tile {
   static_assert(BM % (8 * waves) == 0 && BN % (8 * waves) == 0 && BM % 64 == 0 && BN % 64 == 0, "whole DMA instructions");
 };
 
-// Until at most n vector-memory instructions of the wave are in flight; LDS reads go on.
+// Until at most N vector-memory instructions of the wave are in flight; LDS reads go on.
 template <int N>
 __device__ __forceinline__ void wait_vm() {
   static_assert(N >= 0 && N < 64, "vmcnt range");
@@ -113,7 +116,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void mx_gemm_kernel(
   __shared__ __align__(16) uint8_t buf2[RING > 2 ? T::bytes : 16];
   __shared__ __align__(16) uint8_t buf3[RING > 3 ? T::bytes : 16];
 
-  const int tid = threadIdx.x, lane = tid & 63, n = lane & 31, h = lane >> 5;
+  const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, h = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
   int64_t mt, nt;
@@ -170,48 +173,29 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void mx_gemm_kernel(
     }
   };
 
-  v16f acc[TN][TM];
+  v4f acc[TN][TM];
 #pragma unroll
   for (int i = 0; i < TN; ++i)
 #pragma unroll
-    for (int j = 0; j < TM; ++j) acc[i][j] = v16f{};
+    for (int j = 0; j < TM; ++j) acc[i][j] = v4f{};
 
-  int off[kSteps];  // of the lane's chunk of a step in a tile of 32 rows
+  int off[2];  // of the lane's chunk of a step in a tile of 16 rows
 #pragma unroll
-  for (int k = 0; k < kSteps; ++k) off[k] = n * kStageRow + (((2 * k + h) ^ (n & 7)) * 16);
-  const int base_a = wm * TM * 32 * kStageRow, base_w = (BM + wn * TN * 32) * kStageRow;
-  const int base_xa = T::codes + (wm * TM * 32 + n) * 4, base_xw = T::codes + (BM + wn * TN * 32 + n) * 4;
+  for (int k = 0; k < 2; ++k) off[k] = n * kStageRow + (((4 * k + h) ^ (n & 7)) * 16);
+  const int base_a = wm * TM * 16 * kStageRow, base_w = (BM + wn * TN * 16) * kStageRow;
+  const int base_xa = T::codes + (wm * TM * 16 + n) * 4 + h, base_xw = T::codes + (BM + wn * TN * 16 + n) * 4 + h;
 
-  struct Operands {
-    v4u v[TN + TM];  // weights, then activations
+  constexpr int kSets = T::twice ? 2 : 1, P = TN * TM;
+  v4u w[kSets][TN], t[kSets][TM];
+  uint32_t xw[kSets][TN], xt[kSets][TM];  // scale bytes
+  auto read_w = [&](const uint8_t* from, int k, int set, int i) {
+    w[set][i] = *reinterpret_cast<const v4u*>(from + off[k] + base_w + i * 16 * kStageRow);
+    xw[set][i] = from[base_xw + k * T::words + i * 64];
   };
-  struct Scales {
-    uint32_t v[TN + TM];
+  auto read_t = [&](const uint8_t* from, int k, int set, int j) {
+    t[set][j] = *reinterpret_cast<const v4u*>(from + off[k] + base_a + j * 16 * kStageRow);
+    xt[set][j] = from[base_xa + k * T::words + j * 64];
   };
-  auto read_one = [&](const uint8_t* from, int k, int i, Operands& to) {
-    to.v[i] = *reinterpret_cast<const v4u*>(from + off[k] + (i < TN ? base_w + i * 32 * kStageRow
-                                                                    : base_a + (i - TN) * 32 * kStageRow));
-  };
-  auto read_scale = [&](const uint8_t* from, int half, int i, Scales& to) {
-    to.v[i] = *reinterpret_cast<const uint32_t*>(from + half * T::words + (i < TN ? base_xw + i * 128 : base_xa + (i - TN) * 128));
-  };
-  // The products of a step, `meanwhile` between them.  Scale words are shifted so that
-  // bytes 0 and 2 are the lane half's blocks of the two steps.
-  auto multiply = [&](const Operands& o, const Scales& x, auto second, auto meanwhile) {
-    constexpr int kByte = decltype(second)::value ? 2 : 0;
-#pragma unroll
-    for (int at = 0; at < TN * TM; ++at) {
-      const int i = at / TM, j = at % TM;
-      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fp4_operand(o.v[i]), fp4_operand(o.v[TN + j]), acc[i][j],
-                                                                  kFp4, kFp4, kByte, int(x.v[i]), kByte, int(x.v[TN + j]));
-      meanwhile(at);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  };
-
-  Operands o0, o1;
-  Scales x, now;
-  constexpr int P = TN * TM, R = TN + TM;
   // f(i) for i < COUNT, spread over the P products of a step from the first one on
   auto spread = [&](int at, auto count, auto f) {
     constexpr int kCount = decltype(count)::value, kEach = (kCount + P - 1) / P;
@@ -219,12 +203,30 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void mx_gemm_kernel(
     for (int e = 0; e < kEach; ++e)
       if (at * kEach + e < kCount) f(at * kEach + e);
   };
-  using Reads = std::integral_constant<int, R>;
+  using Reads = std::integral_constant<int, TN + TM>;
   using Loads = std::integral_constant<int, T::loads>;
-  auto shift = [&]() {
+  // The products of a step; operands of step k2 of `from` are read meanwhile.
+  auto step = [&](int set, const uint8_t* from, int k2, auto meanwhile) {
 #pragma unroll
-    for (int i = 0; i < R; ++i) now.v[i] = x.v[i] >> (8 * h);
+    for (int j = 0; j < TM; ++j)
+#pragma unroll
+      for (int i = 0; i < TN; ++i) {
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fp4_operand(w[set][i]), fp4_operand(t[set][j]), acc[i][j],
+                                                                     kFp4, kFp4, 0, int(xw[set][i]), 0, int(xt[set][j]));
+        if constexpr (T::twice) {
+          spread(j * TN + i, Reads{}, [&](int e) {
+            if (e < TN) read_w(from, k2, 1 - set, e);
+            else read_t(from, k2, 1 - set, e - TN);
+          });
+        } else {
+          if (j == TM - 1) read_w(from, k2, 0, i);
+          if (i == TN - 1) read_t(from, k2, 0, j);
+        }
+        meanwhile(j * TN + i);
+        __builtin_amdgcn_sched_barrier(0);
+      }
   };
+
 #pragma unroll
   for (int i = 0; i < T::loads; ++i) bring(buf0, 0, i);
 #pragma unroll
@@ -240,33 +242,15 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void mx_gemm_kernel(
   wait_vm<(RING - 1) * T::loads>();
   block_barrier();
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    read_one(buf0, 0, i, o0);
-    read_scale(buf0, 0, i, x);
-  }
-  using First = std::false_type;
-  using Second = std::true_type;
-  // Stage s in `cur`, whose first operands and scales are read; reads those of the next one.
+  for (int i = 0; i < TN; ++i) read_w(buf0, 0, 0, i);
+#pragma unroll
+  for (int j = 0; j < TM; ++j) read_t(buf0, 0, 0, j);
+  // Stage s in `cur`, whose first operands are read; reads those of the next one.
   auto stage = [&](uint8_t* cur, const uint8_t* next, int s) {
-    shift();
-    multiply(o0, now, First{}, [&](int at) { spread(at, Reads{}, [&](int i) { read_one(cur, 1, i, o1); }); });
-    multiply(o1, now, Second{}, [&](int at) {
-      spread(at, Reads{}, [&](int i) {
-        read_one(cur, 2, i, o0);
-        read_scale(cur, 1, i, x);
-      });
-    });
-    shift();
-    multiply(o0, now, First{}, [&](int at) { spread(at, Reads{}, [&](int i) { read_one(cur, 3, i, o1); }); });
+    step(0, cur, 1, [](int) {});
     wait_vm_lds<(RING - 2) * T::loads>();  // the next stage has arrived, this wave has read the last of this one
     block_barrier();                       // for all waves
-    multiply(o1, now, Second{}, [&](int at) {
-      spread(at, Reads{}, [&](int i) {
-        read_one(next, 0, i, o0);
-        read_scale(next, 0, i, x);
-      });
-      spread(at, Loads{}, [&](int i) { bring(cur, s + RING, i); });
-    });
+    step(kSets - 1, next, 0, [&](int at) { spread(at, Loads{}, [&](int i) { bring(cur, s + RING, i); }); });
   };
   int s = 0;
   for (; s + RING <= stages; s += RING) {
@@ -292,20 +276,20 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void mx_gemm_kernel(
   __syncthreads();  // the DMA behind the last stage included
 
   // Output: 32 tokens at a time through the wave's own part of LDS into rows of 16-byte chunks.
-  constexpr int E = BF16 ? 2 : 4, kCols = TN * 32, kOut = kCols * E + 16, kChunks = kCols * E / 16;
+  constexpr int E = BF16 ? 2 : 4, kCols = TN * 16, kOut = kCols * E + 16, kChunks = kCols * E / 16;
   constexpr int kWaveBytes = 32 * kOut, kEach = T::waves / 2;
   static_assert(kEach * kWaveBytes <= T::bytes, "output rows of half of the waves in each buffer");
   uint8_t* out = (wave < kEach ? buf0 : buf1) + (wave % kEach) * kWaveBytes;
   const bool aligned = (ldy * E) % 16 == 0 && (reinterpret_cast<uintptr_t>(y) & 15) == 0;
   const int64_t c0 = n0 + wn * kCols;
 #pragma unroll
-  for (int j = 0; j < TM; ++j) {
+  for (int j = 0; j < TM / 2; ++j) {
 #pragma unroll
     for (int i = 0; i < TN; ++i)
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const v4f v{acc[i][j][4 * b], acc[i][j][4 * b + 1], acc[i][j][4 * b + 2], acc[i][j][4 * b + 3]};
-        uint8_t* dst = out + n * kOut + (i * 32 + 8 * b + 4 * h) * E;
+      for (int b = 0; b < 2; ++b) {
+        const v4f v = acc[i][2 * j + b];
+        uint8_t* dst = out + (16 * b + n) * kOut + (16 * i + 4 * h) * E;
         if constexpr (BF16) {
           v4bf p;
 #pragma unroll
@@ -317,7 +301,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void mx_gemm_kernel(
       }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    const int64_t first = m0 + (wm * TM + j) * 32;
+    const int64_t first = m0 + wm * TM * 16 + j * 32;
     if (aligned && c0 + kCols <= N) {
 #pragma unroll
       for (int it = 0; it < 32 * kChunks / 64; ++it) {
