@@ -137,9 +137,12 @@ class KVCache:
                 or k_scale.shape != k.shape[:3] or v_scale.shape != k.shape[:3]:
             raise ValueError("k and v must be uint8 [pages, kv_heads, page_size, head_dim / 2] and their scales "
                              "float32 [pages, kv_heads, page_size]")
-        # the stride of a dimension of one entry is not used
-        cs, cv, ss, sv = ([x if n > 1 else 0 for x, n in zip(t.stride(), k.shape[:3])] for t in (k, v, k_scale, v_scale))
-        if cv != cs or sv != ss or k.stride(3) != 1 or v.stride(3) != 1:
+        cs, cv, ss, sv = k.stride(), v.stride(), k_scale.stride(), v_scale.stride()
+        last = cs[3] == 1 and cv[3] == 1
+        cs, cv = cs[:3], cv[:3]
+        if 1 in k.shape[:3]:  # the stride of a dimension of one entry is not used
+            cs, cv, ss, sv = (tuple([x if n > 1 else 0 for x, n in zip(t, k.shape)]) for t in (cs, cv, ss, sv))
+        if cv != cs or sv != ss or not last:
             raise ValueError("k and v must have the same strides, with unit stride in a row (their scales likewise)")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.pages, self.kv_heads, self.page_size, half = k.shape
@@ -389,18 +392,20 @@ def _attention(q, cache, block_table, kv_len, cu_q, max_q_len, scale, causal, wi
     B = kv_len.shape[0]
     table, width = _table(block_table, B, dev)
     if out is None:
-        out = torch.empty((T, heads, D), dtype=q.dtype if out_dtype is None else out_dtype, device=q.device)
-    elif out_dtype is not None and out.dtype is not out_dtype:
-        raise TypeError(f"out must be {out_dtype}")
-    op, ot, oh = _rows("out", out, dev, (T, heads, D))
+        out = torch.empty(T, heads, D, dtype=q.dtype if out_dtype is None else out_dtype, device=q.device)
+        op, ot, oh = out.data_ptr(), (heads * D if T > 1 else 0), (D if heads > 1 else 0)
+    else:
+        if out_dtype is not None and out.dtype is not out_dtype:
+            raise TypeError(f"out must be {out_dtype}")
+        op, ot, oh = _rows("out", out, dev, (T, heads, D))
     if lse is not None:
         _out("lse", lse, (T, heads), torch.float32, dev)
     elif return_lse:
-        lse = torch.empty((T, heads), dtype=torch.float32, device=q.device)
+        lse = torch.empty(T, heads, dtype=torch.float32, device=q.device)
     nbytes = kv_attention_workspace_bytes(T, B, heads, kv_heads, D)
     if workspace is None:
         wbytes = nbytes if nbytes > 16 else 16
-        workspace = torch.empty((wbytes,), dtype=torch.uint8, device=q.device)
+        workspace = torch.empty(wbytes, dtype=torch.uint8, device=q.device)
     else:
         _on_gpu("workspace", workspace, dev)
         wbytes = workspace.numel() * workspace.element_size()

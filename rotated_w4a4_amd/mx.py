@@ -17,8 +17,8 @@ import ctypes
 
 import torch
 
-from . import Transform, _dtype_code, _on_gpu, _out, lib
-from .kv import KVCall, _launch
+from . import Transform, _on_gpu, _out, lib
+from .kv import KVCall, _code, _launch
 
 __all__ = ["mx_quantize_act", "prepare_mx_quantize_act", "mx_pack_weight", "mx_dequantize", "prepare_mx_dequantize",
            "mx_gemm", "prepare_mx_gemm", "mx_scale_rows"]
@@ -31,46 +31,54 @@ lib.rw4_mx_gemm.argtypes = [_p, _p, _p, _p, _i64, _i64, _i64, _p, ctypes.c_int, 
 for _name in ("rw4_mx_quantize_act", "rw4_mx_pack_weight", "rw4_mx_dequantize", "rw4_mx_gemm"):
     getattr(lib, _name).restype = ctypes.c_int
 
+_U8, _BF16 = torch.uint8, torch.bfloat16
 
+
+# The checks below look at each tensor once and in one expression: a small call is
+# bound by the host (3.2 us of a call are the launch), and each attribute costs 0.05 to
+# 0.1 us.  What fails is looked at again for its message.
 def _outputs(rows, K, q, s, device, dev):
     """Codes and scales of `rows` rows: allocated, or checked."""
-    u8 = torch.uint8
-    if K <= 0 or K % 128:
+    if K <= 0 or K & 127:
         raise ValueError(f"K must be a positive multiple of 128, not {K}")
     if q is None:
-        q = torch.empty((rows, K // 2), dtype=u8, device=device)
+        q = torch.empty(rows, K >> 1, dtype=_U8, device=device)
     else:
-        _out("q", q, (rows, K // 2), u8, dev)
+        _out("q", q, (rows, K >> 1), _U8, dev)
     if s is None:
-        s = torch.empty((K // 128, rows, 4), dtype=u8, device=device)
+        s = torch.empty(K >> 7, rows, 4, dtype=_U8, device=device)
     else:
-        _out("s", s, (K // 128, rows, 4), u8, dev)
+        _out("s", s, (K >> 7, rows, 4), _U8, dev)
     return q, s
 
 
 def _operand(name, q, s, dev):
     """(rows, K) of codes and scales that a call reads."""
-    if q.dim() != 2 or q.dtype is not torch.uint8 or s.dtype is not torch.uint8:
-        raise ValueError(f"{name}: codes must be uint8 [rows, K / 2] and scales uint8")
-    rows, K = q.shape[0], 2 * q.shape[1]
-    if K == 0 or K % 128 or s.shape != (K // 128, rows, 4):
+    size = q.shape
+    if len(size) == 2 and q.dtype is _U8 and s.dtype is _U8 and q.get_device() == dev and s.get_device() == dev \
+            and q.is_contiguous() and s.is_contiguous():
+        rows, half = size
+        if half and not half & 63 and s.shape == (half >> 6, rows, 4):
+            return rows, half << 1
         raise ValueError(f"{name}: K must be a multiple of 128 and scales [K / 128, rows, 4]")
     _on_gpu(f"{name} codes", q, dev)
     _on_gpu(f"{name} scales", s, dev)
-    if not (q.is_contiguous() and s.is_contiguous()):
-        raise ValueError(f"{name}: codes and scales must be contiguous")
-    return rows, K
+    if len(size) != 2 or q.dtype is not _U8 or s.dtype is not _U8:
+        raise ValueError(f"{name}: codes must be uint8 [rows, K / 2] and scales uint8")
+    raise ValueError(f"{name}: codes and scales must be contiguous")
 
 
 def _result(out, out_dtype, rows, cols, device, dev):
+    """(output, its dtype's code, elements from one row to the next): allocated, or checked."""
     if out is None:
-        return torch.empty((rows, cols), dtype=torch.bfloat16 if out_dtype is None else out_dtype, device=device)
+        dtype = _BF16 if out_dtype is None else out_dtype
+        return torch.empty(rows, cols, dtype=dtype, device=device), _code(dtype), cols if cols > 0 else 1
     _on_gpu("out", out, dev)
     if out_dtype is not None and out.dtype is not out_dtype:
         raise TypeError(f"out must be {out_dtype}")
     if out.dim() != 2 or out.shape != (rows, cols) or (cols > 1 and out.stride(1) != 1):
         raise ValueError(f"out must be [{rows}, {cols}] with unit stride along its rows")
-    return out
+    return out, _code(out.dtype), _pitch(out)
 
 
 def _pitch(t):
@@ -94,14 +102,19 @@ def prepare_mx_quantize_act(t: Transform | None, x, q=None, s=None) -> KVCall:
 
 
 def _quantize(t, x, q, s):
-    dev = _on_gpu("x", x)
+    dev = x.get_device()
+    if dev < 0:
+        _on_gpu("x", x)
     if x.dim() != 2 or x.stride(1) != 1:
         raise ValueError("x must be 2-D with unit stride along K")
     M, K = x.shape
-    if t is not None and K != t.K:
-        raise ValueError(f"x has {K} channels, the transform {t.K}")
+    handle = None
+    if t is not None:
+        if K != t.K:
+            raise ValueError(f"x has {K} channels, the transform {t.K}")
+        handle = t.handle
     q, s = _outputs(M, K, q, s, x.device, dev)
-    args = (None if t is None else t.handle, x.data_ptr(), _dtype_code(x), M, K, _pitch(x), q.data_ptr(), s.data_ptr())
+    args = (handle, x.data_ptr(), _code(x.dtype), M, K, x.stride(0) if M > 1 else K, q.data_ptr(), s.data_ptr())
     return lib.rw4_mx_quantize_act, args, dev, "rw4_mx_quantize_act", (t, x), (q, s)
 
 
@@ -119,7 +132,7 @@ def mx_pack_weight(t: Transform | None, w, layout: str = "kn", qw=None, sw=None)
     qw, sw = _outputs(N, K, qw, sw, w.device, dev)
     if N == 1:
         sn = K * sk
-    _launch(lib.rw4_mx_pack_weight, (None if t is None else t.handle, w.data_ptr(), _dtype_code(w), N, K, sk, sn,
+    _launch(lib.rw4_mx_pack_weight, (None if t is None else t.handle, w.data_ptr(), _code(w.dtype), N, K, sk, sn,
                                      qw.data_ptr(), sw.data_ptr()), dev, "rw4_mx_pack_weight")
     return qw, sw
 
@@ -137,10 +150,12 @@ def prepare_mx_dequantize(q, s, out_dtype=None, out=None) -> KVCall:
 
 
 def _dequantize(q, s, out_dtype, out):
-    dev = _on_gpu("q", q)
+    dev = q.get_device()
+    if dev < 0:
+        _on_gpu("q", q)
     rows, K = _operand("q", q, s, dev)
-    out = _result(out, out_dtype, rows, K, q.device, dev)
-    args = (q.data_ptr(), s.data_ptr(), rows, K, out.data_ptr(), _dtype_code(out), _pitch(out))
+    out, code, pitch = _result(out, out_dtype, rows, K, q.device, dev)
+    args = (q.data_ptr(), s.data_ptr(), rows, K, out.data_ptr(), code, pitch)
     return lib.rw4_mx_dequantize, args, dev, "rw4_mx_dequantize", (q, s), out
 
 
@@ -157,20 +172,21 @@ def prepare_mx_gemm(qa, sa, qw, sw, out_dtype=None, out=None) -> KVCall:
 
 
 def _gemm(qa, sa, qw, sw, out_dtype, out):
-    dev = _on_gpu("qa", qa)
+    dev = qa.get_device()
+    if dev < 0:
+        _on_gpu("qa", qa)
     M, K = _operand("a", qa, sa, dev)
     N, kw = _operand("w", qw, sw, dev)
     if kw != K:
         raise ValueError(f"activations have {K} channels, weights {kw}")
-    out = _result(out, out_dtype, M, N, qa.device, dev)
-    args = (qa.data_ptr(), sa.data_ptr(), qw.data_ptr(), sw.data_ptr(), M, N, K, out.data_ptr(), _dtype_code(out),
-            _pitch(out))
+    out, code, pitch = _result(out, out_dtype, M, N, qa.device, dev)
+    args = (qa.data_ptr(), sa.data_ptr(), qw.data_ptr(), sw.data_ptr(), M, N, K, out.data_ptr(), code, pitch)
     return lib.rw4_mx_gemm, args, dev, "rw4_mx_gemm", (qa, sa, qw, sw), out
 
 
 def mx_scale_rows(s):
     """Scales [rows, K / 32] stored by rows, as the calls take them: uint8 [K / 128, rows, 4]."""
     rows, blocks = s.shape
-    if s.dtype is not torch.uint8 or blocks % 4:
+    if s.dtype is not _U8 or blocks % 4:
         raise ValueError("scales must be uint8 [rows, K / 32] with K a multiple of 128")
     return s.reshape(rows, blocks // 4, 4).transpose(0, 1).contiguous()
