@@ -337,53 +337,167 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void mx_gemm_kernel(
 }
 
 // ---------------------------------------------------------------------------
-// Few rows: a block takes 16 CT channels and up to 16 MT tokens (grid y: chunks of
-// them), its 8 waves split K in slices of 128 channels, two consecutive ones at a
-// time, so that a wave reads whole 128-byte lines of the rows.  Operands go straight
-// to registers, the next slices are loaded before the current ones are multiplied,
-// the waves' sums meet in LDS.
+// Few tiles (a few dozen rows, or few channels): 32 tokens x 32 channels a block, whose
+// 4 waves take 128 channels each of a stage of 512 (256 bytes of a row) for the whole
+// tile and add up in LDS at the end.  The ring, the DMA and the exchange of chunks (place
+// c ^ (row & 15)) as above; a wave's operands of a stage are read during its products of
+// the stage before.
+//   A CU takes in some 60 GB/s by way of L2 however its tiles are shaped, so where 64 x 64
+// tiles are fewer than the CUs smaller ones are faster, though they read more: 61 tokens
+// x 4096 channels, K = 14336, 8.8 us against 15.6 (64 x 64 tiles whose waves split K like
+// here took 17, 32 x 32 straight from memory to registers 16).
 // ---------------------------------------------------------------------------
-constexpr int kFewWaves = 8, kFewPair = 2;
+constexpr int kSplitTile = 32, kSplitWaves = 4, kSplitRow = 256, kSplitRing = 4;
+constexpr int kSplitCodes = 2 * kSplitTile * kSplitRow, kSplitBytes = kSplitCodes + kSplitWaves * 2 * kSplitTile * 4;
+constexpr int kSplitLoads = kSplitCodes / 1024 / kSplitWaves + 1;  // DMA instructions of a wave for a stage
 
-template <int MT, int CT, bool BF16>
+template <bool BF16>
+__global__ __launch_bounds__(64 * kSplitWaves) void mx_gemm_split_kernel(
+    const uint8_t* __restrict__ qa, const uint32_t* __restrict__ sa, const uint8_t* __restrict__ qw,
+    const uint32_t* __restrict__ sw, int64_t M, int64_t N, int64_t K, void* __restrict__ y, int64_t ldy, int64_t tiles_m) {
+  __shared__ __align__(16) uint8_t buf0[kSplitBytes];
+  __shared__ __align__(16) uint8_t buf1[kSplitBytes];
+  __shared__ __align__(16) uint8_t buf2[kSplitBytes];
+  __shared__ __align__(16) uint8_t buf3[kSplitBytes];
+  const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, h = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int64_t mt, nt;
+  mx_tile(blockIdx.x, gridDim.x, tiles_m, mt, nt);
+  const int64_t m0 = mt * kSplitTile, n0 = nt * kSplitTile, row_bytes = K / 2;
+  const int G = int(K / kGroup), stages = (G + kSplitWaves - 1) / kSplitWaves;
+  const int rows_a = int(M - m0 < kSplitTile ? M - m0 : kSplitTile), rows_w = int(N - n0 < kSplitTile ? N - n0 : kSplitTile);
+
+  // codes: wave 0, 1 bring the tokens' rows, 2, 3 the channels', 4 rows an instruction
+  const bool of_a = wave < 2;
+  const int rows = of_a ? rows_a : rows_w;
+  const __amdgpu_buffer_rsrc_t from = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint8_t*>(of_a ? qa + m0 * row_bytes : qw + n0 * row_bytes), 0, int(rows * row_bytes), 0x00020000);
+  uint32_t src[kSplitLoads - 1];
+#pragma unroll
+  for (int i = 0; i < kSplitLoads - 1; ++i) {
+    const int r = (wave & 1) * 16 + 4 * i + h;  // rows beyond the last one read that again
+    src[i] = uint32_t((r < rows ? r : rows - 1) * row_bytes + (n ^ (r & 15)) * 16);
+  }
+  // scales: a wave brings its own group's words, the tokens' in lanes 0 .. 31, then the channels'
+  const int sr = lane & 31;
+  const uint32_t* const scale0 = lane < 32 ? sa + m0 + (sr < rows_a ? sr : rows_a - 1) : sw + n0 + (sr < rows_w ? sr : rows_w - 1);
+  const int64_t scale_step = lane < 32 ? M : N;
+  auto bring = [&](uint8_t* to, int stage) {  // behind the last stage that again, behind the last channel other codes, not used
+    const int s = stage < stages ? stage : stages - 1;
+#pragma unroll
+    for (int i = 0; i < kSplitLoads - 1; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_void_t*)(to + (wave * (kSplitLoads - 1) + i) * 1024), 16, int(src[i]),
+                                               s * kSplitRow, 0, 0);
+    const int g = s * kSplitWaves + wave < G ? s * kSplitWaves + wave : G - 1;
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(scale0 + g * scale_step),
+                                     (lds_void_t*)(to + kSplitCodes + wave * 256), 4, 0, 0);
+  };
+
+  v4f acc[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) acc[i][j] = v4f{};
+  v4u w[2][2], t[2][2];
+  uint32_t xw[2][2], xt[2][2];
+  const int off = n * kSplitRow + (((4 * wave + h) ^ n) * 16), off_x = kSplitCodes + wave * 256 + n * 4 + h;
+  auto read = [&](const uint8_t* b, int set) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      t[set][i] = *reinterpret_cast<const v4u*>(b + off + i * 16 * kSplitRow);
+      w[set][i] = *reinterpret_cast<const v4u*>(b + off + (2 + i) * 16 * kSplitRow);
+      xt[set][i] = b[off_x + i * 64];
+      xw[set][i] = b[off_x + (2 + i) * 64];
+    }
+  };
+  bring(buf0, 0);
+  bring(buf1, 1);
+  bring(buf2, 2);
+  bring(buf3, 3);
+  wait_vm<(kSplitRing - 1) * kSplitLoads>();
+  block_barrier();
+  read(buf0, 0);
+  // Stage s in `cur`, whose operands are read; reads those of the next one.
+  auto stage = [&](uint8_t* cur, const uint8_t* next, int set, int s) {
+    wait_vm_lds<(kSplitRing - 2) * kSplitLoads>();  // the next stage has arrived, this wave has read this one
+    block_barrier();                                // for all waves
+    bring(cur, s + kSplitRing);
+    read(next, 1 - set);
+    if (s * kSplitWaves + wave < G) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fp4_operand(w[set][i]), fp4_operand(t[set][j]),
+                                                                       acc[i][j], kFp4, kFp4, 0, int(xw[set][i]), 0,
+                                                                       int(xt[set][j]));
+    }
+  };
+  int s = 0;
+  for (; s + kSplitRing <= stages; s += kSplitRing) {
+    stage(buf0, buf1, 0, s);
+    stage(buf1, buf2, 1, s + 1);
+    stage(buf2, buf3, 0, s + 2);
+    stage(buf3, buf0, 1, s + 3);
+  }
+  if (s < stages) stage(buf0, buf1, 0, s);
+  if (s + 1 < stages) stage(buf1, buf2, 1, s + 1);
+  if (s + 2 < stages) stage(buf2, buf3, 0, s + 2);
+  __syncthreads();  // the DMA behind the last stage included
+
+  // the waves' sums, one buffer each: [32 tokens][32 channels], 4 floats of padding a token
+  constexpr int kRow = kSplitTile + 4;
+  static_assert(kSplitTile * kRow * 4 <= kSplitBytes, "sums of a wave in a buffer");
+  float* mine = reinterpret_cast<float*>(wave == 0 ? buf0 : wave == 1 ? buf1 : wave == 2 ? buf2 : buf3);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) *reinterpret_cast<v4f*>(mine + (16 * j + n) * kRow + 16 * i + 4 * h) = acc[i][j];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kSplitTile * kSplitTile / (64 * kSplitWaves); ++i) {
+    const int at = i * 64 * kSplitWaves + tid, token = at / kSplitTile, c = at % kSplitTile, from_at = token * kRow + c;
+    const float v = (reinterpret_cast<const float*>(buf0)[from_at] + reinterpret_cast<const float*>(buf1)[from_at]) +
+                    (reinterpret_cast<const float*>(buf2)[from_at] + reinterpret_cast<const float*>(buf3)[from_at]);
+    if (token < rows_a && c < rows_w) store_one<BF16>(y, (m0 + token) * ldy + n0 + c, v);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Single tokens and a few more: a block takes 16 channels and up to 16 tokens, its 8
+// waves split K in slices of 128 channels, two consecutive ones at a time, so that a
+// wave reads whole 128-byte lines of the rows.  Operands go straight to registers, the
+// next slices are loaded before the current ones are multiplied, the waves' sums meet in
+// LDS.  Bound by the launch and the weights' bytes: 1 x 4096 x 4096 3.5 us, 1 x 14336 x
+// 14336 22.8 us (4.8 TB/s).
+// ---------------------------------------------------------------------------
+constexpr int kFewWaves = 8, kFewPair = 2, kFewTokens = 16, kFewChannels = 16;
+
+template <bool BF16>
 __global__ __launch_bounds__(64 * kFewWaves) void mx_gemm_few_kernel(
     const uint8_t* __restrict__ qa, const uint32_t* __restrict__ sa, const uint8_t* __restrict__ qw,
-    const uint32_t* __restrict__ sw, int64_t M, int64_t N, int64_t K, void* __restrict__ y, int64_t ldy) {
-  constexpr int kCols = 16 * CT, kRow = kCols + 4;  // floats of a token's sums; +4: fewer bank conflicts
-  __shared__ __align__(16) float sums[kFewWaves][16][kRow];
-  const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, g4 = lane >> 4;
+    const uint32_t* __restrict__ sw, int M, int64_t N, int64_t K, void* __restrict__ y, int64_t ldy) {
+  __shared__ __align__(16) float sums[kFewWaves][kFewTokens][kFewChannels + 4];  // +4: fewer bank conflicts
+  const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, h = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int64_t n0 = int64_t(blockIdx.x) * kCols, m0 = int64_t(blockIdx.y) * (16 * MT), row_bytes = K / 2;
+  const int64_t n0 = int64_t(blockIdx.x) * kFewChannels, row_bytes = K / 2;
   const int G = int(K / kGroup);
-  int64_t row_a[MT], row_w[CT];  // rows beyond the last one read that again; what they give is not stored
-#pragma unroll
-  for (int i = 0; i < MT; ++i) row_a[i] = m0 + 16 * i + n < M ? m0 + 16 * i + n : M - 1;
-#pragma unroll
-  for (int i = 0; i < CT; ++i) row_w[i] = n0 + 16 * i + n < N ? n0 + 16 * i + n : N - 1;
+  // rows beyond the last one read that again; what they give is not stored
+  const int64_t row_a = n < M ? n : M - 1, row_w = n0 + n < N ? n0 + n : N - 1;
 
   struct Slice {
-    v4u w[CT], a[MT];
-    uint32_t xw[CT], xa[MT];
+    v4u w, t;
+    uint32_t xw, xt;
   };
   auto load = [&](int g, Slice& s) {
     g = g < G ? g : G - 1;
-    const int64_t at = int64_t(g) * 64 + 16 * g4;
-#pragma unroll
-    for (int i = 0; i < CT; ++i) {
-      s.w[i] = *reinterpret_cast<const v4u*>(qw + row_w[i] * row_bytes + at);
-      s.xw[i] = sw[g * N + row_w[i]];
-    }
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      s.a[i] = *reinterpret_cast<const v4u*>(qa + row_a[i] * row_bytes + at);
-      s.xa[i] = sa[g * M + row_a[i]];
-    }
+    const int64_t at = int64_t(g) * 64 + 16 * h;
+    s.w = *reinterpret_cast<const v4u*>(qw + row_w * row_bytes + at);
+    s.xw = sw[g * N + row_w];
+    s.t = *reinterpret_cast<const v4u*>(qa + row_a * row_bytes + at);
+    s.xt = sa[g * int64_t(M) + row_a];
   };
-  v4f acc[MT][CT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int j = 0; j < CT; ++j) acc[i][j] = v4f{};
+  v4f acc{};
   constexpr int kStep = kFewWaves * kFewPair;
   Slice cur[kFewPair], next[kFewPair];
   int g = wave * kFewPair;
@@ -397,37 +511,21 @@ __global__ __launch_bounds__(64 * kFewWaves) void mx_gemm_few_kernel(
       for (int p = 0; p < kFewPair; ++p) load(g + kStep + p, next[p]);
     }
 #pragma unroll
-    for (int p = 0; p < kFewPair; ++p) {
-      if (g + p < G) {
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int j = 0; j < CT; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                fp4_operand(cur[p].w[j]), fp4_operand(cur[p].a[i]), acc[i][j], kFp4, kFp4, 0,
-                int(cur[p].xw[j] >> (8 * g4)), 0, int(cur[p].xa[i] >> (8 * g4)));
-      }
-    }
+    for (int p = 0; p < kFewPair; ++p)
+      if (g + p < G)
+        acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fp4_operand(cur[p].w), fp4_operand(cur[p].t), acc, kFp4, kFp4,
+                                                               0, int(cur[p].xw >> (8 * h)), 0, int(cur[p].xt >> (8 * h)));
 #pragma unroll
     for (int p = 0; p < kFewPair; ++p) cur[p] = next[p];
   }
+  *reinterpret_cast<v4f*>(&sums[wave][n][4 * h]) = acc;
+  __syncthreads();
+  if (tid < kFewTokens * kFewChannels) {
+    const int token = tid / kFewChannels, c = tid % kFewChannels;
+    float v = 0.0f;
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    if (i > 0) {
-      if (m0 + 16 * i >= M) return;  // the whole block
-      __syncthreads();
-    }
-#pragma unroll
-    for (int j = 0; j < CT; ++j) *reinterpret_cast<v4f*>(&sums[wave][n][16 * j + 4 * g4]) = acc[i][j];
-    __syncthreads();
-    for (int at = tid; at < 16 * kCols; at += 64 * kFewWaves) {
-      const int t = at / kCols, c = at % kCols;
-      float v = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kFewWaves; ++w) v += sums[w][t][c];
-      const int64_t m = m0 + 16 * i + t;
-      if (m < M && n0 + c < N) store_one<BF16>(y, m * ldy + n0 + c, v);
-    }
+    for (int w = 0; w < kFewWaves; ++w) v += sums[w][token][c];
+    if (token < M && n0 + c < N) store_one<BF16>(y, token * ldy + n0 + c, v);
   }
 }
 
@@ -437,22 +535,31 @@ hipError_t launch_mx_gemm(const uint8_t* qa, const uint8_t* sa, const uint8_t* q
                           int64_t N, int64_t K, void* y, bool y_bf16, int64_t ldy, hipStream_t st) {
   const uint32_t* xa = reinterpret_cast<const uint32_t*>(sa);
   const uint32_t* xw = reinterpret_cast<const uint32_t*>(sw);
-  auto few = [&](auto mt, auto ct) {
-    constexpr int MT = decltype(mt)::value, CT = decltype(ct)::value;
-    const int64_t blocks = (N + 16 * CT - 1) / (16 * CT), chunks = (M + 16 * MT - 1) / (16 * MT);
-    if (blocks > (int64_t(1) << 22) || chunks > 65535) return hipErrorInvalidValue;
-    const dim3 grid{unsigned(blocks), unsigned(chunks), 1u};
+  constexpr int64_t kMostBlocks = int64_t(1) << 22;  // a grid has fewer than 2^32 threads
+  auto few = [&]() {
+    const int64_t blocks = (N + kFewChannels - 1) / kFewChannels;
+    if (blocks > kMostBlocks) return hipErrorInvalidValue;
+    const dim3 grid{unsigned(blocks)}, threads{64 * kFewWaves};
     if (y_bf16)
-      hipLaunchKernelGGL((mx_gemm_few_kernel<MT, CT, true>), grid, dim3(64 * kFewWaves), 0, st, qa, xa, qw, xw, M, N, K, y, ldy);
+      hipLaunchKernelGGL((mx_gemm_few_kernel<true>), grid, threads, 0, st, qa, xa, qw, xw, int(M), N, K, y, ldy);
     else
-      hipLaunchKernelGGL((mx_gemm_few_kernel<MT, CT, false>), grid, dim3(64 * kFewWaves), 0, st, qa, xa, qw, xw, M, N, K, y, ldy);
+      hipLaunchKernelGGL((mx_gemm_few_kernel<false>), grid, threads, 0, st, qa, xa, qw, xw, int(M), N, K, y, ldy);
+    return hipGetLastError();
+  };
+  auto split = [&]() {
+    const int64_t tiles_m = (M + kSplitTile - 1) / kSplitTile, blocks = tiles_m * ((N + kSplitTile - 1) / kSplitTile);
+    const dim3 grid{unsigned(blocks)}, threads{64 * kSplitWaves};
+    if (y_bf16)
+      hipLaunchKernelGGL((mx_gemm_split_kernel<true>), grid, threads, 0, st, qa, xa, qw, xw, M, N, K, y, ldy, tiles_m);
+    else
+      hipLaunchKernelGGL((mx_gemm_split_kernel<false>), grid, threads, 0, st, qa, xa, qw, xw, M, N, K, y, ldy, tiles_m);
     return hipGetLastError();
   };
   auto many = [&](auto bm, auto bn, auto wm, auto wn, auto ring) {
     constexpr int BM = decltype(bm)::value, BN = decltype(bn)::value, WM = decltype(wm)::value, WN = decltype(wn)::value,
                   R = decltype(ring)::value;
     const int64_t tiles_m = (M + BM - 1) / BM, blocks = tiles_m * ((N + BN - 1) / BN);
-    if (blocks > (int64_t(1) << 22)) return hipErrorInvalidValue;
+    if (blocks > kMostBlocks) return hipErrorInvalidValue;
     const dim3 grid{unsigned(blocks)}, threads{64 * WM * WN};
     if (y_bf16)
       hipLaunchKernelGGL((mx_gemm_kernel<BM, BN, WM, WN, R, true>), grid, threads, 0, st, qa, xa, qw, xw, M, N, K, y, ldy,
@@ -463,22 +570,20 @@ hipError_t launch_mx_gemm(const uint8_t* qa, const uint8_t* sa, const uint8_t* q
     return hipGetLastError();
   };
   using std::integral_constant;
-  const integral_constant<int, 1> k1{};
   const integral_constant<int, 2> k2{};
+  const integral_constant<int, 3> k3{};
   const integral_constant<int, 4> k4{};
+  const integral_constant<int, 64> k64{};
   const integral_constant<int, 128> k128{};
   const integral_constant<int, 256> k256{};
-  const integral_constant<int, 64> k64{};
-  const integral_constant<int, 3> k3{};
-  // Measured with K = 4096 (times in us, launch included).  The kernel for few rows reads
-  // all of its tokens for every 16 or 32 channels, the tiles wait for the memory once a
-  // stage whatever their number, so the former is for small M N, or few tokens:
-  //   M x N         few / 64 x 64 tiles       M x N         few / 64 x 64 tiles
-  //   1 x 4096      3.8 / 7.1                 61 x 4096     6.6 / 7.1
-  //   1 x 14336     7.6 / 7.3                 61 x 6144     10.0 / 7.1
-  //   16 x 8192     6.2 / 7.0                 61 x 11008    14.0 / 7.4
-  //   16 x 14336    9.9 / 7.1                 100 x 2048    6.4 / 7.1
-  if (M <= 8 || (N <= 8192 && M * N <= (int64_t(1) << 18))) return M <= 16 ? few(k1, k1) : few(k2, k2);
+  // Measured with K = 4096 (in brackets 14336), us, the launch included.
+  //   Single tokens / 32 x 32:  1 x 4096 3.5 (6.9) / 4.4 (8.0), 16 x 4096 4.1 (9.1) / 4.5 (8.1),
+  //   16 x 14336 9.9 / 7.9
+  if (M <= 8) return few();
+  //   32 x 32 / 64 x 64, by small tiles:  61 x 4096 (256) 4.8 (8.8) / 6.1 (15.7), 128 x 4096
+  //   (512) 6.9 (14.4) / 6.4 (15.9), 61 x 11008 (688) 9.4 / 7.1, 256 x 4096 (1024) 11.4 (24.8) /
+  //   7.0 (16.8)
+  if (((M + 31) / 32) * ((N + 31) / 32) <= 384) return split();
   // 64 x 64, 128 x 128: up to 2 1/2 of the small tiles for each CU
   //   512 x 4096 (512 small tiles) 10.0 / 13.2, 256 x 11008 (688) 13.6 / 13.5,
   //   384 x 8192 (768) 14.1 / 13.6, 1024 x 4096 (1024) 18.3 / 14.5

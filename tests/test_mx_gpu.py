@@ -209,7 +209,8 @@ def _gemm_check(ca, sa, cw, sw, dtype, ldy=None, what=""):
 
 GEMMS = [(1, 1, 128), (1, 16, 128), (2, 17, 256), (7, 100, 384), (16, 64, 2176), (17, 33, 512), (33, 130, 1152),
          (64, 48, 4096), (65, 129, 128), (100, 1, 640), (128, 128, 256), (129, 257, 384), (200, 513, 2048),
-         (257, 300, 640), (300, 1000, 1408), (1000, 72, 896), (511, 511, 1152)]
+         (257, 300, 640), (300, 1000, 1408), (1000, 72, 896), (511, 511, 1152), (640, 640, 128), (500, 1100, 384),
+         (449, 1001, 256), (900, 901, 2176)]
 
 
 @pytest.mark.parametrize("M,N,K", GEMMS)
@@ -219,8 +220,8 @@ def test_gemm(M, N, K, dtype):
     _gemm_check(*_operand(rng, M, K), *_operand(rng, N, K), dtype, what=f"{M}x{N}x{K}")
 
 
-@pytest.mark.parametrize("M,N,K", [(5, 40, 14336), (77, 96, 4224), (140, 270, 4096), (600, 520, 1024), (2100, 700, 640),
-                                   (3841, 4093, 640), (4096, 3588, 384), (1700, 1500, 128)])
+@pytest.mark.parametrize("M,N,K", [(5, 40, 14336), (77, 96, 4224), (140, 270, 4096), (61, 800, 14336), (600, 520, 1024),
+                                   (700, 1300, 1152), (2100, 700, 640), (3841, 4093, 640), (4096, 3588, 384), (1700, 1500, 128)])
 def test_gemm_of_whole_numbers_is_exact(M, N, K):
     # scales of 1: products are multiples of 1/4, sums stay below 36 K < 2^22, so fp32 holds each exactly
     rng = np.random.default_rng(M)
@@ -231,7 +232,7 @@ def test_gemm_of_whole_numbers_is_exact(M, N, K):
     assert np.array_equal(np64(got), want)
 
 
-@pytest.mark.parametrize("M,N,K", [(3, 20, 512), (40, 50, 640), (150, 140, 640)])
+@pytest.mark.parametrize("M,N,K", [(3, 20, 512), (40, 50, 640), (150, 140, 640), (520, 700, 640)])
 def test_gemm_places_every_block(M, N, K):
     # one block of one row of each side is not zero: the product shows where its codes and scales went
     rng = np.random.default_rng(9)
@@ -247,7 +248,7 @@ def test_gemm_places_every_block(M, N, K):
         assert np.array_equal(np64(got), want), b
 
 
-@pytest.mark.parametrize("M,N", [(2, 30), (40, 40), (150, 140)])
+@pytest.mark.parametrize("M,N", [(2, 30), (40, 40), (150, 140), (700, 700)])
 def test_gemm_scales_at_their_ends(M, N):
     rng = np.random.default_rng(10)
     ca, sa = _operand(rng, M, 256)
