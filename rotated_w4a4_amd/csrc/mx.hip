@@ -567,7 +567,7 @@ hipError_t launch_mx_pack(const MxRows& a, hipStream_t st) {
   return by_kind(a, [&](auto bf16, auto block, auto sign) {
     using P = Pack<decltype(block)::value>;
     const int64_t spans = a.K / P::span, blocks = (a.rows + P::rows - 1) / P::rows * spans;
-    if (blocks > (int64_t(1) << 23)) return hipErrorInvalidValue;  // a grid has fewer than 2^32 threads
+    if (blocks >= (int64_t(1) << 24)) return hipErrorInvalidValue;  // a grid has fewer than 2^32 threads; 2^37 values
     if (vector)
       hipLaunchKernelGGL((mx_pack_kernel<decltype(bf16)::value, decltype(block)::value, decltype(sign)::value, true>),
                          dim3(unsigned(blocks)), dim3(256), 0, st, a, spans);

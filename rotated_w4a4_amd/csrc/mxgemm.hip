@@ -535,10 +535,9 @@ hipError_t launch_mx_gemm(const uint8_t* qa, const uint8_t* sa, const uint8_t* q
                           int64_t N, int64_t K, void* y, bool y_bf16, int64_t ldy, hipStream_t st) {
   const uint32_t* xa = reinterpret_cast<const uint32_t*>(sa);
   const uint32_t* xw = reinterpret_cast<const uint32_t*>(sw);
-  constexpr int64_t kMostBlocks = int64_t(1) << 22;  // a grid has fewer than 2^32 threads
+  constexpr int64_t kMostBlocks = int64_t(1) << 22;  // of 512 threads: a grid has fewer than 2^32
   auto few = [&]() {
     const int64_t blocks = (N + kFewChannels - 1) / kFewChannels;
-    if (blocks > kMostBlocks) return hipErrorInvalidValue;
     const dim3 grid{unsigned(blocks)}, threads{64 * kFewWaves};
     if (y_bf16)
       hipLaunchKernelGGL((mx_gemm_few_kernel<true>), grid, threads, 0, st, qa, xa, qw, xw, int(M), N, K, y, ldy);
@@ -559,7 +558,7 @@ hipError_t launch_mx_gemm(const uint8_t* qa, const uint8_t* sa, const uint8_t* q
     constexpr int BM = decltype(bm)::value, BN = decltype(bn)::value, WM = decltype(wm)::value, WN = decltype(wn)::value,
                   R = decltype(ring)::value;
     const int64_t tiles_m = (M + BM - 1) / BM, blocks = tiles_m * ((N + BN - 1) / BN);
-    if (blocks > kMostBlocks) return hipErrorInvalidValue;
+    if (blocks > kMostBlocks) return hipErrorInvalidValue;  // 2^38 outputs, or 2^22 times 256 rows: none fits the card
     const dim3 grid{unsigned(blocks)}, threads{64 * WM * WN};
     if (y_bf16)
       hipLaunchKernelGGL((mx_gemm_kernel<BM, BN, WM, WN, R, true>), grid, threads, 0, st, qa, xa, qw, xw, M, N, K, y, ldy,
@@ -579,7 +578,7 @@ hipError_t launch_mx_gemm(const uint8_t* qa, const uint8_t* sa, const uint8_t* q
   // Measured with K = 4096 (in brackets 14336), us, the launch included.
   //   Single tokens / 32 x 32:  1 x 4096 3.5 (6.9) / 4.4 (8.0), 16 x 4096 4.1 (9.1) / 4.5 (8.1),
   //   16 x 14336 9.9 / 7.9
-  if (M <= 8) return few();
+  if (M <= 8 && N <= kMostBlocks * kFewChannels) return few();
   //   32 x 32 / 64 x 64, by small tiles:  61 x 4096 (256) 4.8 (8.8) / 6.1 (15.7), 128 x 4096
   //   (512) 6.9 (14.4) / 6.4 (15.9), 61 x 11008 (688) 9.4 / 7.1, 256 x 4096 (1024) 11.4 (24.8) /
   //   7.0 (16.8)

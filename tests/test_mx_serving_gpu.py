@@ -222,6 +222,24 @@ def test_offsets_beyond_32_bits():
     assert ((y[:, M - last:].double().t() - ref).abs() <= K * 2.0 ** -23 * size + 1e-30).all()
 
 
+@pytest.mark.parametrize("M", [1, 8])
+def test_single_tokens_times_more_channels_than_a_grid_of_16_holds(M):
+    K, N = 128, 2 ** 27 + 40
+    g = torch.Generator(device=ku.DEV)
+    g.manual_seed(2)
+    qw = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device=ku.DEV, generator=g)
+    sw = torch.randint(124, 130, (1, N, 4), dtype=torch.uint8, device=ku.DEV, generator=g)
+    qa, sa = qw[77:77 + M].clone(), sw[:, 77:77 + M].clone()
+    y = rw4.mx_gemm(qa, sa, qw, sw, F32)
+    a = rw4.mx_dequantize(qa, sa, F32).double()
+    for first in (0, 2 ** 26 - 50, 2 ** 27 - 60, N - 100):
+        w = rw4.mx_dequantize(qw[first:first + 100].clone(), sw[:, first:first + 100].clone(), F32).double().t()
+        w = w.contiguous()
+        # fp32 sums of 128 exact products: half a step of at most their sum of sizes each
+        tol = K * 2.0 ** -24 * (a.abs() @ w.abs())
+        assert ((y[:, first:first + 100].double() - a @ w).abs() <= tol).all(), first
+
+
 def test_results_do_not_depend_on_the_other_rows():
     # a row alone, among others, and beside rows of NaN: the same codes; the product of the same kernel the same bits
     rng = np.random.default_rng(31)
