@@ -40,11 +40,11 @@ constexpr bool whole_units(int64_t units, int64_t whole, int64_t grid, int64_t l
 //   64 of 1 to 3000 keys, window 2048   9, 55.1 / 17, 38.5
 //   64 requests, window 512             4, 27.7 / 5, 21.0
 //   64 requests, window 8192            43, 135 / 65, 134
-constexpr int even_most(int equal) { return 2 * equal + 8; }
+constexpr int64_t even_most(int64_t equal) { return 2 * equal + 8; }
 // With more than 64 requests the even share is a whole unit, where there are `whole` of
 // them or more and the grid has blocks for all.
 constexpr bool whole_few(int64_t units, int64_t whole, int64_t grid, int64_t longest, int64_t steps, int blocks) {
-  return whole > 0 && units >= whole && units <= grid && longest <= even_most(int((steps + blocks - 1) / blocks));
+  return whole > 0 && units >= whole && units <= grid && longest <= even_most((steps + blocks - 1) / blocks);
 }
 
 // Blocks of the kernel for many rows, for so many units at most: a block for each,

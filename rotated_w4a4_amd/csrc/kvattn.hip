@@ -207,7 +207,7 @@ __device__ __forceinline__ int even_steps(int steps, int even) { return even > 0
 // takes part.
 __device__ __forceinline__ int even_share(int units, int steps, int total, int blocks) {
   const int longest = __builtin_amdgcn_readlane(wave_upmost_dpp(units > 0 ? steps : 0), kWave - 1);
-  const int equal = total > blocks ? (total + blocks - 1) / blocks : 1, most = even_most(equal);
+  const int equal = total > blocks ? (total + blocks - 1) / blocks : 1, most = int(even_most(equal));  // total < 2^31
   for (int parts = (longest + equal - 1) / equal; parts > 0; parts -= 1 + (parts >> 4)) {
     const int share = (longest + parts - 1) / parts;
     if (share > most) break;
