@@ -72,6 +72,11 @@ __device__ __forceinline__ void store_one(void* y, int64_t at, float v) {
 //   A row of a stage is eight 16-byte chunks, chunk c at place c ^ (row & 7), so that 8
 // lanes reading one chunk of 8 rows hit all banks; the DMA writes LDS in lane order,
 // so the exchange is in the addresses it reads from.
+//   Bound, 256 x 256: matrix units 52 % busy over the launch at 4096 x 4096, K = 14336, 104 us
+// (4.6 PFLOP/s; the products alone 89 us, power-limited, the loads alone 66); 128 x 128:
+// the loads through L2 (a CU takes in 60 to 90 GB/s) and LDS beside the products, 2048 x
+// 4096, K = 4096, 21.4 us (3.2 PFLOP/s, 4.9 of it launch, first loads and output); 64 x 64: the
+// loads' latency, 61 x 11008, K = 4096, 6.9 us (25 MB at 3.7 TB/s).
 // ---------------------------------------------------------------------------
 constexpr int kStageRow = kGroup;  // bytes of 256 channels
 
@@ -465,15 +470,19 @@ __global__ __launch_bounds__(64 * kSplitWaves) void mx_gemm_split_kernel(
 
 // ---------------------------------------------------------------------------
 // Single tokens and a few more: a block takes 16 channels and up to 16 tokens, its 8
-// waves split K in slices of 128 channels, two consecutive ones at a time, so that a
-// wave reads whole 128-byte lines of the rows.  Operands go straight to registers, the
-// next slices are loaded before the current ones are multiplied, the waves' sums meet in
-// LDS.  Bound by the launch and the weights' bytes: 1 x 4096 x 4096 3.5 us, 1 x 14336 x
-// 14336 22.8 us (4.8 TB/s).
+// waves split K in slices of 128 channels, PAIR consecutive ones at a time, so that a
+// wave reads whole lines of the rows: 2 (128 bytes), 4 for longer rows.  Operands go
+// straight to registers, the next slices are loaded before the current ones are
+// multiplied, the waves' sums meet in LDS.
+//   Bound by the launch, then by the weights' bytes: 1 x 4096 x 4096 3.9 us, 1 x 65536 x
+// 4096 26.6 (5.4 TB/s), 1 x 14336 x 14336 21.1 (5.2 TB/s).  PAIR 2 / 4, us: 1 x 65536 x 4096
+// 26.6 / 29.5, 1 x 11008 x 4096 6.4 / 7.2, 1 x 4096 x 14336 7.0 / 7.3, 1 x 14336 x 14336
+// 22.7 / 21.1, 1 x 28672 x 8192 29.5 / 23.8, 1 x 4096 x 8192 6.6 / 5.3 (rows of 4 KB share
+// their memory channels).
 // ---------------------------------------------------------------------------
-constexpr int kFewWaves = 8, kFewPair = 2, kFewTokens = 16, kFewChannels = 16;
+constexpr int kFewWaves = 8, kFewTokens = 16, kFewChannels = 16;
 
-template <bool BF16>
+template <int PAIR, bool BF16>
 __global__ __launch_bounds__(64 * kFewWaves) void mx_gemm_few_kernel(
     const uint8_t* __restrict__ qa, const uint32_t* __restrict__ sa, const uint8_t* __restrict__ qw,
     const uint32_t* __restrict__ sw, int M, int64_t N, int64_t K, void* __restrict__ y, int64_t ldy) {
@@ -498,25 +507,25 @@ __global__ __launch_bounds__(64 * kFewWaves) void mx_gemm_few_kernel(
     s.xt = sa[g * int64_t(M) + row_a];
   };
   v4f acc{};
-  constexpr int kStep = kFewWaves * kFewPair;
-  Slice cur[kFewPair], next[kFewPair];
-  int g = wave * kFewPair;
+  constexpr int kStep = kFewWaves * PAIR;
+  Slice cur[PAIR], next[PAIR];
+  int g = wave * PAIR;
   if (g < G) {
 #pragma unroll
-    for (int p = 0; p < kFewPair; ++p) load(g + p, cur[p]);
+    for (int p = 0; p < PAIR; ++p) load(g + p, cur[p]);
   }
   for (; g < G; g += kStep) {
     if (g + kStep < G) {
 #pragma unroll
-      for (int p = 0; p < kFewPair; ++p) load(g + kStep + p, next[p]);
+      for (int p = 0; p < PAIR; ++p) load(g + kStep + p, next[p]);
     }
 #pragma unroll
-    for (int p = 0; p < kFewPair; ++p)
+    for (int p = 0; p < PAIR; ++p)
       if (g + p < G)
         acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fp4_operand(cur[p].w), fp4_operand(cur[p].t), acc, kFp4, kFp4,
                                                                0, int(cur[p].xw >> (8 * h)), 0, int(cur[p].xt >> (8 * h)));
 #pragma unroll
-    for (int p = 0; p < kFewPair; ++p) cur[p] = next[p];
+    for (int p = 0; p < PAIR; ++p) cur[p] = next[p];
   }
   *reinterpret_cast<v4f*>(&sums[wave][n][4 * h]) = acc;
   __syncthreads();
@@ -536,13 +545,13 @@ hipError_t launch_mx_gemm(const uint8_t* qa, const uint8_t* sa, const uint8_t* q
   const uint32_t* xa = reinterpret_cast<const uint32_t*>(sa);
   const uint32_t* xw = reinterpret_cast<const uint32_t*>(sw);
   constexpr int64_t kMostBlocks = int64_t(1) << 22;  // of 512 threads: a grid has fewer than 2^32
-  auto few = [&]() {
-    const int64_t blocks = (N + kFewChannels - 1) / kFewChannels;
-    const dim3 grid{unsigned(blocks)}, threads{64 * kFewWaves};
+  auto few = [&](auto pair) {
+    constexpr int P = decltype(pair)::value;
+    const dim3 grid{unsigned((N + kFewChannels - 1) / kFewChannels)}, threads{64 * kFewWaves};
     if (y_bf16)
-      hipLaunchKernelGGL((mx_gemm_few_kernel<true>), grid, threads, 0, st, qa, xa, qw, xw, int(M), N, K, y, ldy);
+      hipLaunchKernelGGL((mx_gemm_few_kernel<P, true>), grid, threads, 0, st, qa, xa, qw, xw, int(M), N, K, y, ldy);
     else
-      hipLaunchKernelGGL((mx_gemm_few_kernel<false>), grid, threads, 0, st, qa, xa, qw, xw, int(M), N, K, y, ldy);
+      hipLaunchKernelGGL((mx_gemm_few_kernel<P, false>), grid, threads, 0, st, qa, xa, qw, xw, int(M), N, K, y, ldy);
     return hipGetLastError();
   };
   auto split = [&]() {
@@ -575,23 +584,25 @@ hipError_t launch_mx_gemm(const uint8_t* qa, const uint8_t* sa, const uint8_t* q
   const integral_constant<int, 64> k64{};
   const integral_constant<int, 128> k128{};
   const integral_constant<int, 256> k256{};
-  // Measured with K = 4096 (in brackets 14336), us, the launch included.
-  //   Single tokens / 32 x 32:  1 x 4096 3.5 (6.9) / 4.4 (8.0), 16 x 4096 4.1 (9.1) / 4.5 (8.1),
-  //   16 x 14336 9.9 / 7.9
-  if (M <= 8 && N <= kMostBlocks * kFewChannels) return few();
-  //   32 x 32 / 64 x 64, by small tiles:  61 x 4096 (256) 4.8 (8.8) / 6.1 (15.7), 128 x 4096
-  //   (512) 6.9 (14.4) / 6.4 (15.9), 61 x 11008 (688) 9.4 / 7.1, 256 x 4096 (1024) 11.4 (24.8) /
-  //   7.0 (16.8)
-  if (((M + 31) / 32) * ((N + 31) / 32) <= 384) return split();
-  // 64 x 64, 128 x 128: up to 2 1/2 of the small tiles for each CU
-  //   512 x 4096 (512 small tiles) 10.0 / 13.2, 256 x 11008 (688) 13.6 / 13.5,
-  //   384 x 8192 (768) 14.1 / 13.6, 1024 x 4096 (1024) 18.3 / 14.5
+  // Measured at M x N, K = 4096 (in brackets 14336), us, the launch included.
+  const bool longer = K > 4096;
+  //   Single tokens / 32 x 32:  1 x 4096 3.9 (7.3) / 4.4 (7.9), 4 x 4096 3.8 (7.6) / 4.4 (8.0), 4 x 14336
+  //   8.2 (23.2) / 7.8 (20.0), 8 x 4096 4.0 / 4.4, 8 x 14336 8.7 / 7.8; 1 x 65536 26.6 / 30.9, 8 x 65536 35.6 / 31.5
+  if (M <= 4 && N <= kMostBlocks * kFewChannels) return longer ? few(k4) : few(k2);
+  //   32 x 32 / 64 x 64, by small tiles:  61 x 4096 (256) 4.9 (8.8) / 6.3 (15.6), 32 x 11008 (344)
+  //   7.9 / 6.8, 61 x 6144 (384) 7.0 (14.3) / 6.6 (16.0), 128 x 4096 (512) 6.9 (14.5) / 6.4 (15.8),
+  //   61 x 11008 (688) 9.5 / 6.9, 256 x 4096 (1024) 11.5 (25.2) / 7.0 (16.7)
+  if (((M + 31) / 32) * ((N + 31) / 32) <= (longer ? 512 : 288)) return split();
+  // 64 x 64, 128 x 128: up to 3 of the small tiles for each CU
+  //   512 x 4096 (512 small tiles) 10.1 (25.4) / 13.3 (38.3), 256 x 11008 (688) 13.0 / 13.4,
+  //   384 x 8192 (768) 13.2 / 13.4, 1024 x 4096 (1024) 17.0 (50.2) / 14.2 (42.1)
   const int64_t small = ((M + 63) / 64) * ((N + 63) / 64);
-  if (small <= 640) return many(k64, k64, k2, k2, k3);
+  if (small <= 768) return many(k64, k64, k2, k2, k3);
   // 128 x 128, 256 x 256: the large tiles where they fill 7/8 of the rounds of a block for
   // each CU that they take
-  //   2048 x 4096 (128 large tiles) 22 / 29, 2048 x 6144 (192) 32 / 33, 2048 x 8192 (256) 41 / 37,
-  //   3000 x 6144 (288) 49 / 58, 2048 x 14336 (448) 70 / 65; 4096 x 14336 x 4096 127 / 105
+  //   2048 x 4096 (128 large tiles) 21.4 (62.8) / 29.2 (84.8), 2048 x 6144 (192) 30.5 / 30.7, 2048 x 8192 (256)
+  //   39.8 / 36.6, 3000 x 6144 (288) 47.0 / 58.6, 2048 x 14336 (448) 66.3 / 64.6, 4096 x 4096 (256) (123.7) / (104.2)
+  //   (128 x 256 tiles, 4 or 8 waves: 21.8 to 23.6 at 2048 x 4096, 118 at 4096 x 4096, K = 14336)
   const int64_t large = ((M + 255) / 256) * ((N + 255) / 256), rounds = (large + 255) / 256;
   return 8 * large >= 7 * 256 * rounds ? many(k256, k256, k4, k2, k2) : many(k128, k128, k2, k2, k2);
 }

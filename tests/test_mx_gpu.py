@@ -220,8 +220,9 @@ def test_gemm(M, N, K, dtype):
     _gemm_check(*_operand(rng, M, K), *_operand(rng, N, K), dtype, what=f"{M}x{N}x{K}")
 
 
-@pytest.mark.parametrize("M,N,K", [(5, 40, 14336), (77, 96, 4224), (140, 270, 4096), (61, 800, 14336), (600, 520, 1024),
-                                   (700, 1300, 1152), (2100, 700, 640), (3841, 4093, 640), (4096, 3588, 384), (1700, 1500, 128)])
+@pytest.mark.parametrize("M,N,K", [(5, 40, 14336), (3, 70, 14336), (4, 1001, 8192), (1, 33, 4224), (77, 96, 4224),
+                                   (140, 270, 4096), (61, 800, 14336), (600, 520, 1024), (700, 1300, 1152),
+                                   (2100, 700, 640), (3841, 4093, 640), (4096, 3588, 384), (1700, 1500, 128)])
 def test_gemm_of_whole_numbers_is_exact(M, N, K):
     # scales of 1: products are multiples of 1/4, sums stay below 36 K < 2^22, so fp32 holds each exactly
     rng = np.random.default_rng(M)
