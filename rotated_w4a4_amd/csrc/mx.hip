@@ -289,10 +289,10 @@ __device__ __forceinline__ MxWord encode(const float (&x)[8], int lane) {
 // drops it: a branch around a store would make the compiler wait for everything in
 // flight, the next row's values among it.  Rows are at most 2^28, so the offsets of
 // four groups' scales stay in 32 bits.
-//   Bound by memory and the vector units together: 4096 x 14336 bf16, block 128, 35 us
-// (149 MB at 4.2 TB/s, vector units 70 % busy, where a copy reaches 4.9); 1333 x 8192
-// fp32, block 256, signs, 13 us (49 MB at 3.8 TB/s, 36 % busy: two to three rows a
-// wave, whose first loads nothing covers).
+//   Bound by the vector units, some 20 instructions a channel: 4096 x 14336 bf16, block
+// 128, 35 us (149 MB at 4.2 TB/s, where a copy reaches 4.9; a busy CU issues a vector
+// instruction in all of its cycles).  1333 x 8192 fp32, block 256, signs, 13 us (49 MB at
+// 3.8 TB/s: two to three rows a wave, whose first loads nothing covers).
 // ---------------------------------------------------------------------------
 template <bool BF16, int BLOCK, bool SIGNED, bool QUAD>
 __global__ __launch_bounds__(256) void mx_quantize_kernel(MxRows a, uint32_t spans, uint32_t walkers) {
@@ -385,7 +385,7 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(MxRows a, uint32_t spa
 // lies at k + k / 8, so that lanes reading every ninth word hit all banks; rows are an
 // odd number of words apart for the writes.
 //   Bound by memory: 4096 x 4096 fp32 as [K, N], block 128, 18 us (76 MB at 4.2 TB/s,
-// vector units 38 % busy); 4 blocks a CU, of which some load while others encode.
+// vector units 76 % busy); 4 blocks a CU, of which some load while others encode.
 // ---------------------------------------------------------------------------
 template <int BLOCK>
 struct Pack {
