@@ -16,11 +16,12 @@
 // |y| < 8 each.  With
 //   d = (n + 1/8) 2^-24 S c 2^-E + 2^-20
 // (the eighth for S's own roundings, below 2^-19 of it) a lane converts y - d and y + d:
-// where the codes of both are the same they are the code of the exact value.  Otherwise,
-// or where the maximum could lie on either side of a power of two, the wave evaluates
-// its rows again in fp64 (about one wave of 512 Gaussian values in 60 in blocks of 128).
-// fp64 for every row would take several times as long, fp32 alone would decide ties by
-// the order of its additions: with blocks of 256 and bf16 values, exact ties are common.
+// where the codes of both are the same they are the code of the exact value.  Where they
+// differ (about one wave of 512 Gaussian values in 60 in blocks of 128) the wave
+// evaluates those values again in fp64 (settle), or all of its rows where they are many
+// or the maximum could lie on either side of a power of two (encode64).  fp64 for every
+// row would take several times as long, fp32 alone would decide ties by the order of
+// its additions: with blocks of 256 and bf16 values, exact ties are common.
 #include <type_traits>
 
 #include "mx_internal.h"
@@ -161,6 +162,15 @@ __device__ __forceinline__ void lane_stage64_swap(double (&u)[8], int lane) {
   }
 }
 
+// The sum over lane bit M.
+template <int M>
+__device__ __forceinline__ double sum64_swap(double v) {
+  const uint64_t b = uint64_t(__double_as_longlong(v));
+  const Both lo = both<M>(uint32_t(b)), hi = both<M>(uint32_t(b >> 32));
+  return __longlong_as_double((long long)((uint64_t(hi.clear) << 32) | lo.clear)) +
+         __longlong_as_double((long long)((uint64_t(hi.set) << 32) | lo.set));
+}
+
 // |x| as an fp32 number on the same side of every number of few bits: where x lies
 // between two fp32 numbers, the one whose last bit is 1.
 __device__ __forceinline__ float to_odd(double x) {
@@ -218,6 +228,48 @@ __device__ __forceinline__ MxWord encode64(const float (&v)[8], int lane) {
   return MxWord{fp4_word(f), gather_scales<BLOCK>(finite ? uint32_t(E + 127) : 255u, l), h128_lane_word(l)};
 }
 
+// The codes of y + d (w) and y - d (other) differ here and there: those values again,
+// one of each Hadamard block at a time.  Every lane adds its part of the output in fp64:
+// output (o, e) of a lane and an element takes x of (m, j) with the sign
+// (-1)^(|o & m| + |e & j|).  A few of a wave's values cost less this way than its rows
+// (an eighth of the instructions, which the wave also has to fetch): 2048 x 4096 bf16
+// 7.0 us, 7.8 with encode64 for all of them, 6.1 without either.
+template <int BLOCK>
+__device__ __forceinline__ uint32_t settle(const float (&x)[8], uint32_t w, uint32_t other, float inv, int lane) {
+  constexpr int kLanes = BLOCK / 8;
+  constexpr uint64_t kBits = ~uint64_t(0) >> (64 - kLanes);
+  const int base = lane & (64 - kLanes), m = lane & (kLanes - 1);
+  uint32_t open = w ^ other;
+  for (uint64_t lanes = __builtin_amdgcn_ballot_w64(open != 0); lanes != 0;
+       lanes = __builtin_amdgcn_ballot_w64(open != 0)) {
+    const uint64_t mine = (lanes >> base) & kBits;  // none: the first lane's first value, not stored
+    const int from = base + (mine != 0 ? __builtin_ctzll(mine) : 0);
+    const uint32_t its = uint32_t(__builtin_amdgcn_ds_bpermute(4 * from, int(open)));
+    const int e = its != 0 ? __builtin_ctz(its) >> 2 : 0;
+    const int o = h128_lane_word(from & 15) | (from & (kLanes - 1) & ~15);
+    const uint32_t signs = ((e & 1) ? 0xAAu : 0u) ^ ((e & 2) ? 0xCCu : 0u) ^ ((e & 4) ? 0xF0u : 0u) ^
+                           ((__builtin_popcount(o & m) & 1) ? 0xFFu : 0u);
+    double u = 0.0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      u += double(__uint_as_float(__float_as_uint(x[j]) ^ ((signs << (31 - j)) & 0x80000000u)));
+    u += dpp64<0xB1>(u);
+    u += dpp64<0x4E>(u);
+    u += dpp64<0x141>(u);
+    u += dpp64<0x128>(u);
+    if constexpr (BLOCK >= 256) u = sum64_swap<16>(u);
+    if constexpr (BLOCK >= 512) u = sum64_swap<32>(u);
+    u *= kPost64<BLOCK>;
+    const float a = to_odd(fabs(u) * double(inv)), f = u < 0.0 ? -a : a;
+    const uint32_t code = uint32_t(__builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0, f, f, 1.0f, 0)) & 15u;
+    if (lane == from) {
+      w = (w & ~(15u << (4 * e))) | code << (4 * e);
+      open &= ~(15u << (4 * e));
+    }
+  }
+  return w;
+}
+
 // The lane's 8 channels of a row (16 lanes hold 128, the wave 512), encoded.
 // Every lane of the wave takes part.
 template <int BLOCK>
@@ -270,11 +322,16 @@ __device__ __forceinline__ MxWord encode(const float (&x)[8], int lane) {
       lo[e] = fmaf(v[e], c, -d);
       hi[e] = fmaf(v[e], c, d);
     }
-    const uint32_t w = S != 0.0f ? fp4_word(hi) : 0u;
+    uint32_t w = fp4_word(hi);  // zeros: of d, 0
+    const uint32_t other = S != 0.0f ? fp4_word(lo) : w;
     // Sums beyond 2^100 (and what is not finite) could leave fp32; below 2^-90 the
     // products above could lose bits; without any value all is zero.
-    const bool sure = w == fp4_word(lo) && at == __float_as_uint(most - most_err) >> 23 && S < 0x1p100f && S > 0x1p-90f;
-    if (__builtin_amdgcn_ballot_w64(!sure && S != 0.0f) != 0) return encode64<BLOCK>(x, lane);
+    const bool known = (at == __float_as_uint(most - most_err) >> 23 && S < 0x1p100f && S > 0x1p-90f) || S == 0.0f;
+    const uint64_t open = __builtin_amdgcn_ballot_w64(w != other || !known);
+    if (open != 0) {
+      if (__builtin_popcountll(open) > 4 || __builtin_amdgcn_ballot_w64(!known) != 0) return encode64<BLOCK>(x, lane);
+      w = settle<BLOCK>(x, w, other, inv, lane);
+    }
     return MxWord{w, gather_scales<BLOCK>(uint32_t(E + 127), l), h128_lane_word(l)};
   }
 }
@@ -284,15 +341,15 @@ __device__ __forceinline__ MxWord encode(const float (&x)[8], int lane) {
 // waves of a block side by side along a row.  The next row's values are on their way
 // while the current ones are computed.  QUAD: 4 consecutive rows at a time, whose
 // scales go out together, 16 bytes a group (where there are rows enough for every
-// wave: at 4096 x 14336 single words took 5 us more).
+// wave: at 4096 x 14336 single words took 5 us more); the last ones singly.
 //   Lanes behind the last channel load zeros and store out of range, where the hardware
 // drops it: a branch around a store would make the compiler wait for everything in
 // flight, the next row's values among it.  Rows are at most 2^28, so the offsets of
 // four groups' scales stay in 32 bits.
-//   Bound by the vector units, some 20 instructions a channel: 4096 x 14336 bf16, block
-// 128, 35 us (149 MB at 4.2 TB/s, where a copy reaches 4.9; a busy CU issues a vector
-// instruction in all of its cycles).  1333 x 8192 fp32, block 256, signs, 13 us (49 MB at
-// 3.8 TB/s: two to three rows a wave, whose first loads nothing covers).
+//   Bound by the vector units, some 18 instructions a channel: 4096 x 14336 bf16, block
+// 128, 33 us (149 MB at 4.5 TB/s, where a copy reaches 4.9; with the 4 rows as a loop, whose
+// waits count less exactly, 35).  1333 x 8192 fp32, block 256, signs, 13 us (49 MB at 3.8
+// TB/s: two to three rows a wave, whose first loads nothing covers).
 // ---------------------------------------------------------------------------
 template <bool BF16, int BLOCK, bool SIGNED, bool QUAD>
 __global__ __launch_bounds__(256) void mx_quantize_kernel(MxRows a, uint32_t spans, uint32_t walkers) {
@@ -301,16 +358,17 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(MxRows a, uint32_t spa
   const int lane = threadIdx.x & 63, g = lane >> 4;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
   const int64_t k0 = int64_t(wave % spans) * kSpan;
-  int64_t row = int64_t(wave / spans) * kRows;
-  if (wave / spans >= walkers || row >= a.rows) return;
+  const int rows = int(a.rows), stride = int(walkers) * kRows;
+  int row = int(wave / spans) * kRows;
+  if (wave / spans >= walkers || row >= rows) return;
   const int channels = int(a.K - k0 < kSpan ? a.K - k0 : kSpan);
   const char* const x = reinterpret_cast<const char*>(a.x) + k0 * kSize;
   struct Raw {
     v4u v[kLoads];
   };
-  auto load = [&](int64_t r) {
-    const __amdgpu_buffer_rsrc_t from = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(x + r * a.stride_row * kSize), 0,
-                                                                          channels * kSize, 0x00020000);
+  auto load = [&](int r) {
+    const __amdgpu_buffer_rsrc_t from = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char*>(x + r * a.stride_row * kSize), 0, channels * kSize, 0x00020000);
     Raw raw;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) raw.v[i] = __builtin_amdgcn_raw_buffer_load_b128(from, lane * (8 * kSize) + 16 * i, 0, 0);
@@ -328,16 +386,9 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(MxRows a, uint32_t spa
     }
   }
   const uint32_t group = uint32_t(a.rows) * 4;  // bytes from one group's scales to the next
-  const int scale_range = int(group * ((channels >> 7) - 1) + 4 * kRows);
+  const uint32_t scale_range = group * ((channels >> 7) - 1);  // in front of the last group's
   const int scale_at = (lane & 15) == 0 && 128 * g < channels ? int(g * group) : -1;
-  v4u scales{};
-  Raw next = load(row);
-  for (int i = 0;;) {
-    const Raw raw = next;
-    int64_t row2 = row + 1;
-    if (!QUAD || i == kRows - 1) row2 = row + int64_t(walkers) * kRows - (kRows - 1);
-    const bool last = row2 >= a.rows && (!QUAD || i == kRows - 1 || row + 1 >= a.rows);
-    next = load(row2 < a.rows ? row2 : row);
+  auto encode_row = [&](const Raw& raw, int r) {  // stores its codes; its scales
     float v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -345,35 +396,35 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(MxRows a, uint32_t spa
       else v[e] = __uint_as_float(raw.v[(e >> 2) % kLoads][e & 3]);
       if constexpr (SIGNED) v[e] = __uint_as_float(__float_as_uint(v[e]) ^ sign[e]);
     }
-    const MxWord r = encode<BLOCK>(v, lane);
+    const MxWord w = encode<BLOCK>(v, lane);
     __builtin_amdgcn_raw_buffer_store_b32(
-        r.codes, __builtin_amdgcn_make_buffer_rsrc(a.q + row * (a.K >> 1) + (k0 >> 1), 0, channels >> 1, 0x00020000),
-        64 * g + 4 * r.word, 0, 0);
-    if constexpr (QUAD) {
-      scales = v4u{scales[1], scales[2], scales[3], r.scales};
-      if (i == kRows - 1) {
-        __builtin_amdgcn_raw_buffer_store_b128(
-            scales, __builtin_amdgcn_make_buffer_rsrc(a.s + ((k0 >> 7) * a.rows + row - 3) * 4, 0, scale_range, 0x00020000),
-            scale_at, 0, 0);
-      } else if (row + 1 >= a.rows) {  // the last rows, fewer than 4
-        const int first = 3 - i;       // of their words in `scales`
+        w.codes, __builtin_amdgcn_make_buffer_rsrc(a.q + r * (a.K >> 1) + (k0 >> 1), 0, channels >> 1, 0x00020000),
+        64 * g + 4 * w.word, 0, 0);
+    return w.scales;
+  };
+  auto scales_of = [&](int r) { return a.s + ((k0 >> 7) * a.rows + r) * 4; };
+  Raw next = load(row);
+  if constexpr (QUAD) {
+    for (; row + 4 <= rows; row += stride) {
+      v4u scales;
 #pragma unroll
-        for (int e = 1; e < 4; ++e)
-          if (e >= first)
-            __builtin_amdgcn_raw_buffer_store_b32(
-                scales[e],
-                __builtin_amdgcn_make_buffer_rsrc(a.s + ((k0 >> 7) * a.rows + row - 3 + e) * 4, 0,
-                                                  int(group * ((channels >> 7) - 1) + 4), 0x00020000),
-                scale_at, 0, 0);
+      for (int i = 0; i < 4; ++i) {
+        const Raw raw = next;
+        const int r2 = i < 3 ? row + i + 1 : row + stride;
+        next = load(r2 < rows ? r2 : row);
+        scales[i] = encode_row(raw, row + i);
       }
-      i = (i + 1) & 3;
-    } else {
-      __builtin_amdgcn_raw_buffer_store_b32(
-          r.scales, __builtin_amdgcn_make_buffer_rsrc(a.s + ((k0 >> 7) * a.rows + row) * 4, 0, scale_range, 0x00020000),
-          scale_at, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b128(
+          scales, __builtin_amdgcn_make_buffer_rsrc(scales_of(row), 0, int(scale_range + 16), 0x00020000), scale_at, 0, 0);
     }
-    if (last) return;
-    row = row2;
+  }
+  for (; row < rows; row += QUAD ? 1 : stride) {  // QUAD: the last rows, fewer than 4
+    const Raw raw = next;
+    const int r2 = row + (QUAD ? 1 : stride);
+    next = load(r2 < rows ? r2 : row);
+    const uint32_t scales = encode_row(raw, row);
+    __builtin_amdgcn_raw_buffer_store_b32(
+        scales, __builtin_amdgcn_make_buffer_rsrc(scales_of(row), 0, int(scale_range + 4), 0x00020000), scale_at, 0, 0);
   }
 }
 

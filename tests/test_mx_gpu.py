@@ -106,6 +106,33 @@ def test_many_codes():
     _check(rw4.mx_quantize_act(t, x), omx.rotate(np64(x), 128), "2048x4096")
 
 
+@pytest.mark.parametrize("block", [128, 256, 512])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("kind", ["gauss", "outliers"])
+def test_many_codes_of_every_block(kind, block, dtype):
+    # a few values of a wave near a border, and exact ties (block 256 of bf16)
+    rng = np.random.default_rng(50 + block)
+    x = dev(_rows(kind, rng, 515, 4096), dtype)
+    t, signs = _transform(4096, block, block == 512)
+    y = omx.rotate(np64(x), block, signs)
+    _check(rw4.mx_quantize_act(t, x), y, "rows")
+    _check(rw4.mx_pack_weight(t, x.t().contiguous()), y, "columns")
+
+
+@pytest.mark.parametrize("kind", ["gauss", "integers"])
+def test_many_rows(kind):
+    # rows enough for four at a time, and the last ones fewer: the same rows again in a small call
+    rng = np.random.default_rng(60)
+    x = dev(_rows(kind, rng, 1003, 512), BF16).repeat(34, 1)[:34101]
+    t, signs = _transform(512, 256, False)
+    q, s = rw4.mx_quantize_act(t, x)
+    _check((q[:1003].contiguous(), s[:, :1003].contiguous()), omx.rotate(np64(x[:1003]), 256), "first")
+    assert torch.equal(q[1003:33099].view(-1, 1003, 256), q[:1003].expand(32, 1003, 256))
+    assert torch.equal(q[33099:], q[:1002])
+    assert torch.equal(s[:, 1003:33099].view(4, -1, 1003, 4), s[:, None, :1003].expand(4, 32, 1003, 4))
+    assert torch.equal(s[:, 33099:], s[:, :1002])
+
+
 @pytest.mark.parametrize("block", [1, 128, 512])
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_not_finite(block, dtype):
