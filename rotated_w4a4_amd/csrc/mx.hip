@@ -346,10 +346,10 @@ __device__ __forceinline__ MxWord encode(const float (&x)[8], int lane) {
 // drops it: a branch around a store would make the compiler wait for everything in
 // flight, the next row's values among it.  Rows are at most 2^28, so the offsets of
 // four groups' scales stay in 32 bits.
-//   Bound by the vector units, some 18 instructions a channel: 4096 x 14336 bf16, block
-// 128, 33 us (149 MB at 4.5 TB/s, where a copy reaches 4.9; with the 4 rows as a loop, whose
-// waits count less exactly, 35).  1333 x 8192 fp32, block 256, signs, 13 us (49 MB at 3.8
-// TB/s: two to three rows a wave, whose first loads nothing covers).
+//   Bound by the vector units, some 18 instructions a channel, and memory: 4096 x 14336
+// bf16, block 128, 32 us (149 MB at 4.7 TB/s, where a copy reaches 4.9; with the 4 rows as a
+// loop, whose waits count less exactly, 34).  1333 x 8192 fp32, block 256, signs, 12 us
+// (49 MB at 4.2 TB/s: two to three rows a wave, whose first loads nothing covers).
 // ---------------------------------------------------------------------------
 template <bool BF16, int BLOCK, bool SIGNED, bool QUAD>
 __global__ __launch_bounds__(256) void mx_quantize_kernel(MxRows a, uint32_t spans, uint32_t walkers) {
