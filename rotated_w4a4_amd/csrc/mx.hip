@@ -232,7 +232,7 @@ __device__ __forceinline__ MxWord encode64(const float (&v)[8], int lane) {
 // one of each Hadamard block at a time.  Every lane adds its part of the output in fp64:
 // output (o, e) of a lane and an element takes x of (m, j) with the sign
 // (-1)^(|o & m| + |e & j|).  A few of a wave's values cost less this way than its rows
-// (an eighth of the instructions, which the wave also has to fetch): 2048 x 4096 bf16
+// (a quarter of the instructions, which the wave also has to fetch): 2048 x 4096 bf16
 // 7.0 us, 7.8 with encode64 for all of them, 6.1 without either.
 template <int BLOCK>
 __device__ __forceinline__ uint32_t settle(const float (&x)[8], uint32_t w, uint32_t other, float inv, int lane) {

@@ -26,7 +26,6 @@ namespace {
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef unsigned int v4u __attribute__((ext_vector_type(4)));
-typedef unsigned int v2u __attribute__((ext_vector_type(2)));
 typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void lds_void_t;
 
@@ -115,11 +114,10 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void mx_gemm_kernel(
   using T = Tile<BM, BN, WM, WN>;
   constexpr int TM = T::TM, TN = T::TN;
   // objects of their own: the compiler sees that the DMA into one never writes what is read from another
-  static_assert(RING >= 2 && RING <= 4, "buffers of the ring");
+  static_assert(RING == 2 || RING == 3, "buffers of the ring");
   __shared__ __align__(16) uint8_t buf0[T::bytes];
   __shared__ __align__(16) uint8_t buf1[T::bytes];
   __shared__ __align__(16) uint8_t buf2[RING > 2 ? T::bytes : 16];
-  __shared__ __align__(16) uint8_t buf3[RING > 3 ? T::bytes : 16];
 
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, h = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -240,10 +238,6 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void mx_gemm_kernel(
 #pragma unroll
     for (int i = 0; i < T::loads; ++i) bring(buf2, 2, i);
   }
-  if constexpr (RING > 3) {
-#pragma unroll
-    for (int i = 0; i < T::loads; ++i) bring(buf3, 3, i);
-  }
   wait_vm<(RING - 1) * T::loads>();
   block_barrier();
 #pragma unroll
@@ -262,21 +256,14 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void mx_gemm_kernel(
     stage(buf0, buf1, s);
     if constexpr (RING == 2) {
       stage(buf1, buf0, s + 1);
-    } else if constexpr (RING == 3) {
-      stage(buf1, buf2, s + 1);
-      stage(buf2, buf0, s + 2);
     } else {
       stage(buf1, buf2, s + 1);
-      stage(buf2, buf3, s + 2);
-      stage(buf3, buf0, s + 3);
+      stage(buf2, buf0, s + 2);
     }
   }
   if (s < stages) stage(buf0, buf1, s);
   if constexpr (RING > 2) {
     if (s + 1 < stages) stage(buf1, buf2, s + 1);
-  }
-  if constexpr (RING > 3) {
-    if (s + 2 < stages) stage(buf2, buf3, s + 2);
   }
   __syncthreads();  // the DMA behind the last stage included
 
