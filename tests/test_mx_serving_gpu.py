@@ -240,6 +240,32 @@ def test_single_tokens_times_more_channels_than_a_grid_of_16_holds(M):
         assert ((y[:, first:first + 100].double() - a @ w).abs() <= tol).all(), first
 
 
+@pytest.mark.parametrize("M,N", [(1, 5), (3, 40), (70, 33)])
+def test_longest_rows(M, N):
+    # K = 2^23: codes are those of the row's pieces; the product against sums in 64 bits
+    K, piece = 2 ** 23, 4096
+    g = torch.Generator(device=ku.DEV)
+    g.manual_seed(3)
+    a = torch.randn(M, K, device=ku.DEV, generator=g).to(BF16)
+    w = torch.randn(N, K, device=ku.DEV, generator=g).to(BF16)
+    qa, sa = rw4.mx_quantize_act(None, a)
+    qw, sw = rw4.mx_pack_weight(None, w, layout="nk")
+    eq, es = rw4.mx_quantize_act(None, a.view(-1, piece))
+    assert torch.equal(qa.view(-1, piece // 2), eq)
+    assert torch.equal(sa.view(K // piece, piece // 128, M, 4), es.view(piece // 128, M, K // piece, 4).permute(2, 0, 1, 3))
+    a, w = rw4.mx_dequantize(qa, sa), rw4.mx_dequantize(qw, sw)
+    want = torch.zeros(M, N, dtype=torch.float64, device=ku.DEV)
+    size = torch.zeros_like(want)
+    for k in range(0, K, 2 ** 18):
+        x, z = a[:, k:k + 2 ** 18].double(), w[:, k:k + 2 ** 18].double().t().contiguous()
+        want += x @ z
+        size += x.abs() @ z.abs()
+    y = rw4.mx_gemm(qa, sa, qw, sw, F32)
+    # a product of 128 channels and its addition round within 128 half steps of what they add; K / 128 of them in a row
+    tol = (K / 128 + 128) * 2.0 ** -24 * size
+    assert ((y.double() - want).abs() <= tol).all()
+
+
 def test_results_do_not_depend_on_the_other_rows():
     # a row alone, among others, and beside rows of NaN: the same codes; the product of the same kernel the same bits
     rng = np.random.default_rng(31)
