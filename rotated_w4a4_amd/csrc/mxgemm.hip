@@ -16,6 +16,7 @@
 // lane ends with one token and 4 consecutive channels: D[4 (l / 16) + r][l % 16].
 #include <type_traits>
 
+#include "mx_index.h"
 #include "mx_internal.h"
 #include "rw4_device.h"
 
@@ -339,7 +340,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void mx_gemm_kernel(
 // x 4096 channels, K = 14336, 8.8 us against 15.6 (64 x 64 tiles whose waves split K like
 // here took 17, 32 x 32 straight from memory to registers 16).
 // ---------------------------------------------------------------------------
-constexpr int kSplitTile = 32, kSplitWaves = 4, kSplitRow = 256, kSplitRing = 4;
+constexpr int kSplitTile = kMxSplitTile, kSplitWaves = 4, kSplitRow = 256, kSplitRing = 4;
 constexpr int kSplitCodes = 2 * kSplitTile * kSplitRow, kSplitBytes = kSplitCodes + kSplitWaves * 2 * kSplitTile * 4;
 constexpr int kSplitLoads = kSplitCodes / 1024 / kSplitWaves + 1;  // DMA instructions of a wave for a stage
 
@@ -467,7 +468,7 @@ __global__ __launch_bounds__(64 * kSplitWaves) void mx_gemm_split_kernel(
 // 22.7 / 21.1, 1 x 28672 x 8192 29.5 / 23.8, 1 x 4096 x 8192 6.6 / 5.3 (rows of 4 KB share
 // their memory channels).
 // ---------------------------------------------------------------------------
-constexpr int kFewWaves = 8, kFewTokens = 16, kFewChannels = 16;
+constexpr int kFewWaves = 8, kFewTokens = 16, kFewChannels = kMxFewChannels;
 
 template <int PAIR, bool BF16>
 __global__ __launch_bounds__(64 * kFewWaves) void mx_gemm_few_kernel(
@@ -531,7 +532,6 @@ hipError_t launch_mx_gemm(const uint8_t* qa, const uint8_t* sa, const uint8_t* q
                           int64_t N, int64_t K, void* y, bool y_bf16, int64_t ldy, hipStream_t st) {
   const uint32_t* xa = reinterpret_cast<const uint32_t*>(sa);
   const uint32_t* xw = reinterpret_cast<const uint32_t*>(sw);
-  constexpr int64_t kMostBlocks = int64_t(1) << 22;  // of 512 threads: a grid has fewer than 2^32
   auto few = [&](auto pair) {
     constexpr int P = decltype(pair)::value;
     const dim3 grid{unsigned((N + kFewChannels - 1) / kFewChannels)}, threads{64 * kFewWaves};
@@ -554,7 +554,7 @@ hipError_t launch_mx_gemm(const uint8_t* qa, const uint8_t* sa, const uint8_t* q
     constexpr int BM = decltype(bm)::value, BN = decltype(bn)::value, WM = decltype(wm)::value, WN = decltype(wn)::value,
                   R = decltype(ring)::value;
     const int64_t tiles_m = (M + BM - 1) / BM, blocks = tiles_m * ((N + BN - 1) / BN);
-    if (blocks > kMostBlocks) return hipErrorInvalidValue;  // 2^38 outputs, or 2^22 times 256 rows: none fits the card
+    if (blocks > kMxMostBlocks) return hipErrorInvalidValue;  // 2^38 outputs, or 2^22 times 256 rows: none fits the card
     const dim3 grid{unsigned(blocks)}, threads{64 * WM * WN};
     if (y_bf16)
       hipLaunchKernelGGL((mx_gemm_kernel<BM, BN, WM, WN, R, true>), grid, threads, 0, st, qa, xa, qw, xw, M, N, K, y, ldy,
@@ -571,27 +571,14 @@ hipError_t launch_mx_gemm(const uint8_t* qa, const uint8_t* sa, const uint8_t* q
   const integral_constant<int, 64> k64{};
   const integral_constant<int, 128> k128{};
   const integral_constant<int, 256> k256{};
-  // Measured at M x N, K = 4096 (in brackets 14336), us, the launch included.
-  const bool longer = K > 4096;
-  //   Single tokens / 32 x 32:  1 x 4096 3.9 (7.3) / 4.4 (7.9), 4 x 4096 3.8 (7.6) / 4.4 (8.0), 4 x 14336
-  //   8.2 (23.2) / 7.8 (20.0), 8 x 4096 4.0 / 4.4, 8 x 14336 8.7 / 7.8; 1 x 65536 26.6 / 30.9, 8 x 65536 35.6 / 31.5
-  if (M <= 4 && N <= kMostBlocks * kFewChannels) return longer ? few(k4) : few(k2);
-  //   32 x 32 / 64 x 64, by small tiles:  61 x 4096 (256) 4.9 (8.8) / 6.3 (15.6), 32 x 11008 (344)
-  //   7.9 / 6.8, 61 x 6144 (384) 7.0 (14.3) / 6.6 (16.0), 128 x 4096 (512) 6.9 (14.5) / 6.4 (15.8),
-  //   61 x 11008 (688) 9.5 / 6.9, 256 x 4096 (1024) 11.5 (25.2) / 7.0 (16.7)
-  if (((M + 31) / 32) * ((N + 31) / 32) <= (longer ? 512 : 288)) return split();
-  // 64 x 64, 128 x 128: up to 3 of the small tiles for each CU
-  //   512 x 4096 (512 small tiles) 10.1 (25.4) / 13.3 (38.3), 256 x 11008 (688) 13.0 / 13.4,
-  //   384 x 8192 (768) 13.2 / 13.4, 1024 x 4096 (1024) 17.0 (50.2) / 14.2 (42.1)
-  const int64_t small = ((M + 63) / 64) * ((N + 63) / 64);
-  if (small <= 768) return many(k64, k64, k2, k2, k3);
-  // 128 x 128, 256 x 256: the large tiles where they fill 7/8 of the rounds of a block for
-  // each CU that they take
-  //   2048 x 4096 (128 large tiles) 21.4 (62.8) / 29.2 (84.8), 2048 x 6144 (192) 30.5 / 30.7, 2048 x 8192 (256)
-  //   39.8 / 36.6, 3000 x 6144 (288) 47.0 / 58.6, 2048 x 14336 (448) 66.3 / 64.6, 4096 x 4096 (256) (123.7) / (104.2)
-  //   (128 x 256 tiles, 4 or 8 waves: 21.8 to 23.6 at 2048 x 4096, 118 at 4096 x 4096, K = 14336)
-  const int64_t large = ((M + 255) / 256) * ((N + 255) / 256), rounds = (large + 255) / 256;
-  return 8 * large >= 7 * 256 * rounds ? many(k256, k256, k4, k2, k2) : many(k128, k128, k2, k2, k2);
+  switch (mx_gemm_kernel(M, N, K)) {
+    case MxKernel::Few2: return few(k2);
+    case MxKernel::Few4: return few(k4);
+    case MxKernel::Split: return split();
+    case MxKernel::Tile64: return many(k64, k64, k2, k2, k3);
+    case MxKernel::Tile128: return many(k128, k128, k2, k2, k2);
+    default: return many(k256, k256, k4, k2, k2);
+  }
 }
 
 }  // namespace rw4
