@@ -41,3 +41,9 @@ static_assert(mx_gemm_kernel(1, rows, 128) == MxKernel::Tile256 && mx_gemm_kerne
 // single tokens: the grid they are given holds every channel
 static_assert(((int64_t(1) << 26) + kMxFewChannels - 1) / kMxFewChannels <= kMxMostBlocks);
 """)
+
+
+def test_shapes_of_the_longest_rows_take_their_kernel(tmp_path):
+    from tests.test_mx_longest_gpu import K, SHAPES as longest
+    _compile(tmp_path, "".join(f"static_assert(mx_gemm_kernel({M}, {N}, {K}) == MxKernel::{k});\n"
+                               for k, (M, N) in longest.items()))
