@@ -460,10 +460,15 @@ rw4_status rw4_dequantize_g(const uint8_t* q, const float* s, int64_t M, int64_t
  *   E = clamp(floor(log2 max |y|) - 2, -127, 127)   (-127 for a block of zeros),
  *   code = y 2^-E to the nearest of the values above, ties to the even index,
  *   beyond 6 to 6; a code keeps the sign of a value that rounds to zero.
- * Codes and scales are those of the exact y (evaluated in 32 bits with a bound of
- * the error, in 64 bits where the bound does not decide).  A block whose largest y
- * is infinite or NaN gets the scale 255 and codes 0; a Hadamard spreads one such
- * value over its whole block.
+ * y is evaluated in 32 bits with a bound of the error, and in 64 bits where the bound
+ * does not decide.  So codes and scales are those of the exact y without a transform,
+ * and with one wherever the values of a Hadamard block are multiples of some unit and
+ * their sizes add up to less than 2^46 units (2^53 for blocks of 256): bf16 values
+ * whose exponents differ by less than 29, fp32 values by less than 13, and most blocks
+ * of wider range.  Beyond that they are those of a value that is off by less than
+ * 2^-49 sum |x| / sqrt(block); which one can then depend on the call's other rows.
+ * A block whose largest y is infinite or NaN gets the scale 255 and codes 0; a Hadamard
+ * spreads one such value over its whole block.
  * t: block Hadamards of 128, 256 or 512 channels, plain or signed; NULL for no
  * transform.  Larger blocks and Givens transforms give RW4_ERR_UNSUPPORTED: call
  * rw4_rotate_act with an fp32 output and quantize that with t NULL (codes are then

@@ -7,7 +7,8 @@ import numpy as np
 
 from .reference import hadamard
 
-__all__ = ["VALUES", "rotate", "quantize", "pack", "unpack", "scale_order", "values", "gemm"]
+__all__ = ["VALUES", "rotate", "quantize", "pack", "unpack", "scale_order", "values", "gemm",
+           "quantize_whole"]
 
 VALUES = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
 
@@ -75,3 +76,36 @@ def gemm(ca, sa, cw, sw):
     """(Y, the sums of the products' sizes), float64."""
     a, w = values(ca, sa), values(cw, sw)
     return a @ w.T, np.abs(a) @ np.abs(w).T
+
+
+def quantize_whole(x, block, unit):
+    """Codes and scale bytes of x R for x of whole numbers (int64 [rows, K], sums below 2^63) times 2^unit, in whole
+    numbers throughout: |y| against a border t is u^2 against t^2 block."""
+    rows, K = x.shape
+    u = (x.reshape(rows, -1, block) @ hadamard(block).astype(np.int64)).reshape(rows, K)
+    codes, scales = np.zeros((rows, K), np.uint8), np.zeros((rows, K // 32), np.uint8)
+
+    def at_least(n, quarters, e):
+        """(-1, 0, 1) as n / sqrt(block) is below, at or above quarters 2^(e - 2), n >= 0."""
+        left, right, e = n * n, quarters * quarters * block, 2 * (e - 2)
+        left, right = (left, right << e) if e >= 0 else (left << -e, right)
+        return (left > right) - (left < right)
+
+    for r in range(rows):
+        for b in range(K // 32):
+            part = [int(v) for v in u[r, 32 * b:32 * b + 32]]
+            top = max(abs(v) for v in part)
+            e = -127 - unit
+            if top > 0:
+                two = top.bit_length()  # 2^two > top >= top / sqrt(block)
+                while at_least(top, 4, two) < 0:
+                    two -= 1
+                e = max(-127, min(127, two - 2 + unit)) - unit
+            scales[r, b] = e + unit + 127
+            for i, v in enumerate(part):
+                code = 0
+                for k, quarters in enumerate((1, 3, 5, 7, 10, 14, 20)):  # between code k and k + 1; a tie to the even one
+                    side = at_least(abs(v), quarters, e)
+                    code += side > 0 or (side == 0 and k % 2 == 1)
+                codes[r, 32 * b + i] = code | (8 if v < 0 else 0)
+    return codes, scales

@@ -8,9 +8,9 @@
 //
 // A block whose maximum is not finite gets the scale 255 (NaN) and codes 0.
 //
-// Exactness.  Codes and exponents are those of the exact y.  The butterflies run
-// in fp32 and keep a bound of their error: each of the n stages rounds every
-// intermediate once, and the intermediates of a stage that an output depends on add
+// Exactness.  Codes and exponents are decided in fp32 where that is certain.  The
+// butterflies run in fp32 and keep a bound of their error: each of the n stages rounds
+// every intermediate once, and the intermediates of a stage that an output depends on add
 // up to at most S = sum |x| over the Hadamard block, so |u - exact| <= n 2^-24 S (1 +
 // tiny).  Forming y = u c 2^-E costs the roundings of c 2^-E and of the result, 2^-24 of
 // |y| < 8 each.  With
@@ -22,6 +22,13 @@
 // or the maximum could lie on either side of a power of two (encode64).  fp64 for every
 // row would take several times as long, fp32 alone would decide ties by the order of
 // its additions: with blocks of 256 and bf16 values, exact ties are common.
+//   In fp64 a sum of at most 13 additions, times the rounded 1 / sqrt(block), is off by
+// less than 15 2^-53 S / sqrt(block).  Sums of multiples of a unit below 2^53 units are
+// exact, and so is the factor 1/16.  For 128 and 512 borders are m 2^k sqrt(2) units, m =
+// 1, 3, 5, 7: no whole number below 2^46 comes closer to one of those than 2^-46.9 of it,
+// and the two roundings are 2^-52 together, so such sums are decided as the exact y is.
+// Larger ones can fall on a border's wrong side (124395540479019 is 5 2^44 sqrt(2) but for
+// 2^-54.6), and fp64 loses what is 2^53 times smaller than the sum.
 #include <type_traits>
 
 #include "mx_internal.h"
