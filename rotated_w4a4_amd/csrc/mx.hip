@@ -249,7 +249,7 @@ __device__ __forceinline__ uint32_t settle(const float (&x)[8], uint32_t w, uint
   uint32_t open = w ^ other;
   for (uint64_t lanes = __builtin_amdgcn_ballot_w64(open != 0); lanes != 0;
        lanes = __builtin_amdgcn_ballot_w64(open != 0)) {
-    const uint64_t mine = (lanes >> base) & kBits;  // none: the first lane's first value, not stored
+    const uint64_t mine = (lanes >> base) & kBits;  // none in the lane's block: its first value, not stored
     const int from = base + (mine != 0 ? __builtin_ctzll(mine) : 0);
     const uint32_t its = uint32_t(__builtin_amdgcn_ds_bpermute(4 * from, int(open)));
     const int e = its != 0 ? __builtin_ctz(its) >> 2 : 0;
@@ -269,7 +269,7 @@ __device__ __forceinline__ uint32_t settle(const float (&x)[8], uint32_t w, uint
     u *= kPost64<BLOCK>;
     const float a = to_odd(fabs(u) * double(inv)), f = u < 0.0 ? -a : a;
     const uint32_t code = uint32_t(__builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0, f, f, 1.0f, 0)) & 15u;
-    if (lane == from) {
+    if (its != 0 && lane == from) {
       w = (w & ~(15u << (4 * e))) | code << (4 * e);
       open &= ~(15u << (4 * e));
     }
