@@ -394,7 +394,8 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(MxRows a, uint32_t spa
   }
   const uint32_t group = uint32_t(a.rows) * 4;  // bytes from one group's scales to the next
   const uint32_t scale_range = group * ((channels >> 7) - 1);  // in front of the last group's
-  const int scale_at = (lane & 15) == 0 && 128 * g < channels ? int(g * group) : -1;
+  // -16: beyond every range, and the 16 bytes from there do not pass the end of 32 bits
+  const int scale_at = (lane & 15) == 0 && 128 * g < channels ? int(g * group) : -16;
   auto encode_row = [&](const Raw& raw, int r) {  // stores its codes; its scales
     float v[8];
 #pragma unroll

@@ -1,4 +1,5 @@
-"""Blocks whose codes are decided in fp32 beside blocks that are settled in 64 bits."""
+"""The MXFP4 quantizers write their codes and scales and nothing else: outputs between poisoned bytes, rows that end inside
+a wave's 512 channels, single and many rows; blocks whose codes are decided beside blocks that are settled in 64 bits."""
 import numpy as np
 import pytest
 
@@ -10,9 +11,42 @@ from oracle import mx as omx  # noqa: E402
 
 if torch.cuda.is_available():
     import rotated_w4a4_amd as rw4  # noqa: E402
-    from tests.kv_util import dev  # noqa: E402
+    from tests.kv_util import DEV, dev, np64  # noqa: E402
 
 F32, BF16, U8 = torch.float32, torch.bfloat16, torch.uint8
+AROUND = 1 << 16
+
+
+def _between(*shape):
+    """A contiguous uint8 tensor of `shape` with 64 KB of 0xEE on both sides, and the check that those stay."""
+    n = int(np.prod(shape))
+    flat = torch.full((n + 2 * AROUND + 16,), 0xEE, dtype=U8, device=DEV)
+
+    def stays():
+        assert (flat[:AROUND] == 0xEE).all() and (flat[AROUND + n:] == 0xEE).all()
+
+    return flat[AROUND:AROUND + n].view(*shape), stays
+
+
+@pytest.mark.parametrize("M,K,block", [(1, 128, 1), (1, 384, 128), (3, 640, 128), (2, 512, 256), (5, 512, 512), (257, 1152, 1),
+                                       (35003, 640, 128), (33000, 128, 1), (34001, 512, 256)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_outputs_end_where_they_end(M, K, block, dtype):
+    rng = np.random.default_rng(M + K)
+    few = min(M, 1001)
+    x = dev(rng.standard_normal((few, K)).astype(np.float32), dtype).repeat(-(-M // few), 1)[:M]
+    t = None if block == 1 else rw4.Transform.hadamard(K, block)
+    codes, scales = omx.quantize(omx.rotate(np64(x[:few]), block))
+    for call in (lambda **out: rw4.mx_quantize_act(t, x, q=out["q"], s=out["s"]),
+                 lambda **out: rw4.mx_pack_weight(t, x.t().contiguous(), qw=out["q"], sw=out["s"])):
+        (q, q_stays), (s, s_stays) = _between(M, K // 2), _between(K // 128, M, 4)
+        call(q=q, s=s)
+        q_stays()
+        s_stays()
+        want_q, want_s = dev(omx.pack(codes)), dev(omx.scale_order(scales))
+        rows = torch.arange(M, device=DEV) % few
+        assert torch.equal(q, want_q[rows]) and torch.equal(s, want_s[:, rows])
+
 
 @pytest.mark.parametrize("block", [128, 256])
 def test_settled_blocks_leave_the_others_alone(block):
