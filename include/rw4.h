@@ -475,7 +475,9 @@ rw4_status rw4_dequantize_g(const uint8_t* q, const float* s, int64_t M, int64_t
  * those of the rounded values).
  *
  * rw4_mx_pack_weight: the same for the output channels of w (element (k, n) at
- * w[k stride_k + n stride_n], strides positive), qw [N, K/2], sw [K/128, N, 4].
+ * w[k stride_k + n stride_n], strides positive), qw [N, K/2], sw [K/128, N, 4].  Fewer
+ * than 2^37 values with N counted in full 64s (2^38 for blocks of 256, and for 512, there
+ * in full 32s), where w is not [N, K] by 16-byte rows: RW4_ERR_SHAPE.
  *
  * rw4_mx_dequantize: the values, exact in fp32 and in bf16 (ldo elements a row,
  * 16-byte rows).

@@ -15,6 +15,7 @@
 #include "../../include/rw4.h"
 #include "kv_index.h"
 #include "kv_internal.h"
+#include "mx_index.h"
 #include "mx_internal.h"
 #include "rw4_internal.h"
 
@@ -670,6 +671,7 @@ rw4_status rw4_mx_pack_weight(const rw4_transform* t, const void* w, rw4_dtype w
   if ((reinterpret_cast<uintptr_t>(w) % esz) || !aligned16(qw) || !aligned16(sw)) return RW4_ERR_ARG;
   hipStream_t to = static_cast<hipStream_t>(stream);
   const bool rows = stride_k == 1 && stride_n >= K && aligned16(w) && (stride_n * esz) % 16 == 0;
+  if (!rows && rw4::mx_pack_blocks(N, K, a.block) > rw4::kMxPackMostBlocks) return RW4_ERR_SHAPE;
   return from_hip(rows ? rw4::launch_mx_quantize(a, to) : rw4::launch_mx_pack(a, to));
 }
 

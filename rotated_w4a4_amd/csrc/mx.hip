@@ -31,6 +31,7 @@
 // 2^-54.6), and fp64 loses what is 2^53 times smaller than the sum.
 #include <type_traits>
 
+#include "mx_index.h"
 #include "mx_internal.h"
 #include "rw4_device.h"
 
@@ -448,7 +449,7 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(MxRows a, uint32_t spa
 // ---------------------------------------------------------------------------
 template <int BLOCK>
 struct Pack {
-  static constexpr int span = BLOCK < 128 ? 128 : BLOCK, rows = BLOCK < 512 ? 64 : 32;
+  static constexpr int span = mx_pack_span(BLOCK), rows = mx_pack_rows(BLOCK);
   static constexpr int row = span + span / 8 + 1, lanes = span / 8;
 };
 
@@ -632,8 +633,7 @@ hipError_t launch_mx_pack(const MxRows& a, hipStream_t st) {
                       (reinterpret_cast<uintptr_t>(a.x) & 15) == 0;
   return by_kind(a, [&](auto bf16, auto block, auto sign) {
     using P = Pack<decltype(block)::value>;
-    const int64_t spans = a.K / P::span, blocks = (a.rows + P::rows - 1) / P::rows * spans;
-    if (blocks >= (int64_t(1) << 24)) return hipErrorInvalidValue;  // a grid has fewer than 2^32 threads; 2^37 values
+    const int64_t spans = a.K / P::span, blocks = mx_pack_blocks(a.rows, a.K, a.block);
     if (vector)
       hipLaunchKernelGGL((mx_pack_kernel<decltype(bf16)::value, decltype(block)::value, decltype(sign)::value, true>),
                          dim3(unsigned(blocks)), dim3(256), 0, st, a, spans);

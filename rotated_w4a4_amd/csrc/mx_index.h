@@ -1,5 +1,5 @@
-// Choice of the MXFP4 product's kernel: constants and arithmetic without any device
-// code, so that host compilers can check them too.
+// Grids of the MXFP4 kernels and the choice of the product's: constants and arithmetic
+// without any device code, so that host compilers can check them too.
 #pragma once
 
 #include <stdint.h>
@@ -41,6 +41,16 @@ constexpr MxKernel mx_gemm_kernel(int64_t M, int64_t N, int64_t K) {
   //   (128 x 256 tiles, 4 or 8 waves: 21.8 to 23.6 at 2048 x 4096, 118 at 4096 x 4096, K = 14336)
   const int64_t large = mx_tiles(M, N, 256), rounds = (large + 255) / 256;
   return 8 * large >= 7 * 256 * rounds ? MxKernel::Tile256 : MxKernel::Tile128;
+}
+
+// The kernel for rows of any strides takes so many rows and channels a block (Hadamard
+// blocks of 256 and 512: a whole one).
+constexpr int mx_pack_rows(int block) { return block < 512 ? 64 : 32; }
+constexpr int mx_pack_span(int block) { return block < 128 ? 128 : block; }
+constexpr int64_t kMxPackMostBlocks = (int64_t(1) << 24) - 1;  // of 256 threads: a grid has fewer than 2^32
+// K is a multiple of the block, and of 128.
+constexpr int64_t mx_pack_blocks(int64_t rows, int64_t K, int block) {
+  return (rows + mx_pack_rows(block) - 1) / mx_pack_rows(block) * (K / mx_pack_span(block));
 }
 
 }  // namespace rw4

@@ -19,7 +19,7 @@ struct MxRows {
 
 // Rows with stride_k = 1 and 16-byte rows.
 hipError_t launch_mx_quantize(const MxRows& a, hipStream_t st);
-// Rows of any strides.
+// Rows of any strides, mx_pack_blocks(rows, K, block) <= kMxPackMostBlocks.
 hipError_t launch_mx_pack(const MxRows& a, hipStream_t st);
 hipError_t launch_mx_dequantize(const uint8_t* q, const uint8_t* s, int64_t M, int64_t K, void* out, bool out_bf16,
                                 int64_t ldo, hipStream_t st);
