@@ -483,7 +483,8 @@ rw4_status rw4_dequantize_g(const uint8_t* q, const float* s, int64_t M, int64_t
  * 16-byte rows).
  *
  * rw4_mx_gemm: Y [M, N] = sum over 32-channel blocks of the scales' product times
- * the codes' products, fp32 sums, y_dtype output (ldy elements a row).
+ * the codes' products, fp32 sums, y_dtype output (ldy elements a row), at most 2^22
+ * tiles of 256 x 256 (2^38 values; RW4_ERR_SHAPE).
  * Outputs must not overlap inputs. */
 rw4_status rw4_mx_quantize_act(const rw4_transform* t, const void* x, rw4_dtype x_dtype, int64_t M, int64_t K,
                                int64_t ldx, uint8_t* q, uint8_t* s, void* stream);

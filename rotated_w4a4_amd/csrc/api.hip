@@ -695,6 +695,7 @@ rw4_status rw4_mx_gemm(const uint8_t* qa, const uint8_t* sa, const uint8_t* qw, 
   if (st == RW4_OK) st = mx_sizes(N, K);
   if (st != RW4_OK) return st;
   if (M == 0 || N == 0) return RW4_OK;
+  if (!rw4::mx_gemm_fits(M, N, K)) return RW4_ERR_SHAPE;
   if (!qa || !sa || !qw || !sw || !y) return RW4_ERR_ARG;
   if (ldy < N || ldy >= kMostMxStride || !aligned16(qa) || !aligned16(qw) || !aligned16(sa) || !aligned16(sw) || !aligned16(y))
     return RW4_ERR_ARG;

@@ -43,6 +43,11 @@ constexpr MxKernel mx_gemm_kernel(int64_t M, int64_t N, int64_t K) {
   return 8 * large >= 7 * 256 * rounds ? MxKernel::Tile256 : MxKernel::Tile128;
 }
 
+// Whether the kernel's grid holds the tiles: the other kernels have 2^13 at most.
+constexpr bool mx_gemm_fits(int64_t M, int64_t N, int64_t K) {
+  return mx_gemm_kernel(M, N, K) != MxKernel::Tile256 || mx_tiles(M, N, 256) <= kMxMostBlocks;
+}
+
 // The kernel for rows of any strides takes so many rows and channels a block (Hadamard
 // blocks of 256 and 512: a whole one).
 constexpr int mx_pack_rows(int block) { return block < 512 ? 64 : 32; }

@@ -23,6 +23,7 @@ hipError_t launch_mx_quantize(const MxRows& a, hipStream_t st);
 hipError_t launch_mx_pack(const MxRows& a, hipStream_t st);
 hipError_t launch_mx_dequantize(const uint8_t* q, const uint8_t* s, int64_t M, int64_t K, void* out, bool out_bf16,
                                 int64_t ldo, hipStream_t st);
+// mx_gemm_fits(M, N, K).
 hipError_t launch_mx_gemm(const uint8_t* qa, const uint8_t* sa, const uint8_t* qw, const uint8_t* sw, int64_t M,
                           int64_t N, int64_t K, void* y, bool y_bf16, int64_t ldy, hipStream_t st);
 

@@ -554,7 +554,6 @@ hipError_t launch_mx_gemm(const uint8_t* qa, const uint8_t* sa, const uint8_t* q
     constexpr int BM = decltype(bm)::value, BN = decltype(bn)::value, WM = decltype(wm)::value, WN = decltype(wn)::value,
                   R = decltype(ring)::value;
     const int64_t tiles_m = (M + BM - 1) / BM, blocks = tiles_m * ((N + BN - 1) / BN);
-    if (blocks > kMxMostBlocks) return hipErrorInvalidValue;  // 2^38 outputs, or 2^22 times 256 rows: none fits the card
     const dim3 grid{unsigned(blocks)}, threads{64 * WM * WN};
     if (y_bf16)
       hipLaunchKernelGGL((mx_gemm_kernel<BM, BN, WM, WN, R, true>), grid, threads, 0, st, qa, xa, qw, xw, M, N, K, y, ldy,
