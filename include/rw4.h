@@ -479,8 +479,10 @@ rw4_status rw4_dequantize_g(const uint8_t* q, const float* s, int64_t M, int64_t
  * than 2^37 values with N counted in full 64s (2^38 for blocks of 256, and for 512, there
  * in full 32s), where w is not [N, K] by 16-byte rows: RW4_ERR_SHAPE.
  *
- * rw4_mx_dequantize: the values, exact in fp32 and in bf16 (ldo elements a row,
- * 16-byte rows).
+ * rw4_mx_dequantize: the values (ldo elements a row, 16-byte rows), exact in fp32 and in
+ * bf16 up to 2^127 1.5; 4 and 6 times 2^126, and 2 and more times 2^127, are infinite
+ * there.  Values of 2^128 and more get such scales, which a Hadamard of finite fp32 or
+ * bf16 values can reach; rw4_mx_gemm takes them as they are.
  *
  * rw4_mx_gemm: Y [M, N] = sum over 32-channel blocks of the scales' product times
  * the codes' products, fp32 sums, y_dtype output (ldy elements a row), at most 2^22

@@ -138,7 +138,8 @@ def mx_pack_weight(t: Transform | None, w, layout: str = "kn", qw=None, sw=None)
 
 
 def mx_dequantize(q, s, out_dtype=None, out=None):
-    """The values [rows, K] of codes and scales, exact in bf16 (default) and fp32; a scale of 255 gives NaN."""
+    """The values [rows, K] of codes and scales, exact in bf16 (default) and fp32; a scale of 255 gives NaN, what is 2^128
+    or more (large codes with scales of 2^126 and 2^127) infinity."""
     fn, args, dev, what, _, result = _dequantize(q, s, out_dtype, out)
     _launch(fn, args, dev, what)
     return result

@@ -66,3 +66,25 @@ def test_settled_blocks_leave_the_others_alone(block):
     t = rw4.Transform.hadamard(K, block)
     for q, s in (rw4.mx_quantize_act(t, xf), rw4.mx_pack_weight(t, xf.t().contiguous())):
         assert np.array_equal(omx.unpack(q.cpu().numpy()), codes) and np.array_equal(s.cpu().numpy(), omx.scale_order(scales))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_values_beyond_the_types_range(dtype):
+    # a Hadamard of finite values that reaches 2^130: codes and scales hold it (saturating at 6 2^127), reading it back
+    # gives infinity, the product with small weights is finite again
+    K = 256
+    x = torch.full((3, K), 2.0 ** 127, dtype=dtype, device=DEV)
+    x[1, 128:] = 2.0 ** 124
+    x[2] = -x[2]
+    q, s = rw4.mx_quantize_act(rw4.Transform.hadamard(K, 128), x)
+    codes, scales = omx.quantize(omx.rotate(np64(x), 128))
+    assert np.array_equal(omx.unpack(q.cpu().numpy()), codes) and np.array_equal(s.cpu().numpy(), omx.scale_order(scales))
+    # sqrt(128) 2^127 = 2^130.5 is 6 at 2^127; sqrt(128) 2^124 = 5.66 2^125
+    big = [torch.inf, torch.inf, -torch.inf]
+    small = [torch.inf, 6 * 2.0 ** 125, -torch.inf]
+    back = rw4.mx_dequantize(q, s, dtype)
+    assert back[:, 0].tolist() == big and back[:, 128].tolist() == small
+    w = torch.zeros(2, K, device=DEV)
+    w[0, 0], w[1, 128] = 2.0 ** -100, 2.0 ** -110
+    y = rw4.mx_gemm(q, s, *rw4.mx_quantize_act(None, w), F32)
+    assert y.tolist() == [[6 * 2.0 ** 27, 6 * 2.0 ** 17], [6 * 2.0 ** 27, 6 * 2.0 ** 15], [-6 * 2.0 ** 27, -6 * 2.0 ** 17]]
