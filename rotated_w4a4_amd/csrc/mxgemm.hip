@@ -72,11 +72,12 @@ __device__ __forceinline__ void store_one(void* y, int64_t at, float v) {
 //   A row of a stage is eight 16-byte chunks, chunk c at place c ^ (row & 7), so that 8
 // lanes reading one chunk of 8 rows hit all banks; the DMA writes LDS in lane order,
 // so the exchange is in the addresses it reads from.
-//   Bound, 256 x 256: matrix units 52 % busy over the launch at 4096 x 4096, K = 14336, 104 us
-// (4.6 PFLOP/s; the products alone 89 us, power-limited, the loads alone 66); 128 x 128:
-// the loads through L2 (a CU takes in 60 to 90 GB/s) and LDS beside the products, 2048 x
-// 4096, K = 4096, 21.4 us (3.2 PFLOP/s, 4.9 of it launch, first loads and output); 64 x 64: the
-// loads' latency, 61 x 11008, K = 4096, 6.9 us (25 MB at 3.7 TB/s).
+//   Bound, operands in the cache.  256 x 256: matrix units 60 % of a CU's busy cycles at
+// 4096 x 4096, K = 14336, 104 us (4.6 PFLOP/s; the products alone 89 us, where power limits
+// them, the loads alone 66).  128 x 128: the loads through L2 (55 to 65 GB/s a CU, some
+// 64 KB of them in flight: a microsecond's latency under load) and LDS beside the
+// products, 2048 x 4096, K = 4096, 21.4 us (3.2 PFLOP/s, 4.9 of it launch, first loads and
+// output).  64 x 64: the loads' latency, 61 x 11008, K = 4096, 7.2 us (25 MB at 3.5 TB/s).
 // ---------------------------------------------------------------------------
 constexpr int kStageRow = kGroup;  // bytes of 256 channels
 
@@ -335,10 +336,11 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void mx_gemm_kernel(
 // tile and add up in LDS at the end.  The ring, the DMA and the exchange of chunks (place
 // c ^ (row & 15)) as above; a wave's operands of a stage are read during its products of
 // the stage before.
-//   A CU takes in some 60 GB/s by way of L2 however its tiles are shaped, so where 64 x 64
-// tiles are fewer than the CUs smaller ones are faster, though they read more: 61 tokens
-// x 4096 channels, K = 14336, 8.8 us against 15.6 (64 x 64 tiles whose waves split K like
-// here took 17, 32 x 32 straight from memory to registers 16).
+//   A CU takes in 55 to 65 GB/s by way of L2 in these kernels, as much as it has in flight
+// over the latency, so where 64 x 64 tiles are fewer than the CUs smaller ones are faster,
+// though they read more: 61 tokens x 4096 channels, K = 14336, in the cache 8.8 us against
+// 15.6, from memory 13.1 against 23.3 (64 x 64 tiles whose waves split K like here took
+// 17, 32 x 32 straight from memory to registers 16, both in the cache).
 // ---------------------------------------------------------------------------
 constexpr int kSplitTile = kMxSplitTile, kSplitWaves = 4, kSplitRow = 256, kSplitRing = 4;
 constexpr int kSplitCodes = 2 * kSplitTile * kSplitRow, kSplitBytes = kSplitCodes + kSplitWaves * 2 * kSplitTile * 4;
