@@ -22,7 +22,7 @@ constexpr int64_t mx_tiles(int64_t M, int64_t N, int64_t side) {
 
 // Measured at M x N, us, the launch included, operands from memory (several sets in turn,
 // larger than the cache together): K = 4096, in brackets 14336, or the K that is named.
-constexpr MxKernel mx_gemm_kernel(int64_t M, int64_t N, int64_t K) {
+constexpr MxKernel mx_kernel_for(int64_t M, int64_t N, int64_t K) {
   const bool longer = K > 4096;
   // Single tokens / 32 x 32:  1 x 4096 4.1 (8.2) / 4.4 (10.4), 4 x 4096 4.1 (8.5) / 4.5 (10.4), 1 x 65536
   //   26.7 (83.1) / 31.3 (82.6).  By tokens alone, which costs 4 tokens of many channels some time: 4 x
@@ -56,7 +56,7 @@ constexpr MxKernel mx_gemm_kernel(int64_t M, int64_t N, int64_t K) {
 
 // Whether the kernel's grid holds the tiles: the other kernels have 2^13 at most.
 constexpr bool mx_gemm_fits(int64_t M, int64_t N, int64_t K) {
-  return mx_gemm_kernel(M, N, K) != MxKernel::Tile256 || mx_tiles(M, N, 256) <= kMxMostBlocks;
+  return mx_kernel_for(M, N, K) != MxKernel::Tile256 || mx_tiles(M, N, 256) <= kMxMostBlocks;
 }
 
 // The kernel for rows of any strides takes so many rows and channels a block (Hadamard

@@ -572,7 +572,7 @@ hipError_t launch_mx_gemm(const uint8_t* qa, const uint8_t* sa, const uint8_t* q
   const integral_constant<int, 64> k64{};
   const integral_constant<int, 128> k128{};
   const integral_constant<int, 256> k256{};
-  switch (mx_gemm_kernel(M, N, K)) {
+  switch (mx_kernel_for(M, N, K)) {
     case MxKernel::Few2: return few(k2);
     case MxKernel::Few4: return few(k4);
     case MxKernel::Split: return split();

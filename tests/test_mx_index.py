@@ -29,15 +29,15 @@ def test_every_kernel_has_shapes(tmp_path):
 
 
 def test_shapes_take_their_kernel(tmp_path):
-    _compile(tmp_path, "".join(f"static_assert(mx_gemm_kernel({M}, {N}, {K}) == MxKernel::{kernel});\n"
+    _compile(tmp_path, "".join(f"static_assert(mx_kernel_for({M}, {N}, {K}) == MxKernel::{kernel});\n"
                                for kernel, M, N, K in ALL))
 
 
 def test_largest_operands(tmp_path):
     _compile(tmp_path, """
 constexpr int64_t rows = int64_t(1) << 28, longest = int64_t(1) << 23;
-static_assert(mx_gemm_kernel(rows, rows, longest) == MxKernel::Tile256);
-static_assert(mx_gemm_kernel(1, rows, 128) == MxKernel::Tile256 && mx_gemm_kernel(1, int64_t(1) << 26, 128) == MxKernel::Few2);
+static_assert(mx_kernel_for(rows, rows, longest) == MxKernel::Tile256);
+static_assert(mx_kernel_for(1, rows, 128) == MxKernel::Tile256 && mx_kernel_for(1, int64_t(1) << 26, 128) == MxKernel::Few2);
 // single tokens: the grid they are given holds every channel
 static_assert(((int64_t(1) << 26) + kMxFewChannels - 1) / kMxFewChannels <= kMxMostBlocks);
 """)
@@ -45,5 +45,5 @@ static_assert(((int64_t(1) << 26) + kMxFewChannels - 1) / kMxFewChannels <= kMxM
 
 def test_shapes_of_the_longest_rows_take_their_kernel(tmp_path):
     from tests.test_mx_longest_gpu import K, SHAPES as longest
-    _compile(tmp_path, "".join(f"static_assert(mx_gemm_kernel({M}, {N}, {K}) == MxKernel::{k});\n"
+    _compile(tmp_path, "".join(f"static_assert(mx_kernel_for({M}, {N}, {K}) == MxKernel::{k});\n"
                                for k, (M, N) in longest.items()))
